@@ -413,6 +413,113 @@ int64_t mxw_fwd_grid_size(int E, int R, int N);
 int mxfp8_quantize_tokens(const uint16_t* x, const int32_t* offs, int E, int M, int ld, int H, uint8_t* q,
                           uint8_t* s, void* stream);
 
+/* Element types of entries that take more than one. */
+#define MXW_BF16 0
+#define MXW_F32 1
+
+/*
+ * mxw_orthogonalize -- what an optimiser that orthogonalises its updates does
+ * with the weight gradients (or a momentum of them): for every expert g, with
+ * X = G[g] / (|G[g]|_F + eps), each step replaces
+ *
+ *     X <- a X + (b S + c S S) X,    S = X X^T
+ *
+ * with that step's (a, b, c) (for N > K the same on X^T), which drives the
+ * singular values of X towards 1 and keeps its singular vectors; out[g] is X
+ * after the last step.  The usual five steps of (3.4445, -4.7750, 2.0315) bring
+ * every singular value above about 0.01 |G|_2 into 0.7 .. 1.2.
+ *
+ * Arguments (pointers other than coeffs are caller-owned DEVICE memory):
+ *   G        [E, N, K] elements of `type` (MXW_BF16 or MXW_F32), the last axis
+ *            contiguous; rows row_stride >= K elements apart, experts
+ *            expert_stride >= 0 elements.
+ *   E, N, K  1 <= E <= MXW_MAX_EXPERTS, 1 <= N, K <= 65536; no multiples are
+ *            asked for.
+ *   coeffs   HOST memory, 3 * steps floats: (a, b, c) of each step, read
+ *            during the call.
+ *   steps    1 .. 32.
+ *   eps      >= 0, added to the norm.
+ *   out      bf16 [E, N, K], contiguous, fully overwritten; not overlapping G.
+ *   workspace, workspace_bytes  256-byte aligned device memory of at least
+ *            mxw_orthogonalize_workspace_size(E, N, K) bytes; contents
+ *            undefined on entry and exit, in use until the call's work is done.
+ *
+ * The norm's sum is taken in 64 bits; X, S and P = a I + b S + c S S are held
+ * in f16 times 2^10 between products, whose sums are FP32.  Against the same
+ * formula in 64 bits the result is off by about 0.13% of its norm (its own
+ * rounding to bf16: 0.17%).  An entry of X, S or P beyond +-63 (no published
+ * coefficients come near) overflows to infinity and shows as NaN.  An expert
+ * whose gradient is zero gets zeros; one with a NaN or infinity gets NaN, and
+ * no expert's result depends on another.  Bitwise reproducible run to run.
+ *
+ * Effects: enqueues 2 + 3 * steps kernels on `stream`, allocates nothing, keeps
+ * no state, never writes G, does not synchronise; graph-capturable.
+ * Returns MXW_OK or a negative MXW_ERR_* code.
+ */
+int mxw_orthogonalize(const void* G, int type, int64_t expert_stride, int64_t row_stride, int E, int N, int K,
+                      const float* coeffs, int steps, float eps, uint16_t* out, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* mxw_orthogonalize_workspace_size -- bytes of workspace that mxw_orthogonalize
+ * needs, or MXW_ERR_DIM.  Host-only. */
+int64_t mxw_orthogonalize_workspace_size(int E, int N, int K);
+
+/* Reductions of mxw_vocab_loss. */
+#define MXW_NONE 0
+#define MXW_MEAN 1
+#define MXW_SUM 2
+
+/*
+ * mxw_vocab_loss -- softmax cross entropy of hidden states against a large
+ * vocabulary, with its gradients, without keeping the logits.  For every token
+ * t with target y(t):
+ *
+ *     l_tv = sum_h x[t][h] w[v][h],  loss_t = log sum_v exp(l_tv) - l_t,y(t)
+ *     g_tv = (exp(l_tv) / sum_u exp(l_tu) - [v = y(t)]) * s
+ *     dx[t] = sum_v g_tv w[v],       dw[v] = sum_t g_tv x[t]
+ *
+ * Tokens whose target is ignore_index have loss 0 and no gradient.  MXW_NONE
+ * gives the loss of every token, MXW_SUM their sum, MXW_MEAN the sum divided by
+ * the number of tokens that are not ignored (0 if there is none).  s is
+ * grad_scale, divided by that number for MXW_MEAN: dx and dw are the gradients
+ * of grad_scale times the reduced loss (of the sum, for MXW_NONE).
+ *
+ * Arguments (caller-owned DEVICE memory):
+ *   x, ldx   bf16 [T, H], rows ldx >= H elements apart.
+ *   w, ldw   bf16 [V, H], rows ldw >= H elements apart.
+ *   targets  [T] int32 (target_bytes 4) or int64 (8).  A target outside
+ *            [0, V) that is not ignore_index makes that token's loss (and the
+ *            reduced loss) NaN and gives no gradient.
+ *   T, H, V  1 <= T <= 131072, 1 <= H <= 65536, 1 <= V <= 1048576, no
+ *            multiples asked for.  With H % 64 == 0, 16-byte aligned x and w
+ *            and row strides of whole 16 bytes the operands are read in place;
+ *            otherwise padded copies are made in the workspace, w's by pieces.
+ *   loss     FP32, [T] for MXW_NONE, one value otherwise.
+ *   dx, dw   bf16 [T, H] and [V, H], contiguous, fully overwritten; either may
+ *            be NULL (not wanted).  They overlap no input.
+ *   workspace, workspace_bytes  256-byte aligned device memory of at least
+ *            mxw_vocab_loss_workspace_size(...) bytes; contents undefined on
+ *            entry and exit, in use until the call's work is done.
+ *
+ * Logits, statistics and sums are FP32; the g of a piece of the vocabulary is
+ * rounded to bf16 before the two products that use it.  NaN in a token's x
+ * reaches that token's loss and dx, and dw; a NaN or infinite logit makes its
+ * token's loss NaN.  Bitwise reproducible run to run on the same device.
+ *
+ * Effects: enqueues kernels on `stream`, allocates nothing, keeps no state,
+ * never writes its inputs, does not synchronise; graph-capturable.
+ * Returns MXW_OK or a negative MXW_ERR_* code.
+ */
+int mxw_vocab_loss(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw, const void* targets,
+                   int target_bytes, int64_t ignore_index, int T, int H, int V, int reduction, float grad_scale,
+                   float* loss, uint16_t* dx, uint16_t* dw, void* workspace, size_t workspace_bytes, void* stream);
+
+/* mxw_vocab_loss_workspace_size -- bytes of workspace that mxw_vocab_loss needs
+ * on the current device, or a negative MXW_ERR_* code.  x and w are looked at
+ * for their alignment alone; grads: 1 if dx is wanted, plus 2 if dw is. */
+int64_t mxw_vocab_loss_workspace_size(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw, int T, int H,
+                                      int V, int grads);
+
 /* mxw_strerror -- a static, human-readable message for a return code. */
 const char* mxw_strerror(int code);
 

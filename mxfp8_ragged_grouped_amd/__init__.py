@@ -45,6 +45,8 @@ from .build import LIB as _LIB_PATH
 __all__ = ["wgrad", "mxfp8_wgrad_grouped", "mxfp8_wgrad_grouped_ws", "mxfp8_wgrad_grouped_noalloc", "workspace_size", "wgrad_bf16",
            "bf16_wgrad_grouped", "bf16_wgrad_grouped_ws", "bf16_workspace_size", "grid_size", "columns",
            "scale_shuffle", "tail_split", "fwd", "mxfp8_grouped_fwd", "fwd_grid_size", "quantize_tokens", "mxfp8_quantize_tokens",
+           "orthogonalize", "mxw_orthogonalize", "orthogonalize_workspace_size",
+           "vocab_cross_entropy", "mxw_vocab_loss", "vocab_loss_workspace_size",
            "strerror", "version", "library_path", "MxwError"]
 
 _lib = None
@@ -100,6 +102,16 @@ def _load():
     lib.mxw_fwd_grid_size.argtypes = [I, I, I]
     lib.mxfp8_quantize_tokens.restype = I
     lib.mxfp8_quantize_tokens.argtypes = [P, P, I, I, I, I, P, P, P]
+    L = ctypes.c_int64
+    F = ctypes.c_float
+    lib.mxw_orthogonalize.restype = I
+    lib.mxw_orthogonalize.argtypes = [P, I, L, L, I, I, I, ctypes.POINTER(F), I, F, P, P, S, P]
+    lib.mxw_orthogonalize_workspace_size.restype = L
+    lib.mxw_orthogonalize_workspace_size.argtypes = [I, I, I]
+    lib.mxw_vocab_loss.restype = I
+    lib.mxw_vocab_loss.argtypes = [P, L, P, L, P, I, L, I, I, I, I, F, P, P, P, P, S, P]
+    lib.mxw_vocab_loss_workspace_size.restype = L
+    lib.mxw_vocab_loss_workspace_size.argtypes = [P, L, P, L, I, I, I, I]
     _lib = lib
     return lib
 
@@ -198,6 +210,12 @@ def _workspace(need, dev, stream, workspace):
     with torch.cuda.stream(stream):
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
     return ws.data_ptr(), need, ws
+
+
+def _new(shape, dtype, dev, stream):
+    """A fresh tensor that belongs to the stream the call runs on."""
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _as_u8(t, name):
@@ -438,3 +456,154 @@ def quantize_tokens(x, offs=None, q=None, s=None, stream=None, ld=None):
     if rc != 0:
         raise MxwError("mxfp8_quantize_tokens failed (%d): %s" % (rc, strerror(rc)))
     return q, s
+
+
+def mxw_orthogonalize(G, dtype, expert_stride, row_stride, E, N, K, coeffs, eps, out, workspace, workspace_bytes,
+                      stream=0):
+    """Raw C-ABI call on device addresses (ints); coeffs: a flat sequence of
+    3 * steps numbers; dtype: 0 bf16, 1 float32.  Returns the status code."""
+    host = (ctypes.c_float * max(len(coeffs), 1))(*coeffs)
+    return _load().mxw_orthogonalize(G, int(dtype), int(expert_stride), int(row_stride), int(E), int(N), int(K), host,
+                                     len(coeffs) // 3, float(eps), out, workspace, int(workspace_bytes), stream)
+
+
+def orthogonalize_workspace_size(E, N, K):
+    """Bytes of workspace orthogonalize needs.  Raises MxwError on a status code."""
+    rc = _load().mxw_orthogonalize_workspace_size(int(E), int(N), int(K))
+    if rc < 0:
+        raise MxwError("mxw_orthogonalize_workspace_size failed: %s" % strerror(rc))
+    return int(rc)
+
+
+def orthogonalize(G, out=None, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, stream=None, workspace=None):
+    """The orthogonalised update of a stack of gradients (or momenta), bf16:
+    for every matrix of G, X = G / (|G|_F + eps), then `steps` times
+    X <- a X + (b S + c S S) X with S = X X^T (on X^T where it is taller than
+    wide), which drives the singular values to about 1.
+
+    G: bf16 or float32 [E, N, K] (as wgrad returns it) or [N, K], any sizes,
+    the last axis contiguous, other strides free.  coeffs: (a, b, c), or one
+    such triple per step.  `out` (optional) is a contiguous bf16 tensor of G's
+    shape, fully overwritten.  A zero matrix gives zeros.  Runs on `stream`
+    (default: the current stream) and does not synchronise; `workspace`: a
+    uint8 device tensor of orthogonalize_workspace_size() bytes (default: from
+    torch's caching allocator on that stream)."""
+    if G.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("G must be bfloat16 or float32, got %s" % G.dtype)
+    if G.dim() not in (2, 3) or 0 in G.shape:
+        raise ValueError("G must be [E, N, K] or [N, K] with no empty axis, got %s" % (tuple(G.shape),))
+    dev = G.device
+    if dev.type != "cuda":
+        raise ValueError("G must be on the GPU")
+    E, N, K = G.shape if G.dim() == 3 else (1,) + tuple(G.shape)
+    if K > 1 and G.stride(-1) != 1:
+        raise ValueError("G's last axis must be contiguous")
+    rs = G.stride(-2) if N > 1 else K
+    es = G.stride(0) if G.dim() == 3 and E > 1 else 0
+    if rs < K:
+        raise ValueError("G's rows must be at least a row apart")
+    coeffs = list(coeffs)
+    steps = int(steps)
+    if len(coeffs) == 3 and not any(hasattr(c, "__len__") for c in coeffs):
+        coeffs = [coeffs] * steps
+    if steps < 1 or len(coeffs) != steps or any(len(c) != 3 for c in coeffs):
+        raise ValueError("coeffs must be one (a, b, c) or one for each of the steps")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if out is None:
+        out = _new(G.shape, torch.bfloat16, dev, stream)
+    elif out.dtype != torch.bfloat16 or out.shape != G.shape or not out.is_contiguous() or out.device != dev:
+        raise ValueError("out must be a contiguous bf16 tensor of G's shape on the same device")
+    with torch.cuda.device(dev):
+        wp, wb, ws = _workspace(orthogonalize_workspace_size(E, N, K), dev, stream, workspace)
+        rc = mxw_orthogonalize(G.data_ptr(), 0 if G.dtype == torch.bfloat16 else 1, es, rs, E, N, K,
+                               [float(v) for c in coeffs for v in c], eps, out.data_ptr(), wp, wb, stream.cuda_stream)
+        del ws
+    if rc != 0:
+        raise MxwError("mxw_orthogonalize failed (%d): %s" % (rc, strerror(rc)))
+    return out
+
+
+def mxw_vocab_loss(x, ldx, w, ldw, targets, target_bytes, ignore_index, T, H, V, reduction, grad_scale, loss, dx, dw,
+                   workspace, workspace_bytes, stream=0):
+    """Raw C-ABI call on device addresses (ints; dx, dw may be 0); reduction:
+    0 none, 1 mean, 2 sum.  Returns the status code."""
+    return _load().mxw_vocab_loss(x, int(ldx), w, int(ldw), targets, int(target_bytes), int(ignore_index), int(T),
+                                  int(H), int(V), int(reduction), float(grad_scale), loss, dx, dw, workspace,
+                                  int(workspace_bytes), stream)
+
+
+def vocab_loss_workspace_size(x, ldx, w, ldw, T, H, V, grads=3):
+    """Bytes of workspace mxw_vocab_loss needs (x, w: device addresses; grads:
+    1 for dx, plus 2 for dw).  Raises MxwError on a status code."""
+    rc = _load().mxw_vocab_loss_workspace_size(x, int(ldx), w, int(ldw), int(T), int(H), int(V), int(grads))
+    if rc < 0:
+        raise MxwError("mxw_vocab_loss_workspace_size failed: %s" % strerror(rc))
+    return int(rc)
+
+
+_REDUCTIONS = {"none": 0, "mean": 1, "sum": 2}
+
+
+def vocab_cross_entropy(x, w, targets, ignore_index=-100, reduction="mean", grads=True, grad_scale=1.0, dx=None,
+                        dw=None, stream=None, workspace=None):
+    """Softmax cross entropy of hidden states x [T, H] against the vocabulary
+    w [V, H] (both bf16, last axis contiguous, rows any stride apart) without
+    keeping the logits: (loss, dx, dw), or loss alone with grads=False.
+
+    targets: int32 or int64 [T]; tokens whose target is ignore_index have loss
+    0 and no gradient.  reduction: "mean" over the tokens that count, "sum"
+    (loss: a float32 scalar tensor), or "none" (loss: float32 [T]).  dx [T, H]
+    and dw [V, H], bf16, are the gradients of grad_scale times the reduced loss
+    (of the sum, for "none"); contiguous tensors may be passed for them.  A
+    target outside the vocabulary makes the loss NaN.  Runs on `stream`
+    (default: the current stream) and does not synchronise; `workspace`: a
+    uint8 device tensor of vocab_loss_workspace_size() bytes (default: from
+    torch's caching allocator on that stream)."""
+    if x.dtype != torch.bfloat16 or w.dtype != torch.bfloat16:
+        raise TypeError("x and w must be bfloat16")
+    if targets.dtype not in (torch.int32, torch.int64):
+        raise TypeError("targets must be int32 or int64")
+    if reduction not in _REDUCTIONS:
+        raise ValueError("reduction must be 'mean', 'sum' or 'none'")
+    if x.dim() != 2 or w.dim() != 2 or targets.dim() != 1:
+        raise ValueError("x, w must be 2-D and targets 1-D")
+    T, H = x.shape
+    V = w.shape[0]
+    if w.shape[1] != H or targets.shape[0] != T or 0 in (T, H, V):
+        raise ValueError("shape mismatch: x %s w %s targets %s" % (tuple(x.shape), tuple(w.shape),
+                                                                   tuple(targets.shape)))
+    dev = x.device
+    for name, t in (("x", x), ("w", w), ("targets", targets)):
+        if t.device != dev or dev.type != "cuda":
+            raise ValueError("%s must be on the same GPU as x" % name)
+    strides = []
+    for name, t in (("x", x), ("w", w)):
+        if (H > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < H):
+            raise ValueError("%s must have a contiguous last axis and rows at least a row apart" % name)
+        strides.append(t.stride(0) if t.shape[0] > 1 else H)
+    if T > 1 and targets.stride(0) != 1:
+        raise ValueError("targets must be contiguous")
+    if not grads and (dx is not None or dw is not None):
+        raise ValueError("dx and dw are outputs of grads=True")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    for name, t, shape in (("dx", dx, (T, H)), ("dw", dw, (V, H))):
+        if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != shape or not t.is_contiguous()
+                              or t.device != dev):
+            raise ValueError("%s must be a contiguous bf16 %s tensor on the same device" % (name, list(shape)))
+    if grads:
+        dx = _new((T, H), torch.bfloat16, dev, stream) if dx is None else dx
+        dw = _new((V, H), torch.bfloat16, dev, stream) if dw is None else dw
+    loss = _new((T,) if reduction == "none" else (), torch.float32, dev, stream)
+    with torch.cuda.device(dev):
+        need = vocab_loss_workspace_size(x.data_ptr(), strides[0], w.data_ptr(), strides[1], T, H, V, 3 if grads else 0)
+        wp, wb, ws = _workspace(need, dev, stream, workspace)
+        rc = mxw_vocab_loss(x.data_ptr(), strides[0], w.data_ptr(), strides[1], targets.data_ptr(),
+                            targets.element_size(), ignore_index, T, H, V, _REDUCTIONS[reduction], grad_scale,
+                            loss.data_ptr(), dx.data_ptr() if grads else 0, dw.data_ptr() if grads else 0, wp, wb,
+                            stream.cuda_stream)
+        del ws
+    if rc != 0:
+        raise MxwError("mxw_vocab_loss failed (%d): %s" % (rc, strerror(rc)))
+    return (loss, dx, dw) if grads else loss

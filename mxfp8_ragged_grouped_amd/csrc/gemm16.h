@@ -1,0 +1,385 @@
+// gemm16.h -- the dense matrix product on 16-bit operands (bf16 or f16, FP32
+// sums) under the orthogonalised update and the vocabulary loss, gfx950.
+//
+// C[m][n] = sum_k A(m, k) B(n, k), per batch entry.  Either operand may be
+// stored K-contiguous (rows of k, "row" form) or with k as its slow axis
+// ("column" form, TA / TB = true), so no caller transposes a matrix:
+//
+//     row form      A(m, k) = A[m lda + k]     LDS stage [BM][64 k], 128 B rows
+//     column form   A(m, k) = A[k lda + m]     LDS stage [64 k][BM]
+//
+// A row-form stage is read 16 bytes (8 k) a lane; a column-form stage through
+// the transposing LDS read (within 16 lanes, lane i element j receives element
+// i % 4 of the 8 bytes that lane 4 j + i / 4 addresses; checked on gfx950), so
+// both give the MFMA the same fragment: lane l holds row l % 32 and
+// k = 8 (l / 32) .. + 7 of a 16-deep step.
+//
+// A workgroup owns one BM x BN tile (WM x WN waves) and walks K in steps of 64
+// through two LDS stages filled by 16-byte LDS-direct buffer loads.  The
+// buffer descriptor is rebased every step (64-bit), its range ending with the
+// matrix: rows past the end read as zeros, so K and the tile edges need no
+// masks as long as a row-form operand is stored with its k padded to a multiple
+// of 64 by zeros.
+// In a column-form operand columns past the edge may read a neighbouring
+// row's values: they feed only output rows or columns that are not stored.
+//
+// The MFMA's first operand is B, so a lane ends with 4 consecutive n of one m:
+// register r of block (mi, ni) in lane l is m = 32 mi + l % 32,
+// n = 32 ni + 8 (r / 4) + 4 (l / 32) + r % 4 of the wave's part.
+#ifndef MXW_GEMM16_H
+#define MXW_GEMM16_H
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace mxw {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kGemmStep = 64;  // k per LDS stage: 128 bytes, one cache line a row
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+}
+
+// LDS-direct load: lane l's 16 bytes at byte offset voff of the buffer land at
+// LDS byte lds + 16 l; lanes out of the buffer's range write zeros.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void load_lds16(const __amdgpu_buffer_rsrc_t& rsrc, uint32_t lds, uint32_t voff) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %2, 0 offen lds"
+      :
+      : "s"(lds), "v"(voff), "s"(rsrc)
+      : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// every load of this wave has landed and every LDS read has returned, then the
+// workgroup's barrier; no memory access moves across
+__device__ __forceinline__ void stage_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ v16f mfma16(const v4i& a, const v4i& b, const v16f& c, __bf16) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ v16f mfma16(const v4i& a, const v4i& b, const v16f& c, _Float16) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+}
+
+// two floats rounded to nearest even, packed
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, __bf16) {
+  f32x2 f = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, _Float16) {
+  f32x2 f = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, f16x2));
+}
+
+__device__ __forceinline__ v2i lds_read_tr(const uint8_t* p) {
+  return __builtin_bit_cast(
+      v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(p)));
+}
+
+struct GemmArgs {
+  const uint16_t* A;
+  const uint16_t* B;
+  int64_t strideA, strideB;  // elements from one batch entry to the next
+  int lda, ldb;              // elements from one row (row form) or one k (column form) to the next
+  int M, N, K;               // M (N) a multiple of 8 where A (B) is in column form
+  int tilesM, tilesN;
+  int tiles;    // tiles per (batch entry, split)
+  int batch, splits;
+  int ksplit;   // k per split, a multiple of 64
+};
+
+// what an epilogue gets to know of its tile
+struct TileAt {
+  int batch, split, m0, n0;
+  int wave, lane, wm, wn;  // the wave's part of the tile starts at row wm, column wn
+  bool mirror;             // symmetric product, off the diagonal: the transposed tile is wanted too
+};
+
+// A tile of 16-bit values staged in LDS [BM][BN]: 16-byte chunk c of row r at
+// position c ^ (r % chunks), so rows and columns are both read without bank
+// conflicts that matter.
+template <int BN>
+__device__ __forceinline__ uint32_t tile_at(int r, int chunk) {
+  constexpr int kChunks = BN / 8;
+  return (uint32_t)(r * BN * 2 + ((chunk ^ (r & (kChunks - 1))) << 4));
+}
+
+// The workgroup's block index dealt so that each XCD (block index mod 8) gets
+// one contiguous run of work, for its L2.
+__device__ __forceinline__ int xcd_run(int b, int n) {
+  const int q = n >> 3, r = n & 7, x = b & 7;
+  return x * q + (x < r ? x : r) + (b >> 3);
+}
+
+template <typename T, int BM, int BN, int WM, int WN, bool TA, bool TB, bool SYM, class Epi>
+__global__ __launch_bounds__(WM* WN * 64, 2) void gemm16_kernel(GemmArgs p, typename Epi::Args ea) {
+  constexpr int kWaves = WM * WN;
+  constexpr int kPartM = BM / WM, kPartN = BN / WN;
+  constexpr int MI = kPartM / 32, NI = kPartN / 32;
+  constexpr int kBytesA = BM * 128, kBytesB = BN * 128, kStage = kBytesA + kBytesB;
+  constexpr int kLoadsA = BM / 8, kLoadsB = BN / 8;  // 1 KiB loads per stage
+  constexpr int LA = (kLoadsA + kWaves - 1) / kWaves, LB = (kLoadsB + kWaves - 1) / kWaves;
+  constexpr int kTileLds = Epi::kStaged ? BM * BN * 2 : 0;
+  __shared__ __align__(1024) uint8_t lds[2 * kStage > kTileLds ? 2 * kStage : kTileLds];
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  TileAt at;
+  {
+    const int id = xcd_run(blockIdx.x, p.batch * p.splits * p.tiles);
+    const int t = id % p.tiles, bs = id / p.tiles;
+    at.split = bs % p.splits;
+    at.batch = bs / p.splits;
+    int tm, tn;
+    if (SYM) {  // the lower triangle, row by row
+      tm = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+      while ((tm + 1) * (tm + 2) / 2 <= t) ++tm;
+      while (tm * (tm + 1) / 2 > t) --tm;
+      tn = t - tm * (tm + 1) / 2;
+      at.mirror = tm != tn;
+    } else {  // bands of 4 tile rows
+      const int per = 4 * p.tilesN, band = t / per, in = t - band * per;
+      const int rows = p.tilesM - 4 * band < 4 ? p.tilesM - 4 * band : 4;
+      tn = in / rows;
+      tm = 4 * band + in - tn * rows;
+      at.mirror = false;
+    }
+    at.m0 = tm * BM;
+    at.n0 = tn * BN;
+  }
+  at.wave = wave;
+  at.lane = lane;
+  at.wm = (wave / WN) * kPartM;
+  at.wn = (wave % WN) * kPartN;
+  const int kbeg = at.split * p.ksplit;
+  const int kend = kbeg + p.ksplit < p.K ? kbeg + p.ksplit : p.K;
+  const int steps = (kend - kbeg + kGemmStep - 1) / kGemmStep;
+
+  // operand addressing: the tile's first byte, the bytes left in the matrix
+  // from there, and the bytes a step advances
+  const uint8_t *baseA, *baseB;
+  int64_t leftA, leftB;
+  uint32_t voA[LA], voB[LB];
+  {
+    const uint8_t* A = (const uint8_t*)(p.A + at.batch * p.strideA);
+    const uint8_t* B = (const uint8_t*)(p.B + at.batch * p.strideB);
+    const int64_t la = 2 * (int64_t)p.lda, lb = 2 * (int64_t)p.ldb;
+    if (TA) {
+      baseA = A + kbeg * la + 2 * at.m0;
+      leftA = (kend - 1 - kbeg) * la + 2 * (int64_t)(p.M - at.m0);
+    } else {
+      baseA = A + at.m0 * la + 2 * kbeg;
+      leftA = (p.M - at.m0 - 1) * la + 128 * (int64_t)steps;
+    }
+    if (TB) {
+      baseB = B + kbeg * lb + 2 * at.n0;
+      leftB = (kend - 1 - kbeg) * lb + 2 * (int64_t)(p.N - at.n0);
+    } else {
+      baseB = B + at.n0 * lb + 2 * kbeg;
+      leftB = (p.N - at.n0 - 1) * lb + 128 * (int64_t)steps;
+    }
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+      const int u = wave + i * kWaves;
+      if (TA) {
+        constexpr int kLanes = BM / 8;  // lanes (16-byte chunks) a k
+        const int k = u * (64 / kLanes) + lane / kLanes, c = lane % kLanes;
+        voA[i] = (uint32_t)(k * la + ((c ^ ((k & 3) << 2)) << 4));
+      } else {
+        const int r = u * 8 + (lane >> 3), c = lane & 7;
+        voA[i] = (uint32_t)(r * la + ((c ^ ((r >> 1) & 7)) << 4));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < LB; ++i) {
+      const int u = wave + i * kWaves;
+      if (TB) {
+        constexpr int kLanes = BN / 8;
+        const int k = u * (64 / kLanes) + lane / kLanes, c = lane % kLanes;
+        voB[i] = (uint32_t)(k * lb + ((c ^ ((k & 3) << 2)) << 4));
+      } else {
+        const int r = u * 8 + (lane >> 3), c = lane & 7;
+        voB[i] = (uint32_t)(r * lb + ((c ^ ((r >> 1) & 7)) << 4));
+      }
+    }
+  }
+  const int64_t stepA = TA ? 2 * (int64_t)kGemmStep * p.lda : 2 * kGemmStep;
+  const int64_t stepB = TB ? 2 * (int64_t)kGemmStep * p.ldb : 2 * kGemmStep;
+  const uint32_t ldsBase = (uint32_t)(uintptr_t)lds;
+
+  auto fill = [&](int stage) {
+    const uint32_t ra = leftA <= 0 ? 0u : leftA > 0x7FFFFFFF ? 0x7FFFFFFFu : (uint32_t)leftA;
+    const uint32_t rb = leftB <= 0 ? 0u : leftB > 0x7FFFFFFF ? 0x7FFFFFFFu : (uint32_t)leftB;
+    const __amdgpu_buffer_rsrc_t A = buffer_of(baseA, ra), B = buffer_of(baseB, rb);
+    const uint32_t to = ldsBase + stage * kStage + wave * 1024;
+#pragma unroll
+    for (int i = 0; i < LA; ++i)
+      if (kLoadsA % kWaves == 0 || wave + i * kWaves < kLoadsA) load_lds16(A, to + i * kWaves * 1024, voA[i]);
+#pragma unroll
+    for (int i = 0; i < LB; ++i)
+      if (kLoadsB % kWaves == 0 || wave + i * kWaves < kLoadsB) load_lds16(B, to + kBytesA + i * kWaves * 1024, voB[i]);
+    baseA += stepA;
+    baseB += stepB;
+    leftA -= stepA;
+    leftB -= stepB;
+  };
+
+  // fragment addresses within a stage
+  uint32_t fa[TA ? MI : 4], fb[TB ? NI : 4];
+  {
+    const int hi = lane >> 5, sw = ((lane & 31) >> 1) & 7;
+    const int tk = 8 * hi + ((lane & 15) >> 2), x = (lane & 15) >> 2, tc = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    if (TA) {
+#pragma unroll
+      for (int i = 0; i < (TA ? MI : 0); ++i)
+        fa[i] = tk * BM * 2 + (((((at.wm >> 5) + i) ^ x) * 4 + tc) << 4) + ((lane & 1) << 3);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) fa[j] = (at.wm + (lane & 31)) * 128 + (((2 * j + hi) ^ sw) << 4);
+    }
+    if (TB) {
+#pragma unroll
+      for (int i = 0; i < (TB ? NI : 0); ++i)
+        fb[i] = tk * BN * 2 + (((((at.wn >> 5) + i) ^ x) * 4 + tc) << 4) + ((lane & 1) << 3);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) fb[j] = (at.wn + (lane & 31)) * 128 + (((2 * j + hi) ^ sw) << 4);
+    }
+  }
+
+  v16f acc[MI][NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+  if (steps > 0) fill(0);
+  for (int s = 0; s < steps; ++s) {
+    stage_barrier();  // this stage has landed, the other has been read
+    if (s + 1 < steps) fill((s + 1) & 1);
+    const uint8_t* sa = lds + (s & 1) * kStage;
+    const uint8_t* sb = sa + kBytesA;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v4i a[MI], b[NI];
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        if (TB) {
+          const v2i lo = lds_read_tr(sb + fb[i] + 16 * j * BN * 2), hi = lds_read_tr(sb + fb[i] + (16 * j + 4) * BN * 2);
+          b[i] = (v4i){lo.x, lo.y, hi.x, hi.y};
+        } else {
+          b[i] = *(const v4i*)(sb + fb[TB ? 0 : j] + i * 32 * 128);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        if (TA) {
+          const v2i lo = lds_read_tr(sa + fa[i] + 16 * j * BM * 2), hi = lds_read_tr(sa + fa[i] + (16 * j + 4) * BM * 2);
+          a[i] = (v4i){lo.x, lo.y, hi.x, hi.y};
+        } else {
+          a[i] = *(const v4i*)(sa + fa[TA ? 0 : j] + i * 32 * 128);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int k = 0; k < NI; ++k) acc[i][k] = mfma16(b[k], a[i], acc[i][k], T());
+    }
+  }
+  __syncthreads();  // the stages are free for the epilogue
+  Epi::template run<BM, BN, WM, WN, MI, NI>(p, ea, at, acc, lds);
+}
+
+// ---- helpers for epilogues that stage a 16-bit tile -------------------------
+
+// the wave's part of the tile, its sums passed four at a time (row m, columns
+// n .. n + 3, n a multiple of 4; i: the row's 32-row block in the part) through
+// quad(i, m, n, v), rounded to T and staged
+template <typename T, int BN, int MI, int NI, class F>
+__device__ __forceinline__ void stage_part(const TileAt& at, const v16f (&acc)[MI][NI], uint8_t* lds, F quad) {
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int r = at.wm + 32 * i + (at.lane & 31);
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int c = at.wn + 32 * j + 8 * q + 4 * (at.lane >> 5);
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e];
+        quad(i, at.m0 + r, at.n0 + c, v);
+        const v2i w = {(int)pack2(v[0], v[1], T()), (int)pack2(v[2], v[3], T())};
+        *(v2i*)(lds + tile_at<BN>(r, c >> 3) + ((c & 4) << 1)) = w;
+      }
+    }
+  }
+}
+
+// the staged tile to rows of dst (row stride ld, which is a multiple of 8, as
+// is ncols; dst 16-byte aligned): rows below nrows, columns below ncols
+template <int BM, int BN, int WAVES>
+__device__ __forceinline__ void store_rows(const TileAt& at, const uint8_t* lds, uint16_t* dst, int64_t ld, int nrows,
+                                           int ncols) {
+  constexpr int kChunks = BN / 8;
+  const int tid = at.wave * 64 + at.lane;
+#pragma unroll
+  for (int i = tid; i < BM * kChunks; i += WAVES * 64) {
+    const int r = i / kChunks, c = i % kChunks;
+    const int m = at.m0 + r, n = at.n0 + 8 * c;
+    if (m < nrows && n < ncols) *(v4i*)(dst + m * ld + n) = *(const v4i*)(lds + tile_at<BN>(r, c));
+  }
+}
+
+// the same without any alignment, value by value
+template <int BM, int BN, int WAVES>
+__device__ __forceinline__ void store_rows_any(const TileAt& at, const uint8_t* lds, uint16_t* dst, int64_t ld,
+                                               int nrows, int ncols) {
+  const int tid = at.wave * 64 + at.lane;
+  for (int i = tid; i < BM * BN; i += WAVES * 64) {
+    const int r = i / BN, c = i % BN;
+    const int m = at.m0 + r, n = at.n0 + c;
+    if (m < nrows && n < ncols) dst[m * ld + n] = *(const uint16_t*)(lds + tile_at<BN>(r, c >> 3) + 2 * (c & 7));
+  }
+}
+
+// the staged tile's transpose: dst[n][m], 16 bytes (8 m) a lane
+template <int BM, int BN, int WAVES>
+__device__ __forceinline__ void store_cols(const TileAt& at, const uint8_t* lds, uint16_t* dst, int64_t ld, int nrows,
+                                           int ncols) {
+  const int g = at.lane >> 4, i = at.lane & 15;
+#pragma unroll 2
+  for (int u = at.wave; u < (BM / 32) * (BN / 16); u += WAVES) {
+    const int r0 = (u % (BM / 32)) * 32 + 8 * g, c0 = (u / (BM / 32)) * 16;
+    const int r = r0 + (i >> 2), c = c0 + 4 * (i & 3);
+    const v2i lo = lds_read_tr(lds + tile_at<BN>(r, c >> 3) + ((c & 4) << 1));
+    const v2i hi = lds_read_tr(lds + tile_at<BN>(r + 4, c >> 3) + ((c & 4) << 1));
+    const int n = at.n0 + c0 + i, m = at.m0 + r0;
+    if (n < nrows && m < ncols) *(v4i*)(dst + n * ld + m) = (v4i){lo.x, lo.y, hi.x, hi.y};
+  }
+}
+
+}  // namespace mxw
+
+#endif  // MXW_GEMM16_H

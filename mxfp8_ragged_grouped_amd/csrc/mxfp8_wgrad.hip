@@ -103,14 +103,15 @@
 // tell the stages apart and would drain the prefetch before each LDS read.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
-#include <string.h>
 
-#include <atomic>
 #include <mutex>
 
+#include "device.h"
 #include "mxfp8_wgrad.h"
 
 namespace {
+
+using mxw::check_device;
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef int v4i __attribute__((ext_vector_type(4)));
@@ -1706,35 +1707,6 @@ __global__ __launch_bounds__(256) void quant_kernel(const uint16_t* __restrict__
     const int h = h0 + r, m = m0 + c16 * 16;
     if (h < H && m < M) __builtin_nontemporal_store(*(const v4i*)&sm.q[r][(c16 ^ (r & 15)) * 16], (v4i*)(q + (size_t)h * ld + m));
   }
-}
-
-struct DeviceInfo {
-  std::atomic<int> state;  // 0: not read yet, 1: gfx950, 2: another device
-  int cus;                 // compute units (written before state)
-};
-DeviceInfo g_dev[64];
-std::mutex g_dev_mutex;  // taken only by the first check of a device
-
-// Reads device properties once per device (no allocation, no stream work);
-// after that a check is one atomic load, so calls take no lock.
-int check_device(int* cus = nullptr) {
-  int dev = -1;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return MXW_ERR_DEVICE;
-  DeviceInfo& d = g_dev[dev];
-  int st = d.state.load(std::memory_order_acquire);
-  if (st == 0) {
-    std::lock_guard<std::mutex> lock(g_dev_mutex);
-    st = d.state.load(std::memory_order_relaxed);
-    if (st == 0) {
-      hipDeviceProp_t prop;
-      if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return MXW_ERR_DEVICE;
-      d.cus = prop.multiProcessorCount;
-      st = strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : 2;
-      d.state.store(st, std::memory_order_release);
-    }
-  }
-  if (cus) *cus = d.cus;
-  return st == 1 ? MXW_OK : MXW_ERR_DEVICE;
 }
 
 // whether an E4M3 weight-gradient call with a workspace pre-shuffles its

@@ -1,0 +1,533 @@
+// vocab_loss.hip -- softmax cross entropy over a large vocabulary with its
+// gradients, without keeping the logits (mxw_vocab_loss, declared in
+// include/mxfp8_wgrad.h), for gfx950.
+//
+//     l = x w^T,  lse_t = log sum_v exp l_tv,  loss_t = lse_t - l_t,y(t)
+//     g_tv = (exp(l_tv - lse_t) - [v = y(t)]) s,  dx = g w,  dw = g^T x
+//
+// with s = grad_scale (divided by the number of tokens that count, for the
+// mean); tokens whose target is ignore_index have loss 0 and g = 0.
+//
+// The logits are never written.  A first product walks the whole vocabulary and
+// leaves, per 256 x 256 tile and token, the running maximum and sum of
+// exponentials (8 bytes for 256 logits); they are joined in a fixed order.
+// Then the vocabulary is walked in pieces, each small enough that g of the
+// piece (bf16, unscaled: its entries lie in [-1, 1]) stays in the memory-side
+// cache: one product makes the logits again and turns them into g in its
+// epilogue, one adds g w to the FP32 sums of dx (split over the piece's
+// vocabulary where T x H has few tiles; partial sums are joined in a fixed
+// order at the end), one writes dw = g^T x of the piece's rows.
+// 8 T H V flops with gradients, 2 T H V without: bound by the MFMA except for
+// few tokens, where reading w bounds it.
+//
+// All sums and statistics are FP32 (the mean's over tokens FP64); g is rounded
+// to bf16 because the products that follow take 16-bit operands: at most
+// 2^-8 of each term, about the gradients' own rounding to bf16.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device.h"
+#include "gemm16.h"
+#include "mxfp8_wgrad.h"
+
+namespace {
+
+using namespace mxw;
+
+constexpr int kTileV = 256;                        // vocabulary columns a tile
+constexpr int64_t kPieceBytes = 256LL << 20;       // g of one piece
+constexpr int kMaxTokens = 128 * 1024;
+constexpr int kMaxVocab = 1 << 20;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct Targets {
+  const void* p;
+  int wide;        // 64-bit
+  int64_t ignore;
+  int V;
+  // the target's index, -1: ignored, -2: outside the vocabulary
+  __device__ int at(int t) const {
+    const int64_t y = wide ? ((const int64_t*)p)[t] : (int64_t)((const int32_t*)p)[t];
+    return y == ignore ? -1 : (y < 0 || y >= V ? -2 : (int)y);
+  }
+};
+
+// exp(l - m) with exp(-inf - m) = 0 for every m, NaN kept
+__device__ __forceinline__ float exp_above(float l, float m) {
+  return l == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((l - m) * kLog2e);
+}
+// (m, s) joined with (m2, s2)
+__device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
+  const float top = fmaxf(m, m2);
+  // a side without anything (m = -inf, s = 0, or a NaN sum) is kept as it is
+  const float f = m == -INFINITY ? s : s * __builtin_amdgcn_exp2f((m - top) * kLog2e);
+  const float f2 = m2 == -INFINITY ? s2 : s2 * __builtin_amdgcn_exp2f((m2 - top) * kLog2e);
+  m = top;
+  s = f + f2;
+}
+
+// ---- the logits' statistics -------------------------------------------------
+
+struct EpiStats {
+  static constexpr bool kStaged = false;
+  struct Args {
+    float2* part;      // [tiles of the vocabulary][T]
+    float* hit;        // [T] the target's logit
+    Targets y;
+    int v0, V;         // the piece's first column; columns in all
+  };
+  template <int BM, int BN, int WM, int WN, int MI, int NI>
+  static __device__ void run(const GemmArgs& p, const Args& a, const TileAt& at, v16f (&acc)[MI][NI], uint8_t* lds) {
+    float2(*sh)[BM] = (float2(*)[BM])lds;  // [WN][BM]
+    // columns of the wave's part from this lane's first on, and how many of
+    // them the vocabulary has
+    const int c0 = a.v0 + at.n0 + at.wn + 4 * (at.lane >> 5), left = a.V - c0;
+    if (a.v0 + at.n0 + BN > a.V) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            acc[i][j][q] = 32 * j + 8 * (q >> 2) + (q & 3) < left ? acc[i][j][q] : -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int r = at.wm + 32 * i + (at.lane & 31), t = at.m0 + r;
+      const int y = (t < p.M ? a.y.at(t) : -1) - c0;  // the target among this lane's columns
+      float m = -INFINITY, s = 0.0f, hit = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          m = fmaxf(m, acc[i][j][q]);
+          hit = y == 32 * j + 8 * (q >> 2) + (q & 3) ? acc[i][j][q] : hit;
+        }
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) s += exp_above(acc[i][j][q], m);
+      if (y >= 0 && y < 32 * NI && (y & 4) == 0) a.hit[t] = hit;
+      join(m, s, __shfl_xor(m, 32), __shfl_xor(s, 32));
+      if (at.lane < 32) sh[at.wave % WN][r] = make_float2(m, s);
+    }
+    __syncthreads();
+    const int tid = at.wave * 64 + at.lane;
+    for (int r = tid; r < BM; r += WM * WN * 64) {
+      float m = sh[0][r].x, s = sh[0][r].y;
+#pragma unroll
+      for (int w = 1; w < WN; ++w) join(m, s, sh[w][r].x, sh[w][r].y);
+      if (at.m0 + r < p.M) a.part[(int64_t)((a.v0 + at.n0) / kTileV) * p.M + at.m0 + r] = make_float2(m, s);
+    }
+  }
+};
+
+// one wave a token: its partial statistics joined (lane l: tiles l, l + 64, ...;
+// then across lanes), lse and loss
+__global__ __launch_bounds__(256) void loss_rows_kernel(const float2* part, const float* hit, Targets y, int T, int tiles,
+                                                        float* lse, float* loss) {
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (t >= T) return;
+  float m = -INFINITY, s = 0.0f;
+  for (int i = lane; i < tiles; i += 64) {
+    const float2 v = part[(int64_t)i * T + t];
+    join(m, s, v.x, v.y);
+  }
+  for (int d = 1; d < 64; d <<= 1) join(m, s, __shfl_xor(m, d), __shfl_xor(s, d));
+  if (lane == 0) {
+    const float l = m + __builtin_amdgcn_logf(s) * kLn2;
+    const int at = y.at(t);
+    lse[t] = l;
+    loss[t] = at == -1 ? 0.0f : at < 0 ? NAN : l - hit[t];
+  }
+}
+
+// one workgroup: the reduced loss and the gradients' scale
+__global__ __launch_bounds__(1024) void loss_total_kernel(const float* rows, Targets y, int T, int mean, float grad_scale,
+                                                          float* loss, float* scale) {
+  __shared__ double sums[16];
+  __shared__ int counts[16];
+  double s = 0.0;
+  int n = 0;
+  for (int t = threadIdx.x; t < T; t += 1024) {
+    s += (double)rows[t];
+    n += y.at(t) != -1;
+  }
+  for (int d = 1; d < 64; d <<= 1) {
+    s += __shfl_xor(s, d);
+    n += __shfl_xor(n, d);
+  }
+  if ((threadIdx.x & 63) == 0) {
+    sums[threadIdx.x >> 6] = s;
+    counts[threadIdx.x >> 6] = n;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 16; ++i) {
+      s += sums[i];
+      n += counts[i];
+    }
+    if (n < 1) n = 1;  // no token counts: loss 0, gradients 0
+    if (loss) *loss = (float)(mean ? s / n : s);
+    *scale = mean ? grad_scale / (float)n : grad_scale;
+  }
+}
+
+// ---- the gradients ----------------------------------------------------------
+
+// g of a piece, unscaled bf16
+struct EpiGrad {
+  static constexpr bool kStaged = true;
+  struct Args {
+    uint16_t* g;
+    int64_t ld;
+    const float* lse;
+    Targets y;
+    int v0, V, ncols;  // ncols: the piece's columns, rounded up to 64
+  };
+  template <int BM, int BN, int WM, int WN, int MI, int NI>
+  static __device__ void run(const GemmArgs& p, const Args& a, const TileAt& at, v16f (&acc)[MI][NI], uint8_t* lds) {
+    float lse[MI];
+    int y[MI];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int t = at.m0 + at.wm + 32 * i + (at.lane & 31);
+      y[i] = t < p.M ? a.y.at(t) : -1;
+      lse[i] = t < p.M ? a.lse[t] : 0.0f;
+    }
+    stage_part<__bf16, BN>(at, acc, lds, [&](int i, int, int n, float (&v)[4]) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = a.v0 + n + e;
+        const float pr = __builtin_amdgcn_exp2f((v[e] - lse[i]) * kLog2e) - (c == y[i] ? 1.0f : 0.0f);
+        v[e] = y[i] < 0 || c >= a.V ? 0.0f : pr;
+      }
+    });
+    __syncthreads();
+    store_rows<BM, BN, WM * WN>(at, lds, a.g, a.ld, p.M, a.ncols);
+  }
+};
+
+// FP32 partial sums of dx, per split: written, or added to
+struct EpiSum {
+  static constexpr bool kStaged = false;
+  struct Args {
+    float* sum;      // [splits][M][ld]
+    int64_t stride;  // of a split
+    int ld, add;
+  };
+  template <int BM, int BN, int WM, int WN, int MI, int NI>
+  static __device__ void run(const GemmArgs& p, const Args& a, const TileAt& at, v16f (&acc)[MI][NI], uint8_t*) {
+    float* sum = a.sum + at.split * a.stride;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int m = at.m0 + at.wm + 32 * i + (at.lane & 31);
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int n = at.n0 + at.wn + 32 * j + 8 * q + 4 * (at.lane >> 5);
+          if (m >= p.M || n >= a.ld) continue;
+          float4* to = (float4*)(sum + (int64_t)m * a.ld + n);
+          float4 v = make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+          if (a.add) {
+            const float4 was = *to;
+            v = make_float4(v.x + was.x, v.y + was.y, v.z + was.z, v.w + was.w);
+          }
+          *to = v;
+        }
+    }
+  }
+};
+
+// dx: the splits' sums in order, scaled, to bf16
+__global__ __launch_bounds__(256) void dx_kernel(const float* sum, int64_t stride, int splits, int ld, const float* scale,
+                                                 uint16_t* dx, int T, int H) {
+  const float s = *scale;
+  const int per = ld >> 2;
+  for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < (int64_t)T * per; i += (int64_t)gridDim.x * 256) {
+    const int t = (int)(i / per), c = 4 * (int)(i % per);
+    float4 v = *(const float4*)(sum + (int64_t)t * ld + c);
+    for (int k = 1; k < splits; ++k) {
+      const float4 w = *(const float4*)(sum + k * stride + (int64_t)t * ld + c);
+      v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+    }
+    uint16_t* to = dx + (int64_t)t * H + c;
+    const uint32_t lo = pack2(v.x * s, v.y * s, __bf16()), hi = pack2(v.z * s, v.w * s, __bf16());
+    if ((H & 3) == 0 && ((uintptr_t)dx & 7) == 0) {
+      if (c < H) *(uint2*)to = make_uint2(lo, hi);
+    } else {
+      if (c < H) to[0] = (uint16_t)lo;
+      if (c + 1 < H) to[1] = (uint16_t)(lo >> 16);
+      if (c + 2 < H) to[2] = (uint16_t)hi;
+      if (c + 3 < H) to[3] = (uint16_t)(hi >> 16);
+    }
+  }
+}
+
+// dw of a piece, scaled, to bf16
+struct EpiWeight {
+  static constexpr bool kStaged = true;
+  struct Args {
+    uint16_t* dw;  // the piece's first row
+    const float* scale;
+    int rows, H;
+  };
+  template <int BM, int BN, int WM, int WN, int MI, int NI>
+  static __device__ void run(const GemmArgs&, const Args& a, const TileAt& at, v16f (&acc)[MI][NI], uint8_t* lds) {
+    const float s = *a.scale;
+    stage_part<__bf16, BN>(at, acc, lds, [&](int, int, int, float (&v)[4]) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] *= s;
+    });
+    __syncthreads();
+    if ((a.H & 7) == 0 && ((uintptr_t)a.dw & 15) == 0)
+      store_rows<BM, BN, WM * WN>(at, lds, a.dw, a.H, a.rows, a.H);
+    else
+      store_rows_any<BM, BN, WM * WN>(at, lds, a.dw, a.H, a.rows, a.H);
+  }
+};
+
+// rows copied to rows of ld (a multiple of 64) elements, zeros after H
+__global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* src, int64_t lds, int rows, int H, uint16_t* dst,
+                                                       int ld) {
+  const int per = ld >> 3;
+  for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < (int64_t)rows * per; i += (int64_t)gridDim.x * 256) {
+    const int r = (int)(i / per), c = 8 * (int)(i % per);
+    const uint16_t* from = src + r * lds + c;
+    v4i w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = (c + 2 * j < H ? from[2 * j] : 0) | (uint32_t)(c + 2 * j + 1 < H ? from[2 * j + 1] : 0) << 16;
+    *(v4i*)(dst + (int64_t)r * ld + c) = w;
+  }
+}
+
+// ---- host -------------------------------------------------------------------
+
+struct LossPlan {
+  bool packed;   // x and w are copied to padded rows
+  int ld;        // H rounded up to 64
+  int tilesV, piece, splits, bm;
+  size_t part, hit, lse, rows, scale, xp, wp, g, sum, bytes;
+};
+
+// token rows a tile, for products whose M axis is the tokens
+int token_tile(int T) { return T <= 32 ? 32 : T <= 128 ? 128 : 256; }
+
+bool aligned(const void* x, int64_t ldx, const void* w, int64_t ldw, int H) {
+  return (H & 63) == 0 && (ldx & 7) == 0 && (ldw & 7) == 0 && (((uintptr_t)x | (uintptr_t)w) & 15) == 0;
+}
+
+LossPlan plan_of(bool direct, int T, int H, int V, bool gx, bool gw, int cus) {
+  LossPlan p = {};
+  p.packed = !direct;
+  p.ld = (H + 63) & ~63;
+  p.tilesV = (V + kTileV - 1) / kTileV;
+  p.bm = token_tile(T);
+  const bool grads = gx || gw;
+  // a piece of the vocabulary: all of it unless g (or the padded copy of its
+  // weights) gets too large
+  int64_t most = kPieceBytes / (2LL * (grads ? T : 1));
+  if (p.packed && most > kPieceBytes / (2LL * p.ld)) most = kPieceBytes / (2LL * p.ld);
+  if (most < kTileV) most = kTileV;
+  int64_t pieces = (V + most - 1) / most;
+  p.piece = (int)(((V + pieces - 1) / pieces + kTileV - 1) / kTileV * kTileV);
+  // dx: splits of a piece's vocabulary, so that the tiles fill the device in
+  // whole rounds; a split costs its partial sums' traffic (about one step of
+  // 64 columns in time)
+  p.splits = 1;
+  if (gx) {
+    const int64_t tiles = (int64_t)((T + p.bm - 1) / p.bm) * ((p.ld + 255) / 256);
+    const int64_t slots = p.bm == 32 ? 2 * cus : cus;
+    const int width = V < p.piece ? V : p.piece, steps = (width + kGemmStep - 1) / kGemmStep;
+    int64_t best = INT64_MAX;
+    for (int s = 1; s <= 64 && s * 4 <= steps + 3; ++s) {
+      const int64_t rounds = (tiles * s + slots - 1) / slots;
+      const int64_t cost = rounds * ((steps + s - 1) / s + 4) + s;
+      if (cost < best) {
+        best = cost;
+        p.splits = s;
+      }
+    }
+  }
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t was = at;
+    at = (at + bytes + 255) & ~(size_t)255;
+    return was;
+  };
+  p.part = take((size_t)p.tilesV * T * 8);
+  p.hit = take((size_t)T * 4);
+  p.lse = take((size_t)T * 4);
+  p.rows = take((size_t)T * 4);
+  p.scale = take(4);
+  if (p.packed) {
+    p.xp = take((size_t)T * p.ld * 2);
+    p.wp = take((size_t)(p.piece < V ? p.piece : V) * p.ld * 2);
+  }
+  if (grads) p.g = take((size_t)T * p.piece * 2);
+  if (gx) p.sum = take((size_t)p.splits * T * p.ld * 4);
+  p.bytes = at;
+  return p;
+}
+
+template <int BM, int WM, int WN, bool TA, bool TB, class Epi>
+int launch(GemmArgs g, const typename Epi::Args& e, hipStream_t st) {
+  g.batch = 1;
+  g.tilesM = (g.M + BM - 1) / BM;
+  g.tilesN = (g.N + 255) / 256;
+  g.tiles = g.tilesM * g.tilesN;
+  const int64_t grid = (int64_t)g.tilesM * g.tilesN * g.splits;
+  if (grid > 0x7FFFFFFF / 512) return MXW_ERR_DIM;
+  hipLaunchKernelGGL((gemm16_kernel<__bf16, BM, 256, WM, WN, TA, TB, false, Epi>), dim3((unsigned)grid),
+                     dim3(WM * WN * 64), 0, st, g, e);
+  return MXW_OK;
+}
+
+// products whose M axis is the tokens
+template <bool TB, class Epi>
+int launch_tokens(int bm, const GemmArgs& g, const typename Epi::Args& e, hipStream_t st) {
+  if (bm == 32) return launch<32, 1, 8, false, TB, Epi>(g, e, st);
+  if (bm == 128) return launch<128, 2, 4, false, TB, Epi>(g, e, st);
+  return launch<256, 2, 4, false, TB, Epi>(g, e, st);
+}
+
+int check_loss(int T, int H, int V) {
+  return T < 1 || T > kMaxTokens || H < 1 || H > 65536 || V < 1 || V > kMaxVocab ? MXW_ERR_DIM : MXW_OK;
+}
+
+unsigned copy_blocks(int64_t chunks) {
+  const int64_t b = (chunks + 1023) / 1024;
+  return (unsigned)(b < 1 ? 1 : b > 8192 ? 8192 : b);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t mxw_vocab_loss_workspace_size(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw, int T, int H,
+                                      int V, int grads) {
+  if (check_loss(T, H, V) || ldx < H || ldw < H || grads < 0 || grads > 3) return MXW_ERR_DIM;
+  int cus = 0;
+  const int rc = check_device(&cus);
+  if (rc) return rc;
+  return (int64_t)plan_of(aligned(x, ldx, w, ldw, H), T, H, V, grads & 1, grads & 2, cus).bytes;
+}
+
+int mxw_vocab_loss(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw, const void* targets,
+                   int target_bytes, int64_t ignore_index, int T, int H, int V, int reduction, float grad_scale,
+                   float* loss, uint16_t* dx, uint16_t* dw, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!x || !w || !targets || !loss) return MXW_ERR_NULL;
+  if (check_loss(T, H, V) || ldx < H || ldw < H || (target_bytes != 4 && target_bytes != 8) ||
+      (reduction != MXW_NONE && reduction != MXW_MEAN && reduction != MXW_SUM))
+    return MXW_ERR_DIM;
+  if ((((uintptr_t)x | (uintptr_t)w | (uintptr_t)dx | (uintptr_t)dw) & 1) || ((uintptr_t)loss & 3) ||
+      ((uintptr_t)targets & (target_bytes - 1)))
+    return MXW_ERR_ALIGN;
+  int cus = 0;
+  int rc = check_device(&cus);
+  if (rc) return rc;
+  const LossPlan p = plan_of(aligned(x, ldx, w, ldw, H), T, H, V, dx != nullptr, dw != nullptr, cus);
+  if (!workspace || workspace_bytes < p.bytes || ((uintptr_t)workspace & 255)) return MXW_ERR_WORKSPACE;
+  hipStream_t st = (hipStream_t)stream;
+  uint8_t* ws = (uint8_t*)workspace;
+  const Targets y = {targets, target_bytes == 8, ignore_index, V};
+  float* lse = (float*)(ws + p.lse);
+  float* rows = reduction == MXW_NONE ? loss : (float*)(ws + p.rows);
+  float* scale = (float*)(ws + p.scale);
+
+  const uint16_t* xs = x;
+  int64_t lx = ldx, lw = ldw;
+  if (p.packed) {
+    uint16_t* xp = (uint16_t*)(ws + p.xp);
+    hipLaunchKernelGGL(pad_rows_kernel, dim3(copy_blocks((int64_t)T * p.ld / 8)), dim3(256), 0, st, x, ldx, T, H, xp,
+                       p.ld);
+    xs = xp;
+    lx = lw = p.ld;
+  }
+  if (lx > 0x3FFFFFFF / 64 || lw > 0x3FFFFFFF / 64) return MXW_ERR_DIM;
+  // the piece's weights as the products read them
+  auto weights = [&](int v0, int width) -> const uint16_t* {
+    if (!p.packed) return w + v0 * ldw;
+    uint16_t* wp = (uint16_t*)(ws + p.wp);
+    hipLaunchKernelGGL(pad_rows_kernel, dim3(copy_blocks((int64_t)width * p.ld / 8)), dim3(256), 0, st, w + v0 * ldw, ldw,
+                       width, H, wp, p.ld);
+    return wp;
+  };
+  auto logits = [&](const uint16_t* wv, int width) {
+    GemmArgs g = {};
+    g.A = xs;
+    g.lda = (int)lx;
+    g.B = wv;
+    g.ldb = (int)lw;
+    g.M = T;
+    g.N = width;
+    g.K = p.ld;
+    g.splits = 1;
+    g.ksplit = p.ld;
+    return g;
+  };
+  const bool grads = dx || dw;
+  const uint16_t* kept = nullptr;  // one piece: its padded weights serve both passes
+  for (int v0 = 0; v0 < V; v0 += p.piece) {
+    const int width = V - v0 < p.piece ? V - v0 : p.piece;
+    kept = weights(v0, width);
+    const EpiStats::Args es = {(float2*)(ws + p.part), (float*)(ws + p.hit), y, v0, V};
+    rc = launch_tokens<false, EpiStats>(p.bm, logits(kept, width), es, st);
+    if (rc) return rc;
+  }
+  hipLaunchKernelGGL(loss_rows_kernel, dim3((unsigned)((T + 3) / 4)), dim3(256), 0, st, (const float2*)(ws + p.part),
+                     (const float*)(ws + p.hit), y, T, p.tilesV, lse, rows);
+  if (reduction != MXW_NONE || grads)
+    hipLaunchKernelGGL(loss_total_kernel, dim3(1), dim3(1024), 0, st, (const float*)rows, y, T,
+                       (int)(reduction == MXW_MEAN), grad_scale, reduction == MXW_NONE ? nullptr : loss, scale);
+  if (grads) {
+    uint16_t* gp = (uint16_t*)(ws + p.g);
+    const int64_t sumStride = (int64_t)T * p.ld;
+    for (int v0 = 0; v0 < V; v0 += p.piece) {
+      const int width = V - v0 < p.piece ? V - v0 : p.piece, padded = (width + 63) & ~63;
+      const uint16_t* wv = V <= p.piece ? kept : weights(v0, width);
+      const EpiGrad::Args eg = {gp, p.piece, lse, y, v0, V, padded};
+      rc = launch_tokens<false, EpiGrad>(p.bm, logits(wv, width), eg, st);
+      if (rc) return rc;
+      GemmArgs g = {};
+      if (dx) {
+        g.A = gp;
+        g.lda = p.piece;
+        g.B = wv;
+        g.ldb = (int)lw;
+        g.M = T;
+        g.N = p.ld;
+        g.K = width;
+        g.splits = p.splits;
+        g.ksplit = ((width + kGemmStep - 1) / kGemmStep + p.splits - 1) / p.splits * kGemmStep;
+        const EpiSum::Args e = {(float*)(ws + p.sum), sumStride, p.ld, v0 > 0};
+        rc = launch_tokens<true, EpiSum>(p.bm, g, e, st);
+        if (rc) return rc;
+      }
+      if (dw) {
+        g.A = gp;
+        g.lda = p.piece;
+        g.B = xs;
+        g.ldb = (int)lx;
+        g.M = padded;
+        g.N = p.ld;
+        g.K = T;
+        g.splits = 1;
+        g.ksplit = (T + kGemmStep - 1) / kGemmStep * kGemmStep;
+        const EpiWeight::Args e = {dw + (int64_t)v0 * H, scale, width, H};
+        rc = launch<256, 2, 4, true, true, EpiWeight>(g, e, st);
+        if (rc) return rc;
+      }
+    }
+    if (dx)
+      hipLaunchKernelGGL(dx_kernel, dim3(copy_blocks((int64_t)T * p.ld / 4)), dim3(256), 0, st,
+                         (const float*)(ws + p.sum), sumStride, p.splits, p.ld, (const float*)scale, dx, T, H);
+  }
+  if (hipGetLastError() != hipSuccess) return MXW_ERR_LAUNCH;
+  return MXW_OK;
+}
+
+}  // extern "C"

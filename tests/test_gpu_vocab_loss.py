@@ -1,0 +1,217 @@
+"""mxw.vocab_cross_entropy against the definition in 64 bits (needs an MI355X).
+
+Tolerances.  Loss: the logits are FP32 sums of H exact products (error about
+sqrt(H) 2^-24 of the sum of magnitudes A, taken twice for the largest of many),
+the exponentials and the logarithm are good to a few 2^-24:
+2 sqrt(H) 2^-24 A + 2^-21 max(1, |lse|).  Gradients, element by element: g is
+rounded to bf16 (half an ulp: 2^-8 of each term at most) and so is the result:
+2^-8 |ref| + 1.05 2^-8 sum |g| |w| (likewise sum |g| |x| for dw); the FP32
+errors of g fit in the 0.05.
+"""
+import math
+
+import pytest
+import torch
+
+import mxfp8_ragged_grouped_amd as mxw
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+IGNORE = -100
+
+
+def say(msg):
+    print("[gpu-case] " + msg, flush=True)
+
+
+def make(T, H, V, seed, ignored=0.2, scale=1.5, int32=False):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.randn((T, H), generator=g, device=DEV).to(torch.bfloat16)
+    w = (torch.randn((V, H), generator=g, device=DEV) * (scale / math.sqrt(H))).to(torch.bfloat16)
+    y = torch.randint(0, V, (T,), generator=g, device=DEV)
+    y[torch.rand((T,), generator=g, device=DEV) < ignored] = IGNORE
+    y[-1] = V - 1
+    return x, w, y.to(torch.int32) if int32 else y
+
+
+def reference(x, w, y, reduction="mean", grad_scale=1.0, ignore=IGNORE):
+    x, w = x.double(), w.double()
+    logits = x @ w.mT
+    lse = torch.logsumexp(logits, dim=1)
+    used = y != ignore
+    idx = torch.where(used, y, torch.zeros_like(y)).long()
+    rows = torch.where(used, lse - logits.gather(1, idx[:, None])[:, 0], torch.zeros_like(lse))
+    n = max(int(used.sum()), 1)
+    g = torch.exp(logits - lse[:, None])
+    g[torch.arange(len(y), device=DEV), idx] -= 1.0
+    g = g * used[:, None] * (grad_scale / n if reduction == "mean" else grad_scale)
+    loss = rows if reduction == "none" else rows.sum() / (n if reduction == "mean" else 1)
+    A = (x.abs() @ w.abs().mT).max().item()
+    tol = 2 * math.sqrt(x.shape[1]) * 2.0 ** -24 * A + 2.0 ** -21 * max(1.0, lse.abs().max().item())
+    if reduction == "sum":
+        tol *= n
+    return dict(loss=loss, dx=g @ w, dw=g.mT @ x, tol=tol, dx_terms=g.abs() @ w.abs(), dw_terms=g.abs().mT @ x.abs())
+
+
+def check(got, ref, what=""):
+    loss, dx, dw = got
+    assert (loss.double() - ref["loss"]).abs().max().item() <= ref["tol"], what
+    for name, t in (("dx", dx), ("dw", dw)):
+        r = ref[name]
+        bad = (t.double() - r).abs() > 2.0 ** -8 * r.abs() + 1.05 * 2.0 ** -8 * ref[name + "_terms"] + 1e-37
+        assert not bad.any() and torch.isfinite(t).all(), "%s %s: %d of %d outside" % (what, name, int(bad.sum()),
+                                                                                       bad.numel())
+
+
+SIZES = [(1, 1, 1), (1, 1, 7), (1, 64, 1), (2, 3, 257), (5, 192, 1000), (31, 128, 255), (32, 64, 256), (33, 65, 300),
+         (129, 256, 513), (127, 1001, 999), (256, 128, 4096), (300, 320, 2049), (513, 72, 3001), (1, 2048, 32000),
+         (64, 128, 70001)]
+
+
+@pytest.mark.parametrize("T,H,V", SIZES)
+def test_against_64_bits(T, H, V):
+    say("vocab loss T=%d H=%d V=%d" % (T, H, V))
+    x, w, y = make(T, H, V, 2000 + T + H + V, int32=bool(T & 1))
+    dx = torch.full((T, H), float("nan"), dtype=torch.bfloat16, device=DEV)
+    dw = torch.full((V, H), float("nan"), dtype=torch.bfloat16, device=DEV)
+    got = mxw.vocab_cross_entropy(x, w, y, dx=dx, dw=dw)
+    assert got[1] is dx and got[2] is dw
+    ref = reference(x, w, y)
+    check(got, ref, "T=%d H=%d V=%d" % (T, H, V))
+    alone = mxw.vocab_cross_entropy(x, w, y, grads=False)
+    assert torch.equal(alone, got[0])
+
+
+def test_several_pieces():
+    """A vocabulary walked in several pieces (g of all of it would take over
+    256 MiB), aligned and padded operands, ragged last piece."""
+    for T, H in ((4100, 64), (4100, 66)):
+        V = 70003
+        say("vocab loss in pieces T=%d H=%d V=%d" % (T, H, V))
+        x, w, y = make(T, H, V, 77 + H)
+        check(mxw.vocab_cross_entropy(x, w, y), reference(x, w, y), "H=%d" % H)
+
+
+@pytest.mark.parametrize("reduction", ["mean", "sum", "none"])
+def test_reductions_and_scale(reduction):
+    x, w, y = make(70, 96, 700, 3)
+    got = mxw.vocab_cross_entropy(x, w, y, reduction=reduction, grad_scale=0.37)
+    assert got[0].shape == ((70,) if reduction == "none" else ())
+    check(got, reference(x, w, y, reduction, 0.37), reduction)
+
+
+def test_ignored_tokens():
+    """Ignored tokens give zero rows; a batch without a counting token gives
+    loss 0 and zero gradients; another ignore_index; an ignored row of NaN
+    leaves the others alone in loss and dx."""
+    x, w, y = make(40, 64, 300, 4, ignored=0.5)
+    loss, dx, dw = mxw.vocab_cross_entropy(x, w, y, reduction="none")
+    assert (loss[y == IGNORE] == 0).all() and (dx[y == IGNORE] == 0).all()
+    none = torch.full_like(y, IGNORE)
+    loss, dx, dw = mxw.vocab_cross_entropy(x, w, none)
+    assert loss.item() == 0.0 and (dx == 0).all() and (dw == 0).all()
+    y7 = torch.where(y == IGNORE, torch.full_like(y, 7), y)
+    check(mxw.vocab_cross_entropy(x, w, y7, ignore_index=7), reference(x, w, y7, ignore=7), "ignore 7")
+
+
+def test_targets_outside_the_vocabulary():
+    x, w, y = make(20, 64, 300, 5, ignored=0.0)
+    want = mxw.vocab_cross_entropy(x, w, y, reduction="none")
+    bad = y.clone()
+    bad[3], bad[11], bad[12] = 300, -1, 2 ** 40
+    loss, dx, dw = mxw.vocab_cross_entropy(x, w, bad, reduction="none")
+    out = torch.zeros(20, dtype=torch.bool, device=DEV)
+    out[[3, 11, 12]] = True
+    assert loss[out].isnan().all() and torch.equal(loss[~out], want[0][~out])
+    assert (dx[out] == 0).all() and torch.equal(dx[~out], want[1][~out]) and torch.isfinite(dw).all()
+    assert mxw.vocab_cross_entropy(x, w, bad, grads=False).isnan()
+
+
+def test_large_logits_infinities_and_nan():
+    """Logits of several hundred (a one-hot softmax), a weight row of -inf (its
+    word is never said), NaN in one token."""
+    x, w, y = make(40, 64, 300, 6, ignored=0.1, scale=200.0)
+    check(mxw.vocab_cross_entropy(x, w, y), reference(x, w, y), "large logits")
+    x, w, y = make(40, 64, 300, 7, ignored=0.0)
+    x, xn = x.abs(), None
+    y[y == 9] = 10
+    want = mxw.vocab_cross_entropy(x, torch.cat([w[:9], w[10:]]), torch.where(y > 9, y - 1, y), reduction="none",
+                                   grads=False)
+    gone = w.clone()
+    gone[9] = -float("inf")
+    loss = mxw.vocab_cross_entropy(x, gone, y, reduction="none", grads=False)
+    assert (loss - want).abs().max() < 1e-5
+    broken = x.clone()
+    broken[5, 3] = float("nan")
+    rows = mxw.vocab_cross_entropy(broken, w, y, reduction="none", grads=False)
+    assert rows[5].isnan() and torch.isfinite(rows[torch.arange(40, device=DEV) != 5]).all()
+
+
+def test_gradients_against_differences():
+    """The slope of the loss along a direction of x, and of w, from losses on
+    either side (64-bit reference of the loss on perturbed bf16 inputs' exact
+    values), against the gradients: both come from 2^-8-exact numbers, the
+    difference quotient adds its third-order term."""
+    x, w, y = make(24, 64, 200, 8)
+    _, dx, dw = mxw.vocab_cross_entropy(x, w, y, reduction="sum")
+    g = torch.Generator(device=DEV).manual_seed(1)
+    for which, t, grad in (("x", x, dx), ("w", w, dw)):
+        d = torch.randn(t.shape, generator=g, device=DEV).double()
+        h = 1e-4
+
+        def loss(sign):
+            xs = x.double() + (sign * h * d if which == "x" else 0)
+            ws = w.double() + (sign * h * d if which == "w" else 0)
+            logits = xs @ ws.mT
+            used = y != IGNORE
+            rows = torch.logsumexp(logits, 1) - logits.gather(1, y.clamp(min=0)[:, None])[:, 0]
+            return (rows * used).sum()
+
+        slope = (loss(1) - loss(-1)) / (2 * h)
+        assert abs((grad.double() * d).sum() - slope) <= 2.0 ** -8 * (grad.double() * d).abs().sum()
+
+
+def test_strides_and_alignment():
+    """Rows apart, odd first elements, an odd stride: in place and padded reads
+    give the same bits."""
+    x, w, y = make(50, 128, 700, 9)
+    want = mxw.vocab_cross_entropy(x, w, y)
+    for pad, first in ((8, 0), (64, 8), (1, 0), (8, 1), (3, 5)):
+        xb = torch.full((51 * (128 + pad) + 16,), float("nan"), dtype=torch.bfloat16, device=DEV)
+        wb = torch.full((701 * (128 + pad) + 16,), float("nan"), dtype=torch.bfloat16, device=DEV)
+        xs = xb.as_strided((50, 128), (128 + pad, 1), first)
+        ws = wb.as_strided((700, 128), (128 + pad, 1), first)
+        xs.copy_(x)
+        ws.copy_(w)
+        got = mxw.vocab_cross_entropy(xs, ws, y)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), (pad, first)
+    dw = torch.empty(700 * 128 + 1, dtype=torch.bfloat16, device=DEV)[1:].view(700, 128)
+    dx = torch.empty(50 * 128 + 1, dtype=torch.bfloat16, device=DEV)[1:].view(50, 128)
+    got = mxw.vocab_cross_entropy(x, w, y, dx=dx, dw=dw)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_repeats_streams_and_graphs():
+    x, w, y = make(300, 192, 3000, 10)
+    want = mxw.vocab_cross_entropy(x, w, y)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = mxw.vocab_cross_entropy(x, w, y, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(other, want))
+    need = mxw.vocab_loss_workspace_size(x.data_ptr(), 192, w.data_ptr(), 192, 300, 192, 3000)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        loss, _, _ = mxw.vocab_cross_entropy(x, w, y, dx=dx, dw=dw, workspace=ws)
+    for i in range(3):
+        x.copy_(x.roll(1, 0))
+        graph.replay()
+        torch.cuda.synchronize()
+        now = mxw.vocab_cross_entropy(x, w, y)
+        assert all(torch.equal(a, b) for a, b in zip((loss, dx, dw), now)), "replay %d" % i
+    with pytest.raises(ValueError):
+        mxw.vocab_cross_entropy(x, w, y, workspace=ws[:need - 1])
