@@ -520,6 +520,60 @@ int mxw_vocab_loss(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ld
 int64_t mxw_vocab_loss_workspace_size(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw, int T, int H,
                                       int V, int grads);
 
+/* Most tokens of a mxw_moe_layer call. */
+#define MXW_MOE_MAX_TOKENS 64
+
+/*
+ * mxw_moe_layer -- a whole mixture-of-experts layer for a few tokens (single
+ * tokens and small batches, as in generation; mxfp8_grouped_fwd is the form for
+ * many).  For every token t:
+ *
+ *     r_e   = sum_h x[t][h] router[e][h]
+ *     ids   = the k experts with the largest r, largest first (ties: the lower)
+ *     weight_j = softmax(r) at ids[j], divided by the k values' sum if
+ *             `normalize`, times `scale`
+ *     h_j   = silu(x[t] Wg^T) * (x[t] Wu^T)  of expert ids[j]
+ *     out[t] = sum_j weight_j h_j Wd^T
+ *
+ * Arguments (caller-owned DEVICE memory):
+ *   x, ldx   bf16 [T, H], rows ldx >= H elements apart (a multiple of 8).
+ *   router   bf16 [E, H], or NULL: then ids and weights are inputs (an id
+ *            outside [0, E) is an empty slot; weights are used as they are).
+ *   wgu, sgu E4M3 codes [E, 2 I, H] and E8M0 scales [E, 2 I, H/32]: each
+ *            expert's I gate rows, then its I up rows, 32-element blocks along
+ *            H (the layout mxfp8_grouped_fwd takes).
+ *   wd, sd   E4M3 codes [E, H, I] and E8M0 scales [E, H, I/32].
+ *   active   uint8 [T], 0 for a token that is not there (an unused slot of the
+ *            batch): its ids are -1, its weights 0, its out zeros, and x's row
+ *            is not used.  NULL: all are.
+ *   T        1 .. MXW_MOE_MAX_TOKENS.   E  1 .. MXW_MAX_EXPERTS.
+ *   k        1 .. 16, at most E.        H, I  multiples of 32, 32 .. 65536.
+ *   ids, weights  int32 and FP32 [T, k]: outputs, inputs without a router.
+ *   out      bf16 [T, H], contiguous, fully overwritten.
+ *   x, router, wgu, wd 16-byte aligned; ids, weights 4-byte aligned.
+ *   workspace, workspace_bytes  256-byte aligned device memory of at least
+ *            mxw_moe_workspace_size(T, E, k, H, I) bytes; contents undefined on
+ *            entry and exit, in use until the call's work is done.
+ *
+ * Codes and scales become bf16 exactly where their product has a normal bf16
+ * value (below 2^-126 it is 0, beyond bf16's range infinity; scale 0xFF: NaN);
+ * all sums are FP32; weight_j h_j is rounded to bf16 between the two products.
+ * A NaN or infinite logit makes that token's weights and out NaN; no token's
+ * result depends on another's values.  Bitwise reproducible run to run.
+ *
+ * Effects: enqueues two or three kernels on `stream`, allocates nothing, keeps
+ * no state, does not synchronise; graph-capturable.  Only the chosen experts'
+ * weights are read.  Returns MXW_OK or a negative MXW_ERR_* code.
+ */
+int mxw_moe_layer(const uint16_t* x, int64_t ldx, const uint16_t* router, const uint8_t* wgu, const uint8_t* sgu,
+                  const uint8_t* wd, const uint8_t* sd, const uint8_t* active, int T, int E, int k, int H, int I,
+                  int normalize, float scale, int32_t* ids, float* weights, uint16_t* out, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/* mxw_moe_workspace_size -- bytes of workspace that mxw_moe_layer needs, or
+ * MXW_ERR_DIM.  Host-only. */
+int64_t mxw_moe_workspace_size(int T, int E, int k, int H, int I);
+
 /* mxw_strerror -- a static, human-readable message for a return code. */
 const char* mxw_strerror(int code);
 

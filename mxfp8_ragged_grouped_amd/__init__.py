@@ -47,6 +47,7 @@ __all__ = ["wgrad", "mxfp8_wgrad_grouped", "mxfp8_wgrad_grouped_ws", "mxfp8_wgra
            "scale_shuffle", "tail_split", "fwd", "mxfp8_grouped_fwd", "fwd_grid_size", "quantize_tokens", "mxfp8_quantize_tokens",
            "orthogonalize", "mxw_orthogonalize", "orthogonalize_workspace_size",
            "vocab_cross_entropy", "mxw_vocab_loss", "vocab_loss_workspace_size",
+           "moe_layer", "mxw_moe_layer", "moe_workspace_size",
            "strerror", "version", "library_path", "MxwError"]
 
 _lib = None
@@ -112,6 +113,10 @@ def _load():
     lib.mxw_vocab_loss.argtypes = [P, L, P, L, P, I, L, I, I, I, I, F, P, P, P, P, S, P]
     lib.mxw_vocab_loss_workspace_size.restype = L
     lib.mxw_vocab_loss_workspace_size.argtypes = [P, L, P, L, I, I, I, I]
+    lib.mxw_moe_layer.restype = I
+    lib.mxw_moe_layer.argtypes = [P, L, P, P, P, P, P, P, I, I, I, I, I, I, F, P, P, P, P, S, P]
+    lib.mxw_moe_workspace_size.restype = L
+    lib.mxw_moe_workspace_size.argtypes = [I, I, I, I, I]
     _lib = lib
     return lib
 
@@ -212,10 +217,39 @@ def _workspace(need, dev, stream, workspace):
     return ws.data_ptr(), need, ws
 
 
-def _new(shape, dtype, dev, stream):
-    """A fresh tensor that belongs to the stream the call runs on."""
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+class _On:
+    """The device and stream a call runs on (`with` makes the device current;
+    switching to what is current already costs several microseconds, so it is
+    left out)."""
+
+    def __init__(self, dev, stream):
+        current = torch.cuda.current_stream(dev)
+        self.stream = current if stream is None else stream
+        self._other_stream = self.stream != current
+        self._dev = dev
+        self._switch = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self._switch is not None:
+            self._switch.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self._switch is not None:
+            self._switch.__exit__(*exc)
+
+    def new(self, shape, dtype):
+        """A fresh tensor that belongs to the stream."""
+        if self._other_stream:
+            with torch.cuda.stream(self.stream):
+                return torch.empty(shape, dtype=dtype, device=self._dev)
+        return torch.empty(shape, dtype=dtype, device=self._dev)
+
+    def workspace(self, need, workspace):
+        if workspace is not None:
+            return _workspace(need, self._dev, self.stream, workspace)
+        ws = self.new(need, torch.uint8)
+        return ws.data_ptr(), need, ws
 
 
 def _as_u8(t, name):
@@ -508,16 +542,15 @@ def orthogonalize(G, out=None, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e
         coeffs = [coeffs] * steps
     if steps < 1 or len(coeffs) != steps or any(len(c) != 3 for c in coeffs):
         raise ValueError("coeffs must be one (a, b, c) or one for each of the steps")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    on = _On(dev, stream)
     if out is None:
-        out = _new(G.shape, torch.bfloat16, dev, stream)
+        out = on.new(G.shape, torch.bfloat16)
     elif out.dtype != torch.bfloat16 or out.shape != G.shape or not out.is_contiguous() or out.device != dev:
         raise ValueError("out must be a contiguous bf16 tensor of G's shape on the same device")
-    with torch.cuda.device(dev):
-        wp, wb, ws = _workspace(orthogonalize_workspace_size(E, N, K), dev, stream, workspace)
+    with on:
+        wp, wb, ws = on.workspace(orthogonalize_workspace_size(E, N, K), workspace)
         rc = mxw_orthogonalize(G.data_ptr(), 0 if G.dtype == torch.bfloat16 else 1, es, rs, E, N, K,
-                               [float(v) for c in coeffs for v in c], eps, out.data_ptr(), wp, wb, stream.cuda_stream)
+                               [float(v) for c in coeffs for v in c], eps, out.data_ptr(), wp, wb, on.stream.cuda_stream)
         del ws
     if rc != 0:
         raise MxwError("mxw_orthogonalize failed (%d): %s" % (rc, strerror(rc)))
@@ -586,24 +619,117 @@ def vocab_cross_entropy(x, w, targets, ignore_index=-100, reduction="mean", grad
         raise ValueError("targets must be contiguous")
     if not grads and (dx is not None or dw is not None):
         raise ValueError("dx and dw are outputs of grads=True")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    on = _On(dev, stream)
     for name, t, shape in (("dx", dx, (T, H)), ("dw", dw, (V, H))):
         if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != shape or not t.is_contiguous()
                               or t.device != dev):
             raise ValueError("%s must be a contiguous bf16 %s tensor on the same device" % (name, list(shape)))
     if grads:
-        dx = _new((T, H), torch.bfloat16, dev, stream) if dx is None else dx
-        dw = _new((V, H), torch.bfloat16, dev, stream) if dw is None else dw
-    loss = _new((T,) if reduction == "none" else (), torch.float32, dev, stream)
-    with torch.cuda.device(dev):
+        dx = on.new((T, H), torch.bfloat16) if dx is None else dx
+        dw = on.new((V, H), torch.bfloat16) if dw is None else dw
+    loss = on.new((T,) if reduction == "none" else (), torch.float32)
+    with on:
         need = vocab_loss_workspace_size(x.data_ptr(), strides[0], w.data_ptr(), strides[1], T, H, V, 3 if grads else 0)
-        wp, wb, ws = _workspace(need, dev, stream, workspace)
+        wp, wb, ws = on.workspace(need, workspace)
         rc = mxw_vocab_loss(x.data_ptr(), strides[0], w.data_ptr(), strides[1], targets.data_ptr(),
                             targets.element_size(), ignore_index, T, H, V, _REDUCTIONS[reduction], grad_scale,
                             loss.data_ptr(), dx.data_ptr() if grads else 0, dw.data_ptr() if grads else 0, wp, wb,
-                            stream.cuda_stream)
+                            on.stream.cuda_stream)
         del ws
     if rc != 0:
         raise MxwError("mxw_vocab_loss failed (%d): %s" % (rc, strerror(rc)))
     return (loss, dx, dw) if grads else loss
+
+
+def mxw_moe_layer(x, ldx, router, wgu, sgu, wd, sd, active, T, E, k, H, I, normalize, scale, ids, weights, out, workspace,
+                  workspace_bytes, stream=0):
+    """Raw C-ABI call on device addresses (ints; router and active may be 0).
+    Returns the status code."""
+    return _load().mxw_moe_layer(x, int(ldx), router, wgu, sgu, wd, sd, active, int(T), int(E), int(k), int(H), int(I),
+                                 int(bool(normalize)), float(scale), ids, weights, out, workspace, int(workspace_bytes),
+                                 stream)
+
+
+def moe_workspace_size(T, E, k, H, I):
+    """Bytes of workspace moe_layer needs.  Raises MxwError on a status code."""
+    rc = _load().mxw_moe_workspace_size(int(T), int(E), int(k), int(H), int(I))
+    if rc < 0:
+        raise MxwError("mxw_moe_workspace_size failed: %s" % strerror(rc))
+    return int(rc)
+
+
+def moe_layer(x, router, wgu, sgu, wd, sd, top_k, normalize=True, scale=1.0, active=None, routing=None, out=None,
+              stream=None, workspace=None):
+    """A whole mixture-of-experts layer for a few tokens (up to 64):
+    (out [T, H] bf16, ids [T, top_k] int32, weights [T, top_k] float32).
+
+    x: bf16 [T, H] (rows any multiple of 8 elements apart).  router: bf16
+    [E, H]; each token goes to the top_k experts of the largest router logits
+    (ties: the lower index), weighted by the softmax over all experts, divided
+    by the chosen ones' sum if `normalize`, times `scale`.  Or router=None and
+    routing=(ids, weights), contiguous int32 and float32 [T, top_k]; ids
+    outside [0, E) are empty slots.  wgu, sgu: MXFP8 gate and up weights
+    [E, 2 I, H] (codes uint8 or float8_e4m3fn; gate rows first) and
+    [E, 2 I, H/32]; wd, sd: down weights [E, H, I] and [E, H, I/32]; an
+    expert computes (silu(x Wg^T) * (x Wu^T)) Wd^T.  active: bool [T], False
+    for tokens that are not there (ids -1, weights 0, out 0).  Runs on
+    `stream` (default: the current stream) and does not synchronise;
+    `workspace`: a uint8 device tensor of moe_workspace_size() bytes (default:
+    from torch's caching allocator on that stream)."""
+    wgu, sgu, wd, sd = (t.view(torch.uint8) if t.dtype == getattr(torch, "float8_e4m3fn", None) else t
+                        for t in (wgu, sgu, wd, sd))
+    if x.dtype != torch.bfloat16:
+        raise TypeError("x must be bfloat16")
+    for name, t in (("wgu", wgu), ("sgu", sgu), ("wd", wd), ("sd", sd)):
+        if t.dtype != torch.uint8:
+            raise TypeError("%s must be uint8 (or float8_e4m3fn for codes), got %s" % (name, t.dtype))
+        if t.dim() != 3:
+            raise ValueError("%s must be 3-D" % name)
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    T, H = x.shape
+    E, H2, I = wd.shape
+    if H2 != H or wgu.shape != (E, 2 * I, H) or sgu.shape != (E, 2 * I, H // 32) or sd.shape != (E, H, I // 32):
+        raise ValueError("shape mismatch: x %s wgu %s sgu %s wd %s sd %s" % tuple(
+            tuple(t.shape) for t in (x, wgu, sgu, wd, sd)))
+    k = int(top_k)
+    if (router is None) == (routing is None):
+        raise ValueError("give a router or a routing, and not both")
+    ids = weights = None
+    if router is not None:
+        if router.dtype != torch.bfloat16 or tuple(router.shape) != (E, H):
+            raise ValueError("router must be bf16 [E, H]")
+    else:
+        ids, weights = routing
+        if ids.dtype != torch.int32 or weights.dtype != torch.float32 or tuple(ids.shape) != (T, k) or tuple(
+                weights.shape) != (T, k):
+            raise ValueError("routing must be int32 and float32 [T, top_k]")
+    if active is not None and (active.dtype not in (torch.bool, torch.uint8) or tuple(active.shape) != (T,)):
+        raise ValueError("active must be bool [T]")
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("x must be on the GPU")
+    for name, t in (("router", router), ("wgu", wgu), ("sgu", sgu), ("wd", wd), ("sd", sd), ("ids", ids),
+                    ("weights", weights), ("active", active)):
+        if t is not None and (t.device != dev or not t.is_contiguous()):
+            raise ValueError("%s must be contiguous and on the same GPU as x" % name)
+    if x.stride(1) != 1 or (T > 1 and x.stride(0) < H):
+        raise ValueError("x must have a contiguous last axis and rows at least a row apart")
+    on = _On(dev, stream)
+    if out is None:
+        out = on.new((T, H), torch.bfloat16)
+    elif out.dtype != torch.bfloat16 or tuple(out.shape) != (T, H) or not out.is_contiguous() or out.device != dev:
+        raise ValueError("out must be a contiguous bf16 [T, H] tensor on the same device")
+    if ids is None:
+        ids = on.new((T, k), torch.int32)
+        weights = on.new((T, k), torch.float32)
+    with on:
+        wp, wb, ws = on.workspace(moe_workspace_size(T, E, k, H, I), workspace)
+        rc = mxw_moe_layer(x.data_ptr(), x.stride(0) if T > 1 else H, 0 if router is None else router.data_ptr(),
+                           wgu.data_ptr(), sgu.data_ptr(), wd.data_ptr(), sd.data_ptr(),
+                           0 if active is None else active.data_ptr(), T, E, k, H, I, normalize, scale, ids.data_ptr(),
+                           weights.data_ptr(), out.data_ptr(), wp, wb, on.stream.cuda_stream)
+        del ws
+    if rc != 0:
+        raise MxwError("mxw_moe_layer failed (%d): %s" % (rc, strerror(rc)))
+    return out, ids, weights

@@ -14,7 +14,7 @@ import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = [os.path.join(HERE, "csrc", n) for n in ("mxfp8_wgrad.hip", "ortho.hip", "vocab_loss.hip")]
+SOURCES = [os.path.join(HERE, "csrc", n) for n in ("mxfp8_wgrad.hip", "ortho.hip", "vocab_loss.hip", "moe_layer.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libmxfp8_wgrad.so")

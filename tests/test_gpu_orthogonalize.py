@@ -119,6 +119,13 @@ def test_strides_and_alignment(dtype):
     assert torch.equal(mxw.orthogonalize(G, out=out), want)
 
 
+def test_rows_past_32_bit_offsets():
+    G = spread(1, 2200, 64, 12).to(torch.bfloat16)[0]
+    far = torch.empty(2200 << 20, dtype=torch.bfloat16, device=DEV).view(2200, 1 << 20)[:, 5:69]
+    far.copy_(G)
+    assert torch.equal(mxw.orthogonalize(far), mxw.orthogonalize(G))
+
+
 def test_empty_and_broken_experts_stay_alone():
     """A zero gradient gives zeros; NaN and infinity stay in their expert."""
     G = spread(5, 130, 200, 8).to(torch.bfloat16)

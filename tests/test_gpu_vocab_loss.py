@@ -192,6 +192,30 @@ def test_strides_and_alignment():
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_weights_past_32_bit_offsets():
+    """A vocabulary of more than 4 GiB: the last words' logits and gradients."""
+    T, H, V = 3, 7168, 320001
+    x, _, _ = make(T, H, 8, 13)
+    w = torch.zeros((V, H), dtype=torch.bfloat16, device=DEV)
+    last = make(T, H, 500, 14)[1]
+    w[-500:] = last
+    y = torch.tensor([V - 1, V - 500, 3], device=DEV)
+    loss, dx, dw = mxw.vocab_cross_entropy(x, w, y, reduction="none")
+    # the words of zero weight share logit 0: one word of weight V - 500
+    logits = x.double() @ last.double().mT
+    both = torch.cat([logits, torch.full((T, 1), math.log(V - 500), dtype=torch.float64, device=DEV)], 1)
+    lse = torch.logsumexp(both, 1)
+    ref = lse - torch.stack([logits[0, 499], logits[1, 0], torch.zeros((), dtype=torch.float64, device=DEV)])
+    A = (x.double().abs() @ last.double().abs().mT).max().item()
+    assert (loss.double() - ref).abs().max() <= 2 * math.sqrt(H) * 2.0 ** -24 * A + 2.0 ** -21 * lse.max()
+    g = torch.exp(logits - lse[:, None])
+    g[0, 499] -= 1
+    g[1, 0] -= 1
+    for t, r, terms in ((dw[-500:], g.mT @ x.double(), g.abs().mT @ x.double().abs()),
+                        (dx, g @ last.double(), g.abs() @ last.double().abs())):
+        assert ((t.double() - r).abs() <= 2.0 ** -8 * r.abs() + 1.05 * 2.0 ** -8 * terms + 1e-37).all()
+
+
 def test_repeats_streams_and_graphs():
     x, w, y = make(300, 192, 3000, 10)
     want = mxw.vocab_cross_entropy(x, w, y)

@@ -1,4 +1,4 @@
-"""The host checks of orthogonalize and vocab_cross_entropy: bad arguments come
+"""The host checks of orthogonalize, vocab_cross_entropy and moe_layer: bad arguments come
 back as status codes or exceptions before any device access (CPU only)."""
 import ctypes
 
@@ -110,3 +110,48 @@ def test_vocab_loss_python_face_validates():
         mxw.vocab_cross_entropy(x, w, y[:3])
     with pytest.raises(ValueError):
         mxw.vocab_cross_entropy(x[:0], w, y[:0])
+
+
+def moe_args(**over):
+    a = dict(x=P, ldx=64, router=P, wgu=P, sgu=P, wd=P, sd=P, active=0, T=4, E=8, k=2, H=64, I=32, normalize=1,
+             scale=1.0, ids=P, weights=P, out=P, workspace=P, workspace_bytes=BIG)
+    a.update(over)
+    return tuple(a.values())
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(x=0), -1), (dict(wgu=0), -1), (dict(sgu=0), -1), (dict(wd=0), -1), (dict(sd=0), -1), (dict(ids=0), -1),
+    (dict(weights=0), -1), (dict(out=0), -1),
+    (dict(T=0), -2), (dict(T=65), -2), (dict(E=0), -2), (dict(E=257), -2), (dict(k=0), -2), (dict(k=9), -2),
+    (dict(E=32, k=17), -2), (dict(H=48), -2), (dict(H=0), -2), (dict(I=16), -2), (dict(I=65568), -2),
+    (dict(ldx=63), -2), (dict(ldx=68), -2),
+    (dict(x=P + 8), -3), (dict(router=P + 2), -3), (dict(wgu=P + 4), -3), (dict(wd=P + 8), -3), (dict(out=P + 1), -3),
+    (dict(ids=P + 2), -3), (dict(weights=P + 1), -3),
+    (dict(workspace=0), -6), (dict(workspace_bytes=64), -6), (dict(workspace=P + 128), -6),
+])
+def test_moe_host_checks(over, code):
+    assert mxw.mxw_moe_layer(*moe_args(**over)) == code
+
+
+def test_moe_workspace_size():
+    assert mxw.moe_workspace_size(64, 256, 8, 2048, 1408) >= 64 * 8 * 1408 * 2
+    with pytest.raises(mxw.MxwError):
+        mxw.moe_workspace_size(65, 8, 2, 64, 32)
+
+
+def test_moe_python_face_validates():
+    u8 = torch.uint8
+    a = dict(x=torch.zeros((4, 64), dtype=torch.bfloat16), router=torch.zeros((8, 64), dtype=torch.bfloat16),
+             wgu=torch.zeros((8, 64, 64), dtype=u8), sgu=torch.zeros((8, 64, 2), dtype=u8),
+             wd=torch.zeros((8, 64, 32), dtype=u8), sd=torch.zeros((8, 64, 1), dtype=u8), top_k=2)
+    ids, w = torch.zeros((4, 2), dtype=torch.int32), torch.zeros((4, 2))
+    for error, over in ((ValueError, {}),                                   # CPU tensors: no host fallback
+                        (TypeError, dict(x=a["x"].float())), (TypeError, dict(wgu=a["wgu"].to(torch.int8))),
+                        (ValueError, dict(sgu=a["sgu"][..., :1])), (ValueError, dict(x=a["x"][:, :32])),
+                        (ValueError, dict(router=a["router"][:7])), (ValueError, dict(router=None)),
+                        (ValueError, dict(routing=(ids, w))),               # a router and a routing
+                        (ValueError, dict(router=None, routing=(ids.long(), w))),
+                        (ValueError, dict(router=None, routing=(ids[:, :1], w))),
+                        (ValueError, dict(active=torch.zeros(3, dtype=torch.bool)))):
+        with pytest.raises(error):
+            mxw.moe_layer(**dict(a, **over))
