@@ -11,11 +11,12 @@
 // A row-form stage is read 16 bytes (8 k) a lane; a column-form stage through
 // the transposing LDS read (within 16 lanes, lane i element j receives element
 // i % 4 of the 8 bytes that lane 4 j + i / 4 addresses; checked on gfx950), so
-// both give the MFMA the same fragment: lane l holds row l % 32 and
-// k = 8 (l / 32) .. + 7 of a 16-deep step.
+// both give the MFMA 16 x 16 x 32 the same fragment: lane l holds row l % 16 and
+// k = 8 (l / 16) .. + 7 of a 32-deep part.
 //
 // A workgroup owns one BM x BN tile (WM x WN waves) and walks K in steps of 64
-// through two LDS stages filled by 16-byte LDS-direct buffer loads.  The
+// through LDS stages (three of A, two of B: with 256 x 256 tiles the whole 160 KiB)
+// filled by 16-byte LDS-direct buffer loads.  The
 // buffer descriptor is rebased every step (64-bit), its range ending with the
 // matrix: rows past the end read as zeros, so K and the tile edges need no
 // masks as long as a row-form operand is stored with its k padded to a multiple
@@ -24,8 +25,8 @@
 // row's values: they feed only output rows or columns that are not stored.
 //
 // The MFMA's first operand is B, so a lane ends with 4 consecutive n of one m:
-// register r of block (mi, ni) in lane l is m = 32 mi + l % 32,
-// n = 32 ni + 8 (r / 4) + 4 (l / 32) + r % 4 of the wave's part.
+// register r of block (mi, ni) in lane l is m = 16 mi + l % 16,
+// n = 16 ni + 4 (l / 16) + r of the wave's part.
 #ifndef MXW_GEMM16_H
 #define MXW_GEMM16_H
 
@@ -34,7 +35,7 @@
 
 namespace mxw {
 
-typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float v4f __attribute__((ext_vector_type(4)));
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v2i __attribute__((ext_vector_type(2)));
 typedef short v4s __attribute__((ext_vector_type(4)));
@@ -48,6 +49,11 @@ constexpr int kGemmStep = 64;  // k per LDS stage: 128 bytes, one cache line a r
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+}
+
+// a buffer's range for so many bytes left
+__device__ __forceinline__ uint32_t range_of(int64_t left) {
+  return left <= 0 ? 0u : left > 0x7FFFFFFF ? 0x7FFFFFFFu : (uint32_t)left;
 }
 
 // LDS-direct load: lane l's 16 bytes at byte offset voff of the buffer land at
@@ -65,20 +71,21 @@ __device__ __forceinline__ void load_lds16(const __amdgpu_buffer_rsrc_t& rsrc, u
 }
 #pragma clang diagnostic pop
 
-// every load of this wave has landed and every LDS read has returned, then the
-// workgroup's barrier; no memory access moves across
+// all but the last N loads of this wave have landed and every LDS read has
+// returned, then the workgroup's barrier; no memory access moves across
+template <int N>
 __device__ __forceinline__ void stage_barrier() {
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0070);
+  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
 
-__device__ __forceinline__ v16f mfma16(const v4i& a, const v4i& b, const v16f& c, __bf16) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+__device__ __forceinline__ v4f mfma16(const v4i& a, const v4i& b, const v4f& c, __bf16) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
-__device__ __forceinline__ v16f mfma16(const v4i& a, const v4i& b, const v16f& c, _Float16) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+__device__ __forceinline__ v4f mfma16(const v4i& a, const v4i& b, const v4f& c, _Float16) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
 }
 
 // two floats rounded to nearest even, packed
@@ -108,6 +115,14 @@ struct GemmArgs {
   int ksplit;   // k per split, a multiple of 64
 };
 
+// Where the 16-byte chunks of a stage's rows lie, so that a fragment read, which
+// takes 256 bytes at a time, meets every LDS bank once.  Row form (128-byte
+// rows, 16 lanes at one chunk of 16 rows): chunk c of row r at c ^ (r / 2) % 8.
+// Column form (32 lanes at 32 bytes of 8 different k): chunk c of row k at
+// c ^ (4 (k % 4) + 2 (k / 8 % 2)).
+__device__ __forceinline__ int row_swizzle(int r) { return (r >> 1) & 7; }
+__device__ __forceinline__ int col_swizzle(int k) { return ((k & 3) << 2) | ((k >> 2) & 2); }
+
 // what an epilogue gets to know of its tile
 struct TileAt {
   int batch, split, m0, n0;
@@ -132,15 +147,17 @@ __device__ __forceinline__ int xcd_run(int b, int n) {
 }
 
 template <typename T, int BM, int BN, int WM, int WN, bool TA, bool TB, bool SYM, class Epi>
-__global__ __launch_bounds__(WM* WN * 64, 2) void gemm16_kernel(GemmArgs p, typename Epi::Args ea) {
+__global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) void gemm16_kernel(GemmArgs p, typename Epi::Args ea) {
   constexpr int kWaves = WM * WN;
   constexpr int kPartM = BM / WM, kPartN = BN / WN;
-  constexpr int MI = kPartM / 32, NI = kPartN / 32;
-  constexpr int kBytesA = BM * 128, kBytesB = BN * 128, kStage = kBytesA + kBytesB;
+  constexpr int MI = kPartM / 16, NI = kPartN / 16;
+  constexpr int kBytesA = BM * 128, kBytesB = BN * 128;  // a stage of A, of B
   constexpr int kLoadsA = BM / 8, kLoadsB = BN / 8;  // 1 KiB loads per stage
   constexpr int LA = (kLoadsA + kWaves - 1) / kWaves, LB = (kLoadsB + kWaves - 1) / kWaves;
-  constexpr int kTileLds = Epi::kStaged ? BM * BN * 2 : 0;
-  __shared__ __align__(1024) uint8_t lds[2 * kStage > kTileLds ? 2 * kStage : kTileLds];
+  // three stages of A and two of B; the epilogue's tile takes their place
+  constexpr int kLds = 3 * kBytesA + 2 * kBytesB;
+  static_assert(!Epi::kStaged || BM * BN * 2 <= kLds, "the staged tile fits");
+  __shared__ __align__(1024) uint8_t lds[kLds];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   TileAt at;
@@ -203,10 +220,10 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void gemm16_kernel(GemmArgs p, type
       if (TA) {
         constexpr int kLanes = BM / 8;  // lanes (16-byte chunks) a k
         const int k = u * (64 / kLanes) + lane / kLanes, c = lane % kLanes;
-        voA[i] = (uint32_t)(k * la + ((c ^ ((k & 3) << 2)) << 4));
+        voA[i] = (uint32_t)(k * la + ((c ^ col_swizzle(k)) << 4));
       } else {
         const int r = u * 8 + (lane >> 3), c = lane & 7;
-        voA[i] = (uint32_t)(r * la + ((c ^ ((r >> 1) & 7)) << 4));
+        voA[i] = (uint32_t)(r * la + ((c ^ row_swizzle(r)) << 4));
       }
     }
 #pragma unroll
@@ -215,10 +232,10 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void gemm16_kernel(GemmArgs p, type
       if (TB) {
         constexpr int kLanes = BN / 8;
         const int k = u * (64 / kLanes) + lane / kLanes, c = lane % kLanes;
-        voB[i] = (uint32_t)(k * lb + ((c ^ ((k & 3) << 2)) << 4));
+        voB[i] = (uint32_t)(k * lb + ((c ^ col_swizzle(k)) << 4));
       } else {
         const int r = u * 8 + (lane >> 3), c = lane & 7;
-        voB[i] = (uint32_t)(r * lb + ((c ^ ((r >> 1) & 7)) << 4));
+        voB[i] = (uint32_t)(r * lb + ((c ^ row_swizzle(r)) << 4));
       }
     }
   }
@@ -226,113 +243,165 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void gemm16_kernel(GemmArgs p, type
   const int64_t stepB = TB ? 2 * (int64_t)kGemmStep * p.ldb : 2 * kGemmStep;
   const uint32_t ldsBase = (uint32_t)(uintptr_t)lds;
 
-  auto fill = [&](int stage) {
-    const uint32_t ra = leftA <= 0 ? 0u : leftA > 0x7FFFFFFF ? 0x7FFFFFFFu : (uint32_t)leftA;
-    const uint32_t rb = leftB <= 0 ? 0u : leftB > 0x7FFFFFFF ? 0x7FFFFFFFu : (uint32_t)leftB;
-    const __amdgpu_buffer_rsrc_t A = buffer_of(baseA, ra), B = buffer_of(baseB, rb);
-    const uint32_t to = ldsBase + stage * kStage + wave * 1024;
+  // this wave's loads [from, to) of a stage of A (B); the last one moves on to
+  // the next step
+  auto fillA = [&](uint32_t at, int from, int to) {
 #pragma unroll
-    for (int i = 0; i < LA; ++i)
-      if (kLoadsA % kWaves == 0 || wave + i * kWaves < kLoadsA) load_lds16(A, to + i * kWaves * 1024, voA[i]);
+    for (int i = from; i < to; ++i)
+      if (kLoadsA % kWaves == 0 || wave + i * kWaves < kLoadsA)
+        load_lds16(buffer_of(baseA, range_of(leftA)), at + i * kWaves * 1024, voA[i]);
+    if (to == LA && from < to) {
+      baseA += stepA;
+      leftA -= stepA;
+    }
+  };
+  auto fillB = [&](uint32_t at, int from, int to) {
 #pragma unroll
-    for (int i = 0; i < LB; ++i)
-      if (kLoadsB % kWaves == 0 || wave + i * kWaves < kLoadsB) load_lds16(B, to + kBytesA + i * kWaves * 1024, voB[i]);
-    baseA += stepA;
-    baseB += stepB;
-    leftA -= stepA;
-    leftB -= stepB;
+    for (int i = from; i < to; ++i)
+      if (kLoadsB % kWaves == 0 || wave + i * kWaves < kLoadsB)
+        load_lds16(buffer_of(baseB, range_of(leftB)), at + i * kWaves * 1024, voB[i]);
+    if (to == LB && from < to) {
+      baseB += stepB;
+      leftB -= stepB;
+    }
   };
 
-  // fragment addresses within a stage
-  uint32_t fa[TA ? MI : 4], fb[TB ? NI : 4];
+  // fragment addresses within a stage: of each 32-deep part (row form) or each
+  // block of 16 rows (column form)
+  uint32_t fa[TA ? MI : 2], fb[TB ? NI : 2];
   {
-    const int hi = lane >> 5, sw = ((lane & 31) >> 1) & 7;
-    const int tk = 8 * hi + ((lane & 15) >> 2), x = (lane & 15) >> 2, tc = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    const int g = lane >> 4, r = lane & 15;
+    const int tk = 8 * g + (r >> 2), x = col_swizzle(tk), tc = (lane & 3) >> 1;
     if (TA) {
 #pragma unroll
       for (int i = 0; i < (TA ? MI : 0); ++i)
-        fa[i] = tk * BM * 2 + (((((at.wm >> 5) + i) ^ x) * 4 + tc) << 4) + ((lane & 1) << 3);
+        fa[i] = tk * BM * 2 + (((((at.wm >> 4) + i) * 2 + tc) ^ x) << 4) + ((lane & 1) << 3);
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) fa[j] = (at.wm + (lane & 31)) * 128 + (((2 * j + hi) ^ sw) << 4);
+      for (int j = 0; j < 2; ++j) fa[j] = (at.wm + r) * 128 + (((4 * j + g) ^ row_swizzle(r)) << 4);
     }
     if (TB) {
 #pragma unroll
       for (int i = 0; i < (TB ? NI : 0); ++i)
-        fb[i] = tk * BN * 2 + (((((at.wn >> 5) + i) ^ x) * 4 + tc) << 4) + ((lane & 1) << 3);
+        fb[i] = tk * BN * 2 + (((((at.wn >> 4) + i) * 2 + tc) ^ x) << 4) + ((lane & 1) << 3);
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) fb[j] = (at.wn + (lane & 31)) * 128 + (((2 * j + hi) ^ sw) << 4);
+      for (int j = 0; j < 2; ++j) fb[j] = (at.wn + r) * 128 + (((4 * j + g) ^ row_swizzle(r)) << 4);
     }
   }
 
-  v16f acc[MI][NI];
+  v4f acc[MI][NI];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NI; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+      for (int r = 0; r < 4; ++r) acc[i][j][r] = 0.0f;
 
-  if (steps > 0) fill(0);
-  for (int s = 0; s < steps; ++s) {
-    stage_barrier();  // this stage has landed, the other has been read
-    if (s + 1 < steps) fill((s + 1) & 1);
-    const uint8_t* sa = lds + (s & 1) * kStage;
-    const uint8_t* sb = sa + kBytesA;
+  // fragment i of part j (32 k) of the stage at byte `from`
+  auto readA = [&](uint32_t from, int j, int i) -> v4i {
+    const uint8_t* st = lds + from;
+    if (TA) {
+      const v2i lo = lds_read_tr(st + fa[TA ? i : 0] + 32 * j * BM * 2);
+      const v2i hi = lds_read_tr(st + fa[TA ? i : 0] + (32 * j + 4) * BM * 2);
+      return (v4i){lo.x, lo.y, hi.x, hi.y};
+    }
+    return *(const v4i*)(st + fa[TA ? 0 : j] + i * 16 * 128);
+  };
+  auto readB = [&](uint32_t from, int j, int i) -> v4i {
+    const uint8_t* st = lds + 3 * kBytesA + from;
+    if (TB) {
+      const v2i lo = lds_read_tr(st + fb[TB ? i : 0] + 32 * j * BN * 2);
+      const v2i hi = lds_read_tr(st + fb[TB ? i : 0] + (32 * j + 4) * BN * 2);
+      return (v4i){lo.x, lo.y, hi.x, hi.y};
+    }
+    return *(const v4i*)(st + fb[TB ? 0 : j] + i * 16 * 128);
+  };
+
+  // The pipeline, in rows of NI MFMAs (one A fragment against all of B's): after
+  // a row its A fragment is replaced by the next part's, and B's fragments of
+  // the next part come in meanwhile, so every read has about a part's MFMAs to
+  // return.  A step's only barrier starts its second part: it certifies that
+  // the next step's stages have landed and that everyone has read this one's.
+  // The loads are spread thinly (a CU's vector memory path takes a 1 KiB load
+  // per ~16 clocks, and a wave that waits for it issues no MFMA): B's of the step
+  // after next in the second part, into the stage just read, and A's of the step
+  // after next in the first part, into the third A stage, so that they may be in
+  // flight across the next barrier.
+  constexpr int kOldest = kLoadsA % kWaves == 0 ? LA : 0;  // loads a barrier leaves in flight
+  {
+    static_assert(NI <= MI, "a B fragment of the next part is read in each of the first NI rows");
+    const uint32_t ldsA = ldsBase + wave * 1024, ldsB = ldsA + 3 * kBytesA;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v4i a[MI], b[NI];
+    for (int i = 0; i < 2; ++i) {
+      fillA(ldsA + i * kBytesA, 0, LA);
+      fillB(ldsB + i * kBytesB, 0, LB);
+    }
+    stage_barrier<kLoadsA % kWaves == 0 && kLoadsB % kWaves == 0 ? LA + LB : 0>();
+    // in the order of the loop: a read's age tells the wait before its use
+    v4i a[MI], b[2][NI];
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        if (TB) {
-          const v2i lo = lds_read_tr(sb + fb[i] + 16 * j * BN * 2), hi = lds_read_tr(sb + fb[i] + (16 * j + 4) * BN * 2);
-          b[i] = (v4i){lo.x, lo.y, hi.x, hi.y};
-        } else {
-          b[i] = *(const v4i*)(sb + fb[TB ? 0 : j] + i * 32 * 128);
-        }
+    for (int i = 0; i < MI; ++i) {
+      if (i < NI) b[0][i] = readB(0, 0, i);
+      __builtin_amdgcn_sched_barrier(0);
+      a[i] = readA(0, 0, i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    uint32_t a0 = 0, a1 = kBytesA, a2 = 2 * kBytesA, b0 = 0, b1 = kBytesB;
+    for (int s = 0; s < steps; ++s) {
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) {
+        if (mi < NI) b[1][mi] = readB(b0, 1, mi);
+        fillA(ldsA + a2, mi * LA / MI, (mi + 1) * LA / MI);
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = mfma16(b[0][ni], a[mi], acc[mi][ni], T());
+        a[mi] = readA(a0, 1, mi);
+        __builtin_amdgcn_sched_barrier(0);
       }
+      stage_barrier<kOldest>();
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        if (TA) {
-          const v2i lo = lds_read_tr(sa + fa[i] + 16 * j * BM * 2), hi = lds_read_tr(sa + fa[i] + (16 * j + 4) * BM * 2);
-          a[i] = (v4i){lo.x, lo.y, hi.x, hi.y};
-        } else {
-          a[i] = *(const v4i*)(sa + fa[TA ? 0 : j] + i * 32 * 128);
-        }
+      for (int mi = 0; mi < MI; ++mi) {
+        if (mi < NI) b[0][mi] = readB(b1, 0, mi);
+        fillB(ldsB + b0, mi * LB / MI, (mi + 1) * LB / MI);
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = mfma16(b[1][ni], a[mi], acc[mi][ni], T());
+        a[mi] = readA(a1, 0, mi);
+        __builtin_amdgcn_sched_barrier(0);
       }
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int k = 0; k < NI; ++k) acc[i][k] = mfma16(b[k], a[i], acc[i][k], T());
+      uint32_t t = a0;
+      a0 = a1;
+      a1 = a2;
+      a2 = t;
+      t = b0;
+      b0 = b1;
+      b1 = t;
     }
   }
-  __syncthreads();  // the stages are free for the epilogue
+  // the loads past the last step (their range is empty: zeros) have landed too,
+  // and the stages are free for the epilogue
+  stage_barrier<0>();
   Epi::template run<BM, BN, WM, WN, MI, NI>(p, ea, at, acc, lds);
 }
 
 // ---- helpers for epilogues that stage a 16-bit tile -------------------------
 
 // the wave's part of the tile, its sums passed four at a time (row m, columns
-// n .. n + 3, n a multiple of 4; i: the row's 32-row block in the part) through
+// n .. n + 3, n a multiple of 4; i: the row's 16-row block in the part) through
 // quad(i, m, n, v), rounded to T and staged
 template <typename T, int BN, int MI, int NI, class F>
-__device__ __forceinline__ void stage_part(const TileAt& at, const v16f (&acc)[MI][NI], uint8_t* lds, F quad) {
+__device__ __forceinline__ void stage_part(const TileAt& at, const v4f (&acc)[MI][NI], uint8_t* lds, F quad) {
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
-    const int r = at.wm + 32 * i + (at.lane & 31);
+    const int r = at.wm + 16 * i + (at.lane & 15);
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
+      const int c = at.wn + 16 * j + 4 * (at.lane >> 4);
+      float v[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int c = at.wn + 32 * j + 8 * q + 4 * (at.lane >> 5);
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e];
-        quad(i, at.m0 + r, at.n0 + c, v);
-        const v2i w = {(int)pack2(v[0], v[1], T()), (int)pack2(v[2], v[3], T())};
-        *(v2i*)(lds + tile_at<BN>(r, c >> 3) + ((c & 4) << 1)) = w;
-      }
+      for (int e = 0; e < 4; ++e) v[e] = acc[i][j][e];
+      quad(i, at.m0 + r, at.n0 + c, v);
+      const v2i w = {(int)pack2(v[0], v[1], T()), (int)pack2(v[2], v[3], T())};
+      *(v2i*)(lds + tile_at<BN>(r, c >> 3) + ((c & 4) << 1)) = w;
     }
   }
 }

@@ -39,7 +39,7 @@ using mxw::pack2;
 using mxw::v4i;
 using mxw::v8bf;
 
-typedef float v4f __attribute__((ext_vector_type(4)));
+using mxw::v4f;
 
 constexpr int kMaxTokens = MXW_MOE_MAX_TOKENS;  // a 64-bit mask of tokens per expert
 constexpr int kMaxChoices = 16;

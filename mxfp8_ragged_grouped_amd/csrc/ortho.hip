@@ -137,7 +137,7 @@ struct EpiGram {
     int n, ld;
   };
   template <int BM, int BN, int WM, int WN, int MI, int NI>
-  static __device__ void run(const GemmArgs&, const Args& a, const TileAt& at, v16f (&acc)[MI][NI], uint8_t* lds) {
+  static __device__ void run(const GemmArgs&, const Args& a, const TileAt& at, v4f (&acc)[MI][NI], uint8_t* lds) {
     stage_part<_Float16, BN>(at, acc, lds, [&](int, int, int, float (&v)[4]) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] *= kPerOne;
@@ -160,7 +160,7 @@ struct EpiPoly {
     float a, b, c;
   };
   template <int BM, int BN, int WM, int WN, int MI, int NI>
-  static __device__ void run(const GemmArgs&, const Args& a, const TileAt& at, v16f (&acc)[MI][NI], uint8_t* lds) {
+  static __device__ void run(const GemmArgs&, const Args& a, const TileAt& at, v4f (&acc)[MI][NI], uint8_t* lds) {
     const uint16_t* S = a.S + at.batch * a.stride;
     stage_part<_Float16, BN>(at, acc, lds, [&](int, int m, int n, float (&v)[4]) {
       typedef _Float16 v4h __attribute__((ext_vector_type(4)));
@@ -187,7 +187,7 @@ struct EpiNext {
     int rows, cols, ld;
   };
   template <int BM, int BN, int WM, int WN, int MI, int NI>
-  static __device__ void run(const GemmArgs&, const Args& a, const TileAt& at, v16f (&acc)[MI][NI], uint8_t* lds) {
+  static __device__ void run(const GemmArgs&, const Args& a, const TileAt& at, v4f (&acc)[MI][NI], uint8_t* lds) {
     constexpr float kScale = LAST ? kPerOne * kPerOne : kPerOne;
     auto scale = [&](int, int, int, float (&v)[4]) {
 #pragma unroll

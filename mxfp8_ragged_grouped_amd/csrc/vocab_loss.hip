@@ -78,39 +78,39 @@ struct EpiStats {
     int v0, V;         // the piece's first column; columns in all
   };
   template <int BM, int BN, int WM, int WN, int MI, int NI>
-  static __device__ void run(const GemmArgs& p, const Args& a, const TileAt& at, v16f (&acc)[MI][NI], uint8_t* lds) {
+  static __device__ void run(const GemmArgs& p, const Args& a, const TileAt& at, v4f (&acc)[MI][NI], uint8_t* lds) {
     float2(*sh)[BM] = (float2(*)[BM])lds;  // [WN][BM]
     // columns of the wave's part from this lane's first on, and how many of
     // them the vocabulary has
-    const int c0 = a.v0 + at.n0 + at.wn + 4 * (at.lane >> 5), left = a.V - c0;
+    const int c0 = a.v0 + at.n0 + at.wn + 4 * (at.lane >> 4), left = a.V - c0;
     if (a.v0 + at.n0 + BN > a.V) {
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int j = 0; j < NI; ++j)
 #pragma unroll
-          for (int q = 0; q < 16; ++q)
-            acc[i][j][q] = 32 * j + 8 * (q >> 2) + (q & 3) < left ? acc[i][j][q] : -INFINITY;
+          for (int q = 0; q < 4; ++q) acc[i][j][q] = 16 * j + q < left ? acc[i][j][q] : -INFINITY;
     }
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      const int r = at.wm + 32 * i + (at.lane & 31), t = at.m0 + r;
+      const int r = at.wm + 16 * i + (at.lane & 15), t = at.m0 + r;
       const int y = (t < p.M ? a.y.at(t) : -1) - c0;  // the target among this lane's columns
       float m = -INFINITY, s = 0.0f, hit = 0.0f;
 #pragma unroll
       for (int j = 0; j < NI; ++j)
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
+        for (int q = 0; q < 4; ++q) {
           m = fmaxf(m, acc[i][j][q]);
-          hit = y == 32 * j + 8 * (q >> 2) + (q & 3) ? acc[i][j][q] : hit;
+          hit = y == 16 * j + q ? acc[i][j][q] : hit;
         }
 #pragma unroll
       for (int j = 0; j < NI; ++j)
 #pragma unroll
-        for (int q = 0; q < 16; ++q) s += exp_above(acc[i][j][q], m);
-      if (y >= 0 && y < 32 * NI && (y & 4) == 0) a.hit[t] = hit;
+        for (int q = 0; q < 4; ++q) s += exp_above(acc[i][j][q], m);
+      if (y >= 0 && y < 16 * NI && (y & 12) == 0) a.hit[t] = hit;
+      join(m, s, __shfl_xor(m, 16), __shfl_xor(s, 16));
       join(m, s, __shfl_xor(m, 32), __shfl_xor(s, 32));
-      if (at.lane < 32) sh[at.wave % WN][r] = make_float2(m, s);
+      if (at.lane < 16) sh[at.wave % WN][r] = make_float2(m, s);
     }
     __syncthreads();
     const int tid = at.wave * 64 + at.lane;
@@ -187,12 +187,12 @@ struct EpiGrad {
     int v0, V, ncols;  // ncols: the piece's columns, rounded up to 64
   };
   template <int BM, int BN, int WM, int WN, int MI, int NI>
-  static __device__ void run(const GemmArgs& p, const Args& a, const TileAt& at, v16f (&acc)[MI][NI], uint8_t* lds) {
+  static __device__ void run(const GemmArgs& p, const Args& a, const TileAt& at, v4f (&acc)[MI][NI], uint8_t* lds) {
     float lse[MI];
     int y[MI];
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      const int t = at.m0 + at.wm + 32 * i + (at.lane & 31);
+      const int t = at.m0 + at.wm + 16 * i + (at.lane & 15);
       y[i] = t < p.M ? a.y.at(t) : -1;
       lse[i] = t < p.M ? a.lse[t] : 0.0f;
     }
@@ -218,25 +218,18 @@ struct EpiSum {
     int ld, add;
   };
   template <int BM, int BN, int WM, int WN, int MI, int NI>
-  static __device__ void run(const GemmArgs& p, const Args& a, const TileAt& at, v16f (&acc)[MI][NI], uint8_t*) {
+  static __device__ void run(const GemmArgs& p, const Args& a, const TileAt& at, v4f (&acc)[MI][NI], uint8_t*) {
     float* sum = a.sum + at.split * a.stride;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      const int m = at.m0 + at.wm + 32 * i + (at.lane & 31);
+      const int m = at.m0 + at.wm + 16 * i + (at.lane & 15);
 #pragma unroll
-      for (int j = 0; j < NI; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int n = at.n0 + at.wn + 32 * j + 8 * q + 4 * (at.lane >> 5);
-          if (m >= p.M || n >= a.ld) continue;
-          float4* to = (float4*)(sum + (int64_t)m * a.ld + n);
-          float4 v = make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
-          if (a.add) {
-            const float4 was = *to;
-            v = make_float4(v.x + was.x, v.y + was.y, v.z + was.z, v.w + was.w);
-          }
-          *to = v;
-        }
+      for (int j = 0; j < NI; ++j) {
+        const int n = at.n0 + at.wn + 16 * j + 4 * (at.lane >> 4);
+        if (m >= p.M || n >= a.ld) continue;
+        v4f* to = (v4f*)(sum + (int64_t)m * a.ld + n);
+        *to = a.add ? *to + acc[i][j] : acc[i][j];
+      }
     }
   }
 };
@@ -275,7 +268,7 @@ struct EpiWeight {
     int rows, H;
   };
   template <int BM, int BN, int WM, int WN, int MI, int NI>
-  static __device__ void run(const GemmArgs&, const Args& a, const TileAt& at, v16f (&acc)[MI][NI], uint8_t* lds) {
+  static __device__ void run(const GemmArgs&, const Args& a, const TileAt& at, v4f (&acc)[MI][NI], uint8_t* lds) {
     const float s = *a.scale;
     stage_part<__bf16, BN>(at, acc, lds, [&](int, int, int, float (&v)[4]) {
 #pragma unroll
