@@ -6,16 +6,23 @@
 //     h_j = silu(x Wg[e_j]^T) * (x Wu[e_j]^T);  out = sum_j weight_j h_j Wd[e_j]^T
 //
 // Every weight of an expert that some token chose is read once, everything else
-// is small: bound by reading HBM.  Three kernels:
+// is small: bound by reading HBM.  The kernels:
 //
-//   router  logits r [T, E] (skipped when the caller brings its own routing,
-//           and done by the next kernel where it is small)
-//   gate/up every workgroup first makes the routing for itself from the logits
-//           (a few us against a launch; workgroup 0 also writes it out), then
-//           takes items (expert, rows of Wg and Wu): h of those rows for the
-//           expert's tokens, times the token's weight, to the workspace (bf16)
-//   down    a workgroup owns 16 output columns of all tokens; its waves walk the
-//           chosen experts' rows of Wd and the sums are joined in a fixed order
+//   router  logits r [T, E], in parts of H that the reader adds (skipped when the
+//           caller brings its own routing)
+//   route   for more than 16 tokens, the choice of each (for fewer every
+//           workgroup of the next kernel makes it for itself: cheaper than a
+//           launch)
+//   gate/up items (expert, rows of Wg and Wu): h of those rows for the expert's
+//           tokens, times the token's weight, to the workspace (bf16)
+//   down    few experts: a workgroup owns 16 output columns of all tokens, its
+//           waves split the chosen experts' rows of Wd and join in a fixed order;
+//           many: items (expert, 64 columns) leave FP32 partial outputs per
+//           (token, expert), which a last kernel adds in the order of the choices
+//
+// Where there are many items a wave takes whole ones and never meets another: no
+// barrier and no reduction stands between its loads, which it keeps 16 KiB
+// ahead.  Where there are few the waves of a workgroup split an item's H.
 //
 // The products run on the bf16 MFMA 16 x 16 x 32 with weight rows as the first
 // operand and up to 16 of the expert's tokens as the second: with few tokens the
@@ -60,13 +67,16 @@ struct MoeArgs {
   int32_t* ids;
   float* weights;
   uint16_t* out;
-  float* logits;       // [T][E]
+  float* logits;       // [parts][T][E]
+  int parts;
   // the routing by expert, written by workgroup 0 of the gate/up kernel
   int32_t* count;      // chosen experts
   int32_t* expert;     // [count], ascending
   int32_t* first;      // [count] the expert's first row of h
   uint64_t* tokens;    // [count] its tokens
+  int32_t* row;        // [T][k] the choice's row of h, -1: none, or an expert's second mention
   uint16_t* h;         // [pairs][I]
+  float* part;         // [pairs][H]
 };
 
 __device__ __forceinline__ v4f mfma(const v4i& a, const v4i& b, const v4f& c) {
@@ -102,6 +112,43 @@ __device__ __forceinline__ v4i operand(const Codes& c, int q) {
   return (q & 1) ? decode8(w.z, w.w, s) : decode8(w.x, w.y, s);
 }
 
+// acc[g] += 16 weight rows (row[g] of this lane, scales srow[g]) times up to 16
+// token rows (xt of this lane) over the 128-wide steps s0, s0 + stride, ... below
+// s1 of `blocks` 32-blocks, the loads of D steps ahead in flight.
+template <int G, int D>
+__device__ __forceinline__ void stream(const uint8_t* const (&row)[G], const uint8_t* const (&srow)[G],
+                                       const uint16_t* xt, int blocks, int s0, int stride, int s1, v4f (&acc)[G]) {
+  const int b = (threadIdx.x & 63) >> 4;
+  Codes c[D][G];
+  v4i xv[D][4];
+  auto load = [&](int d, int s) {
+    const int at = 4 * s + b < blocks ? 4 * s + b : 0;
+#pragma unroll
+    for (int g = 0; g < G; ++g) c[d][g] = load_codes(row[g], srow[g], at);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) xv[d][q] = *(const v4i*)(xt + 32 * at + 8 * q);
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+    if (s0 + d * stride < s1) load(d, s0 + d * stride);
+  for (int s = s0; s < s1; s += D * stride) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int now = s + d * stride;
+      if (now >= s1) break;
+      if (4 * now + b >= blocks) {  // past the row's end: the codes of block 0, made zeros
+#pragma unroll
+        for (int g = 0; g < G; ++g) c[d][g] = Codes{};
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int g = 0; g < G; ++g) acc[g] = mfma(operand(c[d][g], q), xv[d][q], acc[g]);
+      if (now + D * stride < s1) load(d, now + D * stride);
+    }
+  }
+}
+
 // ---- reductions over a wave by DPP ------------------------------------------
 
 template <int CTRL, int ROWS>
@@ -132,10 +179,11 @@ __device__ __forceinline__ int wave_min(int v) {
 
 // ---- router -----------------------------------------------------------------
 
-// logits of 16 experts and 16 tokens by one workgroup of 8 waves, K split over
-// the waves; thread i < 256 gets the sum for expert e0 + (i / 64) * 4 ... as the
-// MFMA lays it out: token t0 + (i & 15), expert e0 + 4 ((i & 63) / 16) + i / 64
-__device__ __forceinline__ float router_tile(const MoeArgs& a, int e0, int t0, float (&red)[kWaves][256]) {
+// Logits of 16 experts and 16 tokens over one part of H: workgroup (experts,
+// tokens, part), its waves splitting the part.
+__global__ __launch_bounds__(kWaves * 64) void moe_router_kernel(MoeArgs a) {
+  __shared__ float red[kWaves][256];
+  const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r = lane & 15, b = lane >> 4;
   const int e = e0 + r < a.E ? e0 + r : a.E - 1, t = t0 + r < a.T ? t0 + r : a.T - 1;
@@ -144,7 +192,7 @@ __device__ __forceinline__ float router_tile(const MoeArgs& a, int e0, int t0, f
   const int blocks = a.H >> 5;
   v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 2
-  for (int s = wave; 4 * s < blocks; s += kWaves) {
+  for (int s = blockIdx.z * kWaves + wave; 4 * s < blocks; s += gridDim.z * kWaves) {
     const bool in = 4 * s + b < blocks;
     const int at = 32 * (in ? 4 * s + b : 0);
 #pragma unroll
@@ -157,37 +205,44 @@ __device__ __forceinline__ float router_tile(const MoeArgs& a, int e0, int t0, f
 #pragma unroll
   for (int i = 0; i < 4; ++i) red[wave][i * 64 + lane] = acc[i];
   __syncthreads();
-  float v = 0.0f;
-  if (tid < 256) {
+  // thread i < 256: token i % 16, expert 4 ((i % 64) / 16) + i / 64
+  const int et = e0 + 4 * (lane >> 4) + wave, tt = t0 + (tid & 15);
+  if (tid < 256 && et < a.E && tt < a.T) {
+    float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) v += red[w][tid];
+    a.logits[((int64_t)blockIdx.z * a.T + tt) * a.E + et] = v;
   }
-  __syncthreads();
-  return v;
-}
-
-__global__ __launch_bounds__(kWaves * 64) void moe_router_kernel(MoeArgs a) {
-  __shared__ float red[kWaves][256];
-  const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16, tid = threadIdx.x;
-  const float v = router_tile(a, e0, t0, red);
-  const int e = e0 + 4 * ((tid & 63) >> 4) + (tid >> 6), t = t0 + (tid & 15);
-  if (tid < 256 && e < a.E && t < a.T) a.logits[t * a.E + e] = v;
 }
 
 // The routing of one token by one wave: lane l holds experts l, l + 64, ...
-// Writes the token's choices and weights to LDS.
-__device__ __forceinline__ void route_token(const MoeArgs& a, const float* logits, int32_t* ids, float* weights) {
+// Writes the token's choices and weights.
+__device__ __forceinline__ void route_token(const MoeArgs& a, int t, int32_t* ids, float* weights) {
   const int lane = threadIdx.x & 63;
+  if (a.active && !a.active[t]) {
+    if (lane < a.k) {
+      ids[lane] = -1;
+      weights[lane] = 0.0f;
+    }
+    return;
+  }
   float v[4];
   uint32_t gone = 0;  // experts that are taken, or beyond E
   float top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int e = lane + 64 * i;
-    v[i] = e < a.E ? logits[e] : -INFINITY;
+    v[i] = e < a.E ? 0.0f : -INFINITY;
     gone |= (uint32_t)(e >= a.E) << i;
-    top = fmaxf(top, v[i]);
   }
+  for (int z = 0; z < a.parts; ++z) {
+    const float* from = a.logits + ((int64_t)z * a.T + t) * a.E;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (lane + 64 * i < a.E) v[i] += from[lane + 64 * i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = fmaxf(top, v[i]);
   top = wave_max(top);
   float sum = 0.0f;
 #pragma unroll
@@ -225,68 +280,52 @@ __device__ __forceinline__ void route_token(const MoeArgs& a, const float* logit
   }
 }
 
+__global__ __launch_bounds__(256) void moe_route_kernel(MoeArgs a) {
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t < a.T) route_token(a, t, a.ids + t * a.k, a.weights + t * a.k);
+}
+
 // ---- gate/up ----------------------------------------------------------------
 
-struct GateSmem {
-  float red[kWaves][256];  // shared by the router, one token group's partial sums follow
+struct Routing {
   int32_t ids[kMaxTokens * kMaxChoices];
   float weights[kMaxTokens * kMaxChoices];
-  uint32_t mask[MXW_MAX_EXPERTS][2];
-  int32_t expert[MXW_MAX_EXPERTS];
-  int32_t first[MXW_MAX_EXPERTS];
-  int32_t wsum[4], wpairs[4];
-  int32_t token[kMaxTokens];
-  float share[kMaxTokens];
+  uint32_t mask[MXW_MAX_EXPERTS][2];   // by expert: its tokens
+  int32_t start[MXW_MAX_EXPERTS];      // by expert: its first row of h
+  int32_t expert[MXW_MAX_EXPERTS];     // the chosen ones, ascending
+  int32_t chosen[4], pairs[4];
 };
 
-// routing for the whole batch into LDS: every workgroup for itself
-template <bool FUSED>
-__device__ __forceinline__ int make_routing(const MoeArgs& a, GateSmem& sm, float* logits) {
+// The routing by expert into LDS, by every workgroup for itself; workgroup 0
+// writes out what the down kernels and the caller need.  ROUTE: from the logits;
+// else from ids and weights.  Returns the number of chosen experts.
+template <bool ROUTE, int WAVES>
+__device__ __forceinline__ int make_routing(const MoeArgs& a, Routing& rt) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n = a.T * a.k;
-  if (a.router) {
-    const float* from = a.logits;
-    if (FUSED) {
-      for (int t0 = 0; t0 < a.T; t0 += 16)
-        for (int e0 = 0; e0 < a.E; e0 += 16) {
-          const float v = router_tile(a, e0, t0, sm.red);
-          const int e = e0 + 4 * (lane >> 4) + wave, t = t0 + (tid & 15);
-          if (tid < 256 && e < a.E && t < a.T) logits[t * a.E + e] = v;
-        }
-      __syncthreads();
-      from = logits;
-    }
-    for (int t = wave; t < a.T; t += kWaves) {
-      if (a.active && !a.active[t]) {
-        if (lane < a.k) {
-          sm.ids[t * a.k + lane] = -1;
-          sm.weights[t * a.k + lane] = 0.0f;
-        }
-      } else {
-        route_token(a, from + t * a.E, sm.ids + t * a.k, sm.weights + t * a.k);
-      }
-    }
+  if (ROUTE) {
+    for (int t = wave; t < a.T; t += WAVES) route_token(a, t, rt.ids + t * a.k, rt.weights + t * a.k);
   } else {
-    for (int i = tid; i < n; i += kWaves * 64) {
+    for (int i = tid; i < n; i += WAVES * 64) {
       const int id = a.ids[i];
       const bool in = id >= 0 && id < a.E && !(a.active && !a.active[i / a.k]);
-      sm.ids[i] = in ? id : -1;
-      sm.weights[i] = in ? a.weights[i] : 0.0f;
+      rt.ids[i] = in ? id : -1;
+      rt.weights[i] = in ? a.weights[i] : 0.0f;
     }
   }
-  for (int i = tid; i < 2 * MXW_MAX_EXPERTS; i += kWaves * 64) sm.mask[i >> 1][i & 1] = 0;
+  for (int i = tid; i < 2 * MXW_MAX_EXPERTS; i += WAVES * 64) rt.mask[i >> 1][i & 1] = 0;
   __syncthreads();
-  for (int i = tid; i < n; i += kWaves * 64) {
-    const int e = sm.ids[i], t = i / a.k;
-    if (e >= 0) atomicOr(&sm.mask[e][t >> 5], 1u << (t & 31));
+  for (int i = tid; i < n; i += WAVES * 64) {
+    const int e = rt.ids[i], t = i / a.k;
+    if (e >= 0) atomicOr(&rt.mask[e][t >> 5], 1u << (t & 31));
   }
   __syncthreads();
-  // chosen experts in order, and their first rows of h: ranks by ballot, sums
-  // over 4 waves of 64 experts
+  // chosen experts in order and their first rows of h, a wave per 64 experts
+  static_assert(WAVES >= 4, "64 experts a wave");
   int before = 0, rank = 0;
   bool chosen = false;
   if (wave < 4) {
-    const int pairs = tid < a.E ? __popc(sm.mask[tid][0]) + __popc(sm.mask[tid][1]) : 0;
+    const int pairs = tid < a.E ? __popc(rt.mask[tid][0]) + __popc(rt.mask[tid][1]) : 0;
     chosen = pairs > 0;
     const uint64_t votes = __ballot(chosen);
     int run = pairs;  // inclusive sum over the wave
@@ -297,121 +336,313 @@ __device__ __forceinline__ int make_routing(const MoeArgs& a, GateSmem& sm, floa
     before = run - pairs;
     rank = __popcll(votes & ((1ull << lane) - 1));
     if (lane == 63) {
-      sm.wsum[wave] = __popcll(votes);
-      sm.wpairs[wave] = run;
+      rt.chosen[wave] = __popcll(votes);
+      rt.pairs[wave] = run;
     }
   }
   __syncthreads();
   if (chosen) {
     for (int w = 0; w < wave; ++w) {
-      rank += sm.wsum[w];
-      before += sm.wpairs[w];
+      rank += rt.chosen[w];
+      before += rt.pairs[w];
     }
-    sm.expert[rank] = tid;
-    sm.first[rank] = before;
+    rt.expert[rank] = tid;
+    rt.start[tid] = before;
   }
   __syncthreads();
-  const int count = sm.wsum[0] + sm.wsum[1] + sm.wsum[2] + sm.wsum[3];
+  const int count = rt.chosen[0] + rt.chosen[1] + rt.chosen[2] + rt.chosen[3];
   if (blockIdx.x == 0) {
-    if (a.router)
-      for (int i = tid; i < n; i += kWaves * 64) {
-        a.ids[i] = sm.ids[i];
-        a.weights[i] = sm.weights[i];
+    for (int i = tid; i < n; i += WAVES * 64) {
+      const int e = rt.ids[i], t = i / a.k;
+      if (ROUTE) {
+        a.ids[i] = e;
+        a.weights[i] = rt.weights[i];
       }
+      int row = -1;
+      if (e >= 0) {
+        const uint64_t mask = rt.mask[e][0] | (uint64_t)rt.mask[e][1] << 32;
+        row = rt.start[e] + __popcll(mask & ((1ull << t) - 1));
+        for (int j = t * a.k; j < i; ++j)
+          if (rt.ids[j] == e) row = -1;
+      }
+      a.row[i] = row;
+    }
     if (tid == 0) *a.count = count;
-    for (int i = tid; i < count; i += kWaves * 64) {
-      const int e = sm.expert[i];
+    for (int i = tid; i < count; i += WAVES * 64) {
+      const int e = rt.expert[i];
       a.expert[i] = e;
-      a.first[i] = sm.first[i];
-      a.tokens[i] = sm.mask[e][0] | (uint64_t)sm.mask[e][1] << 32;
+      a.first[i] = rt.start[e];
+      a.tokens[i] = rt.mask[e][0] | (uint64_t)rt.mask[e][1] << 32;
     }
   }
   return count;
 }
 
-// Items (expert, RG * 16 rows of Wg and the same of Wu), workgroups striding
-// over them.
-template <int RG, bool FUSED>
-__global__ __launch_bounds__(kWaves * 64, 2 * kWaves / 4) void moe_gate_kernel(MoeArgs a) {
-  __shared__ GateSmem sm;
-  __shared__ float part[kWaves][2 * RG][256];
+// the n-th token of a mask (n below its count)
+__device__ __forceinline__ int nth_token(uint64_t mask, int n) {
+  int at = 0;
+#pragma unroll
+  for (int w = 32; w > 0; w >>= 1) {  // skip halves that hold no more than n tokens
+    const int low = __popcll(mask & ((1ull << w) - 1));
+    const bool skip = n >= low;
+    n -= skip ? low : 0;
+    mask = skip ? mask >> w : mask;
+    at += skip ? w : 0;
+  }
+  return at;
+}
+__device__ __forceinline__ float share_of(const MoeArgs& a, const Routing& rt, int t, int e) {
+  float share = 0.0f;
+  for (int j = 0; j < a.k; ++j) share += rt.ids[t * a.k + j] == e ? rt.weights[t * a.k + j] : 0.0f;
+  return share;
+}
+// silu(g) u w, rounded once to bf16, the down product's operand type
+__device__ __forceinline__ uint16_t hidden(float g, float u, float w) {
+  return (uint16_t)pack2(g / (1.0f + __builtin_amdgcn_exp2f(-g * kLog2e)) * u * w, 0.0f, __bf16());
+}
+
+// the lane's weight rows of Wg (even g) and Wu (odd g): rows i0 + 16 (g / 2) + l % 16
+template <int G>
+__device__ __forceinline__ void gate_rows(const MoeArgs& a, int e, int i0, const uint8_t* (&row)[G],
+                                          const uint8_t* (&srow)[G]) {
+  const int r = threadIdx.x & 15, blocks = a.H >> 5;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    int i = i0 + 16 * (g >> 1) + r;
+    if (i >= a.I) i = a.I - 1;  // past the last rows: computed, not stored
+    const int64_t at = (int64_t)e * 2 * a.I + (g & 1) * a.I + i;
+    row[g] = a.wgu + at * a.H;
+    srow[g] = a.sgu + at * blocks;
+  }
+}
+
+// few items: (expert, 16 rows of Wg and of Wu), H split over the 8 waves
+template <bool ROUTE>
+__global__ __launch_bounds__(kWaves * 64, 4) void moe_gate_split_kernel(MoeArgs a) {
+  __shared__ Routing rt;
+  __shared__ float part[kWaves][2][256];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int count = make_routing<FUSED>(a, sm, &part[0][0][0]);
-  const int tiles = (a.I + 16 * RG - 1) / (16 * RG);
-  const int blocks = a.H >> 5;
+  const int count = make_routing<ROUTE, kWaves>(a, rt);
+  const int tiles = (a.I + 15) / 16, blocks = a.H >> 5;
   const int r = lane & 15, b = lane >> 4;
   for (int item = blockIdx.x; item < count * tiles; item += gridDim.x) {
-    const int which = item / tiles, i0 = (item - which * tiles) * 16 * RG;
-    const int e = sm.expert[which], first = sm.first[which];
-    const uint64_t mask = sm.mask[e][0] | (uint64_t)sm.mask[e][1] << 32;
+    const int e = rt.expert[item / tiles], i0 = item % tiles * 16;
+    const uint64_t mask = rt.mask[e][0] | (uint64_t)rt.mask[e][1] << 32;
     const int ntok = __popcll(mask);
-    __syncthreads();  // the last item is done with the lists
-    if (wave == 0 && ((mask >> lane) & 1)) {
-      const int at = __popcll(mask & ((1ull << lane) - 1));
-      float share = 0.0f;
-      for (int j = 0; j < a.k; ++j)
-        if (sm.ids[lane * a.k + j] == e) share += sm.weights[lane * a.k + j];
-      sm.token[at] = lane;
-      sm.share[at] = share;
-    }
-    __syncthreads();
-    const uint8_t* row[2 * RG];
-    const uint8_t* srow[2 * RG];
-#pragma unroll
-    for (int g = 0; g < RG; ++g) {
-      int i = i0 + 16 * g + r;
-      if (i >= a.I) i = a.I - 1;  // past the last rows: computed, not stored
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int64_t at = (int64_t)e * 2 * a.I + u * a.I + i;
-        row[2 * g + u] = a.wgu + at * a.H;
-        srow[2 * g + u] = a.sgu + at * blocks;
-      }
-    }
+    const uint8_t *row[2], *srow[2];
+    gate_rows<2>(a, e, i0, row, srow);
     for (int g0 = 0; g0 < ntok; g0 += 16) {
-      const uint16_t* xt = a.x + sm.token[g0 + r < ntok ? g0 + r : g0] * a.ldx;
-      v4f acc[2 * RG];
+      const uint16_t* xt = a.x + nth_token(mask, g0 + r < ntok ? g0 + r : g0) * a.ldx;
+      v4f acc[2] = {};
+      stream<2, 2>(row, srow, xt, blocks, wave, kWaves, (blocks + 3) >> 2, acc);
 #pragma unroll
-      for (int g = 0; g < 2 * RG; ++g) acc[g] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 2
-      for (int s = wave; 4 * s < blocks; s += kWaves) {
-        const bool in = 4 * s + b < blocks;
-        const int at = in ? 4 * s + b : 0;
-        Codes c[2 * RG];
-        v4i xv[4];
-#pragma unroll
-        for (int g = 0; g < 2 * RG; ++g) c[g] = load_codes(row[g], srow[g], at);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) xv[q] = *(const v4i*)(xt + 32 * at + 8 * q);
-        if (!in) {
-#pragma unroll
-          for (int g = 0; g < 2 * RG; ++g) c[g] = Codes{};
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int g = 0; g < 2 * RG; ++g) acc[g] = mfma(operand(c[g], q), xv[q], acc[g]);
-      }
-#pragma unroll
-      for (int g = 0; g < 2 * RG; ++g)
+      for (int g = 0; g < 2; ++g)
 #pragma unroll
         for (int i = 0; i < 4; ++i) part[wave][g][(4 * b + i) * 16 + r] = acc[g][i];  // [row][token]
       __syncthreads();
-      for (int i = tid; i < RG * 256; i += kWaves * 64) {
-        const int tok = i / (16 * RG), rr = i % (16 * RG), g = rr >> 4, at = (rr & 15) * 16 + tok;
+      if (tid < 256) {
+        const int tok = g0 + (tid >> 4), rr = tid & 15, at = rr * 16 + (tid >> 4);
         float gate = 0.0f, up = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-          gate += part[w][2 * g][at];
-          up += part[w][2 * g + 1][at];
+          gate += part[w][0][at];
+          up += part[w][1][at];
         }
-        // silu(g) u w, rounded once to bf16, the down product's operand type
-        const float h = gate / (1.0f + __builtin_amdgcn_exp2f(-gate * kLog2e)) * up * sm.share[g0 + tok < ntok ? g0 + tok : 0];
-        if (g0 + tok < ntok && i0 + rr < a.I)
-          a.h[(int64_t)(first + g0 + tok) * a.I + i0 + rr] = (uint16_t)pack2(h, 0.0f, __bf16());
+        if (tok < ntok && i0 + rr < a.I)
+          a.h[(int64_t)(rt.start[e] + tok) * a.I + i0 + rr] =
+              hidden(gate, up, share_of(a, rt, nth_token(mask, tok), e));
       }
       __syncthreads();
     }
+  }
+}
+
+// ---- streaming through LDS ---------------------------------------------------
+
+// Loads of 16 and 4 bytes a lane straight to LDS (lane l's bytes at lds + 16 l, or
+// 4 l): from a 64-bit address, from a 64-bit base and a 32-bit offset.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void global_lds16(const void* from, uint32_t lds) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, off"
+      :
+      : "s"(lds), "v"(from)
+      : "memory", "m0");
+}
+__device__ __forceinline__ void global_lds4(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dword %1, %2"
+      :
+      : "s"(lds), "v"(off), "s"(base)
+      : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+constexpr int kRing = 66 * 1024;  // LDS of a workgroup's ring: two workgroups a CU
+
+// Weight rows of a workgroup of 4 waves: group g of wave w is 16 rows, the first 8
+// from `first` on, the others from `second` on, `apart` rows after group g - 1's.
+struct Rows {
+  const uint8_t *first, *second;    // codes of row 0 of either
+  int valid_first, valid_second;    // rows there (the rest reads as zeros)
+  const uint8_t *sfirst, *ssecond;  // their scales
+  int apart;
+  int C;                            // row length, a multiple of 128
+};
+
+// acc[g][n] = the wave's group g of weight rows times token group n (16 tokens,
+// source rows token[16 n ...] at src + row * ld elements).  One step is 128 columns:
+// each wave brings its own rows' codes and scales and a quarter of the tokens'
+// rows to the step's slot of the ring, D - 1 steps ahead; every load takes whole
+// cache lines (read straight into the MFMA's operand layout, 16 lanes would touch
+// 16 lines, which made the vector memory path the bound: 3.0 TB/s at 8 of 32
+// experts of the 671B shape).  One barrier a step.
+template <int G, int N>
+__device__ __forceinline__ void stream_rows(const Rows& w, const uint16_t* src, int64_t ld, const int32_t* token,
+                                            int ntok, uint8_t* ring, v4f (&acc)[G][N]) {
+  constexpr int kCodes = 4 * G * 2048, kTokens = N * 4096, kScales = 4 * 256;
+  constexpr int kSlot = kCodes + kTokens + kScales;
+  constexpr int D = kRing / kSlot < 6 ? kRing / kSlot : 6;
+  constexpr int kLoads = 2 * G + N + 1;  // a wave's loads a step
+  static_assert(D >= 2, "two slots");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, b = lane >> 4;
+  const int steps = w.C >> 7, blocks = w.C >> 5;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)ring;
+
+  // codes: 8 rows of 128 bytes a load, chunk c of row i at c ^ (i / 2) % 8
+  uint32_t vo[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = 8 * h + (lane >> 3);
+    vo[h] = (uint32_t)((wave * G * w.apart + (lane >> 3)) * w.C + (((lane & 7) ^ ((i >> 1) & 7)) << 4));
+  }
+  // scales: lane l brings the step's 4 bytes of row l % 16 of group l / 16
+  uint32_t so;
+  {
+    const int g = (lane >> 4) % G, h = (lane >> 3) & 1;
+    int row = (wave * G + g) * w.apart + (lane & 7);
+    const int last = (h ? w.valid_second : w.valid_first) - 1;
+    if (row > last) row = last > 0 ? last : 0;
+    so = (uint32_t)((h ? (uint32_t)(w.ssecond - w.sfirst) : 0u) + (uint32_t)row * (uint32_t)blocks);
+  }
+  // tokens: 4 rows of 256 bytes a load, chunk c of row t at c ^ t % 16
+  const uint16_t* xa[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int t = 4 * wave + b;
+    xa[n] = src + token[16 * n + t < ntok ? 16 * n + t : 0] * ld + ((r ^ t) << 3);
+  }
+  auto load = [&](int s, uint32_t slot) {
+    const int64_t done = (int64_t)s * 128;
+    const bool in = s < steps;
+    const int64_t left1 = in ? (int64_t)w.valid_first * w.C - done : 0;
+    const int64_t left2 = in ? (int64_t)w.valid_second * w.C - done : 0;
+    const auto first = mxw::buffer_of(w.first + done, mxw::range_of(left1));
+    const auto second = mxw::buffer_of(w.second + done, mxw::range_of(left2));
+    const uint32_t to = lds0 + slot * kSlot + wave * G * 2048;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      mxw::load_lds16(first, to + g * 2048, vo[0] + g * w.apart * w.C);
+      mxw::load_lds16(second, to + g * 2048 + 1024, vo[1] + g * w.apart * w.C);
+    }
+    const int at = in ? s : steps - 1;  // past the end: the last step's again, not used
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      global_lds16(xa[n] + 128 * at, lds0 + slot * kSlot + kCodes + n * 4096 + wave * 1024);
+    global_lds4(w.sfirst + 4 * at, so, lds0 + slot * kSlot + kCodes + kTokens + wave * 256);
+  };
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int n = 0; n < N; ++n) acc[g][n] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+  mxw::stage_barrier<0>();  // the ring's last use is over
+  for (int s = 0; s < D - 1; ++s) load(s, s);
+  int slot = 0, next = D - 1;
+  for (int s = 0; s < steps; ++s) {
+    mxw::stage_barrier<(D - 2) * kLoads>();
+    load(s + D - 1, next);
+    const uint8_t* at = ring + slot * kSlot;
+    const uint8_t* codes = at + wave * G * 2048 + r * 128;
+    const int sw = (r >> 1) & 7;
+    Codes c[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      c[g].lo = *(const v4i*)(codes + g * 2048 + (((2 * b) ^ sw) << 4));
+      c[g].hi = *(const v4i*)(codes + g * 2048 + (((2 * b + 1) ^ sw) << 4));
+      c[g].s = *(at + kCodes + kTokens + wave * 256 + (16 * g + r) * 4 + b);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v4i xv[N];
+#pragma unroll
+      for (int n = 0; n < N; ++n) xv[n] = *(const v4i*)(at + kCodes + n * 4096 + r * 256 + (((4 * b + q) ^ r) << 4));
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const v4i a = operand(c[g], q);
+#pragma unroll
+        for (int n = 0; n < N; ++n) acc[g][n] = mfma(a, xv[n], acc[g][n]);
+      }
+    }
+    slot = slot + 1 == D ? 0 : slot + 1;
+    next = next + 1 == D ? 0 : next + 1;
+  }
+}
+
+// Items (expert, 32 G rows of Wg and of Wu) by workgroups of 4 waves: a wave's
+// group is 8 rows of Wg and the same 8 of Wu.
+template <int G, int N>
+__device__ __forceinline__ void gate_item(const MoeArgs& a, const Routing& rt, int e, int i0, const int32_t* token,
+                                          int ntok, uint8_t* ring) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, b = lane >> 4, blocks = a.H >> 5;
+  const int64_t at = (int64_t)e * 2 * a.I + i0;
+  const Rows w = {a.wgu + at * a.H, a.wgu + (at + a.I) * a.H,   a.I - i0, a.I - i0,
+                  a.sgu + at * blocks, a.sgu + (at + a.I) * blocks, 8, a.H};
+  v4f acc[G][N];
+  stream_rows<G, N>(w, a.x, a.ldx, token, ntok, ring, acc);
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int tok = 16 * n + r;
+    const float share = tok < ntok ? share_of(a, rt, token[tok], e) : 0.0f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      // lanes b < 2 hold rows 4 b .. of Wg, lanes b + 2 the same of Wu
+      v4f up;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) up[i] = __shfl_xor(acc[g][n][i], 32);
+      const int i = i0 + 8 * (wave * G + g) + 4 * b;
+      if (b < 2 && tok < ntok && i < a.I) {
+        const v4f& ga = acc[g][n];
+        *(uint2*)(a.h + (int64_t)(rt.start[e] + tok) * a.I + i) =
+            make_uint2(hidden(ga.x, up.x, share) | (uint32_t)hidden(ga.y, up.y, share) << 16,
+                       hidden(ga.z, up.z, share) | (uint32_t)hidden(ga.w, up.w, share) << 16);
+      }
+    }
+  }
+}
+
+template <bool ROUTE, int G, bool MANY>
+__global__ __launch_bounds__(256, 2) void moe_gate_kernel(MoeArgs a) {
+  __shared__ Routing rt;
+  __shared__ int32_t token[kMaxTokens];
+  __shared__ __align__(1024) uint8_t ring[kRing];
+  const int count = make_routing<ROUTE, 4>(a, rt);
+  const int tiles = (a.I + 32 * G - 1) / (32 * G);
+  for (int item = blockIdx.x; item < count * tiles; item += gridDim.x) {
+    const int e = rt.expert[item / tiles], i0 = item % tiles * 32 * G;
+    const uint64_t mask = rt.mask[e][0] | (uint64_t)rt.mask[e][1] << 32;
+    const int ntok = __popcll(mask);
+    __syncthreads();  // the last item is done with the list
+    if ((int)threadIdx.x < ntok) token[threadIdx.x] = nth_token(mask, threadIdx.x);
+    __syncthreads();
+    if (!MANY || ntok <= 16) gate_item<G, 1>(a, rt, e, i0, token, ntok, ring);
+    else if (ntok <= 32) gate_item<G, MANY ? 2 : 1>(a, rt, e, i0, token, ntok, ring);
+    else gate_item<G, MANY ? 4 : 1>(a, rt, e, i0, token, ntok, ring);
   }
 }
 
@@ -419,14 +650,14 @@ __global__ __launch_bounds__(kWaves * 64, 2 * kWaves / 4) void moe_gate_kernel(M
 
 // 16 output columns of all tokens: the waves split the (expert, 128 columns of
 // I) units in order, each keeps its own sums [token][16] in LDS.
-template <int WAVES>
-__global__ __launch_bounds__(WAVES * 64, 4) void moe_down_kernel(MoeArgs a) {
-  extern __shared__ __align__(16) float sums[];  // [WAVES][T][16]
+constexpr int kDownWaves = 16;
+__global__ __launch_bounds__(kDownWaves * 64, 4) void moe_down_kernel(MoeArgs a) {
+  extern __shared__ __align__(16) float sums[];  // [kDownWaves][T][16]
   __shared__ int32_t expert[MXW_MAX_EXPERTS], first[MXW_MAX_EXPERTS];
   __shared__ uint64_t tokens[MXW_MAX_EXPERTS];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int count = *a.count;
-  for (int i = tid; i < count; i += WAVES * 64) {
+  for (int i = tid; i < count; i += kDownWaves * 64) {
     expert[i] = a.expert[i];
     first[i] = a.first[i];
     tokens[i] = a.tokens[i];
@@ -436,69 +667,122 @@ __global__ __launch_bounds__(WAVES * 64, 4) void moe_down_kernel(MoeArgs a) {
   __syncthreads();
   const int h0 = blockIdx.x * 16, r = lane & 15, b = lane >> 4;
   const int blocks = a.I >> 5, steps = (blocks + 3) >> 2, units = count * steps;
-  int u = (int)((int64_t)units * wave / WAVES);
-  const int end = (int)((int64_t)units * (wave + 1) / WAVES);
+  int u = (int)((int64_t)units * wave / kDownWaves);
+  const int end = (int)((int64_t)units * (wave + 1) / kDownWaves);
   while (u < end) {
     const int which = u / steps, s0 = u - which * steps;
     const int s1 = end - which * steps < steps ? end - which * steps : steps;
-    const int e = expert[which], p0 = first[which];
     const uint64_t mask = tokens[which];
     const int ntok = __popcll(mask);
-    const int64_t at = (int64_t)e * a.H + h0 + r;
-    const uint8_t* row = a.wd + at * a.I;
-    const uint8_t* srow = a.sd + at * blocks;
+    const int64_t at = (int64_t)expert[which] * a.H + h0 + r;
+    const uint8_t* const row[1] = {a.wd + at * a.I};
+    const uint8_t* const srow[1] = {a.sd + at * blocks};
     for (int g0 = 0; g0 < ntok; g0 += 16) {
       const int p = g0 + r < ntok ? g0 + r : g0;
-      const uint16_t* hp = a.h + (int64_t)(p0 + p) * a.I;
-      v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-      for (int s = s0; s < s1; ++s) {
-        const bool in = 4 * s + b < blocks;
-        const int k = in ? 4 * s + b : 0;
-        Codes c = load_codes(row, srow, k);
-        if (!in) c = Codes{};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc = mfma(operand(c, q), *(const v4i*)(hp + 32 * k + 8 * q), acc);
-      }
-      // token of this lane's column: the (g0 + r)-th set bit
-      uint64_t left = mask;
-      for (int i = 0; i < g0 + r && left; ++i) left &= left - 1;
+      v4f acc[1] = {};
+      stream<1, 3>(row, srow, a.h + (int64_t)(first[which] + p) * a.I, blocks, s0, 1, s1, acc);
       if (g0 + r < ntok) {
-        v4f* to = (v4f*)(mine + (__ffsll((unsigned long long)left) - 1) * 16 + 4 * b);
-        *to = *to + acc;
+        v4f* to = (v4f*)(mine + nth_token(mask, p) * 16 + 4 * b);
+        *to = *to + acc[0];
       }
     }
     u = which * steps + s1;
   }
   __syncthreads();
-  for (int i = tid; i < a.T * 16; i += WAVES * 64) {
+  for (int i = tid; i < a.T * 16; i += kDownWaves * 64) {
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) v += sums[w * a.T * 16 + i];
+    for (int w = 0; w < kDownWaves; ++w) v += sums[w * a.T * 16 + i];
     a.out[(int64_t)(i >> 4) * a.H + h0 + (i & 15)] = (uint16_t)pack2(v, 0.0f, __bf16());
   }
+}
+
+// many experts: items (expert, 64 G columns), to FP32 partial outputs per
+// (token, expert)
+template <int G, int N>
+__device__ __forceinline__ void down_item(const MoeArgs& a, int e, int h0, int first, int ntok, const int32_t* order,
+                                          uint8_t* ring) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, b = lane >> 4, blocks = a.I >> 5;
+  const int64_t at = (int64_t)e * a.H + h0;
+  const Rows w = {a.wd + at * a.I, a.wd + (at + 8) * a.I, a.H - h0, a.H - h0 - 8,
+                  a.sd + at * blocks, a.sd + (at + 8) * blocks, 16, a.I};
+  v4f acc[G][N];
+  stream_rows<G, N>(w, a.h + (int64_t)first * a.I, a.I, order, ntok, ring, acc);
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int h = h0 + 16 * (wave * G + g) + 4 * b;
+      if (16 * n + r < ntok && h < a.H) *(v4f*)(a.part + (int64_t)(first + 16 * n + r) * a.H + h) = acc[g][n];
+    }
+}
+
+template <int G, bool MANY>
+__global__ __launch_bounds__(256, 2) void moe_down_part_kernel(MoeArgs a) {
+  __shared__ int32_t order[kMaxTokens];
+  __shared__ __align__(1024) uint8_t ring[kRing];
+  if (threadIdx.x < kMaxTokens) order[threadIdx.x] = threadIdx.x;
+  __syncthreads();
+  const int count = *a.count;
+  const int tiles = (a.H + 64 * G - 1) / (64 * G);
+  for (int item = blockIdx.x; item < count * tiles; item += gridDim.x) {
+    const int which = item / tiles, h0 = (item - which * tiles) * 64 * G;
+    const int e = a.expert[which], first = a.first[which], ntok = __popcll(a.tokens[which]);
+    if (!MANY || ntok <= 16) down_item<G, 1>(a, e, h0, first, ntok, order, ring);
+    else if (ntok <= 32) down_item<G, MANY ? 2 : 1>(a, e, h0, first, ntok, order, ring);
+    else down_item<G, MANY ? 4 : 1>(a, e, h0, first, ntok, order, ring);
+  }
+}
+
+// the partial outputs of each token's choices, added in their order
+__global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs a) {
+  const int t = blockIdx.y, c = 4 * (blockIdx.x * 256 + threadIdx.x);
+  if (c >= a.H) return;
+  v4f v = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int j = 0; j < a.k; ++j) {
+    const int row = a.row[t * a.k + j];
+    if (row >= 0) v += *(const v4f*)(a.part + (int64_t)row * a.H + c);
+  }
+  uint16_t* to = a.out + (int64_t)t * a.H + c;
+  const uint32_t lo = pack2(v.x, v.y, __bf16()), hi = pack2(v.z, v.w, __bf16());
+  to[0] = (uint16_t)lo;
+  to[1] = (uint16_t)(lo >> 16);
+  to[2] = (uint16_t)hi;
+  to[3] = (uint16_t)(hi >> 16);
 }
 
 // ---- host -------------------------------------------------------------------
 
 struct MoePlan {
-  size_t logits, count, expert, first, tokens, h, bytes;
+  int parts;     // of H in the router
+  bool by_item;  // down: partial outputs per item
+  size_t logits, count, expert, first, tokens, row, h, part, bytes;
 };
 
-MoePlan plan_of(int T, int E, int k, int I) {
+// experts that can be chosen
+int most_experts(int T, int E, int k) { return T * k < E ? T * k : E; }
+
+MoePlan plan_of(int T, int E, int k, int H, int I) {
   MoePlan p = {};
+  // a step of 128 a wave if there are few workgroups
+  p.parts = (H + 128 * kWaves - 1) / (128 * kWaves);
+  if (p.parts > 8) p.parts = 8;
+  // a workgroup of the down kernel reads 16 rows of I of every chosen expert
+  p.by_item = (I & 127) == 0 && (int64_t)most_experts(T, E, k) * I * 16 > (512 << 10);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t was = at;
     at = (at + bytes + 255) & ~(size_t)255;
     return was;
   };
-  p.logits = take((size_t)T * E * 4);
+  p.logits = take((size_t)p.parts * T * E * 4);
   p.count = take(4);
   p.expert = take(MXW_MAX_EXPERTS * 4);
   p.first = take(MXW_MAX_EXPERTS * 4);
   p.tokens = take(MXW_MAX_EXPERTS * 8);
+  p.row = take((size_t)T * k * 4);
   p.h = take((size_t)T * k * I * 2);
+  if (p.by_item) p.part = take((size_t)T * k * H * 4);
   p.bytes = at;
   return p;
 }
@@ -510,19 +794,22 @@ int check_moe(int T, int E, int k, int H, int I) {
              : MXW_OK;
 }
 
-template <bool FUSED>
+template <bool ROUTE>
 void launch_gate(const MoeArgs& a, int cus, hipStream_t st) {
-  const int most = a.T * a.k < a.E ? a.T * a.k : a.E;  // experts that can be chosen
-  // 16 rows of each half an item while that gives few items, else 32: half the
-  // token loads per weight
-  const int64_t items = (int64_t)most * ((a.I + 31) / 32);
-  const int64_t slots = 2LL * cus;
-  if (items < slots) {
-    const int64_t n = (int64_t)most * ((a.I + 15) / 16);
-    hipLaunchKernelGGL((moe_gate_kernel<1, FUSED>), dim3((unsigned)(n < slots ? n : slots)), dim3(kWaves * 64), 0, st, a);
-  } else {
-    hipLaunchKernelGGL((moe_gate_kernel<2, FUSED>), dim3((unsigned)slots), dim3(kWaves * 64), 0, st, a);
+  const int64_t most = most_experts(a.T, a.E, a.k);
+  if (a.H & 127) {
+    const int64_t n = most * ((a.I + 15) / 16);
+    hipLaunchKernelGGL((moe_gate_split_kernel<ROUTE>), dim3((unsigned)(n < 4 * cus ? n : 4 * cus)), dim3(kWaves * 64), 0,
+                       st, a);
+    return;
   }
+  const int64_t slots = 2 * cus, one = most * ((a.I + 31) / 32), two = most * ((a.I + 63) / 64);
+  if (two < slots)
+    hipLaunchKernelGGL((moe_gate_kernel<ROUTE, 1, true>), dim3((unsigned)(one < slots ? one : slots)), dim3(256), 0, st, a);
+  else if (a.T <= 16)
+    hipLaunchKernelGGL((moe_gate_kernel<ROUTE, 2, false>), dim3((unsigned)slots), dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((moe_gate_kernel<ROUTE, 2, true>), dim3((unsigned)slots), dim3(256), 0, st, a);
 }
 
 }  // namespace
@@ -531,7 +818,7 @@ extern "C" {
 
 int64_t mxw_moe_workspace_size(int T, int E, int k, int H, int I) {
   if (check_moe(T, E, k, H, I)) return MXW_ERR_DIM;
-  return (int64_t)plan_of(T, E, k, I).bytes;
+  return (int64_t)plan_of(T, E, k, H, I).bytes;
 }
 
 int mxw_moe_layer(const uint16_t* x, int64_t ldx, const uint16_t* router, const uint8_t* wgu, const uint8_t* sgu,
@@ -543,7 +830,7 @@ int mxw_moe_layer(const uint16_t* x, int64_t ldx, const uint16_t* router, const 
   if ((((uintptr_t)x | (uintptr_t)router | (uintptr_t)wgu | (uintptr_t)wd) & 15) || ((uintptr_t)out & 1) ||
       (((uintptr_t)ids | (uintptr_t)weights) & 3))
     return MXW_ERR_ALIGN;
-  const MoePlan p = plan_of(T, E, k, I);
+  const MoePlan p = plan_of(T, E, k, H, I);
   if (!workspace || workspace_bytes < p.bytes || ((uintptr_t)workspace & 255)) return MXW_ERR_WORKSPACE;
   int cus = 0;
   const int rc = check_device(&cus);
@@ -570,16 +857,36 @@ int mxw_moe_layer(const uint16_t* x, int64_t ldx, const uint16_t* router, const 
   a.weights = weights;
   a.out = out;
   a.logits = (float*)(ws + p.logits);
+  a.parts = p.parts;
   a.count = (int32_t*)(ws + p.count);
   a.expert = (int32_t*)(ws + p.expert);
   a.first = (int32_t*)(ws + p.first);
   a.tokens = (uint64_t*)(ws + p.tokens);
+  a.row = (int32_t*)(ws + p.row);
   a.h = (uint16_t*)(ws + p.h);
+  a.part = (float*)(ws + p.part);
   if (router)
-    hipLaunchKernelGGL(moe_router_kernel, dim3((unsigned)((E + 15) / 16), (unsigned)((T + 15) / 16)), dim3(kWaves * 64), 0,
-                       st, a);
-  launch_gate<false>(a, cus, st);
-  hipLaunchKernelGGL((moe_down_kernel<16>), dim3((unsigned)(H / 16)), dim3(16 * 64), 16 * T * 16 * 4, st, a);
+    hipLaunchKernelGGL(moe_router_kernel, dim3((unsigned)((E + 15) / 16), (unsigned)((T + 15) / 16), (unsigned)p.parts),
+                       dim3(kWaves * 64), 0, st, a);
+  if (router && T <= 16) {
+    launch_gate<true>(a, cus, st);
+  } else {
+    if (router) hipLaunchKernelGGL(moe_route_kernel, dim3((unsigned)((T + 3) / 4)), dim3(256), 0, st, a);
+    launch_gate<false>(a, cus, st);
+  }
+  if (p.by_item) {
+    const int64_t most = most_experts(T, E, k), slots = 2 * cus, one = most * ((H + 63) / 64),
+                  two = most * ((H + 127) / 128);
+    if (two < slots)
+      hipLaunchKernelGGL((moe_down_part_kernel<1, true>), dim3((unsigned)(one < slots ? one : slots)), dim3(256), 0, st, a);
+    else if (T <= 16)
+      hipLaunchKernelGGL((moe_down_part_kernel<2, false>), dim3((unsigned)slots), dim3(256), 0, st, a);
+    else
+      hipLaunchKernelGGL((moe_down_part_kernel<2, true>), dim3((unsigned)slots), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned)((H + 1023) / 1024), (unsigned)T), dim3(256), 0, st, a);
+  } else {
+    hipLaunchKernelGGL(moe_down_kernel, dim3((unsigned)(H / 16)), dim3(kDownWaves * 64), kDownWaves * T * 16 * 4, st, a);
+  }
   if (hipGetLastError() != hipSuccess) return MXW_ERR_LAUNCH;
   return MXW_OK;
 }
