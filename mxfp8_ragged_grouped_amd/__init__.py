@@ -676,56 +676,55 @@ def moe_layer(x, router, wgu, sgu, wd, sd, top_k, normalize=True, scale=1.0, act
     `stream` (default: the current stream) and does not synchronise;
     `workspace`: a uint8 device tensor of moe_workspace_size() bytes (default:
     from torch's caching allocator on that stream)."""
-    wgu, sgu, wd, sd = (t.view(torch.uint8) if t.dtype == getattr(torch, "float8_e4m3fn", None) else t
-                        for t in (wgu, sgu, wd, sd))
+    codes = getattr(torch, "float8_e4m3fn", None)
+    if wgu.dtype == codes:
+        wgu = wgu.view(torch.uint8)
+    if wd.dtype == codes:
+        wd = wd.view(torch.uint8)
     if x.dtype != torch.bfloat16:
         raise TypeError("x must be bfloat16")
+    if not wgu.dtype == sgu.dtype == wd.dtype == sd.dtype == torch.uint8:
+        raise TypeError("wgu, sgu, wd, sd must be uint8 (or float8_e4m3fn for codes)")
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("x must be on the GPU")
     for name, t in (("wgu", wgu), ("sgu", sgu), ("wd", wd), ("sd", sd)):
-        if t.dtype != torch.uint8:
-            raise TypeError("%s must be uint8 (or float8_e4m3fn for codes), got %s" % (name, t.dtype))
-        if t.dim() != 3:
-            raise ValueError("%s must be 3-D" % name)
-    if x.dim() != 2:
-        raise ValueError("x must be 2-D")
+        if t.dim() != 3 or t.device != dev or not t.is_contiguous():
+            raise ValueError("%s must be 3-D, contiguous and on the same GPU as x" % name)
+    if x.dim() != 2 or x.stride(1) != 1:
+        raise ValueError("x must be 2-D with a contiguous last axis")
     T, H = x.shape
     E, H2, I = wd.shape
     if H2 != H or wgu.shape != (E, 2 * I, H) or sgu.shape != (E, 2 * I, H // 32) or sd.shape != (E, H, I // 32):
         raise ValueError("shape mismatch: x %s wgu %s sgu %s wd %s sd %s" % tuple(
             tuple(t.shape) for t in (x, wgu, sgu, wd, sd)))
+    ldx = x.stride(0) if T > 1 else H
+    if ldx < H:
+        raise ValueError("x's rows must be at least a row apart")
     k = int(top_k)
     if (router is None) == (routing is None):
         raise ValueError("give a router or a routing, and not both")
-    ids = weights = None
-    if router is not None:
-        if router.dtype != torch.bfloat16 or tuple(router.shape) != (E, H):
-            raise ValueError("router must be bf16 [E, H]")
-    else:
-        ids, weights = routing
-        if ids.dtype != torch.int32 or weights.dtype != torch.float32 or tuple(ids.shape) != (T, k) or tuple(
-                weights.shape) != (T, k):
-            raise ValueError("routing must be int32 and float32 [T, top_k]")
-    if active is not None and (active.dtype not in (torch.bool, torch.uint8) or tuple(active.shape) != (T,)):
-        raise ValueError("active must be bool [T]")
-    dev = x.device
-    if dev.type != "cuda":
-        raise ValueError("x must be on the GPU")
-    for name, t in (("router", router), ("wgu", wgu), ("sgu", sgu), ("wd", wd), ("sd", sd), ("ids", ids),
-                    ("weights", weights), ("active", active)):
-        if t is not None and (t.device != dev or not t.is_contiguous()):
-            raise ValueError("%s must be contiguous and on the same GPU as x" % name)
-    if x.stride(1) != 1 or (T > 1 and x.stride(0) < H):
-        raise ValueError("x must have a contiguous last axis and rows at least a row apart")
     on = _On(dev, stream)
-    if out is None:
-        out = on.new((T, H), torch.bfloat16)
-    elif out.dtype != torch.bfloat16 or tuple(out.shape) != (T, H) or not out.is_contiguous() or out.device != dev:
-        raise ValueError("out must be a contiguous bf16 [T, H] tensor on the same device")
-    if ids is None:
+    if router is not None:
+        if router.dtype != torch.bfloat16 or router.shape != (E, H) or router.device != dev or not router.is_contiguous():
+            raise ValueError("router must be a contiguous bf16 [E, H] tensor on the same GPU as x")
         ids = on.new((T, k), torch.int32)
         weights = on.new((T, k), torch.float32)
+    else:
+        ids, weights = routing
+        for name, t, kind in (("ids", ids, torch.int32), ("weights", weights, torch.float32)):
+            if t.dtype != kind or t.shape != (T, k) or t.device != dev or not t.is_contiguous():
+                raise ValueError("routing: %s must be a contiguous %s [T, top_k] tensor on the same GPU as x" % (name, kind))
+    if active is not None and (active.dtype not in (torch.bool, torch.uint8) or active.shape != (T,) or
+                               active.device != dev or not active.is_contiguous()):
+        raise ValueError("active must be a contiguous bool [T] tensor on the same GPU as x")
+    if out is None:
+        out = on.new((T, H), torch.bfloat16)
+    elif out.dtype != torch.bfloat16 or out.shape != (T, H) or not out.is_contiguous() or out.device != dev:
+        raise ValueError("out must be a contiguous bf16 [T, H] tensor on the same device")
     with on:
         wp, wb, ws = on.workspace(moe_workspace_size(T, E, k, H, I), workspace)
-        rc = mxw_moe_layer(x.data_ptr(), x.stride(0) if T > 1 else H, 0 if router is None else router.data_ptr(),
+        rc = mxw_moe_layer(x.data_ptr(), ldx, 0 if router is None else router.data_ptr(),
                            wgu.data_ptr(), sgu.data_ptr(), wd.data_ptr(), sd.data_ptr(),
                            0 if active is None else active.data_ptr(), T, E, k, H, I, normalize, scale, ids.data_ptr(),
                            weights.data_ptr(), out.data_ptr(), wp, wb, on.stream.cuda_stream)

@@ -9,7 +9,7 @@
 // is small: bound by reading HBM.  The kernels:
 //
 //   router  logits r [T, E], in parts of H that the reader adds (skipped when the
-//           caller brings its own routing)
+//           caller brings its own routing; a small router is left to gate/up)
 //   route   for more than 16 tokens, the choice of each (for fewer every
 //           workgroup of the next kernel makes it for itself: cheaper than a
 //           launch)
@@ -179,11 +179,12 @@ __device__ __forceinline__ int wave_min(int v) {
 
 // ---- router -----------------------------------------------------------------
 
-// Logits of 16 experts and 16 tokens over one part of H: workgroup (experts,
-// tokens, part), its waves splitting the part.
-__global__ __launch_bounds__(kWaves * 64) void moe_router_kernel(MoeArgs a) {
-  __shared__ float red[kWaves][256];
-  const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16;
+// Logits of 16 experts and 16 tokens over the steps first, first + stride, ... of
+// 128 of H, split over the workgroup's waves; thread i < 256 gets token t0 + i % 16,
+// expert e0 + 4 ((i % 64) / 16) + i / 64.
+template <int WAVES>
+__device__ __forceinline__ float router_tile(const MoeArgs& a, int e0, int t0, int first, int stride,
+                                             float (*red)[256]) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r = lane & 15, b = lane >> 4;
   const int e = e0 + r < a.E ? e0 + r : a.E - 1, t = t0 + r < a.T ? t0 + r : a.T - 1;
@@ -192,7 +193,7 @@ __global__ __launch_bounds__(kWaves * 64) void moe_router_kernel(MoeArgs a) {
   const int blocks = a.H >> 5;
   v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 2
-  for (int s = blockIdx.z * kWaves + wave; 4 * s < blocks; s += gridDim.z * kWaves) {
+  for (int s = first + wave; 4 * s < blocks; s += stride) {
     const bool in = 4 * s + b < blocks;
     const int at = 32 * (in ? 4 * s + b : 0);
 #pragma unroll
@@ -205,19 +206,28 @@ __global__ __launch_bounds__(kWaves * 64) void moe_router_kernel(MoeArgs a) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) red[wave][i * 64 + lane] = acc[i];
   __syncthreads();
-  // thread i < 256: token i % 16, expert 4 ((i % 64) / 16) + i / 64
-  const int et = e0 + 4 * (lane >> 4) + wave, tt = t0 + (tid & 15);
-  if (tid < 256 && et < a.E && tt < a.T) {
-    float v = 0.0f;
+  float v = 0.0f;
+  if (tid < 256) {
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) v += red[w][tid];
-    a.logits[((int64_t)blockIdx.z * a.T + tt) * a.E + et] = v;
+    for (int w = 0; w < WAVES; ++w) v += red[w][tid];
   }
+  __syncthreads();
+  return v;
+}
+
+// workgroup (experts, tokens, part of H)
+__global__ __launch_bounds__(kWaves * 64) void moe_router_kernel(MoeArgs a) {
+  __shared__ float red[kWaves][256];
+  const int tid = threadIdx.x, e0 = blockIdx.x * 16, t0 = blockIdx.y * 16;
+  const float v = router_tile<kWaves>(a, e0, t0, blockIdx.z * kWaves, gridDim.z * kWaves, red);
+  const int e = e0 + 4 * ((tid & 63) >> 4) + (tid >> 6), t = t0 + (tid & 15);
+  if (tid < 256 && e < a.E && t < a.T) a.logits[((int64_t)blockIdx.z * a.T + t) * a.E + e] = v;
 }
 
 // The routing of one token by one wave: lane l holds experts l, l + 64, ...
-// Writes the token's choices and weights.
-__device__ __forceinline__ void route_token(const MoeArgs& a, int t, int32_t* ids, float* weights) {
+// Writes the token's choices and weights.  logits: [parts][T][E].
+__device__ __forceinline__ void route_token(const MoeArgs& a, const float* logits, int parts, int t, int32_t* ids,
+                                            float* weights) {
   const int lane = threadIdx.x & 63;
   if (a.active && !a.active[t]) {
     if (lane < a.k) {
@@ -235,8 +245,8 @@ __device__ __forceinline__ void route_token(const MoeArgs& a, int t, int32_t* id
     v[i] = e < a.E ? 0.0f : -INFINITY;
     gone |= (uint32_t)(e >= a.E) << i;
   }
-  for (int z = 0; z < a.parts; ++z) {
-    const float* from = a.logits + ((int64_t)z * a.T + t) * a.E;
+  for (int z = 0; z < parts; ++z) {
+    const float* from = logits + ((int64_t)z * a.T + t) * a.E;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (lane + 64 * i < a.E) v[i] += from[lane + 64 * i];
@@ -282,7 +292,7 @@ __device__ __forceinline__ void route_token(const MoeArgs& a, int t, int32_t* id
 
 __global__ __launch_bounds__(256) void moe_route_kernel(MoeArgs a) {
   const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t < a.T) route_token(a, t, a.ids + t * a.k, a.weights + t * a.k);
+  if (t < a.T) route_token(a, a.logits, a.parts, t, a.ids + t * a.k, a.weights + t * a.k);
 }
 
 // ---- gate/up ----------------------------------------------------------------
@@ -296,15 +306,31 @@ struct Routing {
   int32_t chosen[4], pairs[4];
 };
 
+// where a workgroup has the routing from
+enum From { kGiven, kLogits, kRouter };  // ids and weights; the logits; x and the router
+constexpr int kFusedLogits = 1024;       // T E at most, for kRouter
+
 // The routing by expert into LDS, by every workgroup for itself; workgroup 0
-// writes out what the down kernels and the caller need.  ROUTE: from the logits;
-// else from ids and weights.  Returns the number of chosen experts.
-template <bool ROUTE, int WAVES>
-__device__ __forceinline__ int make_routing(const MoeArgs& a, Routing& rt) {
+// writes out what the down kernels and the caller need.  `scratch` (kRouter):
+// kFusedLogits + 256 WAVES floats of LDS.  Returns the number of chosen experts.
+template <From FROM, int WAVES>
+__device__ __forceinline__ int make_routing(const MoeArgs& a, Routing& rt, float* scratch) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n = a.T * a.k;
-  if (ROUTE) {
-    for (int t = wave; t < a.T; t += WAVES) route_token(a, t, rt.ids + t * a.k, rt.weights + t * a.k);
+  if (FROM != kGiven) {
+    const float* logits = a.logits;
+    int parts = a.parts;
+    if (FROM == kRouter) {
+      logits = scratch;
+      parts = 1;
+      for (int e0 = 0; e0 < a.E; e0 += 16) {
+        const float v = router_tile<WAVES>(a, e0, 0, 0, WAVES, (float(*)[256])(scratch + kFusedLogits));
+        const int e = e0 + 4 * (lane >> 4) + wave, t = tid & 15;
+        if (tid < 256 && e < a.E && t < a.T) scratch[t * a.E + e] = v;
+      }
+      __syncthreads();
+    }
+    for (int t = wave; t < a.T; t += WAVES) route_token(a, logits, parts, t, rt.ids + t * a.k, rt.weights + t * a.k);
   } else {
     for (int i = tid; i < n; i += WAVES * 64) {
       const int id = a.ids[i];
@@ -354,7 +380,7 @@ __device__ __forceinline__ int make_routing(const MoeArgs& a, Routing& rt) {
   if (blockIdx.x == 0) {
     for (int i = tid; i < n; i += WAVES * 64) {
       const int e = rt.ids[i], t = i / a.k;
-      if (ROUTE) {
+      if (FROM != kGiven) {
         a.ids[i] = e;
         a.weights[i] = rt.weights[i];
       }
@@ -417,12 +443,13 @@ __device__ __forceinline__ void gate_rows(const MoeArgs& a, int e, int i0, const
 }
 
 // few items: (expert, 16 rows of Wg and of Wu), H split over the 8 waves
-template <bool ROUTE>
+template <From FROM>
 __global__ __launch_bounds__(kWaves * 64, 4) void moe_gate_split_kernel(MoeArgs a) {
   __shared__ Routing rt;
   __shared__ float part[kWaves][2][256];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int count = make_routing<ROUTE, kWaves>(a, rt);
+  const int count = make_routing<FROM, kWaves>(a, rt, &part[0][0][0]);
+  if (FROM == kRouter) __syncthreads();  // `part` was its scratch
   const int tiles = (a.I + 15) / 16, blocks = a.H >> 5;
   const int r = lane & 15, b = lane >> 4;
   for (int item = blockIdx.x; item < count * tiles; item += gridDim.x) {
@@ -626,12 +653,12 @@ __device__ __forceinline__ void gate_item(const MoeArgs& a, const Routing& rt, i
   }
 }
 
-template <bool ROUTE, int G, bool MANY>
+template <From FROM, int G, bool MANY>
 __global__ __launch_bounds__(256, 2) void moe_gate_kernel(MoeArgs a) {
   __shared__ Routing rt;
   __shared__ int32_t token[kMaxTokens];
   __shared__ __align__(1024) uint8_t ring[kRing];
-  const int count = make_routing<ROUTE, 4>(a, rt);
+  const int count = make_routing<FROM, 4>(a, rt, (float*)ring);
   const int tiles = (a.I + 32 * G - 1) / (32 * G);
   for (int item = blockIdx.x; item < count * tiles; item += gridDim.x) {
     const int e = rt.expert[item / tiles], i0 = item % tiles * 32 * G;
@@ -755,6 +782,7 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs a) {
 
 struct MoePlan {
   int parts;     // of H in the router
+  bool fused;    // the gate kernel makes the logits itself
   bool by_item;  // down: partial outputs per item
   size_t logits, count, expert, first, tokens, row, h, part, bytes;
 };
@@ -767,8 +795,11 @@ MoePlan plan_of(int T, int E, int k, int H, int I) {
   // a step of 128 a wave if there are few workgroups
   p.parts = (H + 128 * kWaves - 1) / (128 * kWaves);
   if (p.parts > 8) p.parts = 8;
+  // A router of at most 64 KiB is read by every workgroup of the gate kernel (from
+  // its XCD's L2) in about a us; a kernel of its own costs 3 us and a launch.
+  p.fused = T <= 16 && T * E <= kFusedLogits && E * H <= (32 << 10);
   // a workgroup of the down kernel reads 16 rows of I of every chosen expert
-  p.by_item = (I & 127) == 0 && (int64_t)most_experts(T, E, k) * I * 16 > (512 << 10);
+  p.by_item = (I & 127) == 0 && (int64_t)most_experts(T, E, k) * I * 16 > (192 << 10);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t was = at;
@@ -794,22 +825,22 @@ int check_moe(int T, int E, int k, int H, int I) {
              : MXW_OK;
 }
 
-template <bool ROUTE>
+template <From FROM>
 void launch_gate(const MoeArgs& a, int cus, hipStream_t st) {
   const int64_t most = most_experts(a.T, a.E, a.k);
   if (a.H & 127) {
     const int64_t n = most * ((a.I + 15) / 16);
-    hipLaunchKernelGGL((moe_gate_split_kernel<ROUTE>), dim3((unsigned)(n < 4 * cus ? n : 4 * cus)), dim3(kWaves * 64), 0,
+    hipLaunchKernelGGL((moe_gate_split_kernel<FROM>), dim3((unsigned)(n < 4 * cus ? n : 4 * cus)), dim3(kWaves * 64), 0,
                        st, a);
     return;
   }
   const int64_t slots = 2 * cus, one = most * ((a.I + 31) / 32), two = most * ((a.I + 63) / 64);
   if (two < slots)
-    hipLaunchKernelGGL((moe_gate_kernel<ROUTE, 1, true>), dim3((unsigned)(one < slots ? one : slots)), dim3(256), 0, st, a);
-  else if (a.T <= 16)
-    hipLaunchKernelGGL((moe_gate_kernel<ROUTE, 2, false>), dim3((unsigned)slots), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((moe_gate_kernel<FROM, 1, true>), dim3((unsigned)(one < slots ? one : slots)), dim3(256), 0, st, a);
+  else if (FROM != kGiven)  // at most 16 tokens
+    hipLaunchKernelGGL((moe_gate_kernel<FROM, 2, false>), dim3((unsigned)slots), dim3(256), 0, st, a);
   else
-    hipLaunchKernelGGL((moe_gate_kernel<ROUTE, 2, true>), dim3((unsigned)slots), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((moe_gate_kernel<FROM, 2, true>), dim3((unsigned)slots), dim3(256), 0, st, a);
 }
 
 }  // namespace
@@ -865,14 +896,18 @@ int mxw_moe_layer(const uint16_t* x, int64_t ldx, const uint16_t* router, const 
   a.row = (int32_t*)(ws + p.row);
   a.h = (uint16_t*)(ws + p.h);
   a.part = (float*)(ws + p.part);
-  if (router)
-    hipLaunchKernelGGL(moe_router_kernel, dim3((unsigned)((E + 15) / 16), (unsigned)((T + 15) / 16), (unsigned)p.parts),
-                       dim3(kWaves * 64), 0, st, a);
-  if (router && T <= 16) {
-    launch_gate<true>(a, cus, st);
+  if (p.fused && router) {
+    launch_gate<kRouter>(a, cus, st);
   } else {
-    if (router) hipLaunchKernelGGL(moe_route_kernel, dim3((unsigned)((T + 3) / 4)), dim3(256), 0, st, a);
-    launch_gate<false>(a, cus, st);
+    if (router)
+      hipLaunchKernelGGL(moe_router_kernel, dim3((unsigned)((E + 15) / 16), (unsigned)((T + 15) / 16), (unsigned)p.parts),
+                         dim3(kWaves * 64), 0, st, a);
+    if (router && T <= 16) {
+      launch_gate<kLogits>(a, cus, st);
+    } else {
+      if (router) hipLaunchKernelGGL(moe_route_kernel, dim3((unsigned)((T + 3) / 4)), dim3(256), 0, st, a);
+      launch_gate<kGiven>(a, cus, st);
+    }
   }
   if (p.by_item) {
     const int64_t most = most_experts(T, E, k), slots = 2 * cus, one = most * ((H + 63) / 64),

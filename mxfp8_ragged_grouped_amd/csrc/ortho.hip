@@ -52,10 +52,30 @@ struct LoadArgs {
   float eps;
 };
 
+// elements i .. i + 7 of G, zeros from the `left`-th on.  Rows of any stride start
+// at any element: the 16-byte loads need no alignment beyond the element's.
 template <bool F32>
-__device__ __forceinline__ float element(const void* G, int64_t i) {
-  if (F32) return ((const float*)G)[i];
-  return __uint_as_float((uint32_t)((const uint16_t*)G)[i] << 16);
+__device__ __forceinline__ void load8(const void* G, int64_t i, int left, float (&v)[8]) {
+  if (F32) {
+    const float* p = (const float*)G + i;
+    if (left >= 8) {
+      __builtin_memcpy(v, p, 32);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = j < left ? p[j] : 0.0f;
+    }
+  } else {
+    const uint16_t* p = (const uint16_t*)G + i;
+    uint16_t u[8];
+    if (left >= 8) {
+      __builtin_memcpy(u, p, 16);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] = j < left ? p[j] : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float((uint32_t)u[j] << 16);
+  }
 }
 
 __device__ __forceinline__ double block_sum(double v, double* lds) {
@@ -67,36 +87,27 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
 
 // sums of squares of one part of an expert's rows, in 64 bits: squares of any
 // bf16 or FP32 gradient are in range, and the order is fixed
-template <bool F32, bool VEC>
+template <bool F32>
 __global__ __launch_bounds__(256) void ortho_norm_kernel(LoadArgs a) {
   __shared__ double lds[4];
-  const int e = blockIdx.y, part = blockIdx.x;
+  const int e = blockIdx.y, part = blockIdx.x, per = (a.K + 7) >> 3;
   const int r0 = (int)((int64_t)a.N * part / a.parts), r1 = (int)((int64_t)a.N * (part + 1) / a.parts);
+  const int count = (r1 - r0) * per;
   double sum = 0.0;
-  if (VEC) {  // 8 elements a thread
-    const int per = a.K >> 3;
-    const int64_t count = (int64_t)(r1 - r0) * per;
-    for (int64_t i = threadIdx.x; i < count; i += 256) {
-      const int64_t at = e * a.strideE + (r0 + i / per) * a.strideN + 8 * (i % per);
-      float v[8];
+#pragma unroll 4
+  for (int i = threadIdx.x; i < count; i += 256) {
+    const int row = i / per, col = 8 * (i - row * per);
+    float v[8];
+    load8<F32>(a.G, e * a.strideE + (r0 + row) * a.strideN + col, a.K - col, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = element<F32>(a.G, at + j);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum += (double)v[j] * (double)v[j];
-    }
-  } else {
-    const int64_t count = (int64_t)(r1 - r0) * a.K;
-    for (int64_t i = threadIdx.x; i < count; i += 256) {
-      const double v = element<F32>(a.G, e * a.strideE + (r0 + i / a.K) * a.strideN + i % a.K);
-      sum += v * v;
-    }
+    for (int j = 0; j < 8; ++j) sum += (double)v[j] * (double)v[j];
   }
   sum = block_sum(sum, lds);
   if (threadIdx.x == 0) a.sums[e * a.parts + part] = sum;
 }
 
 // X0 with its zero padding, 8 columns a thread
-template <bool F32, bool VEC>
+template <bool F32>
 __global__ __launch_bounds__(256) void ortho_load_kernel(LoadArgs a) {
   __shared__ double lds[4];
   const int e = blockIdx.y;
@@ -104,25 +115,174 @@ __global__ __launch_bounds__(256) void ortho_load_kernel(LoadArgs a) {
   const float scale = (float)(kOne / (sqrt(total) + (double)a.eps));
   const int per = a.ldx >> 3;
   const int64_t count = (int64_t)a.N * per;
+#pragma unroll 4
   for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < count; i += (int64_t)gridDim.x * 256) {
     const int row = (int)(i / per), col = 8 * (int)(i % per);
-    const int64_t at = e * a.strideE + row * a.strideN + col;
     float v[8];
-    if (VEC) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-      if (col < a.K) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = element<F32>(a.G, at + j);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = col + j < a.K ? element<F32>(a.G, at + j) : 0.0f;
-    }
+    load8<F32>(a.G, e * a.strideE + row * a.strideN + col, a.K - col, v);
     v4i w;
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[j] = (int)pack2(v[2 * j] * scale, v[2 * j + 1] * scale, _Float16());
     *(v4i*)(a.X + ((int64_t)e * a.N + row) * a.ldx + col) = w;
+  }
+}
+
+// ---- small matrices: all steps in one kernel --------------------------------
+
+// One workgroup a matrix, which stays in LDS for all steps: X [np][mp + 8] and S,
+// then P in its place, [np][np + 8] (np, mp: n, m rounded up to 32; the 8 spread
+// the rows over the banks).  A wave owns 32 x 32 blocks: of S and P up to two,
+// kept in registers until everyone has read; of X whole columns of blocks, which
+// P X needs and replaces alone, so X is updated in place.  The same roundings and,
+// element by element, the same sums as the products below.  Bound by latency
+// (barriers, LDS); against the launches of the general way: 128 x 256, four
+// matrices, 96 us to 27 us.
+constexpr int kSmallN = 128;
+constexpr int kSmallLds = 155 * 1024;
+
+struct SmallArgs {
+  LoadArgs in;
+  int tall, n, m, np, mp;
+  int steps;
+  uint16_t* out;
+  float coeffs[3 * kMaxSteps];
+};
+
+size_t small_lds(int n, int m) {
+  const size_t np = (n + 31) & ~31, mp = (m + 31) & ~31;
+  return 2 * (np * (mp + 8) + np * (np + 8));
+}
+
+__device__ __forceinline__ v4f mfma_h(const v4i& a, const v4i& b, const v4f& c) { return mfma16(a, b, c, _Float16()); }
+
+template <bool F32>
+__global__ __launch_bounds__(512, 2) void ortho_small_kernel(SmallArgs a) {
+  extern __shared__ __align__(16) uint16_t dyn[];
+  __shared__ double red[8];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+  const int e = blockIdx.x, ldx = a.mp + 8, lds = a.np + 8;
+  uint16_t* X = dyn;
+  uint16_t* S = dyn + a.np * ldx;
+  const int64_t base = e * a.in.strideE;
+  const int N = a.in.N, K = a.in.K;
+
+  // the norm, summed in 64 bits in a fixed order, then X0
+  const int per = (K + 7) >> 3, chunks = N * per;
+  double sum = 0.0;
+#pragma unroll 4
+  for (int i = tid; i < chunks; i += 512) {
+    const int row = i / per, col = 8 * (i - row * per);
+    float v[8];
+    load8<F32>(a.in.G, base + row * a.in.strideN + col, K - col, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += (double)v[j] * (double)v[j];
+  }
+  for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+  if (lane == 0) red[wave] = sum;
+  for (int i = tid; i < (a.np * (ldx + lds)) >> 3; i += 512) ((v4i*)dyn)[i] = (v4i){0, 0, 0, 0};
+  __syncthreads();
+  sum = 0.0;
+  for (int w = 0; w < 8; ++w) sum += red[w];
+  const float scale = (float)(kOne / (sqrt(sum) + (double)a.in.eps));
+#pragma unroll 4
+  for (int i = tid; i < chunks; i += 512) {
+    const int row = i / per, col = 8 * (i - row * per);
+    float v[8];
+    load8<F32>(a.in.G, base + row * a.in.strideN + col, K - col, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (col + j < K)
+        X[a.tall ? (col + j) * ldx + row : row * ldx + col + j] = (uint16_t)pack2(v[j] * scale, 0.0f, _Float16());
+  }
+  __syncthreads();
+
+  const int nb = a.np >> 5, mb = a.mp >> 5;
+  // lane's fragment of 16 rows from r0 on, columns k .. k + 31 of a matrix of row
+  // stride ld; and the same of its transpose (rows are columns, k the row)
+  auto rows = [&](const uint16_t* M, int ld, int r0, int k) { return *(const v4i*)(M + (r0 + r) * ld + k + 8 * g); };
+  auto cols = [&](const uint16_t* M, int ld, int c0, int k) {
+    const uint8_t* at = (const uint8_t*)(M + (k + 8 * g + (r >> 2)) * ld + c0 + 4 * (r & 3));
+    const v2i lo = lds_read_tr(at), hi = lds_read_tr(at + 8 * ld);
+    return (v4i){lo.x, lo.y, hi.x, hi.y};
+  };
+  for (int s = 0; s < a.steps; ++s) {
+    const float ca = a.coeffs[3 * s], cb = a.coeffs[3 * s + 1], cc = a.coeffs[3 * s + 2];
+    // S = X X^T, then P = a I + b S + c S S over it: blocks wave, wave + 8
+    for (int pass = 0; pass < 2; ++pass) {
+      v4f acc[2][2][2] = {};
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int id = wave + 8 * u;
+        if (id >= nb * nb) continue;
+        const int m0 = id / nb * 32, n0 = id % nb * 32;
+        const uint16_t* M = pass ? S : X;
+        const int ld = pass ? lds : ldx, depth = pass ? a.np : a.mp;
+#pragma unroll 2
+        for (int k = 0; k < depth; k += 32) {
+          const v4i f0 = rows(M, ld, m0, k), f1 = rows(M, ld, m0 + 16, k);
+          const v4i h0 = rows(M, ld, n0, k), h1 = rows(M, ld, n0 + 16, k);
+          acc[u][0][0] = mfma_h(h0, f0, acc[u][0][0]);
+          acc[u][0][1] = mfma_h(h1, f0, acc[u][0][1]);
+          acc[u][1][0] = mfma_h(h0, f1, acc[u][1][0]);
+          acc[u][1][1] = mfma_h(h1, f1, acc[u][1][1]);
+        }
+      }
+      if (pass) __syncthreads();  // S has been read
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int id = wave + 8 * u;
+        if (id >= nb * nb) continue;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int m = id / nb * 32 + 16 * i + r, n = id % nb * 32 + 16 * j + 4 * g;
+            typedef _Float16 v4h __attribute__((ext_vector_type(4)));
+            v4h* to = (v4h*)(S + m * lds + n);
+            float v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              v[q] = kPerOne * acc[u][i][j][q];
+              if (pass) v[q] = cc * v[q] + cb * (float)(*to)[q] + (m == n + q ? ca * kOne : 0.0f);
+            }
+            *(uint2*)to = make_uint2(pack2(v[0], v[1], _Float16()), pack2(v[2], v[3], _Float16()));
+          }
+      }
+      __syncthreads();
+    }
+    // X <- P X, 32 columns at a time
+    for (int c = wave; c < mb; c += 8) {
+      v4f acc[kSmallN / 16][2] = {};
+      for (int k = 0; k < a.np; k += 32) {
+        const v4i h0 = cols(X, ldx, 32 * c, k), h1 = cols(X, ldx, 32 * c + 16, k);
+#pragma unroll
+        for (int i = 0; i < kSmallN / 16; ++i) {
+          if (16 * i >= a.np) break;
+          const v4i f = rows(S, lds, 16 * i, k);
+          acc[i][0] = mfma_h(h0, f, acc[i][0]);
+          acc[i][1] = mfma_h(h1, f, acc[i][1]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kSmallN / 16; ++i) {
+        if (16 * i >= a.np) break;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int m = 16 * i + r, n = 32 * c + 16 * j + 4 * g;
+          if (s + 1 < a.steps) {
+            const v4f v = acc[i][j] * kPerOne;
+            *(uint2*)(X + m * ldx + n) = make_uint2(pack2(v[0], v[1], _Float16()), pack2(v[2], v[3], _Float16()));
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (m < a.n && n + q < a.m)
+                a.out[(int64_t)e * N * K + (a.tall ? (int64_t)(n + q) * K + m : (int64_t)m * K + n + q)] =
+                    (uint16_t)pack2(acc[i][j][q] * (kPerOne * kPerOne), 0.0f, __bf16());
+          }
+        }
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -252,7 +412,7 @@ OrthoPlan plan_of(int E, int N, int K) {
   p.m = p.tall ? N : K;
   p.ldx = round64(K);
   p.lds = round64(p.n);
-  int64_t parts = ((int64_t)N * K + 16383) / 16384;
+  int64_t parts = ((int64_t)N * K + 8191) / 8192;  // 4 chunks a thread, until there are many
   if (parts > kNormParts) parts = kNormParts;
   if (parts > N) parts = N;
   p.parts = (int)parts;
@@ -311,23 +471,31 @@ int mxw_orthogonalize(const void* G, int type, int64_t expert_stride, int64_t ro
   la.X = (uint16_t*)(ws + p.X[0]);
   la.eps = eps;
   const bool f32 = type == MXW_F32;
-  // 8 elements at a time where rows keep them together and aligned
-  const bool vec = (K & 7) == 0 && (row_stride & 7) == 0 && (expert_stride & 7) == 0 && ((uintptr_t)G & 15) == 0;
+  if (p.n <= kSmallN && small_lds(p.n, p.m) <= kSmallLds) {
+    SmallArgs sa = {};
+    sa.in = la;
+    sa.tall = p.tall;
+    sa.n = p.n;
+    sa.m = p.m;
+    sa.np = (p.n + 31) & ~31;
+    sa.mp = (p.m + 31) & ~31;
+    sa.steps = steps;
+    sa.out = out;
+    for (int i = 0; i < 3 * steps; ++i) sa.coeffs[i] = coeffs[i];
+    const unsigned bytes = (unsigned)small_lds(p.n, p.m);
+    if (f32) hipLaunchKernelGGL((ortho_small_kernel<true>), dim3((unsigned)E), dim3(512), bytes, st, sa);
+    else hipLaunchKernelGGL((ortho_small_kernel<false>), dim3((unsigned)E), dim3(512), bytes, st, sa);
+    return hipGetLastError() == hipSuccess ? MXW_OK : MXW_ERR_LAUNCH;
+  }
   int64_t blocks = ((int64_t)N * (p.ldx / 8) + 1023) / 1024;  // about 4 chunks a thread
   if (blocks > 4096) blocks = 4096;
   const dim3 ng((unsigned)p.parts, (unsigned)E), lg((unsigned)blocks, (unsigned)E);
-  if (f32 && vec) {
-    hipLaunchKernelGGL((ortho_norm_kernel<true, true>), ng, dim3(256), 0, st, la);
-    hipLaunchKernelGGL((ortho_load_kernel<true, true>), lg, dim3(256), 0, st, la);
-  } else if (f32) {
-    hipLaunchKernelGGL((ortho_norm_kernel<true, false>), ng, dim3(256), 0, st, la);
-    hipLaunchKernelGGL((ortho_load_kernel<true, false>), lg, dim3(256), 0, st, la);
-  } else if (vec) {
-    hipLaunchKernelGGL((ortho_norm_kernel<false, true>), ng, dim3(256), 0, st, la);
-    hipLaunchKernelGGL((ortho_load_kernel<false, true>), lg, dim3(256), 0, st, la);
+  if (f32) {
+    hipLaunchKernelGGL((ortho_norm_kernel<true>), ng, dim3(256), 0, st, la);
+    hipLaunchKernelGGL((ortho_load_kernel<true>), lg, dim3(256), 0, st, la);
   } else {
-    hipLaunchKernelGGL((ortho_norm_kernel<false, false>), ng, dim3(256), 0, st, la);
-    hipLaunchKernelGGL((ortho_load_kernel<false, false>), lg, dim3(256), 0, st, la);
+    hipLaunchKernelGGL((ortho_norm_kernel<false>), ng, dim3(256), 0, st, la);
+    hipLaunchKernelGGL((ortho_load_kernel<false>), lg, dim3(256), 0, st, la);
   }
 
   const int64_t strideX = (int64_t)N * p.ldx, strideS = (int64_t)p.n * p.lds;
