@@ -113,15 +113,22 @@ struct GemmArgs {
   int tiles;    // tiles per (batch entry, split)
   int batch, splits;
   int ksplit;   // k per split, a multiple of 64
+  int first;    // this launch's first of all batch * splits * tiles
+  int quarters; // a workgroup is a quarter of such a tile, which is twice as large either way
 };
 
 // Where the 16-byte chunks of a stage's rows lie, so that a fragment read, which
 // takes 256 bytes at a time, meets every LDS bank once.  Row form (128-byte
 // rows, 16 lanes at one chunk of 16 rows): chunk c of row r at c ^ (r / 2) % 8.
-// Column form (32 lanes at 32 bytes of 8 different k): chunk c of row k at
-// c ^ (4 (k % 4) + 2 (k / 8 % 2)).
+// Column form (32 lanes at 32 bytes of 8 different k, 0 .. 3 and 8 .. 11 after the
+// first): chunk c of row k at c ^ (4 (k % 4) + 2 (k / 8 % 2)); in 128-byte rows
+// (W = 64), of which two fill the banks, at c ^ (2 (k / 2 % 2) + 4 (k / 8 % 2)).
 __device__ __forceinline__ int row_swizzle(int r) { return (r >> 1) & 7; }
-__device__ __forceinline__ int col_swizzle(int k) { return ((k & 3) << 2) | ((k >> 2) & 2); }
+template <int W>
+__device__ __forceinline__ int col_swizzle(int k) {
+  static_assert(W >= 64, "8 chunks a row");
+  return W == 64 ? (k & 2) | ((k >> 1) & 4) : ((k & 3) << 2) | ((k >> 2) & 2);
+}
 
 // what an epilogue gets to know of its tile
 struct TileAt {
@@ -146,7 +153,10 @@ __device__ __forceinline__ int xcd_run(int b, int n) {
   return x * q + (x < r ? x : r) + (b >> 3);
 }
 
-template <typename T, int BM, int BN, int WM, int WN, bool TA, bool TB, bool SYM, class Epi>
+// DEEP = 0: the rolling pipeline below.  DEEP > 0, for tiles whose step is shorter
+// than a load's latency: a ring of DEEP stages of both operands, filled DEEP - 1
+// steps ahead.
+template <typename T, int BM, int BN, int WM, int WN, int DEEP, bool TA, bool TB, bool SYM, class Epi>
 __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) void gemm16_kernel(GemmArgs p, typename Epi::Args ea) {
   constexpr int kWaves = WM * WN;
   constexpr int kPartM = BM / WM, kPartN = BN / WN;
@@ -154,15 +164,16 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
   constexpr int kBytesA = BM * 128, kBytesB = BN * 128;  // a stage of A, of B
   constexpr int kLoadsA = BM / 8, kLoadsB = BN / 8;  // 1 KiB loads per stage
   constexpr int LA = (kLoadsA + kWaves - 1) / kWaves, LB = (kLoadsB + kWaves - 1) / kWaves;
-  // three stages of A and two of B; the epilogue's tile takes their place
-  constexpr int kLds = 3 * kBytesA + 2 * kBytesB;
+  // three stages of A and two of B, or the ring; the epilogue's tile takes their place
+  constexpr int kLds = DEEP ? DEEP * (kBytesA + kBytesB) : 3 * kBytesA + 2 * kBytesB;
   static_assert(!Epi::kStaged || BM * BN * 2 <= kLds, "the staged tile fits");
   __shared__ __align__(1024) uint8_t lds[kLds];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   TileAt at;
   {
-    const int id = xcd_run(blockIdx.x, p.batch * p.splits * p.tiles);
+    const int run = xcd_run(blockIdx.x, gridDim.x);
+    const int id = p.first + (p.quarters ? run >> 2 : run);
     const int t = id % p.tiles, bs = id / p.tiles;
     at.split = bs % p.splits;
     at.batch = bs / p.splits;
@@ -172,14 +183,18 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
       while ((tm + 1) * (tm + 2) / 2 <= t) ++tm;
       while (tm * (tm + 1) / 2 > t) --tm;
       tn = t - tm * (tm + 1) / 2;
-      at.mirror = tm != tn;
     } else {  // bands of 4 tile rows
       const int per = 4 * p.tilesN, band = t / per, in = t - band * per;
       const int rows = p.tilesM - 4 * band < 4 ? p.tilesM - 4 * band : 4;
       tn = in / rows;
       tm = 4 * band + in - tn * rows;
-      at.mirror = false;
     }
+    if (p.quarters) {
+      tm = 2 * tm + ((run >> 1) & 1);
+      tn = 2 * tn + (run & 1);
+      if (tm * BM >= p.M || tn * BN >= p.N || (SYM && tn > tm)) return;  // the whole workgroup
+    }
+    at.mirror = SYM && tm != tn;
     at.m0 = tm * BM;
     at.n0 = tn * BN;
   }
@@ -220,7 +235,7 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
       if (TA) {
         constexpr int kLanes = BM / 8;  // lanes (16-byte chunks) a k
         const int k = u * (64 / kLanes) + lane / kLanes, c = lane % kLanes;
-        voA[i] = (uint32_t)(k * la + ((c ^ col_swizzle(k)) << 4));
+        voA[i] = (uint32_t)(k * la + ((c ^ col_swizzle<TA ? BM : 64>(k)) << 4));
       } else {
         const int r = u * 8 + (lane >> 3), c = lane & 7;
         voA[i] = (uint32_t)(r * la + ((c ^ row_swizzle(r)) << 4));
@@ -232,7 +247,7 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
       if (TB) {
         constexpr int kLanes = BN / 8;
         const int k = u * (64 / kLanes) + lane / kLanes, c = lane % kLanes;
-        voB[i] = (uint32_t)(k * lb + ((c ^ col_swizzle(k)) << 4));
+        voB[i] = (uint32_t)(k * lb + ((c ^ col_swizzle<TB ? BN : 64>(k)) << 4));
       } else {
         const int r = u * 8 + (lane >> 3), c = lane & 7;
         voB[i] = (uint32_t)(r * lb + ((c ^ row_swizzle(r)) << 4));
@@ -271,11 +286,11 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
   uint32_t fa[TA ? MI : 2], fb[TB ? NI : 2];
   {
     const int g = lane >> 4, r = lane & 15;
-    const int tk = 8 * g + (r >> 2), x = col_swizzle(tk), tc = (lane & 3) >> 1;
+    const int tk = 8 * g + (r >> 2), tc = (lane & 3) >> 1;
     if (TA) {
 #pragma unroll
       for (int i = 0; i < (TA ? MI : 0); ++i)
-        fa[i] = tk * BM * 2 + (((((at.wm >> 4) + i) * 2 + tc) ^ x) << 4) + ((lane & 1) << 3);
+        fa[i] = tk * BM * 2 + (((((at.wm >> 4) + i) * 2 + tc) ^ col_swizzle<TA ? BM : 64>(tk)) << 4) + ((lane & 1) << 3);
     } else {
 #pragma unroll
       for (int j = 0; j < 2; ++j) fa[j] = (at.wm + r) * 128 + (((4 * j + g) ^ row_swizzle(r)) << 4);
@@ -283,7 +298,7 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
     if (TB) {
 #pragma unroll
       for (int i = 0; i < (TB ? NI : 0); ++i)
-        fb[i] = tk * BN * 2 + (((((at.wn >> 4) + i) * 2 + tc) ^ x) << 4) + ((lane & 1) << 3);
+        fb[i] = tk * BN * 2 + (((((at.wn >> 4) + i) * 2 + tc) ^ col_swizzle<TB ? BN : 64>(tk)) << 4) + ((lane & 1) << 3);
     } else {
 #pragma unroll
       for (int j = 0; j < 2; ++j) fb[j] = (at.wn + r) * 128 + (((4 * j + g) ^ row_swizzle(r)) << 4);
@@ -309,7 +324,7 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
     return *(const v4i*)(st + fa[TA ? 0 : j] + i * 16 * 128);
   };
   auto readB = [&](uint32_t from, int j, int i) -> v4i {
-    const uint8_t* st = lds + 3 * kBytesA + from;
+    const uint8_t* st = lds + from;
     if (TB) {
       const v2i lo = lds_read_tr(st + fb[TB ? i : 0] + 32 * j * BN * 2);
       const v2i hi = lds_read_tr(st + fb[TB ? i : 0] + (32 * j + 4) * BN * 2);
@@ -329,30 +344,59 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
   // after next in the first part, into the third A stage, so that they may be in
   // flight across the next barrier.
   constexpr int kOldest = kLoadsA % kWaves == 0 ? LA : 0;  // loads a barrier leaves in flight
-  {
+  if constexpr (DEEP > 0) {
+    static_assert(kLoadsA % kWaves == 0 && kLoadsB % kWaves == 0, "every wave has the same loads");
+    constexpr int kSlot = kBytesA + kBytesB;
+    const uint32_t ldsWave = ldsBase + wave * 1024;
+    auto fill = [&](int slot) {
+      fillA(ldsWave + slot * kSlot, 0, LA);
+      fillB(ldsWave + slot * kSlot + kBytesA, 0, LB);
+    };
+#pragma unroll
+    for (int i = 0; i < DEEP - 1; ++i) fill(i);
+    int slot = 0, next = DEEP - 1;
+    for (int s = 0; s < steps; ++s) {
+      stage_barrier<(DEEP - 2) * (LA + LB)>();  // this step's loads are here, the slot before it is free
+      fill(next);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        v4i a[MI], b[NI];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) b[i] = readB(slot * kSlot + kBytesA, j, i);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) a[i] = readA(slot * kSlot, j, i);
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+          for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = mfma16(b[ni], a[mi], acc[mi][ni], T());
+      }
+      slot = slot + 1 == DEEP ? 0 : slot + 1;
+      next = next + 1 == DEEP ? 0 : next + 1;
+    }
+  } else {
     static_assert(NI <= MI, "a B fragment of the next part is read in each of the first NI rows");
-    const uint32_t ldsA = ldsBase + wave * 1024, ldsB = ldsA + 3 * kBytesA;
+    const uint32_t ldsWave = ldsBase + wave * 1024;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      fillA(ldsA + i * kBytesA, 0, LA);
-      fillB(ldsB + i * kBytesB, 0, LB);
+      fillA(ldsWave + i * kBytesA, 0, LA);
+      fillB(ldsWave + 3 * kBytesA + i * kBytesB, 0, LB);
     }
     stage_barrier<kLoadsA % kWaves == 0 && kLoadsB % kWaves == 0 ? LA + LB : 0>();
     // in the order of the loop: a read's age tells the wait before its use
     v4i a[MI], b[2][NI];
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      if (i < NI) b[0][i] = readB(0, 0, i);
+      if (i < NI) b[0][i] = readB(3 * kBytesA, 0, i);
       __builtin_amdgcn_sched_barrier(0);
       a[i] = readA(0, 0, i);
       __builtin_amdgcn_sched_barrier(0);
     }
-    uint32_t a0 = 0, a1 = kBytesA, a2 = 2 * kBytesA, b0 = 0, b1 = kBytesB;
+    uint32_t a0 = 0, a1 = kBytesA, a2 = 2 * kBytesA, b0 = 3 * kBytesA, b1 = b0 + kBytesB;
     for (int s = 0; s < steps; ++s) {
 #pragma unroll
       for (int mi = 0; mi < MI; ++mi) {
         if (mi < NI) b[1][mi] = readB(b0, 1, mi);
-        fillA(ldsA + a2, mi * LA / MI, (mi + 1) * LA / MI);
+        fillA(ldsWave + a2, mi * LA / MI, (mi + 1) * LA / MI);
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = mfma16(b[0][ni], a[mi], acc[mi][ni], T());
         a[mi] = readA(a0, 1, mi);
@@ -362,7 +406,7 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
 #pragma unroll
       for (int mi = 0; mi < MI; ++mi) {
         if (mi < NI) b[0][mi] = readB(b1, 0, mi);
-        fillB(ldsB + b0, mi * LB / MI, (mi + 1) * LB / MI);
+        fillB(ldsWave + b0, mi * LB / MI, (mi + 1) * LB / MI);
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = mfma16(b[1][ni], a[mi], acc[mi][ni], T());
         a[mi] = readA(a1, 0, mi);

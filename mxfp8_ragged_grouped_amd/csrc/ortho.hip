@@ -52,30 +52,44 @@ struct LoadArgs {
   float eps;
 };
 
-// elements i .. i + 7 of G, zeros from the `left`-th on.  Rows of any stride start
-// at any element: the 16-byte loads need no alignment beyond the element's.
 template <bool F32>
-__device__ __forceinline__ void load8(const void* G, int64_t i, int left, float (&v)[8]) {
+__device__ __forceinline__ float element(const void* G, int64_t i) {
+  if (F32) return ((const float*)G)[i];
+  return __uint_as_float((uint32_t)((const uint16_t*)G)[i] << 16);
+}
+// Elements i .. i + 7.  Rows of any stride start at any element: the 16-byte loads
+// need no alignment beyond the element's.
+template <bool F32>
+__device__ __forceinline__ void load8(const void* G, int64_t i, float (&v)[8]) {
   if (F32) {
-    const float* p = (const float*)G + i;
-    if (left >= 8) {
-      __builtin_memcpy(v, p, 32);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = j < left ? p[j] : 0.0f;
-    }
+    __builtin_memcpy(v, (const float*)G + i, 32);
   } else {
-    const uint16_t* p = (const uint16_t*)G + i;
     uint16_t u[8];
-    if (left >= 8) {
-      __builtin_memcpy(u, p, 16);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] = j < left ? p[j] : 0;
-    }
+    __builtin_memcpy(u, (const uint16_t*)G + i, 16);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = __uint_as_float((uint32_t)u[j] << 16);
   }
+}
+// Sum of squares, in 64 bits, of this thread's share of `rows` rows of K elements,
+// row_stride apart from `at` on: whole eights first, four in flight, then the rest.
+template <bool F32>
+__device__ __forceinline__ double squares(const void* G, int64_t at, int64_t row_stride, int rows, int K, int threads) {
+  const int per = K >> 3, rest = K & 7;
+  double sum = 0.0;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < rows * per; i += threads) {
+    const int row = i / per;
+    float v[8];
+    load8<F32>(G, at + row * row_stride + 8 * (i - row * per), v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += (double)v[j] * (double)v[j];
+  }
+  for (int i = threadIdx.x; i < rows * rest; i += threads) {
+    const int row = i / rest;
+    const double v = element<F32>(G, at + row * row_stride + 8 * per + (i - row * rest));
+    sum += v * v;
+  }
+  return sum;
 }
 
 __device__ __forceinline__ double block_sum(double v, double* lds) {
@@ -90,19 +104,10 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
 template <bool F32>
 __global__ __launch_bounds__(256) void ortho_norm_kernel(LoadArgs a) {
   __shared__ double lds[4];
-  const int e = blockIdx.y, part = blockIdx.x, per = (a.K + 7) >> 3;
+  const int e = blockIdx.y, part = blockIdx.x;
   const int r0 = (int)((int64_t)a.N * part / a.parts), r1 = (int)((int64_t)a.N * (part + 1) / a.parts);
-  const int count = (r1 - r0) * per;
-  double sum = 0.0;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < count; i += 256) {
-    const int row = i / per, col = 8 * (i - row * per);
-    float v[8];
-    load8<F32>(a.G, e * a.strideE + (r0 + row) * a.strideN + col, a.K - col, v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum += (double)v[j] * (double)v[j];
-  }
-  sum = block_sum(sum, lds);
+  const double sum =
+      block_sum(squares<F32>(a.G, e * a.strideE + r0 * a.strideN, a.strideN, r1 - r0, a.K, 256), lds);
   if (threadIdx.x == 0) a.sums[e * a.parts + part] = sum;
 }
 
@@ -113,17 +118,25 @@ __global__ __launch_bounds__(256) void ortho_load_kernel(LoadArgs a) {
   const int e = blockIdx.y;
   const double total = block_sum((int)threadIdx.x < a.parts ? a.sums[e * a.parts + threadIdx.x] : 0.0, lds);
   const float scale = (float)(kOne / (sqrt(total) + (double)a.eps));
-  const int per = a.ldx >> 3;
-  const int64_t count = (int64_t)a.N * per;
+  const int per = a.ldx >> 3, whole = a.K >> 3;
+  uint16_t* X = a.X + (int64_t)e * a.N * a.ldx;
+  const int64_t stride = (int64_t)gridDim.x * 256;
 #pragma unroll 4
-  for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < count; i += (int64_t)gridDim.x * 256) {
-    const int row = (int)(i / per), col = 8 * (int)(i % per);
+  for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < (int64_t)a.N * whole; i += stride) {
+    const int row = (int)(i / whole), col = 8 * (int)(i % whole);
     float v[8];
-    load8<F32>(a.G, e * a.strideE + row * a.strideN + col, a.K - col, v);
+    load8<F32>(a.G, e * a.strideE + row * a.strideN + col, v);
     v4i w;
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[j] = (int)pack2(v[2 * j] * scale, v[2 * j + 1] * scale, _Float16());
-    *(v4i*)(a.X + ((int64_t)e * a.N + row) * a.ldx + col) = w;
+    *(v4i*)(X + (int64_t)row * a.ldx + col) = w;
+  }
+  // the row's rest and padding
+  const int left = per - whole;
+  for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < (int64_t)a.N * left * 8; i += stride) {
+    const int row = (int)(i / (8 * left)), col = 8 * whole + (int)(i % (8 * left));
+    const float v = col < a.K ? element<F32>(a.G, e * a.strideE + row * a.strideN + col) : 0.0f;
+    X[(int64_t)row * a.ldx + col] = (uint16_t)pack2(v * scale, 0.0f, _Float16());
   }
 }
 
@@ -142,7 +155,7 @@ constexpr int kSmallLds = 155 * 1024;
 
 struct SmallArgs {
   LoadArgs in;
-  int tall, n, m, np, mp;
+  int tall, n, m, mp;
   int steps;
   uint16_t* out;
   float coeffs[3 * kMaxSteps];
@@ -155,48 +168,54 @@ size_t small_lds(int n, int m) {
 
 __device__ __forceinline__ v4f mfma_h(const v4i& a, const v4i& b, const v4f& c) { return mfma16(a, b, c, _Float16()); }
 
-template <bool F32>
+template <bool F32, int NB>  // NB: np / 32
 __global__ __launch_bounds__(512, 2) void ortho_small_kernel(SmallArgs a) {
   extern __shared__ __align__(16) uint16_t dyn[];
   __shared__ double red[8];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
-  const int e = blockIdx.x, ldx = a.mp + 8, lds = a.np + 8;
+  constexpr int np = 32 * NB, lds = np + 8, kOwn = NB * NB > 8 ? 2 : 1;  // blocks of S a wave owns
+  const int e = blockIdx.x, ldx = a.mp + 8;
   uint16_t* X = dyn;
-  uint16_t* S = dyn + a.np * ldx;
+  uint16_t* S = dyn + np * ldx;
   const int64_t base = e * a.in.strideE;
   const int N = a.in.N, K = a.in.K;
 
-  // the norm, summed in 64 bits in a fixed order, then X0
-  const int per = (K + 7) >> 3, chunks = N * per;
-  double sum = 0.0;
-#pragma unroll 4
-  for (int i = tid; i < chunks; i += 512) {
-    const int row = i / per, col = 8 * (i - row * per);
-    float v[8];
-    load8<F32>(a.in.G, base + row * a.in.strideN + col, K - col, v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum += (double)v[j] * (double)v[j];
-  }
+  // the norm, then X0
+  double sum = squares<F32>(a.in.G, base, a.in.strideN, N, K, 512);
   for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
   if (lane == 0) red[wave] = sum;
-  for (int i = tid; i < (a.np * (ldx + lds)) >> 3; i += 512) ((v4i*)dyn)[i] = (v4i){0, 0, 0, 0};
+  if (a.n < np || a.m < a.mp)
+    for (int i = tid; i < (np * ldx) >> 3; i += 512) ((v4i*)X)[i] = (v4i){0, 0, 0, 0};
   __syncthreads();
   sum = 0.0;
   for (int w = 0; w < 8; ++w) sum += red[w];
   const float scale = (float)(kOne / (sqrt(sum) + (double)a.in.eps));
+  auto put = [&](int row, int col, float v) {
+    X[a.tall ? col * ldx + row : row * ldx + col] = (uint16_t)pack2(v * scale, 0.0f, _Float16());
+  };
+  const int per = K >> 3, rest = K & 7;
 #pragma unroll 4
-  for (int i = tid; i < chunks; i += 512) {
+  for (int i = tid; i < N * per; i += 512) {
     const int row = i / per, col = 8 * (i - row * per);
     float v[8];
-    load8<F32>(a.in.G, base + row * a.in.strideN + col, K - col, v);
+    load8<F32>(a.in.G, base + row * a.in.strideN + col, v);
+    if (a.tall) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (col + j < K)
-        X[a.tall ? (col + j) * ldx + row : row * ldx + col + j] = (uint16_t)pack2(v[j] * scale, 0.0f, _Float16());
+      for (int j = 0; j < 8; ++j) put(row, col + j, v[j]);
+    } else {
+      v4i w;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = (int)pack2(v[2 * j] * scale, v[2 * j + 1] * scale, _Float16());
+      *(v4i*)(X + row * ldx + col) = w;
+    }
+  }
+  for (int i = tid; i < N * rest; i += 512) {
+    const int row = i / rest, col = 8 * per + (i - row * rest);
+    put(row, col, element<F32>(a.in.G, base + row * a.in.strideN + col));
   }
   __syncthreads();
 
-  const int nb = a.np >> 5, mb = a.mp >> 5;
+  const int mb = a.mp >> 5;
   // lane's fragment of 16 rows from r0 on, columns k .. k + 31 of a matrix of row
   // stride ld; and the same of its transpose (rows are columns, k the row)
   auto rows = [&](const uint16_t* M, int ld, int r0, int k) { return *(const v4i*)(M + (r0 + r) * ld + k + 8 * g); };
@@ -205,84 +224,108 @@ __global__ __launch_bounds__(512, 2) void ortho_small_kernel(SmallArgs a) {
     const v2i lo = lds_read_tr(at), hi = lds_read_tr(at + 8 * ld);
     return (v4i){lo.x, lo.y, hi.x, hi.y};
   };
+  // the wave's blocks of S; one without any does block 0 and does not write it
+  int m0[kOwn], n0[kOwn];
+  bool own[kOwn];
+#pragma unroll
+  for (int u = 0; u < kOwn; ++u) {
+    const int id = wave * kOwn + u;
+    own[u] = id < NB * NB;
+    m0[u] = own[u] ? id / NB * 32 : 0;
+    n0[u] = own[u] ? id % NB * 32 : 0;
+  }
+  typedef _Float16 v4h __attribute__((ext_vector_type(4)));
   for (int s = 0; s < a.steps; ++s) {
     const float ca = a.coeffs[3 * s], cb = a.coeffs[3 * s + 1], cc = a.coeffs[3 * s + 2];
-    // S = X X^T, then P = a I + b S + c S S over it: blocks wave, wave + 8
-    for (int pass = 0; pass < 2; ++pass) {
-      v4f acc[2][2][2] = {};
+    v4f acc[kOwn][2][2];
+    auto block = [&](const uint16_t* M, int ld, int k) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int id = wave + 8 * u;
-        if (id >= nb * nb) continue;
-        const int m0 = id / nb * 32, n0 = id % nb * 32;
-        const uint16_t* M = pass ? S : X;
-        const int ld = pass ? lds : ldx, depth = pass ? a.np : a.mp;
-#pragma unroll 2
-        for (int k = 0; k < depth; k += 32) {
-          const v4i f0 = rows(M, ld, m0, k), f1 = rows(M, ld, m0 + 16, k);
-          const v4i h0 = rows(M, ld, n0, k), h1 = rows(M, ld, n0 + 16, k);
-          acc[u][0][0] = mfma_h(h0, f0, acc[u][0][0]);
-          acc[u][0][1] = mfma_h(h1, f0, acc[u][0][1]);
-          acc[u][1][0] = mfma_h(h0, f1, acc[u][1][0]);
-          acc[u][1][1] = mfma_h(h1, f1, acc[u][1][1]);
-        }
+      for (int u = 0; u < kOwn; ++u) {
+        const v4i f0 = rows(M, ld, m0[u], k), f1 = rows(M, ld, m0[u] + 16, k);
+        const v4i h0 = rows(M, ld, n0[u], k), h1 = rows(M, ld, n0[u] + 16, k);
+        acc[u][0][0] = mfma_h(h0, f0, acc[u][0][0]);
+        acc[u][0][1] = mfma_h(h1, f0, acc[u][0][1]);
+        acc[u][1][0] = mfma_h(h0, f1, acc[u][1][0]);
+        acc[u][1][1] = mfma_h(h1, f1, acc[u][1][1]);
       }
-      if (pass) __syncthreads();  // S has been read
+    };
+    auto each = [&](auto f) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int id = wave + 8 * u;
-        if (id >= nb * nb) continue;
+      for (int u = 0; u < kOwn; ++u)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int m = id / nb * 32 + 16 * i + r, n = id % nb * 32 + 16 * j + 4 * g;
-            typedef _Float16 v4h __attribute__((ext_vector_type(4)));
-            v4h* to = (v4h*)(S + m * lds + n);
-            float v[4];
+          for (int j = 0; j < 2; ++j)
+            if (own[u]) f(acc[u][i][j], m0[u] + 16 * i + r, n0[u] + 16 * j + 4 * g);
+    };
+    auto clear = [&]() {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              v[q] = kPerOne * acc[u][i][j][q];
-              if (pass) v[q] = cc * v[q] + cb * (float)(*to)[q] + (m == n + q ? ca * kOne : 0.0f);
-            }
-            *(uint2*)to = make_uint2(pack2(v[0], v[1], _Float16()), pack2(v[2], v[3], _Float16()));
-          }
-      }
-      __syncthreads();
-    }
-    // X <- P X, 32 columns at a time
+      for (int u = 0; u < kOwn; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[u][i >> 1][i & 1] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+    };
+    // S = X X^T
+    clear();
+#pragma unroll 4
+    for (int k = 0; k < a.mp; k += 32) block(X, ldx, k);
+    each([&](v4f& v, int m, int n) {
+      v *= kPerOne;
+      *(uint2*)(S + m * lds + n) = make_uint2(pack2(v[0], v[1], _Float16()), pack2(v[2], v[3], _Float16()));
+    });
+    __syncthreads();
+    // P = a I + b S + c S S, over S once everyone has read it
+    clear();
+#pragma unroll
+    for (int k = 0; k < np; k += 32) block(S, lds, k);
+    each([&](v4f& v, int m, int n) {
+      const v4h was = *(const v4h*)(S + m * lds + n);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = cc * kPerOne * v[q] + cb * (float)was[q] + (m == n + q ? ca * kOne : 0.0f);
+    });
+    __syncthreads();
+    each([&](v4f& v, int m, int n) {
+      *(uint2*)(S + m * lds + n) = make_uint2(pack2(v[0], v[1], _Float16()), pack2(v[2], v[3], _Float16()));
+    });
+    __syncthreads();
+    // X <- P X, 32 columns at a time; after the last step the result's bf16
+    const bool last = s + 1 == a.steps;
     for (int c = wave; c < mb; c += 8) {
-      v4f acc[kSmallN / 16][2] = {};
-      for (int k = 0; k < a.np; k += 32) {
+      v4f x[2 * NB][2] = {};
+#pragma unroll
+      for (int k = 0; k < np; k += 32) {
         const v4i h0 = cols(X, ldx, 32 * c, k), h1 = cols(X, ldx, 32 * c + 16, k);
 #pragma unroll
-        for (int i = 0; i < kSmallN / 16; ++i) {
-          if (16 * i >= a.np) break;
+        for (int i = 0; i < 2 * NB; ++i) {
           const v4i f = rows(S, lds, 16 * i, k);
-          acc[i][0] = mfma_h(h0, f, acc[i][0]);
-          acc[i][1] = mfma_h(h1, f, acc[i][1]);
+          x[i][0] = mfma_h(h0, f, x[i][0]);
+          x[i][1] = mfma_h(h1, f, x[i][1]);
         }
       }
 #pragma unroll
-      for (int i = 0; i < kSmallN / 16; ++i) {
-        if (16 * i >= a.np) break;
+      for (int i = 0; i < 2 * NB; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int m = 16 * i + r, n = 32 * c + 16 * j + 4 * g;
-          if (s + 1 < a.steps) {
-            const v4f v = acc[i][j] * kPerOne;
-            *(uint2*)(X + m * ldx + n) = make_uint2(pack2(v[0], v[1], _Float16()), pack2(v[2], v[3], _Float16()));
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (m < a.n && n + q < a.m)
-                a.out[(int64_t)e * N * K + (a.tall ? (int64_t)(n + q) * K + m : (int64_t)m * K + n + q)] =
-                    (uint16_t)pack2(acc[i][j][q] * (kPerOne * kPerOne), 0.0f, __bf16());
-          }
+          const v4f v = x[i][j] * (last ? kPerOne * kPerOne : kPerOne);
+          *(uint2*)(X + (16 * i + r) * ldx + 32 * c + 16 * j + 4 * g) =
+              last ? make_uint2(pack2(v[0], v[1], __bf16()), pack2(v[2], v[3], __bf16()))
+                   : make_uint2(pack2(v[0], v[1], _Float16()), pack2(v[2], v[3], _Float16()));
         }
-      }
     }
     __syncthreads();
+  }
+  // out, rows as the caller has them
+  uint16_t* out = a.out + (int64_t)e * N * K;
+  auto at = [&](int row, int col) { return X[a.tall ? col * ldx + row : row * ldx + col]; };
+  for (int i = tid; i < N * per; i += 512) {
+    const int row = i / per, col = 8 * (i - row * per);
+    uint16_t u[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = at(row, col + j);
+    __builtin_memcpy(out + row * K + col, u, 16);
+  }
+  for (int i = tid; i < N * rest; i += 512) {
+    const int row = i / rest, col = 8 * per + (i - row * rest);
+    out[row * K + col] = at(row, col);
   }
 }
 
@@ -369,32 +412,69 @@ struct EpiNext {
   }
 };
 
-template <int B, int WM, int WN, bool TA, bool TB, bool SYM, class Epi>
-int launch_tiles(GemmArgs g, const typename Epi::Args& e, hipStream_t st) {
-  g.tilesM = (g.M + B - 1) / B;
-  g.tilesN = (g.N + B - 1) / B;
+// `count` tiles of edge B from the `first` of all on (quarters: of edge 2 B, cut in four)
+template <int B, int WM, int WN, int DEEP, bool TA, bool TB, bool SYM, class Epi>
+int launch_tiles(GemmArgs g, const typename Epi::Args& e, int64_t first, int64_t count, bool quarters, hipStream_t st) {
+  const int edge = quarters ? 2 * B : B;
+  g.tilesM = (g.M + edge - 1) / edge;
+  g.tilesN = (g.N + edge - 1) / edge;
   g.tiles = SYM ? g.tilesM * (g.tilesM + 1) / 2 : g.tilesM * g.tilesN;
-  const int64_t grid = (int64_t)g.tiles * g.batch;
+  g.first = (int)first;
+  g.quarters = quarters;
+  const int64_t grid = quarters ? 4 * count : count;
   if (grid > 0x7FFFFFFF / 512) return MXW_ERR_DIM;
-  hipLaunchKernelGGL((gemm16_kernel<_Float16, B, B, WM, WN, TA, TB, SYM, Epi>), dim3((unsigned)grid),
+  hipLaunchKernelGGL((gemm16_kernel<_Float16, B, B, WM, WN, DEEP, TA, TB, SYM, Epi>), dim3((unsigned)grid),
                      dim3(WM * WN * 64), 0, st, g, e);
   return MXW_OK;
 }
 
+// The tile edge with the least estimated time.  In hundredths of a us, measured
+// with whole orthogonalize calls forced to one edge (1 to 16 matrices, 256 to
+// 7,168 wide): a step of 64 k costs 145 a round of 256-tiles (one a CU); 43 a
+// round of 128-tiles while they leave a CU one, else 80 (two a CU); 39 a round of
+// 64-tiles, two a CU, else 53; and a launch 1,000, 700 or 350 besides.  So 64
+// wins for one 1408 x 2048 matrix (215 us against 275 with 128 and 571 with 256),
+// 128 for four (474 against 643 and 606), 256 for one 4096 x 7168 (2,054 against
+// 2,359 with 128).  Last, 256-tiles for the whole rounds and quarters of them for
+// the rest, where that would leave most CUs idle.
 template <bool TA, bool TB, bool SYM, class Epi>
 int launch_product(GemmArgs g, const typename Epi::Args& e, int cus, hipStream_t st) {
   auto tiles = [&](int b) {
     const int64_t tm = (g.M + b - 1) / b, tn = (g.N + b - 1) / b;
     return (SYM ? tm * (tm + 1) / 2 : tm * tn) * g.batch;
   };
+  auto rounds = [](int64_t n, int64_t slots) { return (n + slots - 1) / slots; };
   g.splits = 1;
   g.ksplit = (g.K + kGemmStep - 1) / kGemmStep * kGemmStep;
-  const int64_t big = (tiles(256) + cus - 1) / cus * 10, small = (tiles(128) + 2 * cus - 1) / (2 * cus) * 7;
-  if (big <= small) return launch_tiles<256, 2, 4, TA, TB, SYM, Epi>(g, e, st);
-  return launch_tiles<128, 2, 2, TA, TB, SYM, Epi>(g, e, st);
+  const int64_t s = g.ksplit / kGemmStep, t256 = tiles(256), t128 = tiles(128), t64 = tiles(64);
+  auto cost128 = [&](int64_t n) { return 700 + s * (n <= cus ? 43 : 80 * rounds(n, 2 * cus)); };
+  const int64_t whole = t256 / cus * cus, rest = t256 - whole;
+  const int64_t c256 = 1000 + s * 145 * rounds(t256, cus), c128 = cost128(t128);
+  const int64_t c64 = 350 + s * (t64 <= 2 * cus ? 39 : 53 * rounds(t64, 2 * cus));
+  const int64_t both = whole && rest ? 1000 + s * 145 * (whole / cus) + cost128(4 * rest) : INT64_MAX;
+  if (c64 <= c128 && c64 <= c256 && c64 <= both) return launch_tiles<64, 2, 2, 5, TA, TB, SYM, Epi>(g, e, 0, t64, false, st);
+  if (c128 <= c256 && c128 <= both) return launch_tiles<128, 2, 2, 0, TA, TB, SYM, Epi>(g, e, 0, t128, false, st);
+  if (c256 <= both) return launch_tiles<256, 2, 4, 0, TA, TB, SYM, Epi>(g, e, 0, t256, false, st);
+  const int rc = launch_tiles<256, 2, 4, 0, TA, TB, SYM, Epi>(g, e, 0, whole, false, st);
+  return rc ? rc : launch_tiles<128, 2, 2, 0, TA, TB, SYM, Epi>(g, e, whole, rest, true, st);
 }
 
 // ---- host -------------------------------------------------------------------
+
+template <int NB>
+void launch_small_of(bool f32, const SmallArgs& a, int E, unsigned bytes, hipStream_t st) {
+  if (f32) hipLaunchKernelGGL((ortho_small_kernel<true, NB>), dim3((unsigned)E), dim3(512), bytes, st, a);
+  else hipLaunchKernelGGL((ortho_small_kernel<false, NB>), dim3((unsigned)E), dim3(512), bytes, st, a);
+}
+
+void launch_small(bool f32, const SmallArgs& a, int E, unsigned bytes, hipStream_t st) {
+  switch ((a.n + 31) >> 5) {
+    case 1: return launch_small_of<1>(f32, a, E, bytes, st);
+    case 2: return launch_small_of<2>(f32, a, E, bytes, st);
+    case 3: return launch_small_of<3>(f32, a, E, bytes, st);
+    default: return launch_small_of<4>(f32, a, E, bytes, st);
+  }
+}
 
 struct OrthoPlan {
   int n, m, ldx, lds;
@@ -477,14 +557,12 @@ int mxw_orthogonalize(const void* G, int type, int64_t expert_stride, int64_t ro
     sa.tall = p.tall;
     sa.n = p.n;
     sa.m = p.m;
-    sa.np = (p.n + 31) & ~31;
     sa.mp = (p.m + 31) & ~31;
     sa.steps = steps;
     sa.out = out;
     for (int i = 0; i < 3 * steps; ++i) sa.coeffs[i] = coeffs[i];
     const unsigned bytes = (unsigned)small_lds(p.n, p.m);
-    if (f32) hipLaunchKernelGGL((ortho_small_kernel<true>), dim3((unsigned)E), dim3(512), bytes, st, sa);
-    else hipLaunchKernelGGL((ortho_small_kernel<false>), dim3((unsigned)E), dim3(512), bytes, st, sa);
+    launch_small(f32, sa, E, bytes, st);
     return hipGetLastError() == hipSuccess ? MXW_OK : MXW_ERR_LAUNCH;
   }
   int64_t blocks = ((int64_t)N * (p.ldx / 8) + 1023) / 1024;  // about 4 chunks a thread

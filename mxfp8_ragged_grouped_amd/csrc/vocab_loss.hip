@@ -374,7 +374,7 @@ int launch(GemmArgs g, const typename Epi::Args& e, hipStream_t st) {
   g.tiles = g.tilesM * g.tilesN;
   const int64_t grid = (int64_t)g.tilesM * g.tilesN * g.splits;
   if (grid > 0x7FFFFFFF / 512) return MXW_ERR_DIM;
-  hipLaunchKernelGGL((gemm16_kernel<__bf16, BM, 256, WM, WN, TA, TB, false, Epi>), dim3((unsigned)grid),
+  hipLaunchKernelGGL((gemm16_kernel<__bf16, BM, 256, WM, WN, 0, TA, TB, false, Epi>), dim3((unsigned)grid),
                      dim3(WM * WN * 64), 0, st, g, e);
   return MXW_OK;
 }
