@@ -450,30 +450,27 @@ __device__ __forceinline__ void stage_part(const TileAt& at, const v4f (&acc)[MI
   }
 }
 
-// the staged tile to rows of dst (row stride ld, which is a multiple of 8, as
-// is ncols; dst 16-byte aligned): rows below nrows, columns below ncols
+// the staged tile to rows of dst: rows below nrows, columns below ncols.  Rows may
+// start at any element: 16-byte stores need no alignment beyond it.
 template <int BM, int BN, int WAVES>
 __device__ __forceinline__ void store_rows(const TileAt& at, const uint8_t* lds, uint16_t* dst, int64_t ld, int nrows,
                                            int ncols) {
   constexpr int kChunks = BN / 8;
   const int tid = at.wave * 64 + at.lane;
-#pragma unroll
+#pragma unroll 4
   for (int i = tid; i < BM * kChunks; i += WAVES * 64) {
     const int r = i / kChunks, c = i % kChunks;
     const int m = at.m0 + r, n = at.n0 + 8 * c;
-    if (m < nrows && n < ncols) *(v4i*)(dst + m * ld + n) = *(const v4i*)(lds + tile_at<BN>(r, c));
-  }
-}
-
-// the same without any alignment, value by value
-template <int BM, int BN, int WAVES>
-__device__ __forceinline__ void store_rows_any(const TileAt& at, const uint8_t* lds, uint16_t* dst, int64_t ld,
-                                               int nrows, int ncols) {
-  const int tid = at.wave * 64 + at.lane;
-  for (int i = tid; i < BM * BN; i += WAVES * 64) {
-    const int r = i / BN, c = i % BN;
-    const int m = at.m0 + r, n = at.n0 + c;
-    if (m < nrows && n < ncols) dst[m * ld + n] = *(const uint16_t*)(lds + tile_at<BN>(r, c >> 3) + 2 * (c & 7));
+    if (m >= nrows || n >= ncols) continue;
+    const v4i v = *(const v4i*)(lds + tile_at<BN>(r, c));
+    uint16_t* to = dst + m * ld + n;
+    if (n + 8 <= ncols) {
+      __builtin_memcpy(to, &v, 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (n + e < ncols) to[e] = (uint16_t)((uint32_t)v[e >> 1] >> (16 * (e & 1)));
+    }
   }
 }
 

@@ -400,15 +400,11 @@ struct EpiNext {
     if constexpr (LAST) {
       stage_part<__bf16, BN>(at, acc, lds, scale);
       __syncthreads();
-      if ((a.ld & 7) == 0 && ((uintptr_t)a.X & 15) == 0)
-        store_rows<BM, BN, WM * WN>(at, lds, X, a.ld, a.rows, a.cols);
-      else
-        store_rows_any<BM, BN, WM * WN>(at, lds, X, a.ld, a.rows, a.cols);
     } else {
       stage_part<_Float16, BN>(at, acc, lds, scale);
       __syncthreads();
-      store_rows<BM, BN, WM * WN>(at, lds, X, a.ld, a.rows, a.cols);
     }
+    store_rows<BM, BN, WM * WN>(at, lds, X, a.ld, a.rows, a.cols);
   }
 };
 

@@ -9,8 +9,8 @@
 // mean); tokens whose target is ignore_index have loss 0 and g = 0.
 //
 // The logits are never written.  A first product walks the whole vocabulary and
-// leaves, per 256 x 256 tile and token, the running maximum and sum of
-// exponentials (8 bytes for 256 logits); they are joined in a fixed order.
+// leaves, per tile and token, the maximum and sum of exponentials of the tile's
+// 256 (few tokens: 64) logits, 8 bytes for them; they are joined in a fixed order.
 // Then the vocabulary is walked in pieces, each small enough that g of the
 // piece (bf16, unscaled: its entries lie in [-1, 1]) stays in the memory-side
 // cache: one product makes the logits again and turns them into g in its
@@ -34,7 +34,6 @@ namespace {
 
 using namespace mxw;
 
-constexpr int kTileV = 256;                        // vocabulary columns a tile
 constexpr int64_t kPieceBytes = 256LL << 20;       // g of one piece
 constexpr int kMaxTokens = 128 * 1024;
 constexpr int kMaxVocab = 1 << 20;
@@ -118,7 +117,7 @@ struct EpiStats {
       float m = sh[0][r].x, s = sh[0][r].y;
 #pragma unroll
       for (int w = 1; w < WN; ++w) join(m, s, sh[w][r].x, sh[w][r].y);
-      if (at.m0 + r < p.M) a.part[(int64_t)((a.v0 + at.n0) / kTileV) * p.M + at.m0 + r] = make_float2(m, s);
+      if (at.m0 + r < p.M) a.part[(int64_t)((a.v0 + at.n0) / BN) * p.M + at.m0 + r] = make_float2(m, s);
     }
   }
 };
@@ -242,6 +241,7 @@ __global__ __launch_bounds__(256) void dx_kernel(const float* sum, int64_t strid
   for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < (int64_t)T * per; i += (int64_t)gridDim.x * 256) {
     const int t = (int)(i / per), c = 4 * (int)(i % per);
     float4 v = *(const float4*)(sum + (int64_t)t * ld + c);
+#pragma unroll 8
     for (int k = 1; k < splits; ++k) {
       const float4 w = *(const float4*)(sum + k * stride + (int64_t)t * ld + c);
       v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
@@ -275,25 +275,27 @@ struct EpiWeight {
       for (int e = 0; e < 4; ++e) v[e] *= s;
     });
     __syncthreads();
-    if ((a.H & 7) == 0 && ((uintptr_t)a.dw & 15) == 0)
-      store_rows<BM, BN, WM * WN>(at, lds, a.dw, a.H, a.rows, a.H);
-    else
-      store_rows_any<BM, BN, WM * WN>(at, lds, a.dw, a.H, a.rows, a.H);
+    store_rows<BM, BN, WM * WN>(at, lds, a.dw, a.H, a.rows, a.H);
   }
 };
 
-// rows copied to rows of ld (a multiple of 64) elements, zeros after H
+// rows copied to rows of ld (a multiple of 64) elements, zeros after H; rows may
+// start at any element
 __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* src, int64_t lds, int rows, int H, uint16_t* dst,
                                                        int ld) {
-  const int per = ld >> 3;
-  for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < (int64_t)rows * per; i += (int64_t)gridDim.x * 256) {
-    const int r = (int)(i / per), c = 8 * (int)(i % per);
-    const uint16_t* from = src + r * lds + c;
+  const int per = ld >> 3, whole = H >> 3;
+  const int64_t stride = (int64_t)gridDim.x * 256, tid = blockIdx.x * 256 + threadIdx.x;
+#pragma unroll 4
+  for (int64_t i = tid; i < (int64_t)rows * whole; i += stride) {
+    const int r = (int)(i / whole), c = 8 * (int)(i % whole);
     v4i w;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[j] = (c + 2 * j < H ? from[2 * j] : 0) | (uint32_t)(c + 2 * j + 1 < H ? from[2 * j + 1] : 0) << 16;
+    __builtin_memcpy(&w, src + r * lds + c, 16);
     *(v4i*)(dst + (int64_t)r * ld + c) = w;
+  }
+  const int left = 8 * (per - whole);
+  for (int64_t i = tid; i < (int64_t)rows * left; i += stride) {
+    const int r = (int)(i / left), c = 8 * whole + (int)(i % left);
+    dst[(int64_t)r * ld + c] = c < H ? src[r * lds + c] : 0;
   }
 }
 
@@ -302,12 +304,10 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* src, int6
 struct LossPlan {
   bool packed;   // x and w are copied to padded rows
   int ld;        // H rounded up to 64
-  int tilesV, piece, splits, bm;
+  int bm, bn;    // tile of the products whose M axis is the tokens
+  int tilesV, piece, splits;
   size_t part, hit, lse, rows, scale, xp, wp, g, sum, bytes;
 };
-
-// token rows a tile, for products whose M axis is the tokens
-int token_tile(int T) { return T <= 32 ? 32 : T <= 128 ? 128 : 256; }
 
 bool aligned(const void* x, int64_t ldx, const void* w, int64_t ldw, int H) {
   return (H & 63) == 0 && (ldx & 7) == 0 && (ldw & 7) == 0 && (((uintptr_t)x | (uintptr_t)w) & 15) == 0;
@@ -317,31 +317,38 @@ LossPlan plan_of(bool direct, int T, int H, int V, bool gx, bool gw, int cus) {
   LossPlan p = {};
   p.packed = !direct;
   p.ld = (H + 63) & ~63;
-  p.tilesV = (V + kTileV - 1) / kTileV;
-  p.bm = token_tile(T);
+  auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
+  // Few tokens: narrow tiles in deep rings, bound by reading w (one token against
+  // 32,000 words: 43 us with 256 columns a tile, half the CUs without any).  Else
+  // 256 rows, or 128 where fewer rounds of those finish sooner (a step of a round
+  // costs 1.45 us against 0.85).
+  p.bm = 32;
+  p.bn = 64;
+  if (T > 32) {
+    p.bn = 256;
+    p.bm = T <= 128 || 85 * up(up(T, 128) * up(V, 256), cus) < 145 * up(up(T, 256) * up(V, 256), cus) ? 128 : 256;
+  }
+  p.tilesV = (V + p.bn - 1) / p.bn;
   const bool grads = gx || gw;
   // a piece of the vocabulary: all of it unless g (or the padded copy of its
   // weights) gets too large
   int64_t most = kPieceBytes / (2LL * (grads ? T : 1));
   if (p.packed && most > kPieceBytes / (2LL * p.ld)) most = kPieceBytes / (2LL * p.ld);
-  if (most < kTileV) most = kTileV;
-  int64_t pieces = (V + most - 1) / most;
-  p.piece = (int)(((V + pieces - 1) / pieces + kTileV - 1) / kTileV * kTileV);
+  if (most < 256) most = 256;
+  p.piece = (int)(up(up(V, up(V, most)), 256) * 256);
   // dx: splits of a piece's vocabulary, so that the tiles fill the device in
-  // whole rounds; a split costs its partial sums' traffic (about one step of
-  // 64 columns in time)
+  // whole rounds; a split's partial sums are written and read once, at about
+  // 7 MB in the time of a step of 64 columns
   p.splits = 1;
   if (gx) {
-    const int64_t tiles = (int64_t)((T + p.bm - 1) / p.bm) * ((p.ld + 255) / 256);
-    const int64_t slots = p.bm == 32 ? 2 * cus : cus;
-    const int width = V < p.piece ? V : p.piece, steps = (width + kGemmStep - 1) / kGemmStep;
+    const int64_t tiles = up(T, p.bm) * up(p.ld, p.bn), slots = p.bm == 32 ? 2 * cus : cus;
+    const int64_t steps = up(V < p.piece ? V : p.piece, kGemmStep), sums = 8LL * T * p.ld;
     int64_t best = INT64_MAX;
-    for (int s = 1; s <= 64 && s * 4 <= steps + 3; ++s) {
-      const int64_t rounds = (tiles * s + slots - 1) / slots;
-      const int64_t cost = rounds * ((steps + s - 1) / s + 4) + s;
+    for (int n = 1; n <= 64 && n * 4 <= steps + 3; ++n) {
+      const int64_t cost = up(tiles * n, slots) * (up(steps, n) + 8) * 1000 + n * sums / 7000;
       if (cost < best) {
         best = cost;
-        p.splits = s;
+        p.splits = n;
       }
     }
   }
@@ -366,15 +373,15 @@ LossPlan plan_of(bool direct, int T, int H, int V, bool gx, bool gw, int cus) {
   return p;
 }
 
-template <int BM, int WM, int WN, bool TA, bool TB, class Epi>
+template <int BM, int BN, int WM, int WN, int DEEP, bool TA, bool TB, class Epi>
 int launch(GemmArgs g, const typename Epi::Args& e, hipStream_t st) {
   g.batch = 1;
   g.tilesM = (g.M + BM - 1) / BM;
-  g.tilesN = (g.N + 255) / 256;
+  g.tilesN = (g.N + BN - 1) / BN;
   g.tiles = g.tilesM * g.tilesN;
   const int64_t grid = (int64_t)g.tilesM * g.tilesN * g.splits;
   if (grid > 0x7FFFFFFF / 512) return MXW_ERR_DIM;
-  hipLaunchKernelGGL((gemm16_kernel<__bf16, BM, 256, WM, WN, 0, TA, TB, false, Epi>), dim3((unsigned)grid),
+  hipLaunchKernelGGL((gemm16_kernel<__bf16, BM, BN, WM, WN, DEEP, TA, TB, false, Epi>), dim3((unsigned)grid),
                      dim3(WM * WN * 64), 0, st, g, e);
   return MXW_OK;
 }
@@ -382,9 +389,9 @@ int launch(GemmArgs g, const typename Epi::Args& e, hipStream_t st) {
 // products whose M axis is the tokens
 template <bool TB, class Epi>
 int launch_tokens(int bm, const GemmArgs& g, const typename Epi::Args& e, hipStream_t st) {
-  if (bm == 32) return launch<32, 1, 8, false, TB, Epi>(g, e, st);
-  if (bm == 128) return launch<128, 2, 4, false, TB, Epi>(g, e, st);
-  return launch<256, 2, 4, false, TB, Epi>(g, e, st);
+  if (bm == 32) return launch<32, 64, 1, 4, 6, false, TB, Epi>(g, e, st);
+  if (bm == 128) return launch<128, 256, 2, 4, 0, false, TB, Epi>(g, e, st);
+  return launch<256, 256, 2, 4, 0, false, TB, Epi>(g, e, st);
 }
 
 int check_loss(int T, int H, int V) {
@@ -392,7 +399,7 @@ int check_loss(int T, int H, int V) {
 }
 
 unsigned copy_blocks(int64_t chunks) {
-  const int64_t b = (chunks + 1023) / 1024;
+  const int64_t b = (chunks + 255) / 256;
   return (unsigned)(b < 1 ? 1 : b > 8192 ? 8192 : b);
 }
 
@@ -511,7 +518,7 @@ int mxw_vocab_loss(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ld
         g.splits = 1;
         g.ksplit = (T + kGemmStep - 1) / kGemmStep * kGemmStep;
         const EpiWeight::Args e = {dw + (int64_t)v0 * H, scale, width, H};
-        rc = launch<256, 2, 4, true, true, EpiWeight>(g, e, st);
+        rc = launch<256, 256, 2, 4, 0, true, true, EpiWeight>(g, e, st);
         if (rc) return rc;
       }
     }
