@@ -20,10 +20,6 @@
 //           many: items (expert, 64 columns) leave FP32 partial outputs per
 //           (token, expert), which a last kernel adds in the order of the choices
 //
-// Where there are many items a wave takes whole ones and never meets another: no
-// barrier and no reduction stands between its loads, which it keeps 16 KiB
-// ahead.  Where there are few the waves of a workgroup split an item's H.
-//
 // The products run on the bf16 MFMA 16 x 16 x 32 with weight rows as the first
 // operand and up to 16 of the expert's tokens as the second: with few tokens the
 // matrix unit is idle most of the time, and its work is free next to the loads.
@@ -226,7 +222,8 @@ __global__ __launch_bounds__(kWaves * 64) void moe_router_kernel(MoeArgs a) {
 
 // The routing of one token by one wave: lane l holds experts l, l + 64, ...
 // Writes the token's choices and weights.  logits: [parts][T][E].
-__device__ __forceinline__ void route_token(const MoeArgs& a, const float* logits, int parts, int t, int32_t* ids,
+template <class Id>
+__device__ __forceinline__ void route_token(const MoeArgs& a, const float* logits, int parts, int t, Id* ids,
                                             float* weights) {
   const int lane = threadIdx.x & 63;
   if (a.active && !a.active[t]) {
@@ -285,7 +282,7 @@ __device__ __forceinline__ void route_token(const MoeArgs& a, const float* logit
   const float norm = a.normalize ? wave_sum(p) : sum;
   p = broken ? NAN : p / norm * a.scale;
   if (lane < a.k) {
-    ids[lane] = mine;
+    ids[lane] = (Id)mine;
     weights[lane] = p;
   }
 }
@@ -298,11 +295,11 @@ __global__ __launch_bounds__(256) void moe_route_kernel(MoeArgs a) {
 // ---- gate/up ----------------------------------------------------------------
 
 struct Routing {
-  int32_t ids[kMaxTokens * kMaxChoices];
   float weights[kMaxTokens * kMaxChoices];
   uint32_t mask[MXW_MAX_EXPERTS][2];   // by expert: its tokens
-  int32_t start[MXW_MAX_EXPERTS];      // by expert: its first row of h
-  int32_t expert[MXW_MAX_EXPERTS];     // the chosen ones, ascending
+  int16_t ids[kMaxTokens * kMaxChoices];
+  int16_t start[MXW_MAX_EXPERTS];      // by expert: its first row of h
+  int16_t expert[MXW_MAX_EXPERTS];     // the chosen ones, ascending
   int32_t chosen[4], pairs[4];
 };
 
@@ -335,7 +332,7 @@ __device__ __forceinline__ int make_routing(const MoeArgs& a, Routing& rt, float
     for (int i = tid; i < n; i += WAVES * 64) {
       const int id = a.ids[i];
       const bool in = id >= 0 && id < a.E && !(a.active && !a.active[i / a.k]);
-      rt.ids[i] = in ? id : -1;
+      rt.ids[i] = (int16_t)(in ? id : -1);
       rt.weights[i] = in ? a.weights[i] : 0.0f;
     }
   }
@@ -372,8 +369,8 @@ __device__ __forceinline__ int make_routing(const MoeArgs& a, Routing& rt, float
       rank += rt.chosen[w];
       before += rt.pairs[w];
     }
-    rt.expert[rank] = tid;
-    rt.start[tid] = before;
+    rt.expert[rank] = (int16_t)tid;
+    rt.start[tid] = (int16_t)before;
   }
   __syncthreads();
   const int count = rt.chosen[0] + rt.chosen[1] + rt.chosen[2] + rt.chosen[3];
@@ -427,67 +424,11 @@ __device__ __forceinline__ uint16_t hidden(float g, float u, float w) {
   return (uint16_t)pack2(g / (1.0f + __builtin_amdgcn_exp2f(-g * kLog2e)) * u * w, 0.0f, __bf16());
 }
 
-// the lane's weight rows of Wg (even g) and Wu (odd g): rows i0 + 16 (g / 2) + l % 16
-template <int G>
-__device__ __forceinline__ void gate_rows(const MoeArgs& a, int e, int i0, const uint8_t* (&row)[G],
-                                          const uint8_t* (&srow)[G]) {
-  const int r = threadIdx.x & 15, blocks = a.H >> 5;
-#pragma unroll
-  for (int g = 0; g < G; ++g) {
-    int i = i0 + 16 * (g >> 1) + r;
-    if (i >= a.I) i = a.I - 1;  // past the last rows: computed, not stored
-    const int64_t at = (int64_t)e * 2 * a.I + (g & 1) * a.I + i;
-    row[g] = a.wgu + at * a.H;
-    srow[g] = a.sgu + at * blocks;
-  }
-}
-
-// few items: (expert, 16 rows of Wg and of Wu), H split over the 8 waves
-template <From FROM>
-__global__ __launch_bounds__(kWaves * 64, 4) void moe_gate_split_kernel(MoeArgs a) {
-  __shared__ Routing rt;
-  __shared__ float part[kWaves][2][256];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int count = make_routing<FROM, kWaves>(a, rt, &part[0][0][0]);
-  if (FROM == kRouter) __syncthreads();  // `part` was its scratch
-  const int tiles = (a.I + 15) / 16, blocks = a.H >> 5;
-  const int r = lane & 15, b = lane >> 4;
-  for (int item = blockIdx.x; item < count * tiles; item += gridDim.x) {
-    const int e = rt.expert[item / tiles], i0 = item % tiles * 16;
-    const uint64_t mask = rt.mask[e][0] | (uint64_t)rt.mask[e][1] << 32;
-    const int ntok = __popcll(mask);
-    const uint8_t *row[2], *srow[2];
-    gate_rows<2>(a, e, i0, row, srow);
-    for (int g0 = 0; g0 < ntok; g0 += 16) {
-      const uint16_t* xt = a.x + nth_token(mask, g0 + r < ntok ? g0 + r : g0) * a.ldx;
-      v4f acc[2] = {};
-      stream<2, 2>(row, srow, xt, blocks, wave, kWaves, (blocks + 3) >> 2, acc);
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) part[wave][g][(4 * b + i) * 16 + r] = acc[g][i];  // [row][token]
-      __syncthreads();
-      if (tid < 256) {
-        const int tok = g0 + (tid >> 4), rr = tid & 15, at = rr * 16 + (tid >> 4);
-        float gate = 0.0f, up = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-          gate += part[w][0][at];
-          up += part[w][1][at];
-        }
-        if (tok < ntok && i0 + rr < a.I)
-          a.h[(int64_t)(rt.start[e] + tok) * a.I + i0 + rr] =
-              hidden(gate, up, share_of(a, rt, nth_token(mask, tok), e));
-      }
-      __syncthreads();
-    }
-  }
-}
-
 // ---- streaming through LDS ---------------------------------------------------
 
-// Loads of 16 and 4 bytes a lane straight to LDS (lane l's bytes at lds + 16 l, or
-// 4 l): from a 64-bit address, from a 64-bit base and a 32-bit offset.
+// Loads straight to LDS: 16 bytes a lane from a 64-bit address, to lds + 16 l; a
+// dword, or a byte, a lane from a 64-bit base and a 32-bit offset, to the dword at
+// lds + 4 l.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void global_lds16(const void* from, uint32_t lds) {
@@ -508,9 +449,18 @@ __device__ __forceinline__ void global_lds4(const void* base, uint32_t off, uint
       : "s"(lds), "v"(off), "s"(base)
       : "memory", "m0");
 }
+__device__ __forceinline__ void global_lds1(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_ubyte %1, %2"
+      :
+      : "s"(lds), "v"(off), "s"(base)
+      : "memory", "m0");
+}
 #pragma clang diagnostic pop
 
-constexpr int kRing = 66 * 1024;  // LDS of a workgroup's ring: two workgroups a CU
+constexpr int kRing = 68 * 1024;  // LDS of a workgroup's ring: two workgroups a CU, the routing included
 
 // Weight rows of a workgroup of 4 waves: group g of wave w is 16 rows, the first 8
 // from `first` on, the others from `second` on, `apart` rows after group g - 1's.
@@ -519,7 +469,7 @@ struct Rows {
   int valid_first, valid_second;    // rows there (the rest reads as zeros)
   const uint8_t *sfirst, *ssecond;  // their scales
   int apart;
-  int C;                            // row length, a multiple of 128
+  int C;                            // row length, a multiple of 32
 };
 
 // acc[g][n] = the wave's group g of weight rows times token group n (16 tokens,
@@ -528,18 +478,22 @@ struct Rows {
 // rows to the step's slot of the ring, D - 1 steps ahead; every load takes whole
 // cache lines (read straight into the MFMA's operand layout, 16 lanes would touch
 // 16 lines, which made the vector memory path the bound: 3.0 TB/s at 8 of 32
-// experts of the 671B shape).  One barrier a step.
-template <int G, int N>
+// experts of the 671B shape).  One barrier a step.  WORDS: C is a multiple of 128, so
+// a row's 4 scales of a step are one aligned dword; else they come byte by byte
+// (G - 1 more loads a step: 15% more time where both are possible).
+template <int G, int N, bool WORDS>
 __device__ __forceinline__ void stream_rows(const Rows& w, const uint16_t* src, int64_t ld, const int32_t* token,
                                             int ntok, uint8_t* ring, v4f (&acc)[G][N]) {
-  constexpr int kCodes = 4 * G * 2048, kTokens = N * 4096, kScales = 4 * 256;
+  constexpr int kScaleLoads = WORDS ? 1 : G;
+  constexpr int kCodes = 4 * G * 2048, kTokens = N * 4096, kScales = 4 * kScaleLoads * 256;
   constexpr int kSlot = kCodes + kTokens + kScales;
   constexpr int D = kRing / kSlot < 6 ? kRing / kSlot : 6;
-  constexpr int kLoads = 2 * G + N + 1;  // a wave's loads a step
+  constexpr int kLoads = 2 * G + N + kScaleLoads;  // a wave's loads a step
+  static_assert(!WORDS || 16 * G <= 64, "a lane a row");
   static_assert(D >= 2, "two slots");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, b = lane >> 4;
-  const int steps = w.C >> 7, blocks = w.C >> 5;
+  const int blocks = w.C >> 5, steps = (blocks + 3) >> 2;
   const uint32_t lds0 = (uint32_t)(uintptr_t)ring;
 
   // codes: 8 rows of 128 bytes a load, chunk c of row i at c ^ (i / 2) % 8
@@ -549,21 +503,24 @@ __device__ __forceinline__ void stream_rows(const Rows& w, const uint16_t* src, 
     const int i = 8 * h + (lane >> 3);
     vo[h] = (uint32_t)((wave * G * w.apart + (lane >> 3)) * w.C + (((lane & 7) ^ ((i >> 1) & 7)) << 4));
   }
-  // scales: lane l brings the step's 4 bytes of row l % 16 of group l / 16
-  uint32_t so;
-  {
-    const int g = (lane >> 4) % G, h = (lane >> 3) & 1;
-    int row = (wave * G + g) * w.apart + (lane & 7);
-    const int last = (h ? w.valid_second : w.valid_first) - 1;
+  // scales: lane l brings the step's 4 of row l % 16 of group l / 16, or the one of
+  // block l % 4 of row l / 4
+  uint32_t so[kScaleLoads];
+#pragma unroll
+  for (int g = 0; g < kScaleLoads; ++g) {
+    const int i = WORDS ? lane & 15 : lane >> 2, group = WORDS ? (lane >> 4) % G : g;
+    const int h = i >> 3, last = (h ? w.valid_second : w.valid_first) - 1;
+    int row = (wave * G + group) * w.apart + (i & 7);
     if (row > last) row = last > 0 ? last : 0;
-    so = (uint32_t)((h ? (uint32_t)(w.ssecond - w.sfirst) : 0u) + (uint32_t)row * (uint32_t)blocks);
+    so[g] = (uint32_t)((h ? (uint32_t)(w.ssecond - w.sfirst) : 0u) + (uint32_t)row * (uint32_t)blocks);
   }
   // tokens: 4 rows of 256 bytes a load, chunk c of row t at c ^ t % 16
   const uint16_t* xa[N];
+  const int xc = (r ^ (4 * wave + b)) << 3;
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    const int t = 4 * wave + b;
-    xa[n] = src + token[16 * n + t < ntok ? 16 * n + t : 0] * ld + ((r ^ t) << 3);
+    const int t = 16 * n + 4 * wave + b;
+    xa[n] = src + token[t < ntok ? t : 0] * ld;
   }
   auto load = [&](int s, uint32_t slot) {
     const int64_t done = (int64_t)s * 128;
@@ -578,11 +535,21 @@ __device__ __forceinline__ void stream_rows(const Rows& w, const uint16_t* src, 
       mxw::load_lds16(first, to + g * 2048, vo[0] + g * w.apart * w.C);
       mxw::load_lds16(second, to + g * 2048 + 1024, vo[1] + g * w.apart * w.C);
     }
-    const int at = in ? s : steps - 1;  // past the end: the last step's again, not used
+    // past the end: the last step's again, not used; past a row's end in its last
+    // step: the row's first values, which meet zero codes
+    const int at = in ? s : steps - 1;
+    const int col = WORDS || 128 * at + xc < w.C ? 128 * at + xc : 0;
 #pragma unroll
     for (int n = 0; n < N; ++n)
-      global_lds16(xa[n] + 128 * at, lds0 + slot * kSlot + kCodes + n * 4096 + wave * 1024);
-    global_lds4(w.sfirst + 4 * at, so, lds0 + slot * kSlot + kCodes + kTokens + wave * 256);
+      global_lds16(xa[n] + col, lds0 + slot * kSlot + kCodes + n * 4096 + wave * 1024);
+    const uint32_t scales = lds0 + slot * kSlot + kCodes + kTokens + wave * kScaleLoads * 256;
+    if (WORDS) {
+      global_lds4(w.sfirst + 4 * at, so[0], scales);
+    } else {
+      const int block = 4 * at + (lane & 3) < blocks ? 4 * at + (lane & 3) : blocks - 1;
+#pragma unroll
+      for (int g = 0; g < kScaleLoads; ++g) global_lds1(w.sfirst, so[g] + block, scales + g * 256);
+    }
   };
 #pragma unroll
   for (int g = 0; g < G; ++g)
@@ -602,7 +569,13 @@ __device__ __forceinline__ void stream_rows(const Rows& w, const uint16_t* src, 
     for (int g = 0; g < G; ++g) {
       c[g].lo = *(const v4i*)(codes + g * 2048 + (((2 * b) ^ sw) << 4));
       c[g].hi = *(const v4i*)(codes + g * 2048 + (((2 * b + 1) ^ sw) << 4));
-      c[g].s = *(at + kCodes + kTokens + wave * 256 + (16 * g + r) * 4 + b);
+      const uint8_t* scales = at + kCodes + kTokens + wave * kScaleLoads * 256;
+      if (WORDS) {
+        c[g].s = scales[(16 * g + r) * 4 + b];
+      } else {
+        c[g].s = *(const uint32_t*)(scales + g * 256 + (4 * r + b) * 4);
+        if (4 * s + b >= blocks) c[g] = Codes{};  // past the row's end
+      }
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -622,8 +595,8 @@ __device__ __forceinline__ void stream_rows(const Rows& w, const uint16_t* src, 
 }
 
 // Items (expert, 32 G rows of Wg and of Wu) by workgroups of 4 waves: a wave's
-// group is 8 rows of Wg and the same 8 of Wu.
-template <int G, int N>
+// group is 8 rows of Wg and the same 8 of Wu.  MANY: more than 16 tokens possible.
+template <int G, int N, bool WORDS>
 __device__ __forceinline__ void gate_item(const MoeArgs& a, const Routing& rt, int e, int i0, const int32_t* token,
                                           int ntok, uint8_t* ring) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, b = lane >> 4, blocks = a.H >> 5;
@@ -631,7 +604,7 @@ __device__ __forceinline__ void gate_item(const MoeArgs& a, const Routing& rt, i
   const Rows w = {a.wgu + at * a.H, a.wgu + (at + a.I) * a.H,   a.I - i0, a.I - i0,
                   a.sgu + at * blocks, a.sgu + (at + a.I) * blocks, 8, a.H};
   v4f acc[G][N];
-  stream_rows<G, N>(w, a.x, a.ldx, token, ntok, ring, acc);
+  stream_rows<G, N, WORDS>(w, a.x, a.ldx, token, ntok, ring, acc);
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     const int tok = 16 * n + r;
@@ -653,11 +626,12 @@ __device__ __forceinline__ void gate_item(const MoeArgs& a, const Routing& rt, i
   }
 }
 
-template <From FROM, int G, bool MANY>
+template <From FROM, int G, bool MANY, bool WORDS>
 __global__ __launch_bounds__(256, 2) void moe_gate_kernel(MoeArgs a) {
   __shared__ Routing rt;
   __shared__ int32_t token[kMaxTokens];
   __shared__ __align__(1024) uint8_t ring[kRing];
+  static_assert(sizeof(Routing) + sizeof(token) + kRing <= 80 * 1024, "two workgroups a CU");
   const int count = make_routing<FROM, 4>(a, rt, (float*)ring);
   const int tiles = (a.I + 32 * G - 1) / (32 * G);
   for (int item = blockIdx.x; item < count * tiles; item += gridDim.x) {
@@ -667,9 +641,9 @@ __global__ __launch_bounds__(256, 2) void moe_gate_kernel(MoeArgs a) {
     __syncthreads();  // the last item is done with the list
     if ((int)threadIdx.x < ntok) token[threadIdx.x] = nth_token(mask, threadIdx.x);
     __syncthreads();
-    if (!MANY || ntok <= 16) gate_item<G, 1>(a, rt, e, i0, token, ntok, ring);
-    else if (ntok <= 32) gate_item<G, MANY ? 2 : 1>(a, rt, e, i0, token, ntok, ring);
-    else gate_item<G, MANY ? 4 : 1>(a, rt, e, i0, token, ntok, ring);
+    if (!MANY || ntok <= 16) gate_item<G, 1, WORDS>(a, rt, e, i0, token, ntok, ring);
+    else if (ntok <= 32) gate_item<G, MANY ? 2 : 1, WORDS>(a, rt, e, i0, token, ntok, ring);
+    else gate_item<G, MANY ? 4 : 1, WORDS>(a, rt, e, i0, token, ntok, ring);
   }
 }
 
@@ -726,7 +700,7 @@ __global__ __launch_bounds__(kDownWaves * 64, 4) void moe_down_kernel(MoeArgs a)
 
 // many experts: items (expert, 64 G columns), to FP32 partial outputs per
 // (token, expert)
-template <int G, int N>
+template <int G, int N, bool WORDS>
 __device__ __forceinline__ void down_item(const MoeArgs& a, int e, int h0, int first, int ntok, const int32_t* order,
                                           uint8_t* ring) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, b = lane >> 4, blocks = a.I >> 5;
@@ -734,7 +708,7 @@ __device__ __forceinline__ void down_item(const MoeArgs& a, int e, int h0, int f
   const Rows w = {a.wd + at * a.I, a.wd + (at + 8) * a.I, a.H - h0, a.H - h0 - 8,
                   a.sd + at * blocks, a.sd + (at + 8) * blocks, 16, a.I};
   v4f acc[G][N];
-  stream_rows<G, N>(w, a.h + (int64_t)first * a.I, a.I, order, ntok, ring, acc);
+  stream_rows<G, N, WORDS>(w, a.h + (int64_t)first * a.I, a.I, order, ntok, ring, acc);
 #pragma unroll
   for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -744,7 +718,7 @@ __device__ __forceinline__ void down_item(const MoeArgs& a, int e, int h0, int f
     }
 }
 
-template <int G, bool MANY>
+template <int G, bool MANY, bool WORDS>
 __global__ __launch_bounds__(256, 2) void moe_down_part_kernel(MoeArgs a) {
   __shared__ int32_t order[kMaxTokens];
   __shared__ __align__(1024) uint8_t ring[kRing];
@@ -755,9 +729,9 @@ __global__ __launch_bounds__(256, 2) void moe_down_part_kernel(MoeArgs a) {
   for (int item = blockIdx.x; item < count * tiles; item += gridDim.x) {
     const int which = item / tiles, h0 = (item - which * tiles) * 64 * G;
     const int e = a.expert[which], first = a.first[which], ntok = __popcll(a.tokens[which]);
-    if (!MANY || ntok <= 16) down_item<G, 1>(a, e, h0, first, ntok, order, ring);
-    else if (ntok <= 32) down_item<G, MANY ? 2 : 1>(a, e, h0, first, ntok, order, ring);
-    else down_item<G, MANY ? 4 : 1>(a, e, h0, first, ntok, order, ring);
+    if (!MANY || ntok <= 16) down_item<G, 1, WORDS>(a, e, h0, first, ntok, order, ring);
+    else if (ntok <= 32) down_item<G, MANY ? 2 : 1, WORDS>(a, e, h0, first, ntok, order, ring);
+    else down_item<G, MANY ? 4 : 1, WORDS>(a, e, h0, first, ntok, order, ring);
   }
 }
 
@@ -799,7 +773,7 @@ MoePlan plan_of(int T, int E, int k, int H, int I) {
   // its XCD's L2) in about a us; a kernel of its own costs 3 us and a launch.
   p.fused = T <= 16 && T * E <= kFusedLogits && E * H <= (32 << 10);
   // a workgroup of the down kernel reads 16 rows of I of every chosen expert
-  p.by_item = (I & 127) == 0 && (int64_t)most_experts(T, E, k) * I * 16 > (192 << 10);
+  p.by_item = (int64_t)most_experts(T, E, k) * I * 16 > (192 << 10);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t was = at;
@@ -825,22 +799,33 @@ int check_moe(int T, int E, int k, int H, int I) {
              : MXW_OK;
 }
 
-template <From FROM>
-void launch_gate(const MoeArgs& a, int cus, hipStream_t st) {
+// Items of a wave's groups: one each while that leaves workgroups idle, else two,
+// which read a step's tokens half as often.
+template <From FROM, bool WORDS>
+void launch_gate_of(const MoeArgs& a, int cus, hipStream_t st) {
   const int64_t most = most_experts(a.T, a.E, a.k);
-  if (a.H & 127) {
-    const int64_t n = most * ((a.I + 15) / 16);
-    hipLaunchKernelGGL((moe_gate_split_kernel<FROM>), dim3((unsigned)(n < 4 * cus ? n : 4 * cus)), dim3(kWaves * 64), 0,
-                       st, a);
-    return;
-  }
   const int64_t slots = 2 * cus, one = most * ((a.I + 31) / 32), two = most * ((a.I + 63) / 64);
   if (two < slots)
-    hipLaunchKernelGGL((moe_gate_kernel<FROM, 1, true>), dim3((unsigned)(one < slots ? one : slots)), dim3(256), 0, st, a);
-  else if (FROM != kGiven)  // at most 16 tokens
-    hipLaunchKernelGGL((moe_gate_kernel<FROM, 2, false>), dim3((unsigned)slots), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((moe_gate_kernel<FROM, 1, FROM == kGiven, WORDS>), dim3((unsigned)(one < slots ? one : slots)),
+                       dim3(256), 0, st, a);
   else
-    hipLaunchKernelGGL((moe_gate_kernel<FROM, 2, true>), dim3((unsigned)slots), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((moe_gate_kernel<FROM, 2, FROM == kGiven, WORDS>), dim3((unsigned)slots), dim3(256), 0, st, a);
+}
+template <From FROM>
+void launch_gate(const MoeArgs& a, int cus, hipStream_t st) {
+  if (a.H & 127) launch_gate_of<FROM, false>(a, cus, st);
+  else launch_gate_of<FROM, true>(a, cus, st);
+}
+
+template <bool WORDS>
+void launch_down_part(const MoeArgs& a, int cus, hipStream_t st) {
+  const int64_t most = most_experts(a.T, a.E, a.k);
+  const int64_t slots = 2 * cus, one = most * ((a.H + 63) / 64), two = most * ((a.H + 127) / 128);
+  if (two < slots)
+    hipLaunchKernelGGL((moe_down_part_kernel<1, true, WORDS>), dim3((unsigned)(one < slots ? one : slots)), dim3(256), 0,
+                       st, a);
+  else
+    hipLaunchKernelGGL((moe_down_part_kernel<2, true, WORDS>), dim3((unsigned)slots), dim3(256), 0, st, a);
 }
 
 }  // namespace
@@ -910,14 +895,8 @@ int mxw_moe_layer(const uint16_t* x, int64_t ldx, const uint16_t* router, const 
     }
   }
   if (p.by_item) {
-    const int64_t most = most_experts(T, E, k), slots = 2 * cus, one = most * ((H + 63) / 64),
-                  two = most * ((H + 127) / 128);
-    if (two < slots)
-      hipLaunchKernelGGL((moe_down_part_kernel<1, true>), dim3((unsigned)(one < slots ? one : slots)), dim3(256), 0, st, a);
-    else if (T <= 16)
-      hipLaunchKernelGGL((moe_down_part_kernel<2, false>), dim3((unsigned)slots), dim3(256), 0, st, a);
-    else
-      hipLaunchKernelGGL((moe_down_part_kernel<2, true>), dim3((unsigned)slots), dim3(256), 0, st, a);
+    if (I & 127) launch_down_part<false>(a, cus, st);
+    else launch_down_part<true>(a, cus, st);
     hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned)((H + 1023) / 1024), (unsigned)T), dim3(256), 0, st, a);
   } else {
     hipLaunchKernelGGL(moe_down_kernel, dim3((unsigned)(H / 16)), dim3(kDownWaves * 64), kDownWaves * T * 16 * 4, st, a);

@@ -352,6 +352,37 @@ struct EpiGram {
   }
 };
 
+// FP32 partial sums of S over one part of m
+struct EpiPart {
+  static constexpr bool kStaged = false;
+  struct Args {
+    float* part;  // [splits][batch][n][ld]
+    int n, ld, batch;
+  };
+  template <int BM, int BN, int WM, int WN, int MI, int NI>
+  static __device__ void run(const GemmArgs&, const Args& a, const TileAt& at, v4f (&acc)[MI][NI], uint8_t*) {
+    float* part = a.part + ((int64_t)at.split * a.batch + at.batch) * a.n * a.ld;
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        const int m = at.m0 + at.wm + 16 * i + (at.lane & 15), n = at.n0 + at.wn + 16 * j + 4 * (at.lane >> 4);
+        if (m < a.n && n < a.ld) *(v4f*)(part + (int64_t)m * a.ld + n) = acc[i][j];
+      }
+  }
+};
+
+// S from its partial sums, in order
+__global__ __launch_bounds__(256) void ortho_join_kernel(const float* part, int splits, int64_t count, uint16_t* S) {
+  const int64_t i = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+  if (i >= count) return;
+  v4f v = *(const v4f*)(part + i);
+#pragma unroll 8
+  for (int k = 1; k < splits; ++k) v += *(const v4f*)(part + k * count + i);
+  v *= kPerOne;
+  *(uint2*)(S + i) = make_uint2(pack2(v[0], v[1], _Float16()), pack2(v[2], v[3], _Float16()));
+}
+
 // P = a I + b S + c S S
 struct EpiPoly {
   static constexpr bool kStaged = true;
@@ -476,7 +507,8 @@ struct OrthoPlan {
   int n, m, ldx, lds;
   bool tall;
   int parts;
-  size_t sums, X[2], S, P, bytes;
+  int splits;  // of m in S, 1: none
+  size_t sums, X[2], S, P, part, bytes;
 };
 
 int round64(int v) { return (v + 63) & ~63; }
@@ -502,6 +534,14 @@ OrthoPlan plan_of(int E, int N, int K) {
   for (int i = 0; i < 2; ++i) p.X[i] = take((size_t)E * N * p.ldx * 2);
   p.S = take((size_t)E * p.n * p.lds * 2);
   p.P = take((size_t)E * p.n * p.lds * 2);
+  // A long m over few 64-tiles of S (counting both triangles: the halves' saving
+  // is small there) is split so that about 512 workgroups take 4 steps of it or
+  // more; joining costs a launch, about 10 steps.  Two 177 x 6597 matrices: 236 us
+  // without, 138 with.
+  const int64_t tiles = (int64_t)((p.n + 63) / 64) * ((p.n + 63) / 64) * E, steps = (p.m + 63) / 64;
+  p.splits = (int)(512 / tiles < steps / 4 ? 512 / tiles : steps / 4);
+  if (p.splits < 2 || steps - steps / p.splits < 16) p.splits = 1;
+  if (p.splits > 1) p.part = take((size_t)p.splits * E * p.n * p.lds * 4);
   p.bytes = at;
   return p;
 }
@@ -585,10 +625,20 @@ int mxw_orthogonalize(const void* G, int type, int64_t expert_stride, int64_t ro
     g.A = g.B = X;
     g.strideA = g.strideB = strideX;
     g.lda = g.ldb = p.ldx;
-    g.M = g.N = p.tall ? p.ldx : N;
+    g.M = g.N = p.tall ? p.ldx : N;  // whole chunks by columns; their padding is zeros
     g.K = p.m;
     const EpiGram::Args eg = {S, strideS, p.n, p.lds};
-    rc = p.tall ? launch_product<true, true, true, EpiGram>(g, eg, cus, st)
+    if (p.splits > 1) {
+      float* part = (float*)(ws + p.part);
+      const EpiPart::Args es = {part, p.n, p.lds, E};
+      g.splits = p.splits;
+      g.ksplit = ((p.m + kGemmStep - 1) / kGemmStep + p.splits - 1) / p.splits * kGemmStep;
+      const int64_t edge = (p.n + 63) / 64, count = (int64_t)E * strideS;
+      rc = p.tall ? launch_tiles<64, 2, 2, 5, true, true, false, EpiPart>(g, es, 0, edge * edge * E * p.splits, false, st)
+                  : launch_tiles<64, 2, 2, 5, false, false, false, EpiPart>(g, es, 0, edge * edge * E * p.splits, false, st);
+      hipLaunchKernelGGL(ortho_join_kernel, dim3((unsigned)((count / 4 + 255) / 256)), dim3(256), 0, st,
+                         (const float*)part, p.splits, count, S);
+    } else rc = p.tall ? launch_product<true, true, true, EpiGram>(g, eg, cus, st)
                 : launch_product<false, false, true, EpiGram>(g, eg, cus, st);
     if (rc) break;
     // P
