@@ -336,14 +336,18 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
   // The pipeline, in rows of NI MFMAs (one A fragment against all of B's): after
   // a row its A fragment is replaced by the next part's, and B's fragments of
   // the next part come in meanwhile, so every read has about a part's MFMAs to
-  // return.  A step's only barrier starts its second part: it certifies that
-  // the next step's stages have landed and that everyone has read this one's.
+  // return.  A step's only barrier stands kBefore rows into its second part (the
+  // last reads return under those; 8192^3: 828 us with none before, 815 with two,
+  // A by columns 845 and, with one, 839): it certifies that the next step's stages
+  // have landed and that everyone has read this one's.
   // The loads are spread thinly (a CU's vector memory path takes a 1 KiB load
   // per ~16 clocks, and a wave that waits for it issues no MFMA): B's of the step
   // after next in the second part, into the stage just read, and A's of the step
   // after next in the first part, into the third A stage, so that they may be in
   // flight across the next barrier.
   constexpr int kOldest = kLoadsA % kWaves == 0 ? LA : 0;  // loads a barrier leaves in flight
+  constexpr int kBefore = MI >= 8 && !TA ? 2 : 1, kAfter = MI - kBefore;
+  constexpr int kBRow = (NI + kAfter - 1) / kAfter;  // B reads a row after the barrier
   if constexpr (DEEP > 0) {
     static_assert(kLoadsA % kWaves == 0 && kLoadsB % kWaves == 0, "every wave has the same loads");
     constexpr int kSlot = kBytesA + kBytesB;
@@ -374,7 +378,7 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
       next = next + 1 == DEEP ? 0 : next + 1;
     }
   } else {
-    static_assert(NI <= MI, "a B fragment of the next part is read in each of the first NI rows");
+    static_assert(NI <= MI && kBefore <= kAfter, "the rows hold the reads");
     const uint32_t ldsWave = ldsBase + wave * 1024;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -402,14 +406,19 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
         a[mi] = readA(a0, 1, mi);
         __builtin_amdgcn_sched_barrier(0);
       }
-      stage_barrier<kOldest>();
 #pragma unroll
       for (int mi = 0; mi < MI; ++mi) {
-        if (mi < NI) b[0][mi] = readB(b1, 0, mi);
-        fillB(ldsWave + b0, mi * LB / MI, (mi + 1) * LB / MI);
+        const int after = mi - kBefore;
+        if (after == 0) stage_barrier<kOldest>();
+        if (after >= 0) {
+#pragma unroll
+          for (int i = after * kBRow; i < (after + 1) * kBRow && i < NI; ++i) b[0][i] = readB(b1, 0, i);
+          if (after < kBefore) a[after] = readA(a1, 0, after);
+          fillB(ldsWave + b0, after * LB / kAfter, (after + 1) * LB / kAfter);
+        }
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = mfma16(b[1][ni], a[mi], acc[mi][ni], T());
-        a[mi] = readA(a1, 0, mi);
+        if (after >= 0) a[mi] = readA(a1, 0, mi);
         __builtin_amdgcn_sched_barrier(0);
       }
       uint32_t t = a0;
