@@ -42,7 +42,7 @@ extern "C" {
 #define MXW_ERR_NULL (-1)      /* a required pointer is NULL */
 #define MXW_ERR_DIM (-2)       /* a size outside the supported range */
 #define MXW_ERR_ALIGN (-3)     /* A, B or out not 16-byte aligned, or sA / sB
-                                  not 4-byte aligned */
+                                  not 4-byte aligned (or as the entry says) */
 #define MXW_ERR_DEVICE (-4)    /* current device is not gfx950, or no device */
 #define MXW_ERR_LAUNCH (-5)    /* a kernel launch failed (hipGetLastError) */
 #define MXW_ERR_WORKSPACE (-6) /* workspace NULL, smaller than its size query,
@@ -433,8 +433,8 @@ int mxfp8_quantize_tokens(const uint16_t* x, const int32_t* offs, int E, int M, 
  *   G        [E, N, K] elements of `type` (MXW_BF16 or MXW_F32), the last axis
  *            contiguous; rows row_stride >= K elements apart, experts
  *            expert_stride >= 0 elements.
- *   E, N, K  1 <= E <= MXW_MAX_EXPERTS, 1 <= N, K <= 65536; no multiples are
- *            asked for.
+ *   E, N, K  1 <= E <= MXW_MAX_EXPERTS, 1 <= N, K <= 65536, and at most 2^20
+ *            256 x 256 tiles in all; no multiples are asked for.
  *   coeffs   HOST memory, 3 * steps floats: (a, b, c) of each step, read
  *            during the call.
  *   steps    1 .. 32.
@@ -452,7 +452,8 @@ int mxfp8_quantize_tokens(const uint16_t* x, const int32_t* offs, int E, int M, 
  * whose gradient is zero gets zeros; one with a NaN or infinity gets NaN, and
  * no expert's result depends on another.  Bitwise reproducible run to run.
  *
- * Effects: enqueues 2 + 3 * steps kernels on `stream`, allocates nothing, keeps
+ * Effects: enqueues one kernel (matrices that fit in LDS) or 2 + 3 * steps and
+ * some more on `stream`, allocates nothing, keeps
  * no state, never writes G, does not synchronise; graph-capturable.
  * Returns MXW_OK or a negative MXW_ERR_* code.
  */
@@ -492,7 +493,8 @@ int64_t mxw_orthogonalize_workspace_size(int E, int N, int K);
  *            reduced loss) NaN and gives no gradient.
  *   T, H, V  1 <= T <= 131072, 1 <= H <= 65536, 1 <= V <= 1048576, no
  *            multiples asked for.  With H % 64 == 0, 16-byte aligned x and w
- *            and row strides of whole 16 bytes the operands are read in place;
+ *            and row strides of whole 16 bytes (up to 2^21 elements) the
+ *            operands are read in place;
  *            otherwise padded copies are made in the workspace, w's by pieces.
  *   loss     FP32, [T] for MXW_NONE, one value otherwise.
  *   dx, dw   bf16 [T, H] and [V, H], contiguous, fully overwritten; either may
@@ -550,7 +552,7 @@ int64_t mxw_vocab_loss_workspace_size(const uint16_t* x, int64_t ldx, const uint
  *   k        1 .. 16, at most E.        H, I  multiples of 32, 32 .. 65536.
  *   ids, weights  int32 and FP32 [T, k]: outputs, inputs without a router.
  *   out      bf16 [T, H], contiguous, fully overwritten.
- *   x, router, wgu, wd 16-byte aligned; ids, weights 4-byte aligned.
+ *   x, router, wgu, wd 16-byte aligned; sgu, sd, ids, weights 4-byte aligned.
  *   workspace, workspace_bytes  256-byte aligned device memory of at least
  *            mxw_moe_workspace_size(T, E, k, H, I) bytes; contents undefined on
  *            entry and exit, in use until the call's work is done.
@@ -561,8 +563,8 @@ int64_t mxw_vocab_loss_workspace_size(const uint16_t* x, int64_t ldx, const uint
  * A NaN or infinite logit makes that token's weights and out NaN; no token's
  * result depends on another's values.  Bitwise reproducible run to run.
  *
- * Effects: enqueues two or three kernels on `stream`, allocates nothing, keeps
- * no state, does not synchronise; graph-capturable.  Only the chosen experts'
+ * Effects: enqueues two to five kernels on `stream`, allocates nothing, keeps no
+ * state, does not synchronise; graph-capturable.  Only the chosen experts'
  * weights are read.  Returns MXW_OK or a negative MXW_ERR_* code.
  */
 int mxw_moe_layer(const uint16_t* x, int64_t ldx, const uint16_t* router, const uint8_t* wgu, const uint8_t* sgu,

@@ -645,9 +645,8 @@ def mxw_moe_layer(x, ldx, router, wgu, sgu, wd, sd, active, T, E, k, H, I, norma
                   workspace_bytes, stream=0):
     """Raw C-ABI call on device addresses (ints; router and active may be 0).
     Returns the status code."""
-    return _load().mxw_moe_layer(x, int(ldx), router, wgu, sgu, wd, sd, active, int(T), int(E), int(k), int(H), int(I),
-                                 int(bool(normalize)), float(scale), ids, weights, out, workspace, int(workspace_bytes),
-                                 stream)
+    return _load().mxw_moe_layer(x, ldx, router, wgu, sgu, wd, sd, active, T, E, k, H, I, 1 if normalize else 0, scale,
+                                 ids, weights, out, workspace, workspace_bytes, stream)
 
 
 def moe_workspace_size(T, E, k, H, I):

@@ -188,7 +188,7 @@ __device__ __forceinline__ float router_tile(const MoeArgs& a, int e0, int t0, i
   const uint16_t* xt = a.x + t * a.ldx;
   const int blocks = a.H >> 5;
   v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 2
+#pragma unroll 4
   for (int s = first + wave; 4 * s < blocks; s += stride) {
     const bool in = 4 * s + b < blocks;
     const int at = 32 * (in ? 4 * s + b : 0);
@@ -242,11 +242,19 @@ __device__ __forceinline__ void route_token(const MoeArgs& a, const float* logit
     v[i] = e < a.E ? 0.0f : -INFINITY;
     gone |= (uint32_t)(e >= a.E) << i;
   }
-  for (int z = 0; z < parts; ++z) {
-    const float* from = logits + ((int64_t)z * a.T + t) * a.E;
+  // four parts' loads in flight, added in order
+  for (int z0 = 0; z0 < parts; z0 += 4) {
+    float u[4][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (lane + 64 * i < a.E) v[i] += from[lane + 64 * i];
+    for (int z = 0; z < 4; ++z) {
+      const float* from = logits + ((int64_t)(z0 + z < parts ? z0 + z : z0) * a.T + t) * a.E;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[z][i] = from[lane + 64 * i < a.E ? lane + 64 * i : 0];
+    }
+#pragma unroll
+    for (int z = 0; z < 4; ++z)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += z0 + z < parts && lane + 64 * i < a.E ? u[z][i] : 0.0f;
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) top = fmaxf(top, v[i]);
@@ -257,6 +265,24 @@ __device__ __forceinline__ void route_token(const MoeArgs& a, const float* logit
     if (lane + 64 * i < a.E) sum += __builtin_amdgcn_exp2f((v[i] - top) * kLog2e);
   sum = wave_sum(sum);
   const bool broken = !(sum == sum);  // a NaN, or an infinity: no softmax
+  if (a.E <= 64) {
+    // an expert a lane: its rank is the number of experts that come before it
+    const float u = v[0] == v[0] ? v[0] : -INFINITY;
+    int rank = 0;
+#pragma unroll 8
+    for (int e = 0; e < a.E; ++e) {
+      const float o = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(u), e));
+      rank += o > u || (o == u && e < lane);
+    }
+    const bool mine = lane < a.E && rank < a.k;
+    const float p = mine ? __builtin_amdgcn_exp2f((u - top) * kLog2e) : 0.0f;
+    const float norm = a.normalize ? wave_sum(p) : sum;
+    if (mine) {
+      ids[rank] = (Id)lane;
+      weights[rank] = broken ? NAN : p / norm * a.scale;
+    }
+    return;
+  }
   int mine = 0;                       // lane j: the j-th choice and its logit
   float logit = 0.0f;
   for (int j = 0; j < a.k; ++j) {
@@ -592,6 +618,7 @@ __device__ __forceinline__ void stream_rows(const Rows& w, const uint16_t* src, 
     slot = slot + 1 == D ? 0 : slot + 1;
     next = next + 1 == D ? 0 : next + 1;
   }
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no load outlives the ring's use
 }
 
 // Items (expert, 32 G rows of Wg and of Wu) by workgroups of 4 waves: a wave's
@@ -844,7 +871,7 @@ int mxw_moe_layer(const uint16_t* x, int64_t ldx, const uint16_t* router, const 
   if (!x || !wgu || !sgu || !wd || !sd || !ids || !weights || !out) return MXW_ERR_NULL;
   if (check_moe(T, E, k, H, I) || ldx < H || (ldx & 7)) return MXW_ERR_DIM;
   if ((((uintptr_t)x | (uintptr_t)router | (uintptr_t)wgu | (uintptr_t)wd) & 15) || ((uintptr_t)out & 1) ||
-      (((uintptr_t)ids | (uintptr_t)weights) & 3))
+      (((uintptr_t)ids | (uintptr_t)weights | (uintptr_t)sgu | (uintptr_t)sd) & 3))
     return MXW_ERR_ALIGN;
   const MoePlan p = plan_of(T, E, k, H, I);
   if (!workspace || workspace_bytes < p.bytes || ((uintptr_t)workspace & 255)) return MXW_ERR_WORKSPACE;

@@ -2167,8 +2167,8 @@ const char* mxw_strerror(int code) {
   switch (code) {
     case MXW_OK: return "ok";
     case MXW_ERR_NULL: return "a required pointer is NULL";
-    case MXW_ERR_DIM: return "a size (E, M, N, K, R or C) outside the supported range";
-    case MXW_ERR_ALIGN: return "A, B or out is not 16-byte aligned, or sA or sB not 4-byte aligned";
+    case MXW_ERR_DIM: return "a size, stride or option outside the supported range";
+    case MXW_ERR_ALIGN: return "a pointer is not aligned as its entry point asks (16 bytes for codes and outputs, 4 for scales, in general)";
     case MXW_ERR_DEVICE: return "the current device is not gfx950 (or no device)";
     case MXW_ERR_LAUNCH: return "kernel launch failed";
     case MXW_ERR_WORKSPACE: return "workspace missing, smaller than the size query returned, or not 256-byte aligned";
@@ -2177,6 +2177,6 @@ const char* mxw_strerror(int code) {
   }
 }
 
-int mxw_version(void) { return 500; }
+int mxw_version(void) { return 600; }
 
 }  // extern "C"

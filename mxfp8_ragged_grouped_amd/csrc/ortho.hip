@@ -441,7 +441,7 @@ struct EpiNext {
 
 // `count` tiles of edge B from the `first` of all on (quarters: of edge 2 B, cut in four)
 template <int B, int WM, int WN, int DEEP, bool TA, bool TB, bool SYM, class Epi>
-int launch_tiles(GemmArgs g, const typename Epi::Args& e, int64_t first, int64_t count, bool quarters, hipStream_t st) {
+void launch_tiles(GemmArgs g, const typename Epi::Args& e, int64_t first, int64_t count, bool quarters, hipStream_t st) {
   const int edge = quarters ? 2 * B : B;
   g.tilesM = (g.M + edge - 1) / edge;
   g.tilesN = (g.N + edge - 1) / edge;
@@ -449,10 +449,8 @@ int launch_tiles(GemmArgs g, const typename Epi::Args& e, int64_t first, int64_t
   g.first = (int)first;
   g.quarters = quarters;
   const int64_t grid = quarters ? 4 * count : count;
-  if (grid > 0x7FFFFFFF / 512) return MXW_ERR_DIM;
   hipLaunchKernelGGL((gemm16_kernel<_Float16, B, B, WM, WN, DEEP, TA, TB, SYM, Epi>), dim3((unsigned)grid),
                      dim3(WM * WN * 64), 0, st, g, e);
-  return MXW_OK;
 }
 
 // The tile edge with the least estimated time.  In hundredths of a us, measured
@@ -465,7 +463,7 @@ int launch_tiles(GemmArgs g, const typename Epi::Args& e, int64_t first, int64_t
 // 2,359 with 128).  Last, 256-tiles for the whole rounds and quarters of them for
 // the rest, where that would leave most CUs idle.
 template <bool TA, bool TB, bool SYM, class Epi>
-int launch_product(GemmArgs g, const typename Epi::Args& e, int cus, hipStream_t st) {
+void launch_product(GemmArgs g, const typename Epi::Args& e, int cus, hipStream_t st) {
   auto tiles = [&](int b) {
     const int64_t tm = (g.M + b - 1) / b, tn = (g.N + b - 1) / b;
     return (SYM ? tm * (tm + 1) / 2 : tm * tn) * g.batch;
@@ -482,8 +480,8 @@ int launch_product(GemmArgs g, const typename Epi::Args& e, int cus, hipStream_t
   if (c64 <= c128 && c64 <= c256 && c64 <= both) return launch_tiles<64, 2, 2, 5, TA, TB, SYM, Epi>(g, e, 0, t64, false, st);
   if (c128 <= c256 && c128 <= both) return launch_tiles<128, 2, 2, 0, TA, TB, SYM, Epi>(g, e, 0, t128, false, st);
   if (c256 <= both) return launch_tiles<256, 2, 4, 0, TA, TB, SYM, Epi>(g, e, 0, t256, false, st);
-  const int rc = launch_tiles<256, 2, 4, 0, TA, TB, SYM, Epi>(g, e, 0, whole, false, st);
-  return rc ? rc : launch_tiles<128, 2, 2, 0, TA, TB, SYM, Epi>(g, e, whole, rest, true, st);
+  launch_tiles<256, 2, 4, 0, TA, TB, SYM, Epi>(g, e, 0, whole, false, st);
+  launch_tiles<128, 2, 2, 0, TA, TB, SYM, Epi>(g, e, whole, rest, true, st);
 }
 
 // ---- host -------------------------------------------------------------------
@@ -547,7 +545,9 @@ OrthoPlan plan_of(int E, int N, int K) {
 }
 
 int check_sizes(int E, int N, int K) {
-  return E < 1 || E > MXW_MAX_EXPERTS || N < 1 || K < 1 || N > 65536 || K > 65536 ? MXW_ERR_DIM : MXW_OK;
+  if (E < 1 || E > MXW_MAX_EXPERTS || N < 1 || K < 1 || N > 65536 || K > 65536) return MXW_ERR_DIM;
+  // launches of 64-tiles stay below 2^32 threads
+  return (int64_t)E * ((N + 255) / 256) * ((K + 255) / 256) > (1 << 20) ? MXW_ERR_DIM : MXW_OK;
 }
 
 }  // namespace
@@ -615,7 +615,7 @@ int mxw_orthogonalize(const void* G, int type, int64_t expert_stride, int64_t ro
   const int64_t strideX = (int64_t)N * p.ldx, strideS = (int64_t)p.n * p.lds;
   uint16_t* S = (uint16_t*)(ws + p.S);
   uint16_t* P = (uint16_t*)(ws + p.P);
-  for (int s = 0; s < steps && rc == MXW_OK; ++s) {
+  for (int s = 0; s < steps; ++s) {
     const float a = coeffs[3 * s], b = coeffs[3 * s + 1], c = coeffs[3 * s + 2];
     const uint16_t* X = (const uint16_t*)(ws + p.X[s & 1]);
     uint16_t* next = (uint16_t*)(ws + p.X[(s + 1) & 1]);
@@ -634,13 +634,14 @@ int mxw_orthogonalize(const void* G, int type, int64_t expert_stride, int64_t ro
       g.splits = p.splits;
       g.ksplit = ((p.m + kGemmStep - 1) / kGemmStep + p.splits - 1) / p.splits * kGemmStep;
       const int64_t edge = (p.n + 63) / 64, count = (int64_t)E * strideS;
-      rc = p.tall ? launch_tiles<64, 2, 2, 5, true, true, false, EpiPart>(g, es, 0, edge * edge * E * p.splits, false, st)
+      p.tall ? launch_tiles<64, 2, 2, 5, true, true, false, EpiPart>(g, es, 0, edge * edge * E * p.splits, false, st)
                   : launch_tiles<64, 2, 2, 5, false, false, false, EpiPart>(g, es, 0, edge * edge * E * p.splits, false, st);
       hipLaunchKernelGGL(ortho_join_kernel, dim3((unsigned)((count / 4 + 255) / 256)), dim3(256), 0, st,
                          (const float*)part, p.splits, count, S);
-    } else rc = p.tall ? launch_product<true, true, true, EpiGram>(g, eg, cus, st)
-                : launch_product<false, false, true, EpiGram>(g, eg, cus, st);
-    if (rc) break;
+    } else {
+      p.tall ? launch_product<true, true, true, EpiGram>(g, eg, cus, st)
+             : launch_product<false, false, true, EpiGram>(g, eg, cus, st);
+    }
     // P
     g.A = g.B = S;
     g.strideA = g.strideB = strideS;
@@ -648,8 +649,7 @@ int mxw_orthogonalize(const void* G, int type, int64_t expert_stride, int64_t ro
     g.M = g.N = p.n;
     g.K = p.n;
     const EpiPoly::Args ep = {S, P, strideS, p.n, p.lds, a, b, c};
-    rc = launch_product<false, false, true, EpiPoly>(g, ep, cus, st);
-    if (rc) break;
+    launch_product<false, false, true, EpiPoly>(g, ep, cus, st);
     // X
     g.M = N;
     g.N = p.ldx;
@@ -672,15 +672,14 @@ int mxw_orthogonalize(const void* G, int type, int64_t expert_stride, int64_t ro
     }
     if (s + 1 < steps) {
       const EpiNext<false>::Args en = {next, strideX, N, p.ldx, p.ldx};
-      rc = p.tall ? launch_product<false, false, false, EpiNext<false>>(g, en, cus, st)
-                  : launch_product<false, true, false, EpiNext<false>>(g, en, cus, st);
+      p.tall ? launch_product<false, false, false, EpiNext<false>>(g, en, cus, st)
+             : launch_product<false, true, false, EpiNext<false>>(g, en, cus, st);
     } else {
       const EpiNext<true>::Args en = {out, (int64_t)N * K, N, K, K};
-      rc = p.tall ? launch_product<false, false, false, EpiNext<true>>(g, en, cus, st)
-                  : launch_product<false, true, false, EpiNext<true>>(g, en, cus, st);
+      p.tall ? launch_product<false, false, false, EpiNext<true>>(g, en, cus, st)
+             : launch_product<false, true, false, EpiNext<true>>(g, en, cus, st);
     }
   }
-  if (rc) return rc;
   if (hipGetLastError() != hipSuccess) return MXW_ERR_LAUNCH;
   return MXW_OK;
 }

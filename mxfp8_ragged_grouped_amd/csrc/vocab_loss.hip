@@ -309,8 +309,9 @@ struct LossPlan {
   size_t part, hit, lse, rows, scale, xp, wp, g, sum, bytes;
 };
 
+// whether x and w are read in place (a tile of 256 rows stays below 2^31 bytes)
 bool aligned(const void* x, int64_t ldx, const void* w, int64_t ldw, int H) {
-  return (H & 63) == 0 && (ldx & 7) == 0 && (ldw & 7) == 0 && (((uintptr_t)x | (uintptr_t)w) & 15) == 0;
+  return (H & 63) == 0 && ldx <= 1 << 21 && ldw <= 1 << 21 && (ldx & 7) == 0 && (ldw & 7) == 0 && (((uintptr_t)x | (uintptr_t)w) & 15) == 0;
 }
 
 LossPlan plan_of(bool direct, int T, int H, int V, bool gx, bool gw, int cus) {
@@ -380,7 +381,7 @@ int launch(GemmArgs g, const typename Epi::Args& e, hipStream_t st) {
   g.tilesN = (g.N + BN - 1) / BN;
   g.tiles = g.tilesM * g.tilesN;
   const int64_t grid = (int64_t)g.tilesM * g.tilesN * g.splits;
-  if (grid > 0x7FFFFFFF / 512) return MXW_ERR_DIM;
+  if (grid > 0xFFFFFFFFLL / (WM * WN * 64)) return MXW_ERR_DIM;
   hipLaunchKernelGGL((gemm16_kernel<__bf16, BM, BN, WM, WN, DEEP, TA, TB, false, Epi>), dim3((unsigned)grid),
                      dim3(WM * WN * 64), 0, st, g, e);
   return MXW_OK;
@@ -447,7 +448,6 @@ int mxw_vocab_loss(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ld
     xs = xp;
     lx = lw = p.ld;
   }
-  if (lx > 0x3FFFFFFF / 64 || lw > 0x3FFFFFFF / 64) return MXW_ERR_DIM;
   // the piece's weights as the products read them
   auto weights = [&](int v0, int width) -> const uint16_t* {
     if (!p.packed) return w + v0 * ldw;

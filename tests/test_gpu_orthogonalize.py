@@ -84,6 +84,26 @@ def test_large_tiles():
         close(mxw.orthogonalize(G), reference(G, [COEFFS] * 5), "N=%d K=%d" % (N, K))
 
 
+@pytest.mark.parametrize("E,N,K", [(2, 150, 3000), (1, 3000, 150), (1, 64, 8200), (3, 33, 2300), (4, 2100, 130)])
+def test_long_and_narrow(E, N, K):
+    """A short side over a long one: the long sum is split over workgroups."""
+    say("orthogonalize E=%d N=%d K=%d" % (E, N, K))
+    G = (2e-2 * spread(E, N, K, 2000 + N + K)).to(torch.bfloat16)
+    close(mxw.orthogonalize(G, out=poisoned(G.shape)), reference(G, [COEFFS] * 5), "N=%d K=%d" % (N, K))
+
+
+@pytest.mark.parametrize("E,N,K", [(5, 1500, 1100), (4, 1100, 4100), (9, 900, 600), (8, 2300, 2400)])
+def test_whole_rounds_and_quarters(E, N, K):
+    """Sizes that take other tile edges, and 256-tiles with the rest in quarters:
+    the same bits as each matrix alone."""
+    say("orthogonalize E=%d N=%d K=%d" % (E, N, K))
+    g = torch.Generator(device=DEV).manual_seed(N + K)
+    G = torch.randn((E, N, K), generator=g, device=DEV).to(torch.bfloat16)
+    out = mxw.orthogonalize(G, out=poisoned(G.shape))
+    close(out, reference(G, [COEFFS] * 5), "N=%d K=%d" % (N, K))
+    assert torch.equal(out[E // 2], mxw.orthogonalize(G[E // 2]))
+
+
 def test_singular_values_come_near_one():
     G = spread(2, 200, 333, 5).to(torch.bfloat16)
     s = torch.linalg.svdvals(mxw.orthogonalize(G).double())

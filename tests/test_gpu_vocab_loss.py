@@ -216,6 +216,32 @@ def test_weights_past_32_bit_offsets():
         assert ((t.double() - r).abs() <= 2.0 ** -8 * r.abs() + 1.05 * 2.0 ** -8 * terms + 1e-37).all()
 
 
+def test_far_apart_rows():
+    """Row strides beyond what a tile's 32-bit offsets reach (3 Mi elements)."""
+    x, w, y = make(30, 64, 40, 15)
+    want = mxw.vocab_cross_entropy(x, w, y)
+    far = torch.empty((40, 3 << 20), dtype=torch.bfloat16, device=DEV)
+    far[:, :64] = w
+    got = mxw.vocab_cross_entropy(x, far[:, :64], y)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("which", [1, 2])
+def test_one_gradient_alone(which):
+    """The C entry with dx or dw left out."""
+    x, w, y = make(70, 128, 900, 16)
+    want = mxw.vocab_cross_entropy(x, w, y)
+    loss = torch.empty((), device=DEV)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    need = mxw.vocab_loss_workspace_size(x.data_ptr(), 128, w.data_ptr(), 128, 70, 128, 900, which)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    rc = mxw.mxw_vocab_loss(x.data_ptr(), 128, w.data_ptr(), 128, y.data_ptr(), 8, IGNORE, 70, 128, 900, 1, 1.0,
+                            loss.data_ptr(), dx.data_ptr() if which == 1 else 0, dw.data_ptr() if which == 2 else 0,
+                            ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream)
+    assert rc == 0 and torch.equal(loss, want[0])
+    assert torch.equal(dx, want[1]) if which == 1 else torch.equal(dw, want[2])
+
+
 def test_repeats_streams_and_graphs():
     x, w, y = make(300, 192, 3000, 10)
     want = mxw.vocab_cross_entropy(x, w, y)

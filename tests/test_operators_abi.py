@@ -39,7 +39,7 @@ def test_orthogonalize_host_checks(args, code):
 def test_orthogonalize_workspace_size():
     n = mxw.orthogonalize_workspace_size(8, 1408, 2048)
     assert n >= 2 * 8 * (2 * 1408 * 2048 + 2 * 1408 * 1408)
-    for bad in ((0, 8, 8), (1, 0, 8), (1, 8, 65537), (257, 8, 8)):
+    for bad in ((0, 8, 8), (1, 0, 8), (1, 8, 65537), (257, 8, 8), (256, 65536, 65536)):
         with pytest.raises(mxw.MxwError):
             mxw.orthogonalize_workspace_size(*bad)
 
@@ -126,7 +126,7 @@ def moe_args(**over):
     (dict(E=32, k=17), -2), (dict(H=48), -2), (dict(H=0), -2), (dict(I=16), -2), (dict(I=65568), -2),
     (dict(ldx=63), -2), (dict(ldx=68), -2),
     (dict(x=P + 8), -3), (dict(router=P + 2), -3), (dict(wgu=P + 4), -3), (dict(wd=P + 8), -3), (dict(out=P + 1), -3),
-    (dict(ids=P + 2), -3), (dict(weights=P + 1), -3),
+    (dict(ids=P + 2), -3), (dict(weights=P + 1), -3), (dict(sgu=P + 2), -3), (dict(sd=P + 1), -3),
     (dict(workspace=0), -6), (dict(workspace_bytes=64), -6), (dict(workspace=P + 128), -6),
 ])
 def test_moe_host_checks(over, code):
