@@ -395,14 +395,24 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
       a[i] = readA(0, 0, i);
       __builtin_amdgcn_sched_barrier(0);
     }
+    // every MFMA shares an operand with the one before it, across rows too: less
+    // toggling, and under the power limit 1.5% more clock (8192^3: 849 -> 832 us on
+    // one board)
+    auto row = [&](int mi, const v4i& av, const v4i(&bv)[NI]) {
+#pragma unroll
+      for (int n = 0; n < NI; ++n) {
+        const int ni = mi & 1 ? NI - 1 - n : n;
+        acc[mi][ni] = mfma16(bv[ni], av, acc[mi][ni], T());
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
     uint32_t a0 = 0, a1 = kBytesA, a2 = 2 * kBytesA, b0 = 3 * kBytesA, b1 = b0 + kBytesB;
     for (int s = 0; s < steps; ++s) {
 #pragma unroll
       for (int mi = 0; mi < MI; ++mi) {
         if (mi < NI) b[1][mi] = readB(b0, 1, mi);
         fillA(ldsWave + a2, mi * LA / MI, (mi + 1) * LA / MI);
-#pragma unroll
-        for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = mfma16(b[0][ni], a[mi], acc[mi][ni], T());
+        row(mi, a[mi], b[0]);
         a[mi] = readA(a0, 1, mi);
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -416,8 +426,7 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
           if (after < kBefore) a[after] = readA(a1, 0, after);
           fillB(ldsWave + b0, after * LB / kAfter, (after + 1) * LB / kAfter);
         }
-#pragma unroll
-        for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = mfma16(b[1][ni], a[mi], acc[mi][ni], T());
+        row(mi, a[mi], b[1]);
         if (after >= 0) a[mi] = readA(a1, 0, mi);
         __builtin_amdgcn_sched_barrier(0);
       }
