@@ -6,7 +6,11 @@
     out = fwd(A, sA, B, sB, offs)          # bf16 [R, N]
     q, s = quantize_tokens(x, offs)        # MXFP8 operand [H, M] from bf16 [M, H]
 
-computes, for every expert g (blog "Ragged MXFP8 Weight Gradients: A FlyDSL
+    update = orthogonalize(out)            # Newton-Schulz on every expert's gradient
+    loss, dx, dw = vocab_cross_entropy(x, w, targets)   # without keeping the logits
+    y, ids, weights = moe_layer(x, router, wgu, sgu, wd, sd, top_k)   # a few tokens
+
+The first group computes, for every expert g (blog "Ragged MXFP8 Weight Gradients: A FlyDSL
 Grouped GEMM on MI355X", section 1),
 
     dW[g] = dY[g]^T X[g]   over expert g's tokens [offs[g-1], offs[g])
@@ -21,7 +25,11 @@ from A [R, C] and B [E, N, C] (contraction innermost, 32-element E8M0 blocks
 along it); the same weight gradient on plain bf16 operands A = dY^T [N, M],
 B = X^T [K, M] (the XLA blog's "contracting" ragged dot); and the token-axis
 quantiser that makes the weight gradient's
-operands from bf16 activations / gradients.  Everything
+operands from bf16 activations / gradients.  The second group is what stands
+around those products when such a layer is trained and served: the optimiser's
+orthogonalised update of the experts' weights, the loss that the gradients
+start from, and the layer for single tokens and small batches (each described
+at its function).  Everything
 runs in the HIP library ``lib/libmxfp8_wgrad.so`` (C ABI in
 ``include/mxfp8_wgrad.h``); this module only checks tensor metadata and passes
 device pointers and the current stream.  There is no fallback: if the library

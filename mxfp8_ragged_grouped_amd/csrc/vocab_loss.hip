@@ -18,7 +18,12 @@
 // vocabulary where T x H has few tiles; partial sums are joined in a fixed
 // order at the end), one writes dw = g^T x of the piece's rows.
 // 8 T H V flops with gradients, 2 T H V without: bound by the MFMA except for
-// few tokens, where reading w bounds it.
+// few tokens, where reading w bounds it.  (Keeping the logits would save a quarter
+// of the flops and cost 4 T V bytes, 2.1 GB at 4,096 tokens and 128,000 words.)
+//
+// Measured: 4,096 tokens, 128,000 words of 2,048: 6.8 ms, 1,260 TFLOP/s as
+// computed; 2,048 tokens, words of 7,168: 11.2 ms, 1,340; one token's loss against
+// 32,000 words of 2,048 with cold caches: 31 us, 4.2 TB/s.
 //
 // All sums and statistics are FP32 (the mean's over tokens FP64); g is rounded
 // to bf16 because the products that follow take 16-bit operands: at most
