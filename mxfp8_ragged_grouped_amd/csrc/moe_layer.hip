@@ -51,7 +51,7 @@ using mxw::v4f;
 
 constexpr int kMaxTokens = MXW_MOE_MAX_TOKENS;  // a 64-bit mask of tokens per expert
 constexpr int kMaxChoices = 16;
-constexpr int kWaves = 8;  // of the router and gate/up kernels
+constexpr int kWaves = 8;  // of the router kernel
 constexpr float kLog2e = 1.4426950408889634f;
 
 static_assert(kMaxTokens == 64, "token masks are 64-bit, one token a lane");
@@ -113,41 +113,41 @@ __device__ __forceinline__ v4i operand(const Codes& c, int q) {
   return (q & 1) ? decode8(w.z, w.w, s) : decode8(w.x, w.y, s);
 }
 
-// acc[g] += 16 weight rows (row[g] of this lane, scales srow[g]) times up to 16
-// token rows (xt of this lane) over the 128-wide steps s0, s0 + stride, ... below
-// s1 of `blocks` 32-blocks, the loads of D steps ahead in flight.
-template <int G, int D>
-__device__ __forceinline__ void stream(const uint8_t* const (&row)[G], const uint8_t* const (&srow)[G],
-                                       const uint16_t* xt, int blocks, int s0, int stride, int s1, v4f (&acc)[G]) {
+// 16 weight rows (`row` of this lane, scales srow) times up to 16 token rows (xt of
+// this lane) over the 128-wide steps s0 .. s1 - 1 of `blocks` 32-blocks, the loads of
+// D steps in flight.
+template <int D>
+__device__ __forceinline__ v4f stream(const uint8_t* row, const uint8_t* srow, const uint16_t* xt, int blocks, int s0,
+                                      int s1) {
   const int b = (threadIdx.x & 63) >> 4;
-  Codes c[D][G];
+  v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  Codes c[D];
   v4i xv[D][4];
   auto load = [&](int d, int s) {
     const int at = 4 * s + b < blocks ? 4 * s + b : 0;
-#pragma unroll
-    for (int g = 0; g < G; ++g) c[d][g] = load_codes(row[g], srow[g], at);
+    c[d] = load_codes(row, srow, at);
 #pragma unroll
     for (int q = 0; q < 4; ++q) xv[d][q] = *(const v4i*)(xt + 32 * at + 8 * q);
   };
 #pragma unroll
   for (int d = 0; d < D; ++d)
-    if (s0 + d * stride < s1) load(d, s0 + d * stride);
-  for (int s = s0; s < s1; s += D * stride) {
+    if (s0 + d < s1) load(d, s0 + d);
+  for (int s = s0; s < s1; s += D) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      const int now = s + d * stride;
+      const int now = s + d;
       if (now >= s1) break;
-      if (4 * now + b >= blocks) {  // past the row's end: the codes of block 0, made zeros
+      if (4 * now + b >= blocks) {  // past the row's end: block 0 of both, made zeros
+        c[d] = Codes{};
 #pragma unroll
-        for (int g = 0; g < G; ++g) c[d][g] = Codes{};
+        for (int q = 0; q < 4; ++q) xv[d][q] = (v4i){0, 0, 0, 0};
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int g = 0; g < G; ++g) acc[g] = mfma(operand(c[d][g], q), xv[d][q], acc[g]);
-      if (now + D * stride < s1) load(d, now + D * stride);
+      for (int q = 0; q < 4; ++q) acc = mfma(operand(c[d], q), xv[d][q], acc);
+      if (now + D < s1) load(d, now + D);
     }
   }
+  return acc;
 }
 
 // ---- reductions over a wave by DPP ------------------------------------------
@@ -199,9 +199,9 @@ __device__ __forceinline__ float router_tile(const MoeArgs& a, int e0, int t0, i
     const int at = 32 * (in ? 4 * s + b : 0);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      v4i w = *(const v4i*)(re + at + 8 * q);
-      if (!in) w = (v4i){0, 0, 0, 0};
-      acc = mfma(w, *(const v4i*)(xt + at + 8 * q), acc);
+      v4i w = *(const v4i*)(re + at + 8 * q), xv = *(const v4i*)(xt + at + 8 * q);
+      if (!in) w = xv = (v4i){0, 0, 0, 0};
+      acc = mfma(w, xv, acc);
     }
   }
 #pragma unroll
@@ -567,7 +567,7 @@ __device__ __forceinline__ void stream_rows(const Rows& w, const uint16_t* src, 
       mxw::load_lds16(second, to + g * 2048 + 1024, vo[1] + g * w.apart * w.C);
     }
     // past the end: the last step's again, not used; past a row's end in its last
-    // step: the row's first values, which meet zero codes
+    // step: the row's first values, made zeros below like the codes
     const int at = in ? s : steps - 1;
     const int col = WORDS || 128 * at + xc < w.C ? 128 * at + xc : 0;
 #pragma unroll
@@ -612,7 +612,10 @@ __device__ __forceinline__ void stream_rows(const Rows& w, const uint16_t* src, 
     for (int q = 0; q < 4; ++q) {
       v4i xv[N];
 #pragma unroll
-      for (int n = 0; n < N; ++n) xv[n] = *(const v4i*)(at + kCodes + n * 4096 + r * 256 + (((4 * b + q) ^ r) << 4));
+      for (int n = 0; n < N; ++n) {
+        xv[n] = *(const v4i*)(at + kCodes + n * 4096 + r * 256 + (((4 * b + q) ^ r) << 4));
+        if (!WORDS && 4 * s + b >= blocks) xv[n] = (v4i){0, 0, 0, 0};
+      }
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         const v4i a = operand(c[g], q);
@@ -627,7 +630,7 @@ __device__ __forceinline__ void stream_rows(const Rows& w, const uint16_t* src, 
 }
 
 // Items (expert, 32 G rows of Wg and of Wu) by workgroups of 4 waves: a wave's
-// group is 8 rows of Wg and the same 8 of Wu.  MANY: more than 16 tokens possible.
+// group is 8 rows of Wg and the same 8 of Wu.
 template <int G, int N, bool WORDS>
 __device__ __forceinline__ void gate_item(const MoeArgs& a, const Routing& rt, int e, int i0, const int32_t* token,
                                           int ntok, uint8_t* ring) {
@@ -658,8 +661,9 @@ __device__ __forceinline__ void gate_item(const MoeArgs& a, const Routing& rt, i
   }
 }
 
-template <From FROM, int G, bool MANY, bool WORDS>
+template <From FROM, int G, bool WORDS>
 __global__ __launch_bounds__(256, 2) void moe_gate_kernel(MoeArgs a) {
+  constexpr bool MANY = FROM == kGiven;  // the others come with at most 16 tokens
   __shared__ Routing rt;
   __shared__ int32_t token[kMaxTokens];
   __shared__ __align__(1024) uint8_t ring[kRing];
@@ -708,15 +712,13 @@ __global__ __launch_bounds__(kDownWaves * 64, 4) void moe_down_kernel(MoeArgs a)
     const uint64_t mask = tokens[which];
     const int ntok = __popcll(mask);
     const int64_t at = (int64_t)expert[which] * a.H + h0 + r;
-    const uint8_t* const row[1] = {a.wd + at * a.I};
-    const uint8_t* const srow[1] = {a.sd + at * blocks};
     for (int g0 = 0; g0 < ntok; g0 += 16) {
       const int p = g0 + r < ntok ? g0 + r : g0;
-      v4f acc[1] = {};
-      stream<1, 3>(row, srow, a.h + (int64_t)(first[which] + p) * a.I, blocks, s0, 1, s1, acc);
+      const v4f acc =
+          stream<3>(a.wd + at * a.I, a.sd + at * blocks, a.h + (int64_t)(first[which] + p) * a.I, blocks, s0, s1);
       if (g0 + r < ntok) {
         v4f* to = (v4f*)(mine + nth_token(mask, p) * 16 + 4 * b);
-        *to = *to + acc[0];
+        *to = *to + acc;
       }
     }
     u = which * steps + s1;
@@ -750,7 +752,7 @@ __device__ __forceinline__ void down_item(const MoeArgs& a, int e, int h0, int f
     }
 }
 
-template <int G, bool MANY, bool WORDS>
+template <int G, bool WORDS>
 __global__ __launch_bounds__(256, 2) void moe_down_part_kernel(MoeArgs a) {
   __shared__ int32_t order[kMaxTokens];
   __shared__ __align__(1024) uint8_t ring[kRing];
@@ -761,9 +763,9 @@ __global__ __launch_bounds__(256, 2) void moe_down_part_kernel(MoeArgs a) {
   for (int item = blockIdx.x; item < count * tiles; item += gridDim.x) {
     const int which = item / tiles, h0 = (item - which * tiles) * 64 * G;
     const int e = a.expert[which], first = a.first[which], ntok = __popcll(a.tokens[which]);
-    if (!MANY || ntok <= 16) down_item<G, 1, WORDS>(a, e, h0, first, ntok, order, ring);
-    else if (ntok <= 32) down_item<G, MANY ? 2 : 1, WORDS>(a, e, h0, first, ntok, order, ring);
-    else down_item<G, MANY ? 4 : 1, WORDS>(a, e, h0, first, ntok, order, ring);
+    if (ntok <= 16) down_item<G, 1, WORDS>(a, e, h0, first, ntok, order, ring);
+    else if (ntok <= 32) down_item<G, 2, WORDS>(a, e, h0, first, ntok, order, ring);
+    else down_item<G, 4, WORDS>(a, e, h0, first, ntok, order, ring);
   }
 }
 
@@ -838,10 +840,10 @@ void launch_gate_of(const MoeArgs& a, int cus, hipStream_t st) {
   const int64_t most = most_experts(a.T, a.E, a.k);
   const int64_t slots = 2 * cus, one = most * ((a.I + 31) / 32), two = most * ((a.I + 63) / 64);
   if (two < slots)
-    hipLaunchKernelGGL((moe_gate_kernel<FROM, 1, FROM == kGiven, WORDS>), dim3((unsigned)(one < slots ? one : slots)),
+    hipLaunchKernelGGL((moe_gate_kernel<FROM, 1, WORDS>), dim3((unsigned)(one < slots ? one : slots)),
                        dim3(256), 0, st, a);
   else
-    hipLaunchKernelGGL((moe_gate_kernel<FROM, 2, FROM == kGiven, WORDS>), dim3((unsigned)slots), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((moe_gate_kernel<FROM, 2, WORDS>), dim3((unsigned)slots), dim3(256), 0, st, a);
 }
 template <From FROM>
 void launch_gate(const MoeArgs& a, int cus, hipStream_t st) {
@@ -854,10 +856,10 @@ void launch_down_part(const MoeArgs& a, int cus, hipStream_t st) {
   const int64_t most = most_experts(a.T, a.E, a.k);
   const int64_t slots = 2 * cus, one = most * ((a.H + 63) / 64), two = most * ((a.H + 127) / 128);
   if (two < slots)
-    hipLaunchKernelGGL((moe_down_part_kernel<1, true, WORDS>), dim3((unsigned)(one < slots ? one : slots)), dim3(256), 0,
+    hipLaunchKernelGGL((moe_down_part_kernel<1, WORDS>), dim3((unsigned)(one < slots ? one : slots)), dim3(256), 0,
                        st, a);
   else
-    hipLaunchKernelGGL((moe_down_part_kernel<2, true, WORDS>), dim3((unsigned)slots), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((moe_down_part_kernel<2, WORDS>), dim3((unsigned)slots), dim3(256), 0, st, a);
 }
 
 }  // namespace

@@ -131,6 +131,28 @@ def test_weights(normalize, scale):
     check(mxw.moe_layer(**a, top_k=5, normalize=normalize, scale=scale), a, 5, normalize, scale)
 
 
+@pytest.mark.parametrize("T,E,k,H,I", [(2, 4, 2, 160, 96), (16, 16, 16, 96, 1056), (20, 6, 3, 288, 32)])
+def test_infinities_in_x(T, E, k, H, I):
+    """x[t][0] infinite, every weight positive (row lengths that end inside a
+    step of 128 columns): the outputs are inf, not the NaN of inf times a zero
+    that fills a step up; the choices are the experts whose logit is inf."""
+    say("moe_layer infinities T=%d E=%d k=%d H=%d I=%d" % (T, E, k, H, I))
+    a = make(T, E, k, H, I, 21)
+    a["wgu"], a["wd"] = (a["wgu"] & 0x70) | 0x08, (a["wd"] & 0x70) | 0x08
+    a["x"] = a["x"].abs()
+    a["x"][:, 0] = float("inf")
+    ids = torch.arange(T * k, device=DEV, dtype=torch.int32).reshape(T, k) % E
+    weights = torch.full((T, k), 0.5, device=DEV)
+    b = dict(a)
+    b.pop("router")
+    out = mxw.moe_layer(router=None, routing=(ids, weights), top_k=k, **b)[0]
+    assert (out == float("inf")).all()
+    router = a["router"].abs() + 0.01
+    router[: E - k, 0] *= -1
+    got = mxw.moe_layer(**dict(a, router=router), top_k=k)
+    assert torch.equal(got[1].long(), torch.arange(E - k, E, device=DEV).expand(T, k)) and got[2].isnan().all()
+
+
 def test_tokens_that_are_not_there():
     """Their x is not used (NaN), their rows are zero, no expert is read for
     them; a batch of none at all."""
