@@ -479,7 +479,8 @@ int64_t mxw_orthogonalize_workspace_size(int E, int N, int K);
  *     g_tv = (exp(l_tv) / sum_u exp(l_tu) - [v = y(t)]) * s
  *     dx[t] = sum_v g_tv w[v],       dw[v] = sum_t g_tv x[t]
  *
- * Tokens whose target is ignore_index have loss 0 and no gradient.  MXW_NONE
+ * Tokens whose target is ignore_index have loss 0 and no gradient, whatever
+ * their x holds (NaN included).  MXW_NONE
  * gives the loss of every token, MXW_SUM their sum, MXW_MEAN the sum divided by
  * the number of tokens that are not ignored (0 if there is none).  s is
  * grad_scale, divided by that number for MXW_MEAN: dx and dw are the gradients
@@ -490,12 +491,13 @@ int64_t mxw_orthogonalize_workspace_size(int E, int N, int K);
  *   w, ldw   bf16 [V, H], rows ldw >= H elements apart.
  *   targets  [T] int32 (target_bytes 4) or int64 (8).  A target outside
  *            [0, V) that is not ignore_index makes that token's loss (and the
- *            reduced loss) NaN and gives no gradient.
+ *            reduced loss) NaN and gives no gradient either.
  *   T, H, V  1 <= T <= 131072, 1 <= H <= 65536, 1 <= V <= 1048576, no
  *            multiples asked for.  With H % 64 == 0, 16-byte aligned x and w
  *            and row strides of whole 16 bytes (up to 2^21 elements) the
- *            operands are read in place;
- *            otherwise padded copies are made in the workspace, w's by pieces.
+ *            operands are read in place (x is copied, without the tokens that
+ *            give no gradient, if dw is wanted); otherwise padded copies are
+ *            made in the workspace, w's by pieces.
  *   loss     FP32, [T] for MXW_NONE, one value otherwise.
  *   dx, dw   bf16 [T, H] and [V, H], contiguous, fully overwritten; either may
  *            be NULL (not wanted).  They overlap no input.
@@ -504,8 +506,8 @@ int64_t mxw_orthogonalize_workspace_size(int E, int N, int K);
  *            entry and exit, in use until the call's work is done.
  *
  * Logits, statistics and sums are FP32; the g of a piece of the vocabulary is
- * rounded to bf16 before the two products that use it.  NaN in a token's x
- * reaches that token's loss and dx, and dw; a NaN or infinite logit makes its
+ * rounded to bf16 before the two products that use it.  NaN in the x of a token
+ * that counts reaches that token's loss and dx, and dw; a NaN or infinite logit makes its
  * token's loss NaN.  Bitwise reproducible run to run on the same device.
  *
  * Effects: enqueues kernels on `stream`, allocates nothing, keeps no state,

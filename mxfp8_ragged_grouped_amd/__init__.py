@@ -593,7 +593,7 @@ def vocab_cross_entropy(x, w, targets, ignore_index=-100, reduction="mean", grad
     keeping the logits: (loss, dx, dw), or loss alone with grads=False.
 
     targets: int32 or int64 [T]; tokens whose target is ignore_index have loss
-    0 and no gradient.  reduction: "mean" over the tokens that count, "sum"
+    0 and no gradient, whatever their x holds.  reduction: "mean" over the tokens that count, "sum"
     (loss: a float32 scalar tensor), or "none" (loss: float32 [T]).  dx [T, H]
     and dw [V, H], bf16, are the gradients of grad_scale times the reduced loss
     (of the sum, for "none"); contiguous tensors may be passed for them.  A

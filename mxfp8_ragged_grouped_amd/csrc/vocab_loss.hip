@@ -285,9 +285,11 @@ struct EpiWeight {
 };
 
 // rows copied to rows of ld (a multiple of 64) elements, zeros after H; rows may
-// start at any element
+// start at any element.  TOKENS: rows whose token does not count become zeros,
+// whatever they hold: their g is 0, and 0 times a NaN would reach all of dw.
+template <bool TOKENS>
 __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* src, int64_t lds, int rows, int H, uint16_t* dst,
-                                                       int ld) {
+                                                       int ld, Targets y) {
   const int per = ld >> 3, whole = H >> 3;
   const int64_t stride = (int64_t)gridDim.x * 256, tid = blockIdx.x * 256 + threadIdx.x;
 #pragma unroll 4
@@ -295,12 +297,13 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* src, int6
     const int r = (int)(i / whole), c = 8 * (int)(i % whole);
     v4i w;
     __builtin_memcpy(&w, src + r * lds + c, 16);
+    if (TOKENS && y.at(r) < 0) w = (v4i){0, 0, 0, 0};
     *(v4i*)(dst + (int64_t)r * ld + c) = w;
   }
   const int left = 8 * (per - whole);
   for (int64_t i = tid; i < (int64_t)rows * left; i += stride) {
     const int r = (int)(i / left), c = 8 * whole + (int)(i % left);
-    dst[(int64_t)r * ld + c] = c < H ? src[r * lds + c] : 0;
+    dst[(int64_t)r * ld + c] = c < H && !(TOKENS && y.at(r) < 0) ? src[r * lds + c] : 0;
   }
 }
 
@@ -308,6 +311,8 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* src, int6
 
 struct LossPlan {
   bool packed;   // x and w are copied to padded rows
+  bool copied;   // x is copied: packed, or for dw (0.1% of its time at 4,096 tokens and
+                 // 128,000 words), which must not meet the rows that do not count
   int ld;        // H rounded up to 64
   int bm, bn;    // tile of the products whose M axis is the tokens
   int tilesV, piece, splits;
@@ -322,6 +327,7 @@ bool aligned(const void* x, int64_t ldx, const void* w, int64_t ldw, int H) {
 LossPlan plan_of(bool direct, int T, int H, int V, bool gx, bool gw, int cus) {
   LossPlan p = {};
   p.packed = !direct;
+  p.copied = p.packed || gw;
   p.ld = (H + 63) & ~63;
   auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
   // Few tokens: narrow tiles in deep rings, bound by reading w (one token against
@@ -369,8 +375,8 @@ LossPlan plan_of(bool direct, int T, int H, int V, bool gx, bool gw, int cus) {
   p.lse = take((size_t)T * 4);
   p.rows = take((size_t)T * 4);
   p.scale = take(4);
+  if (p.copied) p.xp = take((size_t)T * p.ld * 2);
   if (p.packed) {
-    p.xp = take((size_t)T * p.ld * 2);
     p.wp = take((size_t)(p.piece < V ? p.piece : V) * p.ld * 2);
   }
   if (grads) p.g = take((size_t)T * p.piece * 2);
@@ -446,19 +452,20 @@ int mxw_vocab_loss(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ld
 
   const uint16_t* xs = x;
   int64_t lx = ldx, lw = ldw;
-  if (p.packed) {
+  if (p.copied) {
     uint16_t* xp = (uint16_t*)(ws + p.xp);
-    hipLaunchKernelGGL(pad_rows_kernel, dim3(copy_blocks((int64_t)T * p.ld / 8)), dim3(256), 0, st, x, ldx, T, H, xp,
-                       p.ld);
+    hipLaunchKernelGGL((pad_rows_kernel<true>), dim3(copy_blocks((int64_t)T * p.ld / 8)), dim3(256), 0, st, x, ldx, T,
+                       H, xp, p.ld, y);
     xs = xp;
-    lx = lw = p.ld;
+    lx = p.ld;
   }
+  if (p.packed) lw = p.ld;
   // the piece's weights as the products read them
   auto weights = [&](int v0, int width) -> const uint16_t* {
     if (!p.packed) return w + v0 * ldw;
     uint16_t* wp = (uint16_t*)(ws + p.wp);
-    hipLaunchKernelGGL(pad_rows_kernel, dim3(copy_blocks((int64_t)width * p.ld / 8)), dim3(256), 0, st, w + v0 * ldw, ldw,
-                       width, H, wp, p.ld);
+    hipLaunchKernelGGL((pad_rows_kernel<false>), dim3(copy_blocks((int64_t)width * p.ld / 8)), dim3(256), 0, st,
+                       w + v0 * ldw, ldw, width, H, wp, p.ld, Targets{});
     return wp;
   };
   auto logits = [&](const uint16_t* wv, int width) {

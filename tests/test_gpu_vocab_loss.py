@@ -115,6 +115,26 @@ def test_ignored_tokens():
     check(mxw.vocab_cross_entropy(x, w, y7, ignore_index=7), reference(x, w, y7, ignore=7), "ignore 7")
 
 
+@pytest.mark.parametrize("T,H,V", [(40, 64, 300), (40, 65, 300), (300, 320, 2049), (3, 128, 513)])
+def test_what_ignored_tokens_hold_is_not_used(T, H, V):
+    """NaN and infinities in the x of tokens that do not count, or whose target
+    is no word: the same bits as zeros there."""
+    say("ignored tokens of NaN T=%d H=%d V=%d" % (T, H, V))
+    x, w, y = make(T, H, V, 15, ignored=0.4)
+    y[0], y[1] = IGNORE, V + 5
+    out = (y < 0) | (y >= V)
+    zeros = torch.where(out[:, None], torch.zeros_like(x), x)
+    junk = torch.where(out[:, None], torch.full_like(x, float("nan")), x)
+    junk[0] = float("inf")
+    a = mxw.vocab_cross_entropy(zeros, w, y, reduction="none")
+    b = mxw.vocab_cross_entropy(junk, w, y, reduction="none")
+    assert a[0][1].isnan() and b[0][1].isnan() and (b[0][y == IGNORE] == 0).all()
+    assert torch.equal(a[0][~out], b[0][~out]) and torch.equal(a[1], b[1]) and torch.equal(a[2], b[2])
+    assert torch.isfinite(b[1]).all() and torch.isfinite(b[2]).all()
+    alone = mxw.vocab_cross_entropy(junk, w, y, reduction="none", grads=False)
+    assert torch.equal(alone[~out], b[0][~out])
+
+
 def test_targets_outside_the_vocabulary():
     x, w, y = make(20, 64, 300, 5, ignored=0.0)
     want = mxw.vocab_cross_entropy(x, w, y, reduction="none")
