@@ -10,9 +10,8 @@
 //
 //   router  logits r [T, E], in parts of H that the reader adds (skipped when the
 //           caller brings its own routing; a small router is left to gate/up)
-//   route   for more than 16 tokens, the choice of each (for fewer every
-//           workgroup of the next kernel makes it for itself: cheaper than a
-//           launch)
+//   route   for more than 4 tokens, the choice of each (for fewer every
+//           workgroup of the next kernel makes it for itself, a wave a token)
 //   gate/up items (expert, rows of Wg and Wu): h of those rows for the expert's
 //           tokens, times the token's weight, to the workspace (bf16)
 //   down    few experts: a workgroup owns 16 output columns of all tokens, its
@@ -804,10 +803,19 @@ MoePlan plan_of(int T, int E, int k, int H, int I) {
   p.parts = (H + 128 * kWaves - 1) / (128 * kWaves);
   if (p.parts > 8) p.parts = 8;
   // A router of at most 64 KiB is read by every workgroup of the gate kernel (from
-  // its XCD's L2) in about a us; a kernel of its own costs 3 us and a launch.
+  // its XCD's L2) in about a us; a kernel of its own costs 3 us and a launch: 1 token,
+  // router 8 x 2048, 18.8 us against 20.0; 16 x 2048 (16 tokens) 31.0 against 33.0,
+  // but 32 x 2048 78.0 against 75.8 and 8 x 7168 100 against 95.
   p.fused = T <= 16 && T * E <= kFusedLogits && E * H <= (32 << 10);
-  // a workgroup of the down kernel reads 16 rows of I of every chosen expert
-  p.by_item = (int64_t)most_experts(T, E, k) * I * 16 > (192 << 10);
+  // A workgroup of the plain down kernel reads 16 rows of I of every chosen expert;
+  // by items the same bytes spread over the device, for a launch and the FP32
+  // partial outputs.  Plain against by items, us: 1 token, H 2048, 88 KiB of rows a
+  // workgroup 22.0 and 24.9, 176 KiB 34.1 and 33.0; from H 4096 on it has a workgroup
+  // for each of 256 CUs: 192 KiB 50.0 and 53.8, 7168 wide 256 KiB 95 and 91.  More than
+  // 16 tokens an expert read its rows again: 64 tokens, 64 KiB even, 128 KiB 32.5 and
+  // 30.3, 176 KiB 53.8 and 38.8.
+  const int most = T > 16 ? 64 : H < 4096 ? 96 : 192;
+  p.by_item = (int64_t)most_experts(T, E, k) * I * 16 > (most << 10);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t was = at;
@@ -833,8 +841,10 @@ int check_moe(int T, int E, int k, int H, int I) {
              : MXW_OK;
 }
 
-// Items of a wave's groups: one each while that leaves workgroups idle, else two,
-// which read a step's tokens half as often.
+// Two groups a wave read a step's tokens half as often, one makes twice the items.
+// Gate/up: two only where they fill two workgroups a CU (64 tokens, 256 experts of
+// 2048 x 1408: 362 us against 392 with one; 16 tokens over 8 experts of 2048 x 512,
+// where one fills half the device and two a quarter: 28.6 against 24.0).
 template <From FROM, bool WORDS>
 void launch_gate_of(const MoeArgs& a, int cus, hipStream_t st) {
   const int64_t most = most_experts(a.T, a.E, a.k);
@@ -851,15 +861,19 @@ void launch_gate(const MoeArgs& a, int cus, hipStream_t st) {
   else launch_gate_of<FROM, true>(a, cus, st);
 }
 
+// Down, whose steps are few (I is short): two groups from a workgroup a CU on (one
+// token through 8 of 32 experts of 7168 x 2048, the layer: 90.0 us against 93.0 with
+// one; 64 tokens over 8 of 2048 x 1408, half the CUs idle with two: 41.4 against 37.1).
 template <bool WORDS>
 void launch_down_part(const MoeArgs& a, int cus, hipStream_t st) {
   const int64_t most = most_experts(a.T, a.E, a.k);
   const int64_t slots = 2 * cus, one = most * ((a.H + 63) / 64), two = most * ((a.H + 127) / 128);
-  if (two < slots)
+  if (two < cus)
     hipLaunchKernelGGL((moe_down_part_kernel<1, WORDS>), dim3((unsigned)(one < slots ? one : slots)), dim3(256), 0,
                        st, a);
   else
-    hipLaunchKernelGGL((moe_down_part_kernel<2, WORDS>), dim3((unsigned)slots), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((moe_down_part_kernel<2, WORDS>), dim3((unsigned)(two < slots ? two : slots)), dim3(256),
+                       0, st, a);
 }
 
 }  // namespace
@@ -921,7 +935,9 @@ int mxw_moe_layer(const uint16_t* x, int64_t ldx, const uint16_t* router, const 
     if (router)
       hipLaunchKernelGGL(moe_router_kernel, dim3((unsigned)((E + 15) / 16), (unsigned)((T + 15) / 16), (unsigned)p.parts),
                          dim3(kWaves * 64), 0, st, a);
-    if (router && T <= 16) {
+    // 4 tokens over 32 experts: 43.2 us with the choices made in every workgroup,
+    // 44.9 with a launch for them; 12 tokens 71.9 and 69.9; 16 tokens 77.7 and 73.3
+    if (router && T <= 4) {
       launch_gate<kLogits>(a, cus, st);
     } else {
       if (router) hipLaunchKernelGGL(moe_route_kernel, dim3((unsigned)((T + 3) / 4)), dim3(256), 0, st, a);
