@@ -453,6 +453,27 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
 
 // ---- helpers for epilogues that stage a 16-bit tile -------------------------
 
+// where the 4 values of row r from column c (a multiple of 4) on are staged
+template <int BN>
+__device__ __forceinline__ uint32_t staged_at(int r, int c) {
+  return tile_at<BN>(r, c >> 3) + ((c & 4) << 1);
+}
+
+// a matrix's tile (16-byte aligned rows of ld elements, `rows` of them; what lies
+// outside is not defined) to where one is staged; the caller waits for the loads
+template <int BM, int BN, int WAVES>
+__device__ __forceinline__ void load_tile(const TileAt& at, const uint8_t* lds, const uint16_t* src, int ld, int rows) {
+  constexpr int kChunks = BN / 8, kRows = 64 / kChunks;  // rows a load
+  static_assert(kChunks <= 64 && BM % (kRows * WAVES) == 0, "every wave has the same loads");
+  const auto rsrc = buffer_of((const uint8_t*)(src + (int64_t)at.m0 * ld + at.n0),
+                              range_of(2 * ((int64_t)(rows - at.m0) * ld - at.n0)));
+#pragma unroll
+  for (int u = at.wave; u < BM / kRows; u += WAVES) {
+    const int r = u * kRows + at.lane / kChunks, c = at.lane % kChunks;
+    load_lds16(rsrc, (uint32_t)(uintptr_t)lds + u * 1024, 2 * (r * ld + ((c ^ (r & (kChunks - 1))) << 3)));
+  }
+}
+
 // the wave's part of the tile, its sums passed four at a time (row m, columns
 // n .. n + 3, n a multiple of 4; i: the row's 16-row block in the part) through
 // quad(i, m, n, v), rounded to T and staged
@@ -469,7 +490,7 @@ __device__ __forceinline__ void stage_part(const TileAt& at, const v4f (&acc)[MI
       for (int e = 0; e < 4; ++e) v[e] = acc[i][j][e];
       quad(i, at.m0 + r, at.n0 + c, v);
       const v2i w = {(int)pack2(v[0], v[1], T()), (int)pack2(v[2], v[3], T())};
-      *(v2i*)(lds + tile_at<BN>(r, c >> 3) + ((c & 4) << 1)) = w;
+      *(v2i*)(lds + staged_at<BN>(r, c)) = w;
     }
   }
 }
@@ -507,8 +528,8 @@ __device__ __forceinline__ void store_cols(const TileAt& at, const uint8_t* lds,
   for (int u = at.wave; u < (BM / 32) * (BN / 16); u += WAVES) {
     const int r0 = (u % (BM / 32)) * 32 + 8 * g, c0 = (u / (BM / 32)) * 16;
     const int r = r0 + (i >> 2), c = c0 + 4 * (i & 3);
-    const v2i lo = lds_read_tr(lds + tile_at<BN>(r, c >> 3) + ((c & 4) << 1));
-    const v2i hi = lds_read_tr(lds + tile_at<BN>(r + 4, c >> 3) + ((c & 4) << 1));
+    const v2i lo = lds_read_tr(lds + staged_at<BN>(r, c));
+    const v2i hi = lds_read_tr(lds + staged_at<BN>(r + 4, c));
     const int n = at.n0 + c0 + i, m = at.m0 + r0;
     if (n < nrows && m < ncols) *(v4i*)(dst + n * ld + m) = (v4i){lo.x, lo.y, hi.x, hi.y};
   }

@@ -390,7 +390,9 @@ __global__ __launch_bounds__(256) void ortho_join_kernel(const float* part, int 
   *(uint2*)(S + i) = make_uint2(pack2(v[0], v[1], _Float16()), pack2(v[2], v[3], _Float16()));
 }
 
-// P = a I + b S + c S S
+// P = a I + b S + c S S.  S's tile comes to where P's is staged, by whole rows (from
+// the accumulators' layout, 32 bytes a row, a product took 4 us more: eight 1408 x
+// 2048 783 -> 762 us); every lane replaces what it reads.
 struct EpiPoly {
   static constexpr bool kStaged = true;
   struct Args {
@@ -402,11 +404,11 @@ struct EpiPoly {
   };
   template <int BM, int BN, int WM, int WN, int MI, int NI>
   static __device__ void run(const GemmArgs&, const Args& a, const TileAt& at, v4f (&acc)[MI][NI], uint8_t* lds) {
-    const uint16_t* S = a.S + at.batch * a.stride;
+    load_tile<BM, BN, WM * WN>(at, lds, a.S + at.batch * a.stride, a.ld, a.n);
+    stage_barrier<0>();
     stage_part<_Float16, BN>(at, acc, lds, [&](int, int m, int n, float (&v)[4]) {
       typedef _Float16 v4h __attribute__((ext_vector_type(4)));
-      v4h s = {};
-      if (m < a.n && n < a.ld) s = *(const v4h*)(S + (int64_t)m * a.ld + n);
+      const v4h s = *(const v4h*)(lds + staged_at<BN>(m - at.m0, n - at.n0));
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         v[e] = a.c * kPerOne * v[e] + a.b * (float)s[e] + (m == n + e ? a.a * kOne : 0.0f);
@@ -460,30 +462,42 @@ void launch_tiles(GemmArgs g, const typename Epi::Args& e, int64_t first, int64_
                      dim3(WM * WN * 64), 0, st, g, e);
 }
 
-// The tile edge with the least estimated time.  In hundredths of a us, measured
-// with whole orthogonalize calls forced to one edge (1 to 16 matrices, 256 to
-// 7,168 wide): a step of 64 k costs 145 a round of 256-tiles (one a CU); 43 a
-// round of 128-tiles while they leave a CU one, else 80 (two a CU); 39 a round of
-// 64-tiles, two a CU, else 53; and a launch 1,000, 700 or 350 besides.  So 64
-// wins for one 1408 x 2048 matrix (215 us against 275 with 128 and 571 with 256),
-// 128 for four (474 against 643 and 606), 256 for one 4096 x 7168 (2,054 against
-// 2,359 with 128).  Last, 256-tiles for the whole rounds and quarters of them for
-// the rest, where that would leave most CUs idle.
+// Hundredths of a us that `tiles` tiles of s steps of 64 k take on `cus` CUs, fitted to
+// the products of 14 shapes (1 to 32 matrices, 515 to 7,168 wide) forced to one edge,
+// most within a tenth.  256-tiles, one a CU: every round pays its first loads and its
+// stores; a step is shorter while CUs are idle (the clock is the power limit's).
+int64_t cost256(int64_t tiles, int64_t s, int64_t cus) {
+  const int64_t rest = tiles % cus;
+  return tiles / cus * (1100 + 145 * s) + (rest ? 1100 + s * (105 + 40 * rest / cus) : 0);
+}
+// two a CU, which hide that from each other; a last round that leaves a CU one is faster
+int64_t cost128(int64_t tiles, int64_t s, int64_t cus) {
+  const int64_t rest = tiles % (2 * cus);
+  return 500 + tiles / (2 * cus) * (200 + 105 * s) +
+         (rest ? 100 + s * (rest <= cus ? 48 : 80 + 25 * (rest - cus) / cus) : 0);
+}
+int64_t cost64(int64_t tiles, int64_t s, int64_t cus) {
+  const int64_t rest = tiles % (2 * cus);
+  return 100 + tiles / (2 * cus) * (120 + 50 * s) + (rest ? 200 + s * (rest <= cus ? 37 : 50) : 0);
+}
+
+// The tile edge with the least estimated time.  For P X of 1408 x 2048 matrices, us
+// with 64, 128 and 256: four 63, 39, 39; 32 of them 486, 294, 251; S of three 777 x 515
+// 7.8, 12.2, 24.7; of two 2560 x 2560 80, 44, 57.  Last, 256-tiles for the whole rounds
+// and quarters of them for the rest (S of four 4096 x 7168: 544 tiles), which costs
+// a launch more.
 template <bool TA, bool TB, bool SYM, class Epi>
 void launch_product(GemmArgs g, const typename Epi::Args& e, int cus, hipStream_t st) {
   auto tiles = [&](int b) {
     const int64_t tm = (g.M + b - 1) / b, tn = (g.N + b - 1) / b;
     return (SYM ? tm * (tm + 1) / 2 : tm * tn) * g.batch;
   };
-  auto rounds = [](int64_t n, int64_t slots) { return (n + slots - 1) / slots; };
   g.splits = 1;
   g.ksplit = (g.K + kGemmStep - 1) / kGemmStep * kGemmStep;
   const int64_t s = g.ksplit / kGemmStep, t256 = tiles(256), t128 = tiles(128), t64 = tiles(64);
-  auto cost128 = [&](int64_t n) { return 700 + s * (n <= cus ? 43 : 80 * rounds(n, 2 * cus)); };
   const int64_t whole = t256 / cus * cus, rest = t256 - whole;
-  const int64_t c256 = 1000 + s * 145 * rounds(t256, cus), c128 = cost128(t128);
-  const int64_t c64 = 350 + s * (t64 <= 2 * cus ? 39 : 53 * rounds(t64, 2 * cus));
-  const int64_t both = whole && rest ? 1000 + s * 145 * (whole / cus) + cost128(4 * rest) : INT64_MAX;
+  const int64_t c256 = cost256(t256, s, cus), c128 = cost128(t128, s, cus), c64 = cost64(t64, s, cus);
+  const int64_t both = whole && rest ? cost256(whole, s, cus) + cost128(4 * rest, s, cus) + 500 : INT64_MAX;
   if (c64 <= c128 && c64 <= c256 && c64 <= both) return launch_tiles<64, 2, 2, 5, TA, TB, SYM, Epi>(g, e, 0, t64, false, st);
   if (c128 <= c256 && c128 <= both) return launch_tiles<128, 2, 2, 0, TA, TB, SYM, Epi>(g, e, 0, t128, false, st);
   if (c256 <= both) return launch_tiles<256, 2, 4, 0, TA, TB, SYM, Epi>(g, e, 0, t256, false, st);
