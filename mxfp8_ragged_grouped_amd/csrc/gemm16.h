@@ -535,6 +535,28 @@ __device__ __forceinline__ void store_cols(const TileAt& at, const uint8_t* lds,
   }
 }
 
+// ---- host: which tile -----------------------------------------------------------
+
+// Hundredths of a us that `tiles` tiles of s steps take on `cus` CUs, fitted to the
+// products of the two operators that use this at 35 shapes, forced to one tile (1 to
+// 4,781 rows, 75 to 127,930 columns, 1 to 112 steps; most are met within a tenth).
+// 256 x 256 and 128 x 256 stand alone on a CU: every round pays its first loads and
+// its stores, and a step is shorter while CUs are idle (the clock is the power
+// limit's).  Of the others two share a CU and hide that from each other; a last
+// round that leaves a CU one is faster.
+template <int BM, int BN>
+inline int64_t tiles_cost(int64_t tiles, int64_t s, int64_t cus) {
+  constexpr bool kAlone = BN == 256;
+  const int64_t slots = kAlone ? cus : 2 * cus, full = tiles / slots, rest = tiles % slots;
+  const bool single = rest <= cus;
+  if (BM == 256) return full * (1100 + 145 * s) + (rest ? 1100 + s * (105 + 40 * rest / cus) : 0);
+  if (kAlone) return full * (600 + 110 * s) + (rest ? 600 + s * (58 + 42 * rest / cus) : 0);
+  if (BM == 128)
+    return 500 + full * (400 + 95 * s) + (rest ? 100 + s * (single ? 48 : 80 + 25 * (rest - cus) / cus) : 0);
+  if (BM == 64) return 100 + full * (220 + 43 * s) + (rest ? 200 + s * (single ? 37 : 50) : 0);
+  return 300 + full * (250 + 31 * s) + (rest ? 200 + s * (single ? 20 : 29) : 0);  // 32 x 64
+}
+
 }  // namespace mxw
 
 #endif  // MXW_GEMM16_H

@@ -462,25 +462,6 @@ void launch_tiles(GemmArgs g, const typename Epi::Args& e, int64_t first, int64_
                      dim3(WM * WN * 64), 0, st, g, e);
 }
 
-// Hundredths of a us that `tiles` tiles of s steps of 64 k take on `cus` CUs, fitted to
-// the products of 14 shapes (1 to 32 matrices, 515 to 7,168 wide) forced to one edge,
-// most within a tenth.  256-tiles, one a CU: every round pays its first loads and its
-// stores; a step is shorter while CUs are idle (the clock is the power limit's).
-int64_t cost256(int64_t tiles, int64_t s, int64_t cus) {
-  const int64_t rest = tiles % cus;
-  return tiles / cus * (1100 + 145 * s) + (rest ? 1100 + s * (105 + 40 * rest / cus) : 0);
-}
-// two a CU, which hide that from each other; a last round that leaves a CU one is faster
-int64_t cost128(int64_t tiles, int64_t s, int64_t cus) {
-  const int64_t rest = tiles % (2 * cus);
-  return 500 + tiles / (2 * cus) * (200 + 105 * s) +
-         (rest ? 100 + s * (rest <= cus ? 48 : 80 + 25 * (rest - cus) / cus) : 0);
-}
-int64_t cost64(int64_t tiles, int64_t s, int64_t cus) {
-  const int64_t rest = tiles % (2 * cus);
-  return 100 + tiles / (2 * cus) * (120 + 50 * s) + (rest ? 200 + s * (rest <= cus ? 37 : 50) : 0);
-}
-
 // The tile edge with the least estimated time.  For P X of 1408 x 2048 matrices, us
 // with 64, 128 and 256: four 63, 39, 39; 32 of them 486, 294, 251; S of three 777 x 515
 // 7.8, 12.2, 24.7; of two 2560 x 2560 80, 44, 57.  Last, 256-tiles for the whole rounds
@@ -496,8 +477,10 @@ void launch_product(GemmArgs g, const typename Epi::Args& e, int cus, hipStream_
   g.ksplit = (g.K + kGemmStep - 1) / kGemmStep * kGemmStep;
   const int64_t s = g.ksplit / kGemmStep, t256 = tiles(256), t128 = tiles(128), t64 = tiles(64);
   const int64_t whole = t256 / cus * cus, rest = t256 - whole;
-  const int64_t c256 = cost256(t256, s, cus), c128 = cost128(t128, s, cus), c64 = cost64(t64, s, cus);
-  const int64_t both = whole && rest ? cost256(whole, s, cus) + cost128(4 * rest, s, cus) + 500 : INT64_MAX;
+  const int64_t c256 = tiles_cost<256, 256>(t256, s, cus), c128 = tiles_cost<128, 128>(t128, s, cus);
+  const int64_t c64 = tiles_cost<64, 64>(t64, s, cus);
+  const int64_t both =
+      whole && rest ? tiles_cost<256, 256>(whole, s, cus) + tiles_cost<128, 128>(4 * rest, s, cus) + 500 : INT64_MAX;
   if (c64 <= c128 && c64 <= c256 && c64 <= both) return launch_tiles<64, 2, 2, 5, TA, TB, SYM, Epi>(g, e, 0, t64, false, st);
   if (c128 <= c256 && c128 <= both) return launch_tiles<128, 2, 2, 0, TA, TB, SYM, Epi>(g, e, 0, t128, false, st);
   if (c256 <= both) return launch_tiles<256, 2, 4, 0, TA, TB, SYM, Epi>(g, e, 0, t256, false, st);

@@ -10,7 +10,7 @@
 //
 // The logits are never written.  A first product walks the whole vocabulary and
 // leaves, per tile and token, the maximum and sum of exponentials of the tile's
-// 256 (few tokens: 64) logits, 8 bytes for them; they are joined in a fixed order.
+// 256 (narrow tiles: 64) logits, 8 bytes for them; they are joined in a fixed order.
 // Then the vocabulary is walked in pieces, each small enough that g of the
 // piece (bf16, unscaled: its entries lie in [-1, 1]) stays in the memory-side
 // cache: one product makes the logits again and turns them into g in its
@@ -42,6 +42,9 @@ using namespace mxw;
 // g of one piece: 4,096 tokens, 128,000 words of 2,048 take 6.83 ms with 64 MiB, 6.65
 // with 128 or 256, 6.59 with 512, 6.64 with 1,024
 constexpr int64_t kPieceBytes = 256LL << 20;
+// the padded copy of a piece's weights: one piece is copied once, more are copied for
+// either pass (61 tokens, 49,036 words of 4,106: 140 us of 912)
+constexpr int64_t kCopyBytes = 2LL << 30;
 constexpr int kMaxTokens = 128 * 1024;
 constexpr int kMaxVocab = 1 << 20;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -129,48 +132,69 @@ struct EpiStats {
   }
 };
 
-// one wave a token: its partial statistics joined (lane l: tiles l, l + 64, ...;
-// then across lanes), lse and loss
-__global__ __launch_bounds__(256) void loss_rows_kernel(const float2* part, const float* hit, Targets y, int T, int tiles,
-                                                        float* lse, float* loss) {
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (t >= T) return;
+// A token's lse and loss by one wave: its partial statistics joined (lane l: tiles l,
+// l + 64, ...; then across lanes).  All lanes return the loss.
+__device__ __forceinline__ float loss_row(const float2* part, const float* hit, const Targets& y, int T, int t, int tiles,
+                                          float* lse, float* rows) {
+  const int lane = threadIdx.x & 63;
   float m = -INFINITY, s = 0.0f;
+#pragma unroll 4
   for (int i = lane; i < tiles; i += 64) {
     const float2 v = part[(int64_t)i * T + t];
     join(m, s, v.x, v.y);
   }
   for (int d = 1; d < 64; d <<= 1) join(m, s, __shfl_xor(m, d), __shfl_xor(s, d));
+  const float l = m + __builtin_amdgcn_logf(s) * kLn2;
+  const int at = y.at(t);
+  const float loss = at == -1 ? 0.0f : at < 0 ? NAN : l - hit[t];
   if (lane == 0) {
-    const float l = m + __builtin_amdgcn_logf(s) * kLn2;
-    const int at = y.at(t);
     lse[t] = l;
-    loss[t] = at == -1 ? 0.0f : at < 0 ? NAN : l - hit[t];
+    rows[t] = loss;
   }
+  return loss;
 }
 
-// one workgroup: the reduced loss and the gradients' scale
-__global__ __launch_bounds__(1024) void loss_total_kernel(const float* rows, Targets y, int T, int mean, float grad_scale,
-                                                          float* loss, float* scale) {
-  __shared__ double sums[16];
-  __shared__ int counts[16];
+__global__ __launch_bounds__(256) void loss_rows_kernel(const float2* part, const float* hit, Targets y, int T, int tiles,
+                                                        float* lse, float* rows) {
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t < T) loss_row(part, hit, y, T, t, tiles, lse, rows);
+}
+
+// The reduced loss and the gradients' scale by one workgroup of 16 waves.  ROWS: it
+// makes the tokens' losses as well, a wave each (at most 16 tokens: saves a launch,
+// 4 us of 31 for one token against 32,000 words).
+constexpr int kTotalWaves = 16;
+template <bool ROWS>
+__global__ __launch_bounds__(kTotalWaves * 64) void loss_total_kernel(const float2* part, const float* hit, Targets y, int T,
+                                                                      int tiles, float* lse, float* rows, int mean,
+                                                                      float grad_scale, float* loss, float* scale) {
+  __shared__ double sums[kTotalWaves];
+  __shared__ int counts[kTotalWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   double s = 0.0;
   int n = 0;
-  for (int t = threadIdx.x; t < T; t += 1024) {
-    s += (double)rows[t];
-    n += y.at(t) != -1;
+  if (ROWS) {
+    if (wave < T) {
+      s = (double)loss_row(part, hit, y, T, wave, tiles, lse, rows);
+      n = y.at(wave) != -1;
+    }
+  } else {
+    for (int t = threadIdx.x; t < T; t += kTotalWaves * 64) {
+      s += (double)rows[t];
+      n += y.at(t) != -1;
+    }
+    for (int d = 1; d < 64; d <<= 1) {
+      s += __shfl_xor(s, d);
+      n += __shfl_xor(n, d);
+    }
   }
-  for (int d = 1; d < 64; d <<= 1) {
-    s += __shfl_xor(s, d);
-    n += __shfl_xor(n, d);
-  }
-  if ((threadIdx.x & 63) == 0) {
-    sums[threadIdx.x >> 6] = s;
-    counts[threadIdx.x >> 6] = n;
+  if (lane == 0) {
+    sums[wave] = s;
+    counts[wave] = n;
   }
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int i = 1; i < 16; ++i) {
+    for (int i = 1; i < kTotalWaves; ++i) {
       s += sums[i];
       n += counts[i];
     }
@@ -316,7 +340,8 @@ struct LossPlan {
   bool copied;   // x is copied: packed, or for dw (0.1% of its time at 4,096 tokens and
                  // 128,000 words), which must not meet the rows that do not count
   int ld;        // H rounded up to 64
-  int bm, bn;    // tile of the products whose M axis is the tokens
+  int bm, bn;    // the logits' tile
+  int bx, bw;    // rows of dx's tile; edge of dw's
   int tilesV, piece, splits;
   size_t part, hit, lse, rows, scale, xp, wp, g, sum, bytes;
 };
@@ -332,42 +357,54 @@ LossPlan plan_of(bool direct, int T, int H, int V, bool gx, bool gw, int cus) {
   p.copied = p.packed || gw;
   p.ld = (H + 63) & ~63;
   auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
-  // Few tokens: narrow tiles in deep rings, bound by reading w (one token against
-  // 32,000 words of 2,048: 31 us, with tiles of 128 x 256 34, of 256 x 256 47; 33
-  // tokens with gradients 140 against 138, 128 tokens 202 against 155).  Else 256 rows,
-  // or 128 where fewer rounds of those finish sooner (a step of a round costs 1.45 us
-  // against 0.85): 128 tokens 155 us with 128 rows and 178 with 256; 1,000 tokens,
-  // 64,000 words 1,152 and 916.
-  p.bm = 32;
-  p.bn = 64;
-  if (T > 32) {
-    p.bn = 256;
-    p.bm = T <= 128 || 85 * up(up(T, 128) * up(V, 256), cus) < 145 * up(up(T, 256) * up(V, 256), cus) ? 128 : 256;
-  }
+  const int64_t steps = p.ld / kGemmStep;
+  // The logits' tile.  Few tokens: narrow tiles in deep rings, which bring w to all CUs
+  // (one token against 32,000 words of 2,048: 31 us, with tiles of 128 x 256 34, of
+  // 256 x 256 47; 43 tokens, 6,223 words of 4,992, the statistics alone: 21, 55, 84;
+  // 200 tokens, 32,000 words of 2,048: 92, 38, 56; 365, 95,641 of 5,184: 1,194, 504, 412).
+  const int64_t c32 = tiles_cost<32, 64>(up(T, 32) * up(V, 64), steps, cus);
+  const int64_t c128 = tiles_cost<128, 256>(up(T, 128) * up(V, 256), steps, cus);
+  const int64_t c256 = tiles_cost<256, 256>(up(T, 256) * up(V, 256), steps, cus);
+  p.bm = c32 <= c128 && c32 <= c256 ? 32 : c128 <= c256 ? 128 : 256;
+  p.bn = p.bm == 32 ? 64 : 256;
   p.tilesV = (V + p.bn - 1) / p.bn;
   const bool grads = gx || gw;
   // a piece of the vocabulary: all of it unless g (or the padded copy of its
   // weights) gets too large
   int64_t most = kPieceBytes / (2LL * (grads ? T : 1));
-  if (p.packed && most > kPieceBytes / (2LL * p.ld)) most = kPieceBytes / (2LL * p.ld);
+  if (p.packed && most > kCopyBytes / (2LL * p.ld)) most = kCopyBytes / (2LL * p.ld);
   if (most < 256) most = 256;
   p.piece = (int)(up(up(V, up(V, most)), 256) * 256);
-  // dx: splits of a piece's vocabulary, so that the tiles fill the device in
-  // whole rounds; a split's partial sums are written and read once, at about
-  // 7 MB in the time of a step of 64 columns.  Without splits: 33 tokens, 32,000 words
-  // of 2,048 418 us against 138; 1,000 tokens, 64,000 words 1,753 against 920.
+  // dx: rows of its tile, and splits of a piece's vocabulary, so that the tiles fill
+  // the device in whole rounds; a split's partial sums are written and read once, at
+  // about 4 MB a us.  Without splits: 33 tokens, 32,000 words of 2,048 418 us against
+  // 138; 1,000 tokens, 64,000 words 1,753 against 920.
+  const int width = V < p.piece ? V : p.piece;
   p.splits = 1;
   if (gx) {
-    const int64_t tiles = up(T, p.bm) * up(p.ld, p.bn), slots = p.bm == 32 ? 2 * cus : cus;
-    const int64_t steps = up(V < p.piece ? V : p.piece, kGemmStep), sums = 8LL * T * p.ld;
+    const int64_t along = up(width, kGemmStep), sums = 8LL * T * p.ld / 40000;
     int64_t best = INT64_MAX;
-    for (int n = 1; n <= 64 && n * 4 <= steps + 3; ++n) {
-      const int64_t cost = up(tiles * n, slots) * (up(steps, n) + 8) * 1000 + n * sums / 7000;
-      if (cost < best) {
-        best = cost;
-        p.splits = n;
-      }
+    for (int n = 1; n <= 64 && n * 4 <= along + 3; ++n) {
+      const int64_t s = up(along, n);
+      const int64_t cost[3] = {tiles_cost<32, 64>(up(T, 32) * up(p.ld, 64) * n, s, cus),
+                               tiles_cost<128, 256>(up(T, 128) * up(p.ld, 256) * n, s, cus),
+                               tiles_cost<256, 256>(up(T, 256) * up(p.ld, 256) * n, s, cus)};
+      for (int i = 0; i < 3; ++i)
+        if (cost[i] + n * sums < best) {
+          best = cost[i] + n * sums;
+          p.splits = n;
+          p.bx = i == 0 ? 32 : i == 1 ? 128 : 256;
+        }
     }
+  }
+  // dw: 2,576 tokens, 1,073 words of 846: 15 us with tiles of 64, 25 with 128, 53 with
+  // 256; 1,000, 4,096 of 2,048: 36, 22, 30; 600, 32,000 of 4,096: 383, 214, 183
+  if (gw) {
+    const int64_t s = up(T, kGemmStep);
+    const int64_t w64 = tiles_cost<64, 64>(up(width, 64) * up(p.ld, 64), s, cus);
+    const int64_t w128 = tiles_cost<128, 128>(up(width, 128) * up(p.ld, 128), s, cus);
+    const int64_t w256 = tiles_cost<256, 256>(up(width, 256) * up(p.ld, 256), s, cus);
+    p.bw = w64 <= w128 && w64 <= w256 ? 64 : w128 <= w256 ? 128 : 256;
   }
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -495,11 +532,22 @@ int mxw_vocab_loss(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ld
     rc = launch_tokens<false, EpiStats>(p.bm, logits(kept, width), es, st);
     if (rc) return rc;
   }
-  hipLaunchKernelGGL(loss_rows_kernel, dim3((unsigned)((T + 3) / 4)), dim3(256), 0, st, (const float2*)(ws + p.part),
-                     (const float*)(ws + p.hit), y, T, p.tilesV, lse, rows);
-  if (reduction != MXW_NONE || grads)
-    hipLaunchKernelGGL(loss_total_kernel, dim3(1), dim3(1024), 0, st, (const float*)rows, y, T,
-                       (int)(reduction == MXW_MEAN), grad_scale, reduction == MXW_NONE ? nullptr : loss, scale);
+  {
+    const float2* part = (const float2*)(ws + p.part);
+    const float* hit = (const float*)(ws + p.hit);
+    float* total = reduction == MXW_NONE ? nullptr : loss;
+    const int mean = reduction == MXW_MEAN;
+    if (T <= kTotalWaves) {
+      hipLaunchKernelGGL((loss_total_kernel<true>), dim3(1), dim3(kTotalWaves * 64), 0, st, part, hit, y, T, p.tilesV, lse,
+                         rows, mean, grad_scale, total, scale);
+    } else {
+      hipLaunchKernelGGL(loss_rows_kernel, dim3((unsigned)((T + 3) / 4)), dim3(256), 0, st, part, hit, y, T, p.tilesV, lse,
+                         rows);
+      if (total || grads)
+        hipLaunchKernelGGL((loss_total_kernel<false>), dim3(1), dim3(kTotalWaves * 64), 0, st, part, hit, y, T, p.tilesV,
+                           lse, rows, mean, grad_scale, total, scale);
+    }
+  }
   if (grads) {
     uint16_t* gp = (uint16_t*)(ws + p.g);
     const int64_t sumStride = (int64_t)T * p.ld;
@@ -521,7 +569,7 @@ int mxw_vocab_loss(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ld
         g.splits = p.splits;
         g.ksplit = ((width + kGemmStep - 1) / kGemmStep + p.splits - 1) / p.splits * kGemmStep;
         const EpiSum::Args e = {(float*)(ws + p.sum), sumStride, p.ld, v0 > 0};
-        rc = launch_tokens<true, EpiSum>(p.bm, g, e, st);
+        rc = launch_tokens<true, EpiSum>(p.bx, g, e, st);
         if (rc) return rc;
       }
       if (dw) {
@@ -535,7 +583,9 @@ int mxw_vocab_loss(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ld
         g.splits = 1;
         g.ksplit = (T + kGemmStep - 1) / kGemmStep * kGemmStep;
         const EpiWeight::Args e = {dw + (int64_t)v0 * H, scale, width, H};
-        rc = launch<256, 256, 2, 4, 0, true, true, EpiWeight>(g, e, st);
+        rc = p.bw == 64    ? launch<64, 64, 2, 2, 5, true, true, EpiWeight>(g, e, st)
+             : p.bw == 128 ? launch<128, 128, 2, 2, 0, true, true, EpiWeight>(g, e, st)
+                           : launch<256, 256, 2, 4, 0, true, true, EpiWeight>(g, e, st);
         if (rc) return rc;
       }
     }
