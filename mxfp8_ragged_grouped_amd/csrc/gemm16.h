@@ -496,8 +496,9 @@ __device__ __forceinline__ void stage_part(const TileAt& at, const v4f (&acc)[MI
 }
 
 // the staged tile to rows of dst: rows below nrows, columns below ncols.  Rows may
-// start at any element: 16-byte stores need no alignment beyond it.
-template <int BM, int BN, int WAVES>
+// start at any element: 16-byte stores need no alignment beyond it.  ONCE: nobody reads
+// them soon, they need no place in the caches.
+template <int BM, int BN, int WAVES, bool ONCE = false>
 __device__ __forceinline__ void store_rows(const TileAt& at, const uint8_t* lds, uint16_t* dst, int64_t ld, int nrows,
                                            int ncols) {
   constexpr int kChunks = BN / 8;
@@ -510,7 +511,8 @@ __device__ __forceinline__ void store_rows(const TileAt& at, const uint8_t* lds,
     const v4i v = *(const v4i*)(lds + tile_at<BN>(r, c));
     uint16_t* to = dst + m * ld + n;
     if (n + 8 <= ncols) {
-      __builtin_memcpy(to, &v, 16);
+      if (ONCE) __builtin_nontemporal_store(v, (v4i*)to);
+      else __builtin_memcpy(to, &v, 16);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
