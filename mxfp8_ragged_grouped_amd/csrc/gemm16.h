@@ -120,7 +120,7 @@ struct GemmArgs {
   int batch, splits;
   int ksplit;   // k per split, a multiple of 64
   int first;    // this launch's first of all batch * splits * tiles
-  int quarters; // a workgroup is a quarter of such a tile, which is twice as large either way
+  int cut;      // a workgroup's tile is one of 2^cut x 2^cut that such a tile is cut into
 };
 
 // Where the 16-byte chunks of a stage's rows lie, so that a fragment read, which
@@ -179,7 +179,7 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
   TileAt at;
   {
     const int run = xcd_run(blockIdx.x, gridDim.x);
-    const int id = p.first + (p.quarters ? run >> 2 : run);
+    const int id = p.first + (run >> (2 * p.cut));
     const int t = id % p.tiles, bs = id / p.tiles;
     at.split = bs % p.splits;
     at.batch = bs / p.splits;
@@ -195,9 +195,10 @@ __global__ __launch_bounds__(WM* WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
       tn = in / rows;
       tm = 4 * band + in - tn * rows;
     }
-    if (p.quarters) {
-      tm = 2 * tm + ((run >> 1) & 1);
-      tn = 2 * tn + (run & 1);
+    if (p.cut) {
+      const int mask = (1 << p.cut) - 1;
+      tm = (tm << p.cut) + ((run >> p.cut) & mask);
+      tn = (tn << p.cut) + (run & mask);
       if (tm * BM >= p.M || tn * BN >= p.N || (SYM && tn > tm)) return;  // the whole workgroup
     }
     at.mirror = SYM && tm != tn;

@@ -448,16 +448,16 @@ struct EpiNext {
   }
 };
 
-// `count` tiles of edge B from the `first` of all on (quarters: of edge 2 B, cut in four)
+// `count` tiles of edge B 2^cut from the `first` of all on, each cut into tiles of edge B
 template <int B, int WM, int WN, int DEEP, bool TA, bool TB, bool SYM, class Epi>
-void launch_tiles(GemmArgs g, const typename Epi::Args& e, int64_t first, int64_t count, bool quarters, hipStream_t st) {
-  const int edge = quarters ? 2 * B : B;
+void launch_tiles(GemmArgs g, const typename Epi::Args& e, int64_t first, int64_t count, int cut, hipStream_t st) {
+  const int edge = B << cut;
   g.tilesM = (g.M + edge - 1) / edge;
   g.tilesN = (g.N + edge - 1) / edge;
   g.tiles = SYM ? g.tilesM * (g.tilesM + 1) / 2 : g.tilesM * g.tilesN;
   g.first = (int)first;
-  g.quarters = quarters;
-  const int64_t grid = quarters ? 4 * count : count;
+  g.cut = cut;
+  const int64_t grid = count << (2 * cut);
   hipLaunchKernelGGL((gemm16_kernel<_Float16, B, B, WM, WN, DEEP, TA, TB, SYM, Epi>), dim3((unsigned)grid),
                      dim3(WM * WN * 64), 0, st, g, e);
 }
@@ -465,8 +465,9 @@ void launch_tiles(GemmArgs g, const typename Epi::Args& e, int64_t first, int64_
 // The tile edge with the least estimated time.  For P X of 1408 x 2048 matrices, us
 // with 64, 128 and 256: four 63, 39, 39; 32 of them 486, 294, 251; S of three 777 x 515
 // 7.8, 12.2, 24.7; of two 2560 x 2560 80, 44, 57.  Last, 256-tiles for the whole rounds
-// and quarters of them for the rest (S of four 4096 x 7168: 544 tiles), which costs
-// a launch more.
+// and the rest cut into 128- or 64-tiles, which costs a launch more (S of four 4096 x
+// 7168, 544 tiles: 368 us and 81 for the rest with 128, 58 with 64; the whole of six
+// 3998 x 2200 2,241 and 2,104).
 template <bool TA, bool TB, bool SYM, class Epi>
 void launch_product(GemmArgs g, const typename Epi::Args& e, int cus, hipStream_t st) {
   auto tiles = [&](int b) {
@@ -479,13 +480,15 @@ void launch_product(GemmArgs g, const typename Epi::Args& e, int cus, hipStream_
   const int64_t whole = t256 / cus * cus, rest = t256 - whole;
   const int64_t c256 = tiles_cost<256, 256>(t256, s, cus), c128 = tiles_cost<128, 128>(t128, s, cus);
   const int64_t c64 = tiles_cost<64, 64>(t64, s, cus);
+  const int64_t r128 = tiles_cost<128, 128>(4 * rest, s, cus), r64 = tiles_cost<64, 64>(16 * rest, s, cus);
   const int64_t both =
-      whole && rest ? tiles_cost<256, 256>(whole, s, cus) + tiles_cost<128, 128>(4 * rest, s, cus) + 500 : INT64_MAX;
-  if (c64 <= c128 && c64 <= c256 && c64 <= both) return launch_tiles<64, 2, 2, 5, TA, TB, SYM, Epi>(g, e, 0, t64, false, st);
-  if (c128 <= c256 && c128 <= both) return launch_tiles<128, 2, 2, 0, TA, TB, SYM, Epi>(g, e, 0, t128, false, st);
-  if (c256 <= both) return launch_tiles<256, 2, 4, 0, TA, TB, SYM, Epi>(g, e, 0, t256, false, st);
-  launch_tiles<256, 2, 4, 0, TA, TB, SYM, Epi>(g, e, 0, whole, false, st);
-  launch_tiles<128, 2, 2, 0, TA, TB, SYM, Epi>(g, e, whole, rest, true, st);
+      whole && rest ? tiles_cost<256, 256>(whole, s, cus) + (r128 < r64 ? r128 : r64) + 500 : INT64_MAX;
+  if (c64 <= c128 && c64 <= c256 && c64 <= both) return launch_tiles<64, 2, 2, 5, TA, TB, SYM, Epi>(g, e, 0, t64, 0, st);
+  if (c128 <= c256 && c128 <= both) return launch_tiles<128, 2, 2, 0, TA, TB, SYM, Epi>(g, e, 0, t128, 0, st);
+  if (c256 <= both) return launch_tiles<256, 2, 4, 0, TA, TB, SYM, Epi>(g, e, 0, t256, 0, st);
+  launch_tiles<256, 2, 4, 0, TA, TB, SYM, Epi>(g, e, 0, whole, 0, st);
+  if (r128 < r64) return launch_tiles<128, 2, 2, 0, TA, TB, SYM, Epi>(g, e, whole, rest, 1, st);
+  launch_tiles<64, 2, 2, 5, TA, TB, SYM, Epi>(g, e, whole, rest, 2, st);
 }
 
 // ---- host -------------------------------------------------------------------
@@ -638,8 +641,8 @@ int mxw_orthogonalize(const void* G, int type, int64_t expert_stride, int64_t ro
       g.splits = p.splits;
       g.ksplit = ((p.m + kGemmStep - 1) / kGemmStep + p.splits - 1) / p.splits * kGemmStep;
       const int64_t edge = (p.n + 63) / 64, count = (int64_t)E * strideS;
-      p.tall ? launch_tiles<64, 2, 2, 5, true, true, false, EpiPart>(g, es, 0, edge * edge * E * p.splits, false, st)
-                  : launch_tiles<64, 2, 2, 5, false, false, false, EpiPart>(g, es, 0, edge * edge * E * p.splits, false, st);
+      p.tall ? launch_tiles<64, 2, 2, 5, true, true, false, EpiPart>(g, es, 0, edge * edge * E * p.splits, 0, st)
+                  : launch_tiles<64, 2, 2, 5, false, false, false, EpiPart>(g, es, 0, edge * edge * E * p.splits, 0, st);
       hipLaunchKernelGGL(ortho_join_kernel, dim3((unsigned)((count / 4 + 255) / 256)), dim3(256), 0, st,
                          (const float*)part, p.splits, count, S);
     } else {
