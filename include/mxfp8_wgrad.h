@@ -472,8 +472,8 @@ int64_t mxw_orthogonalize_workspace_size(int E, int N, int K);
 
 /*
  * mxw_vocab_loss -- softmax cross entropy of hidden states against a large
- * vocabulary, with its gradients, without keeping the logits.  For every token
- * t with target y(t):
+ * vocabulary, with its gradients, in bounded memory.  For every token t with
+ * target y(t):
  *
  *     l_tv = sum_h x[t][h] w[v][h],  loss_t = log sum_v exp(l_tv) - l_t,y(t)
  *     g_tv = (exp(l_tv) / sum_u exp(l_tu) - [v = y(t)]) * s
@@ -503,7 +503,11 @@ int64_t mxw_orthogonalize_workspace_size(int E, int N, int K);
  *            be NULL (not wanted).  They overlap no input.
  *   workspace, workspace_bytes  256-byte aligned device memory of at least
  *            mxw_vocab_loss_workspace_size(...) bytes; contents undefined on
- *            entry and exit, in use until the call's work is done.
+ *            entry and exit, in use until the call's work is done.  If
+ *            gradients are wanted it has room for the FP32 logits where they
+ *            take at most 4 GiB (64 MiB for H < 1024); with a smaller one, of
+ *            at least the size for MXW_LOSS_SMALL, they are made twice
+ *            instead: up to a quarter more time, the same bits.
  *
  * Logits, statistics and sums are FP32; the g of a piece of the vocabulary is
  * rounded to bf16 before the two products that use it.  NaN in the x of a token
@@ -520,7 +524,9 @@ int mxw_vocab_loss(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ld
 
 /* mxw_vocab_loss_workspace_size -- bytes of workspace that mxw_vocab_loss needs
  * on the current device, or a negative MXW_ERR_* code.  x and w are looked at
- * for their alignment alone; grads: 1 if dx is wanted, plus 2 if dw is. */
+ * for their alignment alone; grads: 1 if dx is wanted, plus 2 if dw is, plus
+ * MXW_LOSS_SMALL for the size without room for the logits. */
+#define MXW_LOSS_SMALL 8
 int64_t mxw_vocab_loss_workspace_size(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw, int T, int H,
                                       int V, int grads);
 

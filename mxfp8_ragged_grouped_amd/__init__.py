@@ -7,7 +7,7 @@
     q, s = quantize_tokens(x, offs)        # MXFP8 operand [H, M] from bf16 [M, H]
 
     update = orthogonalize(out)            # Newton-Schulz on every expert's gradient
-    loss, dx, dw = vocab_cross_entropy(x, w, targets)   # without keeping the logits
+    loss, dx, dw = vocab_cross_entropy(x, w, targets)   # over a large vocabulary
     y, ids, weights = moe_layer(x, router, wgu, sgu, wd, sd, top_k)   # a few tokens
 
 The first group computes, for every expert g (blog "Ragged MXFP8 Weight Gradients: A FlyDSL
@@ -578,7 +578,8 @@ def mxw_vocab_loss(x, ldx, w, ldw, targets, target_bytes, ignore_index, T, H, V,
 
 def vocab_loss_workspace_size(x, ldx, w, ldw, T, H, V, grads=3):
     """Bytes of workspace mxw_vocab_loss needs (x, w: device addresses; grads:
-    1 for dx, plus 2 for dw).  Raises MxwError on a status code."""
+    1 for dx, plus 2 for dw, plus 8 for the size without room for the logits).
+    Raises MxwError on a status code."""
     rc = _load().mxw_vocab_loss_workspace_size(x, int(ldx), w, int(ldw), int(T), int(H), int(V), int(grads))
     if rc < 0:
         raise MxwError("mxw_vocab_loss_workspace_size failed: %s" % strerror(rc))
@@ -589,17 +590,20 @@ _REDUCTIONS = {"none": 0, "mean": 1, "sum": 2}
 
 
 def vocab_cross_entropy(x, w, targets, ignore_index=-100, reduction="mean", grads=True, grad_scale=1.0, dx=None,
-                        dw=None, stream=None, workspace=None):
+                        dw=None, stream=None, workspace=None, keep_logits=True):
     """Softmax cross entropy of hidden states x [T, H] against the vocabulary
-    w [V, H] (both bf16, last axis contiguous, rows any stride apart) without
-    keeping the logits: (loss, dx, dw), or loss alone with grads=False.
+    w [V, H] (both bf16, last axis contiguous, rows any stride apart) in bounded
+    memory: (loss, dx, dw), or loss alone with grads=False.
 
     targets: int32 or int64 [T]; tokens whose target is ignore_index have loss
     0 and no gradient, whatever their x holds.  reduction: "mean" over the tokens that count, "sum"
     (loss: a float32 scalar tensor), or "none" (loss: float32 [T]).  dx [T, H]
     and dw [V, H], bf16, are the gradients of grad_scale times the reduced loss
     (of the sum, for "none"); contiguous tensors may be passed for them.  A
-    target outside the vocabulary makes the loss NaN.  Runs on `stream`
+    target outside the vocabulary makes the loss NaN.  keep_logits: for the
+    gradients the workspace holds the float32 logits if they take at most 4 GiB
+    (64 MiB for H < 1024); False makes them twice instead, which takes up to a
+    quarter more time and gives the same bits.  Runs on `stream`
     (default: the current stream) and does not synchronise; `workspace`: a
     uint8 device tensor of vocab_loss_workspace_size() bytes (default: from
     torch's caching allocator on that stream)."""
@@ -639,11 +643,12 @@ def vocab_cross_entropy(x, w, targets, ignore_index=-100, reduction="mean", grad
         dw = on.new((V, H), torch.bfloat16) if dw is None else dw
     loss = on.new((T,) if reduction == "none" else (), torch.float32)
     with on:
-        need = vocab_loss_workspace_size(x.data_ptr(), strides[0], w.data_ptr(), strides[1], T, H, V, 3 if grads else 0)
-        wp, wb, ws = on.workspace(need, workspace)
+        need = vocab_loss_workspace_size(x.data_ptr(), strides[0], w.data_ptr(), strides[1], T, H, V,
+                                         (3 if keep_logits else 11) if grads else 0)
+        wp, _, ws = on.workspace(need, workspace)
         rc = mxw_vocab_loss(x.data_ptr(), strides[0], w.data_ptr(), strides[1], targets.data_ptr(),
                             targets.element_size(), ignore_index, T, H, V, _REDUCTIONS[reduction], grad_scale,
-                            loss.data_ptr(), dx.data_ptr() if grads else 0, dw.data_ptr() if grads else 0, wp, wb,
+                            loss.data_ptr(), dx.data_ptr() if grads else 0, dw.data_ptr() if grads else 0, wp, need,
                             on.handle)
         del ws
     if rc != 0:

@@ -1,5 +1,5 @@
 // vocab_loss.hip -- softmax cross entropy over a large vocabulary with its
-// gradients, without keeping the logits (mxw_vocab_loss, declared in
+// gradients, in bounded memory (mxw_vocab_loss, declared in
 // include/mxfp8_wgrad.h), for gfx950.
 //
 //     l = x w^T,  lse_t = log sum_v exp l_tv,  loss_t = lse_t - l_t,y(t)
@@ -8,22 +8,23 @@
 // with s = grad_scale (divided by the number of tokens that count, for the
 // mean); tokens whose target is ignore_index have loss 0 and g = 0.
 //
-// The logits are never written.  A first product walks the whole vocabulary and
-// leaves, per tile and token, the maximum and sum of exponentials of the tile's
-// 256 (narrow tiles: 64) logits, 8 bytes for them; they are joined in a fixed order.
-// Then the vocabulary is walked in pieces, each small enough that g of the
-// piece (bf16, unscaled: its entries lie in [-1, 1]) stays in the memory-side
-// cache: one product makes the logits again and turns them into g in its
-// epilogue, one adds g w to the FP32 sums of dx (split over the piece's
-// vocabulary where T x H has few tiles; partial sums are joined in a fixed
-// order at the end), one writes dw = g^T x of the piece's rows.
-// 8 T H V flops with gradients, 2 T H V without: bound by the MFMA except for
-// few tokens, where reading w bounds it.  (Keeping the logits would save a quarter
-// of the flops and cost 4 T V bytes, 2.1 GB at 4,096 tokens and 128,000 words.)
+// A first product walks the whole vocabulary and leaves, per tile and token, the
+// maximum and sum of exponentials of the tile's 256 (narrow tiles: 64) logits, 8 bytes
+// for them; they are joined in a fixed order.  It also leaves the logits (FP32) if
+// gradients are wanted and they take at most 4 GiB.  Then the vocabulary is walked in
+// pieces, each small enough that g of the piece (bf16, unscaled: its entries lie in
+// [-1, 1]) stays in the memory-side cache: g comes from the kept logits, or else a
+// product makes them again and turns them into g in its epilogue (the same bits);
+// one product adds g w to the FP32 sums of dx (split over the piece's vocabulary where
+// T x H has few tiles; partial sums are joined in a fixed order at the end), one
+// writes dw = g^T x of the piece's rows.
+// 6 T H V flops with gradients (8 without room for the logits), 2 T H V without:
+// bound by the MFMA except for few tokens, where reading w (twice with gradients)
+// bounds it.
 //
-// Measured: 4,096 tokens, 128,000 words of 2,048: 6.8 ms, 1,260 TFLOP/s as
-// computed; 2,048 tokens, words of 7,168: 11.2 ms, 1,340; one token's loss against
-// 32,000 words of 2,048 with cold caches: 31 us, 4.2 TB/s.
+// Measured: 4,096 tokens, 128,000 words of 2,048: 5.8 ms, 1,100 TFLOP/s; 2,048 tokens,
+// words of 7,168: 8.8 ms, 1,280; one token's loss against 32,000 words of 2,048 with
+// cold caches: 31 us, 4.2 TB/s.
 //
 // All sums and statistics are FP32 (the mean's over tokens FP64); g is rounded
 // to bf16 because the products that follow take 16-bit operands: at most
@@ -42,6 +43,12 @@ using namespace mxw;
 // g of one piece: 4,096 tokens, 128,000 words of 2,048 take 6.83 ms with 64 MiB, 6.65
 // with 128 or 256, 6.59 with 512, 6.64 with 1,024
 constexpr int64_t kPieceBytes = 256LL << 20;
+// The logits kept for g at most (of 288 GB): 4,096 tokens, 128,000 words of 2,048 5.83 ms
+// against 6.74 with the logits made again, 2,048 tokens of 7,168 8.84 and 11.04, 32
+// tokens 1.26 and 1.56.  Words of fewer than 1,024 values make them again in less time
+// than a copy out of the caches takes: 2,048 tokens, 32,000 words of 256 291 us kept,
+// 224 made again; 905 tokens, 4,629 of 896 (17 MB) 82 and 88.
+constexpr int64_t kKeepBytes = 4LL << 30, kKeepShort = 64LL << 20;
 // the padded copy of a piece's weights: one piece is copied once, more are copied for
 // either pass (61 tokens, 49,036 words of 4,106: 140 us of 912)
 constexpr int64_t kCopyBytes = 2LL << 30;
@@ -78,6 +85,8 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
 
 // ---- the logits' statistics -------------------------------------------------
 
+// KEEP: the logits are written as well
+template <bool KEEP>
 struct EpiStats {
   static constexpr bool kStaged = false;
   struct Args {
@@ -85,6 +94,8 @@ struct EpiStats {
     float* hit;        // [T] the target's logit
     Targets y;
     int v0, V;         // the piece's first column; columns in all
+    float* logits;     // KEEP: [T][ld], ld at least V rounded up to 4
+    int ld;
   };
   template <int BM, int BN, int WM, int WN, int MI, int NI>
   static __device__ void run(const GemmArgs& p, const Args& a, const TileAt& at, v4f (&acc)[MI][NI], uint8_t* lds) {
@@ -99,6 +110,15 @@ struct EpiStats {
         for (int j = 0; j < NI; ++j)
 #pragma unroll
           for (int q = 0; q < 4; ++q) acc[i][j][q] = 16 * j + q < left ? acc[i][j][q] : -INFINITY;
+    }
+    if (KEEP) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const int t = at.m0 + at.wm + 16 * i + (at.lane & 15);
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+          if (t < p.M && 16 * j < left) *(v4f*)(a.logits + (int64_t)t * a.ld + c0 + 16 * j) = acc[i][j];
+      }
     }
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
@@ -239,6 +259,32 @@ struct EpiGrad {
   }
 };
 
+// the same from kept logits, 8 columns a thread, `per` workgroups a token
+__global__ __launch_bounds__(256) void grad_kernel(const float* logits, int ldl, const float* lse, Targets y, int v0,
+                                                   int ncols, int per, uint16_t* g, int64_t ld) {
+  const int t = blockIdx.x / per, n = 8 * ((blockIdx.x - t * per) * 256 + threadIdx.x);
+  if (n >= ncols) return;
+  const int at = y.at(t), c = v0 + n;
+  const float l = lse[t];
+  const float* from = logits + (int64_t)t * ldl + c;
+  uint32_t w[4] = {0, 0, 0, 0};
+  if (at >= 0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      v4f v = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      if (c + 4 * h < y.V) v = *(const v4f*)(from + 4 * h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v[e] = c + 4 * h + e < y.V
+                   ? __builtin_amdgcn_exp2f((v[e] - l) * kLog2e) - (c + 4 * h + e == at ? 1.0f : 0.0f)
+                   : 0.0f;
+      w[2 * h] = pack2(v[0], v[1], __bf16());
+      w[2 * h + 1] = pack2(v[2], v[3], __bf16());
+    }
+  }
+  *(uint4*)(g + (int64_t)t * ld + n) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // FP32 partial sums of dx, per split: written, or added to
 struct EpiSum {
   static constexpr bool kStaged = false;
@@ -346,7 +392,9 @@ struct LossPlan {
   int bm, bn;    // the logits' tile
   int bx, bw;    // rows of dx's tile; edge of dw's
   int tilesV, piece, splits;
-  size_t part, hit, lse, rows, scale, xp, wp, g, sum, bytes;
+  bool keep;     // the logits, for g
+  int ldl;       // their rows
+  size_t logits, part, hit, lse, rows, scale, xp, wp, g, sum, bytes;
 };
 
 // whether x and w are read in place (a tile of 256 rows stays below 2^31 bytes)
@@ -354,7 +402,7 @@ bool aligned(const void* x, int64_t ldx, const void* w, int64_t ldw, int H) {
   return (H & 63) == 0 && ldx <= 1 << 21 && ldw <= 1 << 21 && (ldx & 7) == 0 && (ldw & 7) == 0 && (((uintptr_t)x | (uintptr_t)w) & 15) == 0;
 }
 
-LossPlan plan_of(bool direct, int T, int H, int V, bool gx, bool gw, int cus) {
+LossPlan plan_of(bool direct, int T, int H, int V, bool gx, bool gw, bool may_keep, int cus) {
   LossPlan p = {};
   p.packed = !direct;
   p.copied = p.packed || gw;
@@ -409,6 +457,9 @@ LossPlan plan_of(bool direct, int T, int H, int V, bool gx, bool gw, int cus) {
     const int64_t w256 = tiles_cost<256, 256>(up(width, 256) * up(p.ld, 256), s, cus);
     p.bw = w64 <= w128 && w64 <= w256 ? 64 : w128 <= w256 ? 128 : 256;
   }
+  p.ldl = (V + 63) & ~63;
+  const int64_t kept = 4LL * T * p.ldl;
+  p.keep = may_keep && grads && kept <= (H < 1024 ? kKeepShort : kKeepBytes);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t was = at;
@@ -424,6 +475,7 @@ LossPlan plan_of(bool direct, int T, int H, int V, bool gx, bool gw, int cus) {
   if (p.packed) {
     p.wp = take((size_t)(p.piece < V ? p.piece : V) * p.ld * 2);
   }
+  if (p.keep) p.logits = take((size_t)T * p.ldl * 4);
   if (grads) p.g = take((size_t)T * p.piece * 2);
   if (gx) p.sum = take((size_t)p.splits * T * p.ld * 4);
   p.bytes = at;
@@ -473,11 +525,12 @@ extern "C" {
 
 int64_t mxw_vocab_loss_workspace_size(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw, int T, int H,
                                       int V, int grads) {
-  if (check_loss(T, H, V) || ldx < H || ldw < H || grads < 0 || grads > 3) return MXW_ERR_DIM;
+  const int which = grads & ~MXW_LOSS_SMALL;
+  if (check_loss(T, H, V) || ldx < H || ldw < H || which < 0 || which > 3) return MXW_ERR_DIM;
   int cus = 0;
   const int rc = check_device(&cus);
   if (rc) return rc;
-  return (int64_t)plan_of(aligned(x, ldx, w, ldw, H), T, H, V, grads & 1, grads & 2, cus).bytes;
+  return (int64_t)plan_of(aligned(x, ldx, w, ldw, H), T, H, V, which & 1, which & 2, which == grads, cus).bytes;
 }
 
 int mxw_vocab_loss(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw, const void* targets,
@@ -493,7 +546,9 @@ int mxw_vocab_loss(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ld
   int cus = 0;
   int rc = check_device(&cus);
   if (rc) return rc;
-  const LossPlan p = plan_of(aligned(x, ldx, w, ldw, H), T, H, V, dx != nullptr, dw != nullptr, cus);
+  LossPlan p = plan_of(aligned(x, ldx, w, ldw, H), T, H, V, dx != nullptr, dw != nullptr, true, cus);
+  if (workspace_bytes < p.bytes)
+    p = plan_of(aligned(x, ldx, w, ldw, H), T, H, V, dx != nullptr, dw != nullptr, false, cus);
   if (!workspace || workspace_bytes < p.bytes || ((uintptr_t)workspace & 255)) return MXW_ERR_WORKSPACE;
   hipStream_t st = (hipStream_t)stream;
   uint8_t* ws = (uint8_t*)workspace;
@@ -538,8 +593,11 @@ int mxw_vocab_loss(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ld
   for (int v0 = 0; v0 < V; v0 += p.piece) {
     const int width = V - v0 < p.piece ? V - v0 : p.piece;
     kept = weights(v0, width);
-    const EpiStats::Args es = {(float2*)(ws + p.part), (float*)(ws + p.hit), y, v0, V};
-    rc = launch_tokens<false, EpiStats>(p.bm, logits(kept, width), es, st);
+    float2* part = (float2*)(ws + p.part);
+    float* hit = (float*)(ws + p.hit);
+    rc = p.keep ? launch_tokens<false, EpiStats<true>>(p.bm, logits(kept, width),
+                                                       {part, hit, y, v0, V, (float*)(ws + p.logits), p.ldl}, st)
+                : launch_tokens<false, EpiStats<false>>(p.bm, logits(kept, width), {part, hit, y, v0, V, nullptr, 0}, st);
     if (rc) return rc;
   }
   {
@@ -564,9 +622,15 @@ int mxw_vocab_loss(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ld
     for (int v0 = 0; v0 < V; v0 += p.piece) {
       const int width = V - v0 < p.piece ? V - v0 : p.piece, padded = (width + 63) & ~63;
       const uint16_t* wv = V <= p.piece ? kept : weights(v0, width);
-      const EpiGrad::Args eg = {gp, p.piece, lse, y, v0, V, padded};
-      rc = launch_tokens<false, EpiGrad>(p.bm, logits(wv, width), eg, st);
-      if (rc) return rc;
+      if (p.keep) {
+        const int per = (padded + 2047) / 2048;
+        hipLaunchKernelGGL(grad_kernel, dim3((unsigned)(T * per)), dim3(256), 0, st, (const float*)(ws + p.logits), p.ldl,
+                           (const float*)lse, y, v0, padded, per, gp, (int64_t)p.piece);
+      } else {
+        const EpiGrad::Args eg = {gp, p.piece, lse, y, v0, V, padded};
+        rc = launch_tokens<false, EpiGrad>(p.bm, logits(wv, width), eg, st);
+        if (rc) return rc;
+      }
       GemmArgs g = {};
       if (dx) {
         g.A = gp;

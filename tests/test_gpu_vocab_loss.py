@@ -93,6 +93,23 @@ def test_several_pieces():
         check(mxw.vocab_cross_entropy(x, w, y), reference(x, w, y), "H=%d" % H)
 
 
+@pytest.mark.parametrize("T,H,V", [(4100, 1024, 33001), (4100, 64, 3001), (40, 1100, 20003), (33, 4992, 3001)])
+def test_logits_kept_or_made_twice(T, H, V):
+    """With room for the logits and without: the same bits, against 64 bits; in
+    several pieces, padded operands, narrow and wide tiles."""
+    say("vocab loss kept logits T=%d H=%d V=%d" % (T, H, V))
+    x, w, y = make(T, H, V, 90 + H)
+    small = mxw.vocab_loss_workspace_size(x.data_ptr(), H, w.data_ptr(), H, T, H, V, 11)
+    assert small <= mxw.vocab_loss_workspace_size(x.data_ptr(), H, w.data_ptr(), H, T, H, V) - 4 * T * V
+    got = mxw.vocab_cross_entropy(x, w, y)
+    check(got, reference(x, w, y), "T=%d H=%d V=%d" % (T, H, V))
+    again = mxw.vocab_cross_entropy(x, w, y, keep_logits=False)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    ws = torch.empty(small, dtype=torch.uint8, device=DEV)
+    again = mxw.vocab_cross_entropy(x, w, y, keep_logits=False, workspace=ws)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
 @pytest.mark.parametrize("reduction", ["mean", "sum", "none"])
 def test_reductions_and_scale(reduction):
     x, w, y = make(70, 96, 700, 3)
