@@ -29,9 +29,9 @@
 // No atomics on data: the result is bitwise reproducible.
 //
 // Measured: 64 tokens over 256 experts of the 16B shape (2.0 GB of weights) 353 us,
-// 5.6 TB/s; one token through 8 of 32 experts of the 671B shape 87 us, 4.2 TB/s
+// 5.6 TB/s; one token through 8 of 32 experts of the 671B shape 85 us, 4.3 TB/s
 // (gate/up 52 us, of them 6 before the first weight is asked for); through 2 of 8 of
-// the 16B shape 21 us, launches and latency.
+// the 16B shape 19 us, launches and latency.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -22,10 +22,10 @@
 // same MFMA rate.  2^10 keeps the entries (at most |X|_2, about 1.2) clear of
 // f16's subnormals and leaves a factor of 50 before its largest value.
 //
-// Measured, five steps: four 4096 x 7168 matrices 7.3 ms, 1,170 TFLOP/s of the flops
+// Measured, five steps: four 4096 x 7168 matrices 7.2 ms, 1,190 TFLOP/s of the flops
 // above (the library's f16 product reaches 1,520 at its best size): at the board's
-// power limit, 1.7 GHz.  Eight 1408 x 2048: 0.85 ms, 710 TFLOP/s: 168 tiles of S on
-// 256 CUs, and a fixed 7 to 10 us a product.  Three 777 x 515: 126 us, 17 launches
+// power limit, 1.7 GHz.  Eight 1408 x 2048: 0.77 ms, 780 TFLOP/s: 168 tiles of S on
+// 256 CUs, and a fixed 7 to 10 us a round of tiles.  Three 777 x 515: 124 us, 17 launches
 // of 7 us.
 //
 // X stays [N, K] as the caller has it: for N > K the products read it by
