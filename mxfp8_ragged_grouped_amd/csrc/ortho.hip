@@ -24,7 +24,7 @@
 //
 // Measured, five steps: four 4096 x 7168 matrices 7.2 ms, 1,190 TFLOP/s of the flops
 // above (the library's f16 product reaches 1,520 at its best size): at the board's
-// power limit, 1.7 GHz.  Eight 1408 x 2048: 0.77 ms, 780 TFLOP/s: 168 tiles of S on
+// power limit, 1.7 GHz.  Eight 1408 x 2048: 0.80 ms, 750 TFLOP/s: 168 tiles of S on
 // 256 CUs, and a fixed 7 to 10 us a round of tiles.  Three 777 x 515: 124 us, 17 launches
 // of 7 us.
 //
