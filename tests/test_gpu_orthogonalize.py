@@ -104,6 +104,21 @@ def test_whole_rounds_and_quarters(E, N, K):
     assert torch.equal(out[E // 2], mxw.orthogonalize(G[E // 2]))
 
 
+@pytest.mark.parametrize("E,N,K,split", [(6, 2300, 2400, False), (6, 2400, 2300, False), (17, 900, 3900, True),
+                                         (12, 1000, 1300, False)])
+def test_whole_rounds_and_smaller_tiles(E, N, K, split):
+    """256-tiles with the rest cut into 64- or 128-tiles, in either form of the
+    products: the same bits as each matrix alone (split: one alone has few tiles
+    of S, and its sums over the long axis are joined from two parts)."""
+    say("orthogonalize cut tiles E=%d N=%d K=%d" % (E, N, K))
+    g = torch.Generator(device=DEV).manual_seed(N + K)
+    G = torch.randn((E, N, K), generator=g, device=DEV).to(torch.bfloat16)
+    out = mxw.orthogonalize(G, out=poisoned(G.shape))
+    close(out, reference(G, [COEFFS] * 5), "N=%d K=%d" % (N, K))
+    for e in (0, E - 1):
+        assert split or torch.equal(out[e], mxw.orthogonalize(G[e]))
+
+
 def test_singular_values_come_near_one():
     G = spread(2, 200, 333, 5).to(torch.bfloat16)
     s = torch.linalg.svdvals(mxw.orthogonalize(G).double())
