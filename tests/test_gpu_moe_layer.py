@@ -125,6 +125,16 @@ def test_against_64_bits(T, E, k, H, I):
     check(got, a, k)
 
 
+@pytest.mark.parametrize("T,E,k,H,I", [(4, 130, 8, 512, 352), (5, 130, 8, 512, 352), (12, 64, 4, 1024, 96),
+                                       (40, 8, 2, 2048, 704), (17, 8, 2, 2048, 256), (1, 16, 8, 4096, 1568)])
+def test_either_side_of_the_rules(T, E, k, H, I):
+    """The choices in the gate kernel or by a launch, the down product whole or by
+    items, one group of rows a wave or two."""
+    say("moe_layer rules T=%d E=%d k=%d H=%d I=%d" % (T, E, k, H, I))
+    a = make(T, E, k, H, I, 4000 + T + E + H + I)
+    check(mxw.moe_layer(**a, top_k=k), a, k)
+
+
 @pytest.mark.parametrize("normalize,scale", [(True, 2.5), (False, 1.0), (False, 0.3)])
 def test_weights(normalize, scale):
     a = make(9, 24, 5, 192, 64, 1)
