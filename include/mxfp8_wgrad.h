@@ -449,8 +449,8 @@ int mxfp8_quantize_tokens(const uint16_t* x, const int32_t* offs, int E, int M, 
  * formula in 64 bits the result is off by about 0.13% of its norm (its own
  * rounding to bf16: 0.17%).  An entry of X, S or P beyond +-63 (no published
  * coefficients come near) overflows to infinity and shows as NaN.  An expert
- * whose gradient is zero gets zeros; one with a NaN or infinity gets NaN, and
- * no expert's result depends on another.  Bitwise reproducible run to run.
+ * whose gradient is zero gets zeros, with eps = 0 too; one with a NaN or
+ * infinity gets NaN, and no expert's result depends on another.  Bitwise reproducible run to run.
  *
  * Effects: enqueues one kernel (matrices that fit in LDS) or 2 + 3 * steps and
  * some more on `stream`, allocates nothing, keeps

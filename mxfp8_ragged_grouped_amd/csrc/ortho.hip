@@ -105,6 +105,21 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
   return lds[0] + lds[1] + lds[2] + lds[3];
 }
 
+// kOne / (|G| + eps) as a power of two and a factor of about kOne: as one float it
+// would overflow for norms below 3e-36.  A zero matrix with eps = 0 stays zero; a
+// NaN or infinite sum makes the factor NaN or 0, and NaN of what is infinite.
+struct Scale {
+  int exponent;
+  float factor;
+  __device__ __forceinline__ Scale(double total, float eps) {
+    const double d = sqrt(total) + (double)eps;
+    const bool plain = d > 0.0 && d < INFINITY;
+    exponent = plain ? -ilogb(d) : 0;
+    factor = d == 0.0 ? 0.0f : (float)((double)kOne / ldexp(d, exponent));
+  }
+  __device__ __forceinline__ float operator()(float v) const { return ldexpf(v, exponent) * factor; }
+};
+
 // sums of squares of one part of an expert's rows, in 64 bits: squares of any
 // bf16 or FP32 gradient are in range, and the order is fixed
 template <bool F32>
@@ -123,7 +138,7 @@ __global__ __launch_bounds__(256) void ortho_load_kernel(LoadArgs a) {
   __shared__ double lds[4];
   const int e = blockIdx.y;
   const double total = block_sum((int)threadIdx.x < a.parts ? a.sums[e * a.parts + threadIdx.x] : 0.0, lds);
-  const float scale = (float)(kOne / (sqrt(total) + (double)a.eps));
+  const Scale scale(total, a.eps);
   const int per = a.ldx >> 3, whole = a.K >> 3;
   uint16_t* X = a.X + (int64_t)e * a.N * a.ldx;
   const int64_t stride = (int64_t)gridDim.x * 256;
@@ -134,7 +149,7 @@ __global__ __launch_bounds__(256) void ortho_load_kernel(LoadArgs a) {
     load8<F32>(a.G, e * a.strideE + row * a.strideN + col, v);
     v4i w;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = (int)pack2(v[2 * j] * scale, v[2 * j + 1] * scale, _Float16());
+    for (int j = 0; j < 4; ++j) w[j] = (int)pack2(scale(v[2 * j]), scale(v[2 * j + 1]), _Float16());
     *(v4i*)(X + (int64_t)row * a.ldx + col) = w;
   }
   // the row's rest and padding
@@ -142,7 +157,7 @@ __global__ __launch_bounds__(256) void ortho_load_kernel(LoadArgs a) {
   for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < (int64_t)a.N * left * 8; i += stride) {
     const int row = (int)(i / (8 * left)), col = 8 * whole + (int)(i % (8 * left));
     const float v = col < a.K ? element<F32>(a.G, e * a.strideE + row * a.strideN + col) : 0.0f;
-    X[(int64_t)row * a.ldx + col] = (uint16_t)pack2(v * scale, 0.0f, _Float16());
+    X[(int64_t)row * a.ldx + col] = (uint16_t)pack2(scale(v), 0.0f, _Float16());
   }
 }
 
@@ -196,9 +211,9 @@ __global__ __launch_bounds__(512, 2) void ortho_small_kernel(SmallArgs a) {
   __syncthreads();
   sum = 0.0;
   for (int w = 0; w < 8; ++w) sum += red[w];
-  const float scale = (float)(kOne / (sqrt(sum) + (double)a.in.eps));
+  const Scale scale(sum, a.in.eps);
   auto put = [&](int row, int col, float v) {
-    X[a.tall ? col * ldx + row : row * ldx + col] = (uint16_t)pack2(v * scale, 0.0f, _Float16());
+    X[a.tall ? col * ldx + row : row * ldx + col] = (uint16_t)pack2(scale(v), 0.0f, _Float16());
   };
   const int per = K >> 3, rest = K & 7;
 #pragma unroll 4
@@ -212,7 +227,7 @@ __global__ __launch_bounds__(512, 2) void ortho_small_kernel(SmallArgs a) {
     } else {
       v4i w;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = (int)pack2(v[2 * j] * scale, v[2 * j + 1] * scale, _Float16());
+      for (int j = 0; j < 4; ++j) w[j] = (int)pack2(scale(v[2 * j]), scale(v[2 * j + 1]), _Float16());
       *(v4i*)(X + row * ldx + col) = w;
     }
   }

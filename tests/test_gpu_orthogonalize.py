@@ -215,3 +215,24 @@ def test_workspace_is_checked():
     big = torch.empty(need + 256, dtype=torch.uint8, device=DEV)
     with pytest.raises(mxw.MxwError):
         mxw.orthogonalize(G, workspace=big[1:])
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-45, 1e-38])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N,K", [(40, 70), (70, 40), (130, 200), (200, 130)])
+def test_zero_tiny_and_huge_experts_with_a_small_eps(N, K, dtype, eps):
+    """An expert without a gradient gives zeros for every eps; norms from below
+    2^-118, where their reciprocal leaves float32's range, up to above 2^127."""
+    say("orthogonalize small eps N=%d K=%d %s eps=%g" % (N, K, dtype, eps))
+    G = spread(5, N, K, 40 + N).float()
+    G[1] = 0
+    G[2] *= 2.0 ** -122
+    G[3] *= 2.0 ** -124
+    G[4] /= G[4].abs().max()
+    G[4] *= 2.0 ** 127
+    G = G.to(dtype)
+    assert torch.isfinite(G).all()
+    out = mxw.orthogonalize(G, eps=eps, out=poisoned(G.shape))
+    assert (out[1] == 0).all()
+    live = [0, 2, 3, 4]
+    close(out[live], reference(G[live], [COEFFS] * 5, eps), "eps=%g" % eps)
