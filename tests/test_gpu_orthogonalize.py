@@ -236,3 +236,25 @@ def test_zero_tiny_and_huge_experts_with_a_small_eps(N, K, dtype, eps):
     assert (out[1] == 0).all()
     live = [0, 2, 3, 4]
     close(out[live], reference(G[live], [COEFFS] * 5, eps), "eps=%g" % eps)
+
+
+@pytest.mark.parametrize("E,N,K", [(4, 128, 256), (3, 100, 400), (2, 257, 129), (3, 300, 520), (1, 777, 515), (2, 150, 3000),
+                                   (4, 2100, 130), (8, 1400, 2000), (8, 2000, 1400), (5, 1500, 1100), (12, 1000, 1300),
+                                   (6, 2300, 2400), (6, 2400, 2300)])
+def test_every_element(E, N, K):
+    """Every entry, so that one wrong chunk of a tile shows.  Of the tolerance at
+    the top the f16 part, 3 * 9.1 * 2^-12 of the 2-norm, is a rounding noise that
+    the random directions of these inputs spread evenly: that times the matrix's
+    rms is an entry's standard deviation at most, and six of them are passed by
+    none of 10^8 entries; the result's rounding to bf16 adds 2^-8 of the entry.
+    An entry from a wrong place is off by about 1.4 rms, 35 times the noise's share."""
+    say("orthogonalize every element E=%d N=%d K=%d" % (E, N, K))
+    g = torch.Generator(device=DEV).manual_seed(5 * N + K)
+    G = torch.randn((E, N, K), generator=g, device=DEV).to(torch.bfloat16)
+    out = mxw.orthogonalize(G, out=poisoned(G.shape))
+    ref = reference(G, [COEFFS] * 5)
+    for e in range(E):
+        rms = ref[e].square().mean().sqrt()
+        bad = ~((out[e].double() - ref[e]).abs() <= 2.0 ** -8 * ref[e].abs() + 6 * 3 * 9.1 * 2.0 ** -12 * rms)
+        assert not bad.any(), "matrix %d: %d of %d outside, first %s" % (e, int(bad.sum()), bad.numel(),
+                                                                         bad.nonzero()[0].tolist())
