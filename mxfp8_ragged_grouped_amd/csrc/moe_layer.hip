@@ -15,9 +15,11 @@
 //   gate/up items (expert, rows of Wg and Wu): h of those rows for the expert's
 //           tokens, times the token's weight, to the workspace (bf16)
 //   down    few experts: a workgroup owns 16 output columns of all tokens, its
-//           waves split the chosen experts' rows of Wd and join in a fixed order;
-//           many: items (expert, 64 columns) leave FP32 partial outputs per
-//           (token, expert), which a last kernel adds in the order of the choices
+//           waves split the chosen experts' rows of Wd in steps of 128 columns and
+//           leave a partial sum of each step in LDS; many: items (expert, 64
+//           columns) leave FP32 partial outputs per (token, expert).  Either way a
+//           token's are added in the order of its own choices, so that its result
+//           does not depend on what the other tokens chose
 //
 // The products run on the bf16 MFMA 16 x 16 x 32 with weight rows as the first
 // operand and up to 16 of the expert's tokens as the second: with few tokens the
@@ -114,12 +116,11 @@ __device__ __forceinline__ v4i operand(const Codes& c, int q) {
 
 // 16 weight rows (`row` of this lane, scales srow) times up to 16 token rows (xt of
 // this lane) over the 128-wide steps s0 .. s1 - 1 of `blocks` 32-blocks, the loads of
-// D steps in flight.
-template <int D>
-__device__ __forceinline__ v4f stream(const uint8_t* row, const uint8_t* srow, const uint16_t* xt, int blocks, int s0,
-                                      int s1) {
+// D steps in flight; each step's sums go to sink(step, sums).
+template <int D, class Sink>
+__device__ __forceinline__ void stream(const uint8_t* row, const uint8_t* srow, const uint16_t* xt, int blocks, int s0,
+                                       int s1, Sink sink) {
   const int b = (threadIdx.x & 63) >> 4;
-  v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
   Codes c[D];
   v4i xv[D][4];
   auto load = [&](int d, int s) {
@@ -141,12 +142,13 @@ __device__ __forceinline__ v4f stream(const uint8_t* row, const uint8_t* srow, c
 #pragma unroll
         for (int q = 0; q < 4; ++q) xv[d][q] = (v4i){0, 0, 0, 0};
       }
+      v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int q = 0; q < 4; ++q) acc = mfma(operand(c[d], q), xv[d][q], acc);
       if (now + D < s1) load(d, now + D);
+      sink(now, acc);
     }
   }
-  return acc;
 }
 
 // ---- reductions over a wave by DPP ------------------------------------------
@@ -685,21 +687,26 @@ __global__ __launch_bounds__(256, 2) void moe_gate_kernel(MoeArgs a) {
 // ---- down -------------------------------------------------------------------
 
 // 16 output columns of all tokens: the waves split the (expert, 128 columns of
-// I) units in order, each keeps its own sums [token][16] in LDS.
+// I) units in order and leave every unit's sums in LDS.  Which wave takes a unit
+// depends on how many experts the whole batch chose; the units do not, and a
+// token's are added over its choices and their steps, by `lanes` lanes an output
+// that take every lanes-th step and join in a fixed order.
 constexpr int kDownWaves = 16;
+constexpr int kDownLds = 144 << 10;  // of the sums, beside 8 KiB of lists
+size_t down_lds(int T, int k, int I) { return (size_t)((I + 127) / 128) * T * k * 64; }
+
 __global__ __launch_bounds__(kDownWaves * 64, 4) void moe_down_kernel(MoeArgs a) {
-  extern __shared__ __align__(16) float sums[];  // [kDownWaves][T][16]
-  __shared__ int32_t expert[MXW_MAX_EXPERTS], first[MXW_MAX_EXPERTS];
+  extern __shared__ __align__(16) float sums[];  // [steps][T k][16]
+  __shared__ int32_t expert[MXW_MAX_EXPERTS], first[MXW_MAX_EXPERTS], row[kMaxTokens * kMaxChoices];
   __shared__ uint64_t tokens[MXW_MAX_EXPERTS];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int count = *a.count;
+  const int count = *a.count, pairs = a.T * a.k;
   for (int i = tid; i < count; i += kDownWaves * 64) {
     expert[i] = a.expert[i];
     first[i] = a.first[i];
     tokens[i] = a.tokens[i];
   }
-  float* mine = sums + wave * a.T * 16;
-  for (int i = lane; i < a.T * 16; i += 64) mine[i] = 0.0f;
+  for (int i = tid; i < pairs; i += kDownWaves * 64) row[i] = a.row[i];
   __syncthreads();
   const int h0 = blockIdx.x * 16, r = lane & 15, b = lane >> 4;
   const int blocks = a.I >> 5, steps = (blocks + 3) >> 2, units = count * steps;
@@ -708,26 +715,35 @@ __global__ __launch_bounds__(kDownWaves * 64, 4) void moe_down_kernel(MoeArgs a)
   while (u < end) {
     const int which = u / steps, s0 = u - which * steps;
     const int s1 = end - which * steps < steps ? end - which * steps : steps;
-    const uint64_t mask = tokens[which];
-    const int ntok = __popcll(mask);
+    const int ntok = __popcll(tokens[which]);
     const int64_t at = (int64_t)expert[which] * a.H + h0 + r;
     for (int g0 = 0; g0 < ntok; g0 += 16) {
-      const int p = g0 + r < ntok ? g0 + r : g0;
-      const v4f acc =
-          stream<3>(a.wd + at * a.I, a.sd + at * blocks, a.h + (int64_t)(first[which] + p) * a.I, blocks, s0, s1);
-      if (g0 + r < ntok) {
-        v4f* to = (v4f*)(mine + nth_token(mask, p) * 16 + 4 * b);
-        *to = *to + acc;
-      }
+      const int p = first[which] + (g0 + r < ntok ? g0 + r : g0);
+      stream<3>(a.wd + at * a.I, a.sd + at * blocks, a.h + (int64_t)p * a.I, blocks, s0, s1, [&](int s, const v4f& acc) {
+        if (g0 + r < ntok) *(v4f*)(sums + (s * pairs + p) * 16 + 4 * b) = acc;
+      });
     }
     u = which * steps + s1;
   }
   __syncthreads();
-  for (int i = tid; i < a.T * 16; i += kDownWaves * 64) {
+  const int shift = a.T <= 4 ? 4 : a.T <= 16 ? 2 : 0, lanes = 1 << shift;
+  for (int i = tid; i < a.T * 16 << shift; i += kDownWaves * 64) {
+    const int c = i >> shift & 15, t = i >> (shift + 4);
     float v = 0.0f;
+    for (int j = 0; j < a.k; j += 4) {  // four choices' reads in flight
+      int p[4];
 #pragma unroll
-    for (int w = 0; w < kDownWaves; ++w) v += sums[w * a.T * 16 + i];
-    a.out[(int64_t)(i >> 4) * a.H + h0 + (i & 15)] = (uint16_t)pack2(v, 0.0f, __bf16());
+      for (int q = 0; q < 4; ++q) p[q] = j + q < a.k ? row[t * a.k + j + q] : -1;
+      for (int s = i & (lanes - 1); s < steps; s += lanes) {
+        float w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[q] = sums[(s * pairs + (p[q] < 0 ? 0 : p[q])) * 16 + c];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v += p[q] < 0 ? 0.0f : w[q];
+      }
+    }
+    for (int d = 1; d < lanes; d <<= 1) v += __shfl_xor(v, d);
+    if ((i & (lanes - 1)) == 0) a.out[(int64_t)t * a.H + h0 + c] = (uint16_t)pack2(v, 0.0f, __bf16());
   }
 }
 
@@ -815,7 +831,7 @@ MoePlan plan_of(int T, int E, int k, int H, int I) {
   // 16 tokens an expert read its rows again: 64 tokens, 64 KiB even, 128 KiB 32.5 and
   // 30.3, 176 KiB 53.8 and 38.8.
   const int most = T > 16 ? 64 : H < 4096 ? 96 : 192;
-  p.by_item = (int64_t)most_experts(T, E, k) * I * 16 > (most << 10);
+  p.by_item = (int64_t)most_experts(T, E, k) * I * 16 > (most << 10) || down_lds(T, k, I) > kDownLds;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t was = at;
@@ -949,7 +965,7 @@ int mxw_moe_layer(const uint16_t* x, int64_t ldx, const uint16_t* router, const 
     else launch_down_part<true>(a, cus, st);
     hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned)((H + 1023) / 1024), (unsigned)T), dim3(256), 0, st, a);
   } else {
-    hipLaunchKernelGGL(moe_down_kernel, dim3((unsigned)(H / 16)), dim3(kDownWaves * 64), kDownWaves * T * 16 * 4, st, a);
+    hipLaunchKernelGGL(moe_down_kernel, dim3((unsigned)(H / 16)), dim3(kDownWaves * 64), down_lds(T, k, I), st, a);
   }
   if (hipGetLastError() != hipSuccess) return MXW_ERR_LAUNCH;
   return MXW_OK;

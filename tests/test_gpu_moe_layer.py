@@ -306,3 +306,40 @@ def test_repeats_streams_and_graphs():
         assert all(torch.equal(p, q) for p, q in zip(got, now)), "replay %d" % i
     with pytest.raises(ValueError):
         mxw.moe_layer(**a, top_k=4, workspace=ws[:need - 1])
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(2, 16, 2, 2048, 1408), (4, 32, 2, 1024, 704), (3, 20, 3, 4128, 576),
+                                       (16, 24, 2, 512, 192), (20, 12, 2, 256, 320), (64, 9, 2, 96, 448),
+                                       (8, 64, 4, 512, 704), (40, 40, 3, 288, 832)])
+def test_neighbours_do_not_move_a_bit(T, E, k, H, I):
+    """A token's result is bit for bit the same whatever the other tokens of the
+    batch hold and choose, and whether they are there, in both forms of the down
+    product.  The second half of every expert's hidden values repeats the first
+    with the opposite down weights, so out is nothing but its sums' rounding
+    errors, which another order or grouping of the terms changes nearly everywhere."""
+    say("moe_layer neighbours T=%d E=%d k=%d H=%d I=%d" % (T, E, k, H, I))
+    a = make(T, E, k, H, I, 5000 + T + E + H + I)
+    h = I // 2
+    for n in ("wgu", "sgu"):
+        a[n][:, h:I], a[n][:, I + h:] = a[n][:, :h].clone(), a[n][:, I:I + h].clone()
+    a["wd"][..., h:], a["sd"][..., h // 32:] = a["wd"][..., :h] ^ 0x80, a["sd"][..., :h // 32].clone()
+    want = mxw.moe_layer(**a, top_k=k)
+    for t in sorted({0, T // 2, T - 1}):
+        alone = torch.zeros(T, dtype=torch.bool, device=DEV)
+        alone[t] = True
+        few = alone.clone()
+        few[(t + 1) % T] = True
+        others = dict(a, x=torch.where(alone[:, None], a["x"], a["x"].flip(1)))
+        for b, active in ((a, alone), (a, few), (others, None), (others, few)):
+            got = mxw.moe_layer(**b, top_k=k, active=active)
+            assert all(torch.equal(p[t], q[t]) for p, q in zip(got, want)), "token %d" % t
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(64, 16, 16, 64, 256), (64, 14, 14, 64, 288), (16, 7, 7, 4096, 1728),
+                                       (16, 256, 16, 4096, 32)])
+def test_down_at_the_room_for_its_sums(T, E, k, H, I):
+    """Partial sums of every step and choice that just fit in LDS, that do not
+    (by items then), and the most experts."""
+    say("moe_layer down sums T=%d E=%d k=%d H=%d I=%d" % (T, E, k, H, I))
+    a = make(T, E, k, H, I, 6000 + T + E + H + I)
+    check(mxw.moe_layer(**a, top_k=k), a, k)
