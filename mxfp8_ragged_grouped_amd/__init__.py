@@ -602,8 +602,9 @@ def vocab_cross_entropy(x, w, targets, ignore_index=-100, reduction="mean", grad
     (of the sum, for "none"); contiguous tensors may be passed for them.  A
     target outside the vocabulary makes the loss NaN.  keep_logits: for the
     gradients the workspace holds the float32 logits if they take at most 4 GiB
-    (64 MiB for H < 1024); False makes them twice instead, which takes up to a
-    quarter more time and gives the same bits.  Runs on `stream`
+    (64 MiB for H < 1024) and there is memory for them; else, or with False,
+    they are made twice, which takes up to a quarter more time and gives the
+    same bits.  Runs on `stream`
     (default: the current stream) and does not synchronise; `workspace`: a
     uint8 device tensor of vocab_loss_workspace_size() bytes (default: from
     torch's caching allocator on that stream)."""
@@ -643,9 +644,17 @@ def vocab_cross_entropy(x, w, targets, ignore_index=-100, reduction="mean", grad
         dw = on.new((V, H), torch.bfloat16) if dw is None else dw
     loss = on.new((T,) if reduction == "none" else (), torch.float32)
     with on:
-        need = vocab_loss_workspace_size(x.data_ptr(), strides[0], w.data_ptr(), strides[1], T, H, V,
-                                         (3 if keep_logits else 11) if grads else 0)
-        wp, _, ws = on.workspace(need, workspace)
+        def size(which):
+            return vocab_loss_workspace_size(x.data_ptr(), strides[0], w.data_ptr(), strides[1], T, H, V, which)
+
+        need = size((3 if keep_logits else 11) if grads else 0)
+        try:
+            wp, _, ws = on.workspace(need, workspace)
+        except torch.OutOfMemoryError:
+            if not grads or not keep_logits:
+                raise
+            need = size(11)
+            wp, _, ws = on.workspace(need, None)
         rc = mxw_vocab_loss(x.data_ptr(), strides[0], w.data_ptr(), strides[1], targets.data_ptr(),
                             targets.element_size(), ignore_index, T, H, V, _REDUCTIONS[reduction], grad_scale,
                             loss.data_ptr(), dx.data_ptr() if grads else 0, dw.data_ptr() if grads else 0, wp, need,

@@ -302,3 +302,23 @@ def test_repeats_streams_and_graphs():
         assert all(torch.equal(a, b) for a, b in zip((loss, dx, dw), now)), "replay %d" % i
     with pytest.raises(ValueError):
         mxw.vocab_cross_entropy(x, w, y, workspace=ws[:need - 1])
+
+
+def test_room_for_less_than_the_logits():
+    """With memory for the smaller workspace but not for the logits, the call
+    makes them twice instead of failing: the same bits."""
+    T, H, V = 2000, 1024, 30000
+    x, w, y = make(T, H, V, 21)
+    want = mxw.vocab_cross_entropy(x, w, y)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    small = mxw.vocab_loss_workspace_size(x.data_ptr(), H, w.data_ptr(), H, T, H, V, 11)
+    assert mxw.vocab_loss_workspace_size(x.data_ptr(), H, w.data_ptr(), H, T, H, V) >= small + 4 * T * V
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    room = torch.cuda.memory_reserved() + small + (64 << 20)  # the logits take 240 MB
+    torch.cuda.set_per_process_memory_fraction(room / torch.cuda.get_device_properties(0).total_memory)
+    try:
+        got = mxw.vocab_cross_entropy(x, w, y, dx=dx, dw=dw)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
