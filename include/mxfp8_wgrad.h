@@ -511,8 +511,11 @@ int64_t mxw_orthogonalize_workspace_size(int E, int N, int K);
  *
  * Logits, statistics and sums are FP32; the g of a piece of the vocabulary is
  * rounded to bf16 before the two products that use it.  NaN in the x of a token
- * that counts reaches that token's loss and dx, and dw; a NaN or infinite logit makes its
- * token's loss NaN.  Bitwise reproducible run to run on the same device.
+ * that counts reaches that token's loss and dx, and dw; a NaN or +infinite logit makes
+ * its token's loss NaN.  A -infinite one is a word of probability 0: the loss stays
+ * finite (infinite if it is the target).  The gradients are the formula's there too: a
+ * g of 0 times an infinite value of w or x is NaN, in every dx that meets it or in dw.
+ * Bitwise reproducible run to run on the same device.
  *
  * Effects: enqueues kernels on `stream`, allocates nothing, keeps no state,
  * never writes its inputs, does not synchronise; graph-capturable.
@@ -568,7 +571,8 @@ int64_t mxw_vocab_loss_workspace_size(const uint16_t* x, int64_t ldx, const uint
  * Codes and scales become bf16 exactly where their product has a normal bf16
  * value (below 2^-126 it is 0, beyond bf16's range infinity; scale 0xFF: NaN);
  * all sums are FP32; weight_j h_j is rounded to bf16 between the two products.
- * A NaN or infinite logit makes that token's weights and out NaN; no token's
+ * A NaN or +infinite logit, or -infinite ones alone, make that token's weights and
+ * out NaN; else an expert of -infinite logit is chosen last, with weight 0.  No token's
  * result depends on another's values.  Bitwise reproducible run to run.
  *
  * Effects: enqueues two to five kernels on `stream`, allocates nothing, keeps no

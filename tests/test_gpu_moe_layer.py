@@ -343,3 +343,20 @@ def test_down_at_the_room_for_its_sums(T, E, k, H, I):
     say("moe_layer down sums T=%d E=%d k=%d H=%d I=%d" % (T, E, k, H, I))
     a = make(T, E, k, H, I, 6000 + T + E + H + I)
     check(mxw.moe_layer(**a, top_k=k), a, k)
+
+
+def test_minus_infinite_router_logit():
+    """An expert whose logit is -inf is never chosen and changes nothing else;
+    where it has to be chosen its weight is 0."""
+    a = make(9, 8, 3, 96, 64, 31)
+    a["x"] = a["x"].abs() + 0.1
+    fewer = {n: torch.cat([t[:2], t[3:]]) if n != "x" else t for n, t in a.items()}
+    want = mxw.moe_layer(**fewer, top_k=3)
+    a["router"][2] = -float("inf")
+    got = mxw.moe_layer(**a, top_k=3)
+    assert torch.equal(got[1], torch.where(want[1] >= 2, want[1] + 1, want[1])) and torch.isfinite(got[2]).all()
+    # the weights' sums run over the lanes in another order
+    assert (got[2] - want[2]).abs().max() <= 2.0 ** -20
+    assert (got[0].double() - want[0].double()).norm() <= 2.0 ** -8 * want[0].double().norm()
+    out, ids, w = mxw.moe_layer(**a, top_k=8)
+    assert (ids[:, 7] == 2).all() and (w[:, 7] == 0).all() and torch.isfinite(w).all() and torch.isfinite(out).all()

@@ -322,3 +322,23 @@ def test_room_for_less_than_the_logits():
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_minus_infinite_logits():
+    """A word of weights -inf (x positive) is never said: the losses and the dw of
+    the other words are those without it, its own dw is 0, and dx is the NaN of
+    g = 0 times its weights.  As a target it makes the loss inf."""
+    x, w, y = make(40, 64, 300, 22, ignored=0.0)
+    x = x.abs() + 0.01
+    y[y == 9] = 10
+    without = torch.cat([w[:9], w[10:]])
+    gone = w.clone()
+    gone[9] = -float("inf")
+    loss, dx, dw = mxw.vocab_cross_entropy(x, gone, y, reduction="none")
+    ref = reference(x, without, torch.where(y > 9, y - 1, y), reduction="none")
+    assert ((loss.double() - ref["loss"]).abs() <= ref["tol"]).all() and dx.isnan().all() and (dw[9] == 0).all()
+    rest = torch.cat([dw[:9], dw[10:]]).double()
+    assert ((rest - ref["dw"]).abs() <= 2.0 ** -8 * ref["dw"].abs() + 1.05 * 2.0 ** -8 * ref["dw_terms"] + 1e-37).all()
+    y[3] = 9
+    loss = mxw.vocab_cross_entropy(x, gone, y, reduction="none", grads=False)
+    assert loss[3] == float("inf") and torch.isfinite(loss[torch.arange(40, device=DEV) != 3]).all()
