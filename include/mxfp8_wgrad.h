@@ -450,7 +450,10 @@ int mxfp8_quantize_tokens(const uint16_t* x, const int32_t* offs, int E, int M, 
  * rounding to bf16: 0.17%).  An entry of X, S or P beyond +-63 (no published
  * coefficients come near) overflows to infinity and shows as NaN.  An expert
  * whose gradient is zero gets zeros, with eps = 0 too; one with a NaN or
- * infinity gets NaN, and no expert's result depends on another.  Bitwise reproducible run to run.
+ * infinity gets NaN, and no expert's result depends on another's values.  Their
+ * number can: with few short matrices the sums over a long side are split by how many
+ * there are, and a matrix's last bits differ between calls of another E.  Bitwise
+ * reproducible run to run.
  *
  * Effects: enqueues one kernel (matrices that fit in LDS) or 2 + 3 * steps and
  * some more on `stream`, allocates nothing, keeps
@@ -557,8 +560,8 @@ int64_t mxw_vocab_loss_workspace_size(const uint16_t* x, int64_t ldx, const uint
  *            H (the layout mxfp8_grouped_fwd takes).
  *   wd, sd   E4M3 codes [E, H, I] and E8M0 scales [E, H, I/32].
  *   active   uint8 [T], 0 for a token that is not there (an unused slot of the
- *            batch): its ids are -1, its weights 0, its out zeros, and x's row
- *            is not used.  NULL: all are.
+ *            batch): its out is zeros and x's row is not used; with a router
+ *            its ids are -1 and its weights 0.  NULL: all are.
  *   T        1 .. MXW_MOE_MAX_TOKENS.   E  1 .. MXW_MAX_EXPERTS.
  *   k        1 .. 16, at most E.        H, I  multiples of 32, 32 .. 65536.
  *   ids, weights  int32 and FP32 [T, k]: outputs, inputs without a router.

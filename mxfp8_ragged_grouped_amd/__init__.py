@@ -528,7 +528,9 @@ def orthogonalize(G, out=None, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e
     G: bf16 or float32 [E, N, K] (as wgrad returns it) or [N, K], any sizes,
     the last axis contiguous, other strides free.  coeffs: (a, b, c), or one
     such triple per step.  `out` (optional) is a contiguous bf16 tensor of G's
-    shape, fully overwritten.  A zero matrix gives zeros.  Runs on `stream`
+    shape, fully overwritten.  A zero matrix gives zeros.  No matrix's result
+    depends on another's values; its last bits can depend on how many there are
+    (a long side of few matrices is summed in parts).  Runs on `stream`
     (default: the current stream) and does not synchronise; `workspace`: a
     uint8 device tensor of orthogonalize_workspace_size() bytes (default: from
     torch's caching allocator on that stream)."""
@@ -695,7 +697,7 @@ def moe_layer(x, router, wgu, sgu, wd, sd, top_k, normalize=True, scale=1.0, act
     [E, 2 I, H] (codes uint8 or float8_e4m3fn; gate rows first) and
     [E, 2 I, H/32]; wd, sd: down weights [E, H, I] and [E, H, I/32]; an
     expert computes (silu(x Wg^T) * (x Wu^T)) Wd^T.  active: bool [T], False
-    for tokens that are not there (ids -1, weights 0, out 0).  Runs on
+    for tokens that are not there (out 0; with a router ids -1, weights 0).  Runs on
     `stream` (default: the current stream) and does not synchronise;
     `workspace`: a uint8 device tensor of moe_workspace_size() bytes (default:
     from torch's caching allocator on that stream)."""
