@@ -26,9 +26,9 @@
 // Tiles of 256 x 256 by 8 waves, one workgroup a CU, are the fastest where there
 // are enough of them: the tile's bytes per flop are the least that LDS and the
 // registers allow, and moving bytes costs the power that the MFMA runs on.  8192^3
-// in bf16: 805 us (1,366 TFLOP/s, MFMA 77% busy at 1.65 GHz; the library's product
-// 735 us), without the loads 663 us.  A step costs 1.40 us, a tile 10 us besides, 7
-// of them the burst of everyone's stores.
+// in bf16, calls in a row: 817 us (1,345 TFLOP/s; the library's product on the same
+// board 733 us), MFMA 82% busy at 1.65 GHz.  By the fit below a step costs 1.45 us and
+// a tile 11 us besides, most of them the burst of everyone's stores.
 //
 // The MFMA's first operand is B, so a lane ends with 4 consecutive n of one m:
 // register r of block (mi, ni) in lane l is m = 16 mi + l % 16,

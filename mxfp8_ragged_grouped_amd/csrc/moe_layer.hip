@@ -30,10 +30,10 @@
 // two) to 4 MFMA operands.  The tokens' operand is loaded in the same order of k.
 // No atomics on data: the result is bitwise reproducible.
 //
-// Measured: 64 tokens over 256 experts of the 16B shape (2.0 GB of weights) 353 us,
-// 5.6 TB/s; one token through 8 of 32 experts of the 671B shape 85 us, 4.3 TB/s
-// (gate/up 52 us, of them 6 before the first weight is asked for); through 2 of 8 of
-// the 16B shape 19 us, launches and latency.
+// Measured: 64 tokens over 256 experts of the 16B shape (2.0 GB of weights) 361 us,
+// 5.5 TB/s (reading alone reaches 7.0); one token through 8 of 32 experts of the 671B
+// shape 85 us, 4.3 TB/s (gate/up 51 us, of them 6 before the first weight is asked
+// for); through 2 of 8 of the 16B shape 19 us, launches and latency.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -826,10 +826,13 @@ MoePlan plan_of(int T, int E, int k, int H, int I) {
   // A workgroup of the plain down kernel reads 16 rows of I of every chosen expert;
   // by items the same bytes spread over the device, for a launch and the FP32
   // partial outputs.  Plain against by items, us: 1 token, H 2048, 88 KiB of rows a
-  // workgroup 22.0 and 24.9, 176 KiB 34.1 and 33.0; from H 4096 on it has a workgroup
-  // for each of 256 CUs: 192 KiB 50.0 and 53.8, 7168 wide 256 KiB 95 and 91.  More than
-  // 16 tokens an expert read its rows again: 64 tokens, 64 KiB even, 128 KiB 32.5 and
-  // 30.3, 176 KiB 53.8 and 38.8.
+  // workgroup 22.8 and 23.7, 110 KiB 24.6 and 24.5, 176 KiB 32.7 and 30.5; from H 4096
+  // on it has a workgroup for each of 256 CUs (the whole device's: the size query runs
+  // without one): 4096 wide 192 KiB 46.3 and 48.1, 256 KiB 52.3 and 57.2, 7168 wide
+  // 192 KiB 81.2 and 76.5, 256 KiB 93.4 and 85.3, so that one bound loses up to a
+  // tenth on one side of it or the other.  More than 16 tokens an expert read its rows
+  // again: 64 tokens, 64 KiB 29.4 and 26.3 (the bound's edge), 128 KiB 38.6 and 27.8,
+  // 176 KiB 47.5 and 32.6.  And the plain kernel's sums have to fit in LDS.
   const int most = T > 16 ? 64 : H < 4096 ? 96 : 192;
   p.by_item = (int64_t)most_experts(T, E, k) * I * 16 > (most << 10) || down_lds(T, k, I) > kDownLds;
   size_t at = 0;

@@ -22,10 +22,10 @@
 // same MFMA rate.  2^10 keeps the entries (at most |X|_2, about 1.2) clear of
 // f16's subnormals and leaves a factor of 50 before its largest value.
 //
-// Measured, five steps: four 4096 x 7168 matrices 7.2 ms, 1,190 TFLOP/s of the flops
+// Measured, five steps: four 4096 x 7168 matrices 7.0 ms, 1,220 TFLOP/s of the flops
 // above (the library's f16 product reaches 1,520 at its best size): at the board's
-// power limit, 1.7 GHz.  Eight 1408 x 2048: 0.80 ms, 750 TFLOP/s: 168 tiles of S on
-// 256 CUs, and a fixed 7 to 10 us a round of tiles.  Three 777 x 515: 124 us, 17 launches
+// power limit, 1.7 GHz.  Eight 1408 x 2048: 0.82 ms, 730 TFLOP/s: 168 tiles of S on
+// 256 CUs, and a fixed 7 to 10 us a round of tiles.  Three 777 x 515: 125 us, 17 launches
 // of 7 us.
 //
 // X stays [N, K] as the caller has it: for N > K the products read it by
@@ -555,9 +555,10 @@ OrthoPlan plan_of(int E, int N, int K) {
   p.S = take((size_t)E * p.n * p.lds * 2);
   p.P = take((size_t)E * p.n * p.lds * 2);
   // A long m over few 64-tiles of S (counting both triangles: the halves' saving
-  // is small there) is split so that about 512 workgroups take 4 steps of it or
-  // more; joining costs a launch, about 10 steps.  Two 177 x 6597 matrices: 236 us
-  // without, 138 with.
+  // is small there) is split so that about 512 workgroups (two for each of the whole
+  // device's 256 CUs: the size query runs without one) take 4 steps of it or more;
+  // joining costs a launch, about 10 steps.  Two 177 x 6597 matrices: 236 us without,
+  // 138 with.  So a matrix's bits depend on E here.
   const int64_t tiles = (int64_t)((p.n + 63) / 64) * ((p.n + 63) / 64) * E, steps = (p.m + 63) / 64;
   p.splits = (int)(512 / tiles < steps / 4 ? 512 / tiles : steps / 4);
   if (p.splits < 2 || steps - steps / p.splits < 16) p.splits = 1;

@@ -22,8 +22,8 @@
 // bound by the MFMA except for few tokens, where reading w (twice with gradients)
 // bounds it.
 //
-// Measured: 4,096 tokens, 128,000 words of 2,048: 5.8 ms, 1,100 TFLOP/s; 2,048 tokens,
-// words of 7,168: 8.8 ms, 1,280; one token's loss against 32,000 words of 2,048 with
+// Measured: 4,096 tokens, 128,000 words of 2,048: 5.6 ms, 1,150 TFLOP/s; 2,048 tokens,
+// words of 7,168: 8.7 ms, 1,290; one token's loss against 32,000 words of 2,048 with
 // cold caches: 31 us, 4.2 TB/s.
 //
 // All sums and statistics are FP32 (the mean's over tokens FP64); g is rounded
