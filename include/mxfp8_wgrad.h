@@ -49,6 +49,8 @@ extern "C" {
                                   or not 256-byte aligned */
 #define MXW_ERR_SCRATCH (-7)   /* the shape needs more workspace than
                                   MXW_SCRATCH_BYTES (no-allocation entry) */
+#define MXW_ERR_OVERLAP (-8)   /* what the call writes overlaps itself or an
+                                  input */
 
 /* Size of the static device scratch of mxfp8_wgrad_grouped_noalloc. */
 #define MXW_SCRATCH_BYTES (160u * 1024u * 1024u)
@@ -590,6 +592,196 @@ int mxw_moe_layer(const uint16_t* x, int64_t ldx, const uint16_t* router, const 
 /* mxw_moe_workspace_size -- bytes of workspace that mxw_moe_layer needs, or
  * MXW_ERR_DIM.  Host-only. */
 int64_t mxw_moe_workspace_size(int T, int E, int k, int H, int I);
+
+/* Most choices (experts) of a token in the entries below. */
+#define MXW_MAX_CHOICES 64
+
+/*
+ * mxw_sort_tokens -- which row every token goes to when tokens are grouped by
+ * expert, as the grouped products above take them.  With e = ids[t][j], choices in the
+ * order (t, j):
+ *
+ *     counts[e] = the number of choices of expert e
+ *     offs[e]   = sum over e' <= e of counts[e'] rounded up to a multiple of `align`
+ *     rows[t][j] = offs[e-1] + the number of earlier choices of e;  -1 for an id
+ *                  outside [0, E) (an empty slot)
+ *
+ * offs is the cumulative ends that the grouped products read; the rows from an
+ * expert's last choice to its end are padding.
+ *
+ * Arguments (caller-owned DEVICE memory):
+ *   ids, id_bytes, ld  [T, k] int32 (4) or int64 (8), rows ld >= k elements apart.
+ *   T, k     T >= 0, 1 <= k <= MXW_MAX_CHOICES, T k <= MXW_MAX_ROWS.  An expert may
+ *            be named more than once by a token: each is a row of its own.
+ *   E        1 .. MXW_MAX_EXPERTS.
+ *   align    1 .. 1024 (32 is what mxfp8_wgrad_grouped needs, 16 bf16_wgrad_grouped).
+ *   offs, counts  int32 [E];  rows  int32 [T, k]; fully overwritten.
+ *   workspace, workspace_bytes  256-byte aligned device memory of at least
+ *            mxw_sort_workspace_size(T, k, E) bytes (NULL if that is 0: up to 16,384
+ *            choices); contents undefined on entry and exit.
+ *
+ * mxw_token_rows gives the rows that any ids of these sizes fit in, a multiple of
+ * align: what to allocate without reading offs on the host.  MXW_ERR_DIM if that is
+ * over MXW_MAX_ROWS.
+ *
+ * Effects: enqueues one or two kernels on `stream`, allocates nothing, keeps no state,
+ * does not synchronise; graph-capturable.  Returns MXW_OK or a negative code.
+ */
+int mxw_sort_tokens(const void* ids, int id_bytes, int64_t ld, int T, int k, int E, int align, int32_t* offs,
+                    int32_t* counts, int32_t* rows, void* workspace, size_t workspace_bytes, void* stream);
+int64_t mxw_token_rows(int T, int k, int E, int align);
+int64_t mxw_sort_workspace_size(int T, int k, int E);
+
+/*
+ * mxw_dispatch_tokens -- tokens copied to their rows, as they are, as MXFP8 or both:
+ *
+ *     xs[rows[t][j]] = x[t],   (q, s)[rows[t][j]] = MXFP8 of x[t]
+ *
+ * with blocks of 32 along H and the codes and scales of mxw_quantize_rows (bit for
+ * bit): A and sA of mxfp8_grouped_fwd.  The padding rows of every expert (from
+ * offs[e-1] + counts[e] to offs[e]) become zeros (codes 0, scales 127); rows from
+ * offs[E-1] on are left as they were.  The gradient with respect to x is
+ * mxw_combine_tokens of the rows' gradient, without weights.
+ *
+ * Arguments (caller-owned DEVICE memory):
+ *   x, type, ldx  [T, H] MXW_BF16 or MXW_F32, rows ldx >= H elements apart.
+ *   offs, counts, rows  as mxw_sort_tokens leaves them.  A row outside [0, R) is
+ *            skipped (an empty slot, or rows that were cut); whatever they hold, no
+ *            store leaves the outputs.
+ *   T, k, E  as above.  H  1 .. 65536, a multiple of 32 with q.
+ *   R        rows of the outputs, 0 .. MXW_MAX_ROWS.
+ *   xs       [R, H] of `type`, contiguous, or NULL.
+ *   q, s     uint8 [R, H] and [R, H/32], contiguous, or both NULL; q 8-byte aligned.
+ * The outputs overlap no input.  Effects: one kernel on `stream`, allocates nothing,
+ * keeps no state, does not synchronise; graph-capturable.
+ */
+int mxw_dispatch_tokens(const void* x, int type, int64_t ldx, const int32_t* offs, const int32_t* counts,
+                        const int32_t* rows, int T, int k, int E, int H, int R, void* xs, uint8_t* q, uint8_t* s,
+                        void* stream);
+
+/*
+ * mxw_combine_tokens -- the experts' rows joined to tokens again:
+ *
+ *     out[t] = sum_j weights[t][j] y[rows[t][j]] + residual[t]
+ *
+ * summed in FP32 in the order of j, the residual last, and rounded once.  Choices
+ * whose row is outside [0, R) count nothing, whatever their weight holds.
+ *
+ *   y, type, ldy  [R, H] MXW_BF16 or MXW_F32, rows ldy >= H elements apart.
+ *   weights  FP32 [T, k], contiguous, or NULL: 1.
+ *   residual, ldr  [T, H] of `type`, rows ldr >= H elements apart, or NULL: none.
+ *   out      [T, H] of `type`, contiguous; it may be residual itself (ldr == H).
+ * Effects: as above.  A token's result depends on its own rows and weights alone.
+ */
+int mxw_combine_tokens(const void* y, int type, int64_t ldy, const int32_t* rows, const float* weights,
+                       const void* residual, int64_t ldr, int T, int k, int H, int R, void* out, void* stream);
+
+/*
+ * mxw_combine_tokens_grad -- the gradients of mxw_combine_tokens from that of out:
+ *
+ *     dy[rows[t][j]] = weights[t][j] dout[t],   dweights[t][j] = <dout[t], y[rows[t][j]]>
+ *
+ * (that of the residual is dout).  dy in the type of dout, and/or as MXFP8 rows of what
+ * dy would hold (q, s, as in mxw_dispatch_tokens: A and sA of the data gradient's
+ * product); padding rows become zeros and rows from offs[E-1] on are left as they were.
+ * dweights FP32 [T, k], 0 for empty slots; sums in FP32.  Any of the three outputs may
+ * be NULL (not wanted), and offs and counts if dy and q are.  y is read only for
+ * dweights; dy may be y itself (ldy == H).  Other sizes, checks and effects: as above.
+ */
+int mxw_combine_tokens_grad(const void* dout, int type, int64_t ldo, const void* y, int64_t ldy, const int32_t* offs,
+                            const int32_t* counts, const int32_t* rows, const float* weights, int T, int k, int E, int H,
+                            int R, void* dy, uint8_t* q, uint8_t* s, float* dweights, void* stream);
+
+/* Formats of quantised rows and weights. */
+#define MXW_MXFP8 0 /* E4M3 codes, an E8M0 scale for 32 */
+#define MXW_MXFP4 1 /* E2M1 codes, two a byte, an E8M0 scale for 32 */
+#define MXW_INT4 2  /* unsigned 4-bit codes, two a byte, a bf16 scale (and a zero) for a group */
+
+/*
+ * mxw_quantize_rows -- the row-wise MX quantiser: operands whose blocks of 32 lie
+ * along the rows, as mxfp8_grouped_fwd takes them (MXFP8) and mxw_linear_4bit takes its
+ * weights (MXFP4).  For every block, with amax = max |x|:
+ *
+ *     s = clamp(floor(log2 amax) - b + 127, 0, 254), 127 if amax == 0, and 255 (NaN) if
+ *         the block holds an infinity or a NaN
+ *     q = the format's number nearest to x / 2^(s - 127): ties to even, saturated at
+ *         its largest, zeros as +0 (under a NaN scale: 0x7F in MXFP8, 0 in MXFP4)
+ *
+ * with b = 8 and the largest 448 (MXFP8, as mxfp8_quantize_tokens), b = 2 and 6 (MXFP4).
+ *
+ *   x, type, ldx  [R, C] MXW_BF16 or MXW_F32, rows ldx >= C elements apart.
+ *   R        >= 0, at most 2^31 and 2^36 elements in all.  C  a multiple of 32, 32 .. 65536.
+ *   q        uint8 [R, C] (MXFP8) or [R, C/2] (MXFP4: element 2 i in the low half of byte
+ *            i), contiguous, 8-byte aligned.  s  uint8 [R, C/32], contiguous.
+ * Effects: one kernel on `stream`, allocates nothing, keeps no state, does not
+ * synchronise; graph-capturable.
+ */
+int mxw_quantize_rows(const void* x, int type, int64_t ldx, int64_t R, int C, int format, uint8_t* q, uint8_t* s,
+                      void* stream);
+
+/* Norms of mxw_clip_grads, and its most tensors. */
+#define MXW_NORM_2 2
+#define MXW_NORM_MAX 0
+#define MXW_MAX_TENSORS 65536
+
+/*
+ * mxw_clip_grads -- the norm of many gradients together, and the gradients clipped to
+ * it:
+ *
+ *     n = (sum over all elements of g^2)^(1/2)   or   max |g|
+ *     out[i] = g[i] min(1, max_norm / (n + eps))
+ *
+ * Arguments:
+ *   grads, outs, sizes, types  HOST arrays of `count` entries, read during the call:
+ *            device addresses, element counts (0 .. 2^40; a NULL address with 0) and
+ *            MXW_BF16 or MXW_F32.  outs[i] may be grads[i] (in place); otherwise nothing
+ *            that is written may overlap (MXW_ERR_OVERLAP).  outs NULL: the norm alone.
+ *   count    0 .. MXW_MAX_TENSORS (0: norm 0).
+ *   norm_type  MXW_NORM_2 or MXW_NORM_MAX.   max_norm, eps  >= 0.
+ *   norm     DEVICE memory, one FP32: n before clipping.
+ *   workspace, workspace_bytes  256-byte aligned device memory of at least
+ *            mxw_clip_workspace_size(count) bytes; contents undefined on entry and exit.
+ *
+ * Squares are summed in 64 bits: the norm neither overflows nor vanishes before FP32
+ * does.  The product with the factor is FP32, rounded once.  A NaN makes the norm and
+ * all outputs NaN; an infinity makes the norm infinite and the factor 0 (its own element
+ * NaN), unless max_norm is infinite too (NaN).  Bitwise reproducible run to run.
+ * Effects: enqueues two kernels for every 96 tensors on `stream`, allocates nothing on
+ * the device, keeps no state, does not synchronise; graph-capturable (the addresses are
+ * the kernels' arguments).
+ */
+int mxw_clip_grads(const void* const* grads, void* const* outs, const int64_t* sizes, const int32_t* types, int count,
+                   int norm_type, double max_norm, double eps, float* norm, void* workspace, size_t workspace_bytes,
+                   void* stream);
+int64_t mxw_clip_workspace_size(int count);
+
+/*
+ * mxw_linear_4bit -- a dense product of a few tokens with 4-bit weights (the
+ * projections and the vocabulary around mxw_moe_layer in generation):
+ *
+ *     out[t][n] = sum_k x[t][k] v[n][k]
+ *     MXW_MXFP4:  v = e2m1(code) 2^(scale - 127)        (scale 0xFF: NaN)
+ *     MXW_INT4:   v = (code - zero) scale
+ *
+ * Arguments (caller-owned DEVICE memory):
+ *   x, ldx   bf16 [T, K], rows ldx >= K elements apart (a multiple of 8), 16-byte aligned.
+ *   codes    uint8 [N, K/2], element 2 i of a row in the low half of byte i; contiguous,
+ *            16-byte aligned.
+ *   scales   [N, K/group]: E8M0 bytes (MXW_MXFP4) or bf16 (MXW_INT4), contiguous.
+ *   zeros    uint8 [N, K/group], 0 .. 15, MXW_INT4 only, or NULL: 8.
+ *   group    32 (MXW_MXFP4) or 32, 64, 128 (MXW_INT4).
+ *   T        0 .. MXW_MOE_MAX_TOKENS.  N  1 .. 2^20.  K  a multiple of group, up to 65536.
+ *   out, out_type  [T, N] MXW_BF16 or MXW_F32, contiguous, fully overwritten.
+ *
+ * The numbers that MXFP4 codes stand for are exact in bf16 where they are normal there
+ * (below 2^-126 they are 0, beyond bf16's range infinity); integer codes enter as whole
+ * numbers, and each group's FP32 sum is scaled.  All sums are FP32.  A token's result
+ * does not depend on the other tokens' values.  Bitwise reproducible run to run.
+ * Effects: one kernel on `stream`, allocates nothing, keeps no state, does not
+ * synchronise; graph-capturable.
+ */
+int mxw_linear_4bit(const uint16_t* x, int64_t ldx, const uint8_t* codes, const void* scales, const uint8_t* zeros,
+                    int format, int group, int T, int K, int N, void* out, int out_type, void* stream);
 
 /* mxw_strerror -- a static, human-readable message for a return code. */
 const char* mxw_strerror(int code);

@@ -10,6 +10,14 @@
     loss, dx, dw = vocab_cross_entropy(x, w, targets)   # over a large vocabulary
     y, ids, weights = moe_layer(x, router, wgu, sgu, wd, sd, top_k)   # a few tokens
 
+    plan = sort_tokens(ids, E)             # tokens grouped by expert: ends, counts, rows
+    xs, q, s = dispatch_tokens(x, plan, mxfp8=True)      # to their rows, bf16 and MXFP8
+    out = combine_tokens(y, plan, weights)               # and back
+    dy, dweights = combine_tokens_grad(dout, y, plan, weights)
+    q, s = quantize_rows(x)                # MXFP8 rows, fwd's operands
+    norm = clip_grad_norm(grads, 1.0)      # many tensors, in place
+    logits = linear_4bit(x, codes, scales) # a few tokens, 4-bit weights
+
 The first group computes, for every expert g (blog "Ragged MXFP8 Weight Gradients: A FlyDSL
 Grouped GEMM on MI355X", section 1),
 
@@ -29,7 +37,9 @@ operands from bf16 activations / gradients.  The second group is what stands
 around those products when such a layer is trained and served: the optimiser's
 orthogonalised update of the experts' weights, the loss that the gradients
 start from, and the layer for single tokens and small batches (each described
-at its function).  Everything
+at its function).  The third moves tokens between their own order and the experts'
+rows with the gradients of that, makes row-wise operands, clips gradients, and has the
+dense products of generation on 4-bit weights.  Everything
 runs in the HIP library ``lib/libmxfp8_wgrad.so`` (C ABI in
 ``include/mxfp8_wgrad.h``); this module only checks tensor metadata and passes
 device pointers and the current stream.  There is no fallback: if the library
@@ -43,6 +53,7 @@ scale pre-shuffle.  wgrad() and wgrad_bf16() use the _ws variants unless
 plain=True, taking the workspace from torch's caching allocator on the
 stream the call runs on (or from `workspace`, a uint8 device tensor).
 """
+import collections
 import ctypes
 import os
 
@@ -56,6 +67,10 @@ __all__ = ["wgrad", "mxfp8_wgrad_grouped", "mxfp8_wgrad_grouped_ws", "mxfp8_wgra
            "orthogonalize", "mxw_orthogonalize", "orthogonalize_workspace_size",
            "vocab_cross_entropy", "mxw_vocab_loss", "vocab_loss_workspace_size",
            "moe_layer", "mxw_moe_layer", "moe_workspace_size",
+           "TokenPlan", "sort_tokens", "mxw_sort_tokens", "sort_workspace_size", "token_rows",
+           "dispatch_tokens", "mxw_dispatch_tokens", "combine_tokens", "mxw_combine_tokens",
+           "combine_tokens_grad", "mxw_combine_tokens_grad", "quantize_rows", "mxw_quantize_rows",
+           "clip_grad_norm", "grad_norm", "mxw_clip_grads", "clip_workspace_size", "linear_4bit", "mxw_linear_4bit",
            "strerror", "version", "library_path", "MxwError"]
 
 _lib = None
@@ -125,6 +140,26 @@ def _load():
     lib.mxw_moe_layer.argtypes = [P, L, P, P, P, P, P, P, I, I, I, I, I, I, F, P, P, P, P, S, P]
     lib.mxw_moe_workspace_size.restype = L
     lib.mxw_moe_workspace_size.argtypes = [I, I, I, I, I]
+    lib.mxw_token_rows.restype = L
+    lib.mxw_token_rows.argtypes = [I, I, I, I]
+    lib.mxw_sort_workspace_size.restype = L
+    lib.mxw_sort_workspace_size.argtypes = [I, I, I]
+    lib.mxw_sort_tokens.restype = I
+    lib.mxw_sort_tokens.argtypes = [P, I, L, I, I, I, I, P, P, P, P, S, P]
+    lib.mxw_dispatch_tokens.restype = I
+    lib.mxw_dispatch_tokens.argtypes = [P, I, L, P, P, P, I, I, I, I, I, P, P, P, P]
+    lib.mxw_combine_tokens.restype = I
+    lib.mxw_combine_tokens.argtypes = [P, I, L, P, P, P, L, I, I, I, I, P, P]
+    lib.mxw_combine_tokens_grad.restype = I
+    lib.mxw_combine_tokens_grad.argtypes = [P, I, L, P, L, P, P, P, P, I, I, I, I, I, P, P, P, P, P]
+    lib.mxw_quantize_rows.restype = I
+    lib.mxw_quantize_rows.argtypes = [P, I, L, L, I, I, P, P, P]
+    lib.mxw_clip_grads.restype = I
+    lib.mxw_clip_grads.argtypes = [P, P, P, P, I, I, ctypes.c_double, ctypes.c_double, P, P, S, P]
+    lib.mxw_clip_workspace_size.restype = L
+    lib.mxw_clip_workspace_size.argtypes = [I]
+    lib.mxw_linear_4bit.restype = I
+    lib.mxw_linear_4bit.argtypes = [P, L, P, P, P, I, I, I, I, I, P, I, P]
     _lib = lib
     return lib
 
@@ -757,3 +792,446 @@ def moe_layer(x, router, wgu, sgu, wd, sd, top_k, normalize=True, scale=1.0, act
     if rc != 0:
         raise MxwError("mxw_moe_layer failed (%d): %s" % (rc, strerror(rc)))
     return out, ids, weights
+
+
+# ---- tokens to their experts' rows and back -----------------------------------
+
+TokenPlan = collections.namedtuple("TokenPlan", "offs counts rows size")
+TokenPlan.__doc__ = """Where sort_tokens puts every token: offs int32 [E], the cumulative ends of the
+experts' runs of rows (as the grouped products take them); counts int32 [E], each
+expert's choices; rows int32 [T, k], every choice's row, -1 for empty slots; size,
+the rows that the runs fit in whatever the ids (a Python number)."""
+
+_TYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def token_rows(T, k, E, align=32):
+    """Rows that T tokens' k choices among E experts fit in, each expert's run a
+    multiple of align.  Raises MxwError if that is over 8,388,608."""
+    rc = _load().mxw_token_rows(int(T), int(k), int(E), int(align))
+    if rc < 0:
+        raise MxwError("mxw_token_rows failed: %s" % strerror(rc))
+    return int(rc)
+
+
+def sort_workspace_size(T, k, E):
+    """Bytes of workspace sort_tokens needs (0: none).  Raises MxwError on a
+    status code."""
+    rc = _load().mxw_sort_workspace_size(int(T), int(k), int(E))
+    if rc < 0:
+        raise MxwError("mxw_sort_workspace_size failed: %s" % strerror(rc))
+    return int(rc)
+
+
+def mxw_sort_tokens(ids, id_bytes, ld, T, k, E, align, offs, counts, rows, workspace, workspace_bytes, stream=0):
+    """Raw C-ABI call on device addresses (ints).  Returns the status code."""
+    return _load().mxw_sort_tokens(ids, id_bytes, ld, T, k, E, align, offs, counts, rows, workspace, workspace_bytes,
+                                   stream)
+
+
+def sort_tokens(ids, E, align=32, stream=None, workspace=None):
+    """The rows that tokens go to when they are grouped by expert: a TokenPlan.
+
+    ids: int32 or int64 [T, k] (rows any stride apart), each token's experts; an id
+    outside [0, E) is an empty slot.  Choices keep their order (token, then choice)
+    within an expert, and each expert's run is padded to a multiple of `align` (32: what
+    wgrad needs; 16: wgrad_bf16).  Runs on `stream` (default: the current stream) and
+    does not synchronise; `workspace`: a uint8 device tensor of sort_workspace_size()
+    bytes (default: from torch's caching allocator on that stream)."""
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("ids must be int32 or int64, got %s" % ids.dtype)
+    if ids.dim() != 2 or ids.shape[1] == 0:
+        raise ValueError("ids must be [T, k], got %s" % (tuple(ids.shape),))
+    dev = ids.device
+    if dev.type != "cuda":
+        raise ValueError("ids must be on the GPU")
+    T, k = ids.shape
+    if k > 1 and ids.stride(1) != 1 or T > 1 and ids.stride(0) < k:
+        raise ValueError("ids must have a contiguous last axis and rows at least a row apart")
+    E, align = int(E), int(align)
+    size = token_rows(T, k, E, align)
+    on = _On(dev, stream)
+    offs, counts, rows = on.new((E,), torch.int32), on.new((E,), torch.int32), on.new((T, k), torch.int32)
+    with on:
+        need = sort_workspace_size(T, k, E)
+        wp, wb, ws = on.workspace(need, workspace) if need else (0, 0, None)
+        rc = mxw_sort_tokens(ids.data_ptr(), ids.element_size(), ids.stride(0) if T > 1 else k, T, k, E, align,
+                             offs.data_ptr(), counts.data_ptr(), rows.data_ptr(), wp, wb, on.handle)
+        del ws
+    if rc != 0:
+        raise MxwError("mxw_sort_tokens failed (%d): %s" % (rc, strerror(rc)))
+    return TokenPlan(offs, counts, rows, size)
+
+
+def _plan(plan, dev):
+    """(offs, counts, rows, size, T, k, E) of a plan, checked."""
+    offs, counts, rows, size = plan
+    if rows.dim() != 2 or offs.dim() != 1 or counts.shape != offs.shape:
+        raise ValueError("plan: offs and counts must be [E] and rows [T, k]")
+    for name, t in (("offs", offs), ("counts", counts), ("rows", rows)):
+        if t.dtype != torch.int32 or t.device != dev or not t.is_contiguous():
+            raise ValueError("plan: %s must be a contiguous int32 tensor on the same GPU" % name)
+    return offs, counts, rows, int(size), rows.shape[0], rows.shape[1], offs.shape[0]
+
+
+def _matrix(t, name, rows, H=None, dtype=None, dev=None):
+    """Row stride of a [rows, H] matrix with a contiguous last axis, checked."""
+    if t.dtype not in _TYPES or (dtype is not None and t.dtype != dtype):
+        raise TypeError("%s must be %s, got %s" % (name, "bfloat16 or float32" if dtype is None else dtype, t.dtype))
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (H is not None and t.shape[1] != H) or not t.shape[1]:
+        raise ValueError("%s must be [%s, %s], got %s" % (name, "rows" if rows is None else rows, "H" if H is None else H,
+                                                          tuple(t.shape)))
+    if t.device.type != "cuda" or (dev is not None and t.device != dev):
+        raise ValueError("%s must be on %s" % (name, "the GPU" if dev is None else dev))
+    if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError("%s must have a contiguous last axis and rows at least a row apart" % name)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _output(t, name, shape, dtype, on):
+    """`t` checked, or a new tensor."""
+    if t is None:
+        return on.new(shape, dtype)
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != on._dev:
+        raise ValueError("%s must be a contiguous %s %s tensor on the same device" % (name, dtype, list(shape)))
+    return t
+
+
+def _codes_output(q, s, R, H, on):
+    if q is not None and q.dtype == getattr(torch, "float8_e4m3fn", None):
+        q = q.view(torch.uint8)
+    if H % 32:
+        raise ValueError("MXFP8 rows need a multiple of 32 columns, got %d" % H)
+    return _output(q, "q", (R, H), torch.uint8, on), _output(s, "s", (R, H // 32), torch.uint8, on)
+
+
+def mxw_dispatch_tokens(x, dtype, ldx, offs, counts, rows, T, k, E, H, R, xs, q, s, stream=0):
+    """Raw C-ABI call on device addresses (ints; xs, or q and s, may be 0); dtype:
+    0 bf16, 1 float32.  Returns the status code."""
+    return _load().mxw_dispatch_tokens(x, dtype, ldx, offs, counts, rows, T, k, E, H, R, xs, q, s, stream)
+
+
+def dispatch_tokens(x, plan, rows=True, mxfp8=False, out=None, q=None, s=None, stream=None):
+    """Tokens x [T, H] (bf16 or float32, rows any stride apart) copied to the rows that
+    a TokenPlan gives them: xs [R, H] of x's type, R = plan.size; with mxfp8=True
+    (xs, codes uint8 [R, H], scales uint8 [R, H/32]), the codes being what fwd takes;
+    with rows=False as well (codes, scales) alone.
+
+    The padding rows of every expert become zeros; rows past the last run are left as
+    they were (uninitialised in new tensors; the grouped products do not read them).
+    `out`, `q` and `s` (optional) are contiguous tensors of at most or more rows than
+    plan.size: rows that they do not have are skipped.  The gradient with respect to x is
+    combine_tokens(dxs, plan).  Runs on `stream` (default: the current stream) and does
+    not synchronise."""
+    ldx = _matrix(x, "x", None)
+    dev = x.device
+    offs, counts, where, R, T, k, E = _plan(plan, dev)
+    H = x.shape[1]
+    if x.shape[0] != T:
+        raise ValueError("x has %d tokens, the plan %d" % (x.shape[0], T))
+    if not rows and not mxfp8:
+        raise ValueError("nothing to write: rows and mxfp8 are both False")
+    if (out is not None and not rows) or ((q is not None or s is not None) and not mxfp8):
+        raise ValueError("out is an output of rows=True, q and s are outputs of mxfp8=True")
+    for t in (out, q, s):
+        if t is not None and t.dim() == 2:
+            R = t.shape[0]
+    on = _On(dev, stream)
+    if rows:
+        out = _output(out, "out", (R, H), x.dtype, on)
+    if mxfp8:
+        q, s = _codes_output(q, s, R, H, on)
+    with on:
+        rc = mxw_dispatch_tokens(x.data_ptr(), _TYPES[x.dtype], ldx, offs.data_ptr(), counts.data_ptr(), where.data_ptr(),
+                                 T, k, E, H, R, out.data_ptr() if rows else 0, q.data_ptr() if mxfp8 else 0,
+                                 s.data_ptr() if mxfp8 else 0, on.handle) if T and R else 0
+    if rc != 0:
+        raise MxwError("mxw_dispatch_tokens failed (%d): %s" % (rc, strerror(rc)))
+    return out if not mxfp8 else (out, q, s) if rows else (q, s)
+
+
+def mxw_combine_tokens(y, dtype, ldy, rows, weights, residual, ldr, T, k, H, R, out, stream=0):
+    """Raw C-ABI call on device addresses (ints; weights and residual may be 0);
+    dtype: 0 bf16, 1 float32.  Returns the status code."""
+    return _load().mxw_combine_tokens(y, dtype, ldy, rows, weights, residual, ldr, T, k, H, R, out, stream)
+
+
+def _weights(weights, T, k, dev):
+    if weights.dtype != torch.float32 or tuple(weights.shape) != (T, k) or weights.device != dev or (
+            not weights.is_contiguous()):
+        raise ValueError("weights must be a contiguous float32 [T, k] tensor on the same GPU")
+
+
+def combine_tokens(y, plan, weights=None, residual=None, out=None, stream=None):
+    """The experts' rows y [R, H] (bf16 or float32, rows any stride apart) joined to
+    tokens: out[t] = sum_j weights[t, j] y[plan.rows[t, j]] (+ residual[t]), [T, H] of
+    y's type, summed in float32 in the order of j and rounded once.
+
+    weights: float32 [T, k] (None: 1).  residual: [T, H] of y's type, rows any stride
+    apart; `out` may be the residual itself.  Empty slots count nothing, whatever their
+    weight holds.  Without weights it is the gradient of dispatch_tokens.  Runs on
+    `stream` (default: the current stream) and does not synchronise."""
+    ldy = _matrix(y, "y", None)
+    dev = y.device
+    offs, counts, rows, _, T, k, E = _plan(plan, dev)
+    R, H = y.shape
+    ldr = 0 if residual is None else _matrix(residual, "residual", T, H, y.dtype, dev)
+    if weights is not None:
+        _weights(weights, T, k, dev)
+    on = _On(dev, stream)
+    out = _output(out, "out", (T, H), y.dtype, on)
+    with on:
+        rc = mxw_combine_tokens(y.data_ptr(), _TYPES[y.dtype], ldy, rows.data_ptr(),
+                                0 if weights is None else weights.data_ptr(),
+                                0 if residual is None else residual.data_ptr(), ldr, T, k, H, R, out.data_ptr(),
+                                on.handle) if T else 0
+    if rc != 0:
+        raise MxwError("mxw_combine_tokens failed (%d): %s" % (rc, strerror(rc)))
+    return out
+
+
+def mxw_combine_tokens_grad(dout, dtype, ldo, y, ldy, offs, counts, rows, weights, T, k, E, H, R, dy, q, s, dweights,
+                            stream=0):
+    """Raw C-ABI call on device addresses (ints; dy, q and s, dweights may be 0);
+    dtype: 0 bf16, 1 float32.  Returns the status code."""
+    return _load().mxw_combine_tokens_grad(dout, dtype, ldo, y, ldy, offs, counts, rows, weights, T, k, E, H, R, dy, q, s,
+                                           dweights, stream)
+
+
+def combine_tokens_grad(dout, y, plan, weights, rows=True, mxfp8=False, dy=None, q=None, s=None, stream=None):
+    """The gradients of combine_tokens(y, plan, weights) from that of its output,
+    dout [T, H] (rows any stride apart): (dy [R, H], dweights float32 [T, k]), with
+    mxfp8=True (dy, codes, scales, dweights), the codes and scales being those of
+    quantize_rows(dy), and with rows=False as well (codes, scales, dweights).
+
+    dy[plan.rows[t, j]] = weights[t, j] dout[t] in dout's type; padding rows become
+    zeros, rows past the last run are left as they were.  dweights[t, j] is the dot
+    product of dout[t] and y[plan.rows[t, j]] in float32, 0 for empty slots.  The
+    residual's gradient is dout.  `dy` may be y itself.  Runs on `stream` (default: the
+    current stream) and does not synchronise."""
+    ldo = _matrix(dout, "dout", None)
+    dev = dout.device
+    offs, counts, where, _, T, k, E = _plan(plan, dev)
+    H = dout.shape[1]
+    if dout.shape[0] != T:
+        raise ValueError("dout has %d tokens, the plan %d" % (dout.shape[0], T))
+    ldy = _matrix(y, "y", None, H, dout.dtype, dev)
+    R = y.shape[0]
+    _weights(weights, T, k, dev)
+    if not rows and not mxfp8:
+        raise ValueError("nothing to write: rows and mxfp8 are both False")
+    if (dy is not None and not rows) or ((q is not None or s is not None) and not mxfp8):
+        raise ValueError("dy is an output of rows=True, q and s are outputs of mxfp8=True")
+    on = _On(dev, stream)
+    dweights = on.new((T, k), torch.float32)
+    if rows:
+        dy = _output(dy, "dy", (R, H), dout.dtype, on)
+    if mxfp8:
+        q, s = _codes_output(q, s, R, H, on)
+    with on:
+        rc = mxw_combine_tokens_grad(dout.data_ptr(), _TYPES[dout.dtype], ldo, y.data_ptr(), ldy, offs.data_ptr(),
+                                     counts.data_ptr(), where.data_ptr(), weights.data_ptr(), T, k, E, H, R,
+                                     dy.data_ptr() if rows and R else 0, q.data_ptr() if mxfp8 and R else 0,
+                                     s.data_ptr() if mxfp8 and R else 0, dweights.data_ptr(), on.handle) if T else 0
+    if rc != 0:
+        raise MxwError("mxw_combine_tokens_grad failed (%d): %s" % (rc, strerror(rc)))
+    return ((dy,) if rows else ()) + ((q, s) if mxfp8 else ()) + (dweights,)
+
+
+# ---- row-wise operands --------------------------------------------------------
+
+_FORMATS = {"mxfp8": 0, "mxfp4": 1}
+
+
+def mxw_quantize_rows(x, dtype, ldx, R, C, format, q, s, stream=0):
+    """Raw C-ABI call on device addresses (ints); dtype: 0 bf16, 1 float32; format:
+    0 MXFP8, 1 MXFP4.  Returns the status code."""
+    return _load().mxw_quantize_rows(x, dtype, ldx, R, C, format, q, s, stream)
+
+
+def quantize_rows(x, format="mxfp8", q=None, s=None, stream=None):
+    """MX quantisation of bf16 or float32 x [..., C] in blocks of 32 along the last
+    axis: (codes, scales uint8 [..., C/32]), as fwd and moe_layer take their operands
+    ("mxfp8": codes uint8 [..., C]) and linear_4bit its weights ("mxfp4": codes uint8
+    [..., C/2], element 2 i in the low half of byte i).
+
+    Scales and rounding are those of quantize_tokens (MXFP4: the same with the largest
+    value 6); a block that holds an infinity or a NaN gets the NaN scale 255.  The last
+    axis is contiguous and the rows one stride apart (a transposed weight's operand is
+    quantize_tokens of the weight).  Runs on `stream` (default: the current stream) and
+    does not synchronise."""
+    if x.dtype not in _TYPES:
+        raise TypeError("x must be bfloat16 or float32, got %s" % x.dtype)
+    if format not in _FORMATS:
+        raise ValueError("format must be 'mxfp8' or 'mxfp4'")
+    if x.dim() < 1 or x.device.type != "cuda":
+        raise ValueError("x must be a tensor of at least one axis on the GPU")
+    shape = tuple(x.shape)
+    C = shape[-1]
+    if C == 0 or C % 32:
+        raise ValueError("x's last axis must be a multiple of 32, got %d" % C)
+    if x.is_contiguous():
+        R, ldx = x.numel() // C, C
+    else:
+        try:
+            ldx = _matrix(x.view(-1, C), "x", None)
+        except RuntimeError:
+            raise ValueError("x's rows must be one stride apart") from None
+        R = x.numel() // C
+    on = _On(x.device, stream)
+    if q is not None and q.dtype == getattr(torch, "float8_e4m3fn", None):
+        q = q.view(torch.uint8)
+    q = _output(q, "q", shape[:-1] + (C if format == "mxfp8" else C // 2,), torch.uint8, on)
+    s = _output(s, "s", shape[:-1] + (C // 32,), torch.uint8, on)
+    with on:
+        rc = mxw_quantize_rows(x.data_ptr(), _TYPES[x.dtype], ldx, R, C, _FORMATS[format], q.data_ptr(), s.data_ptr(),
+                               on.handle) if R else 0
+    if rc != 0:
+        raise MxwError("mxw_quantize_rows failed (%d): %s" % (rc, strerror(rc)))
+    return q, s
+
+
+# ---- gradients together -------------------------------------------------------
+
+def clip_workspace_size(count):
+    """Bytes of workspace clip_grad_norm and grad_norm need for so many tensors.
+    Raises MxwError on a status code."""
+    rc = _load().mxw_clip_workspace_size(int(count))
+    if rc < 0:
+        raise MxwError("mxw_clip_workspace_size failed: %s" % strerror(rc))
+    return int(rc)
+
+
+def mxw_clip_grads(grads, outs, sizes, types, norm_type, max_norm, eps, norm, workspace, workspace_bytes, stream=0):
+    """Raw C-ABI call: lists of device addresses (outs None: the norm alone), element
+    counts and types (0 bf16, 1 float32); norm_type: 2, or 0 for the largest magnitude.
+    Returns the status code."""
+    n = len(grads)
+    P = ctypes.c_void_p * n
+    return _load().mxw_clip_grads(P(*grads), None if outs is None else P(*outs), (ctypes.c_int64 * n)(*sizes),
+                                  (ctypes.c_int32 * n)(*types), n, norm_type, max_norm, eps, norm, workspace,
+                                  workspace_bytes, stream)
+
+
+def _dense(t):
+    """Whether a tensor's elements fill its memory from its address on, in any order."""
+    if t.is_contiguous():
+        return True
+    want = 1
+    for size, stride in sorted(((n, d) for n, d in zip(t.shape, t.stride()) if n > 1), key=lambda a: a[1]):
+        if stride != want:
+            return False
+        want *= size
+    return True
+
+
+def _norm_call(grads, outs, max_norm, norm_type, eps, stream, workspace, device=None):
+    grads = [grads] if isinstance(grads, torch.Tensor) else [g for g in grads if g is not None]
+    if norm_type not in (2, float("inf")):
+        raise ValueError("norm_type must be 2 or infinity")
+    if not grads:
+        raise ValueError("no gradients")
+    dev = grads[0].device
+    for g in grads:
+        if g.dtype not in _TYPES:
+            raise TypeError("gradients must be bfloat16 or float32, got %s" % g.dtype)
+        if g.device != dev or dev.type != "cuda":
+            raise ValueError("gradients must be on one GPU")
+        if not _dense(g):
+            raise ValueError("gradients must fill their memory (contiguous or permuted axes)")
+    if outs is not None:
+        outs = [outs] if isinstance(outs, torch.Tensor) else list(outs)
+        if len(outs) != len(grads):
+            raise ValueError("out must hold a tensor for every gradient")
+        for g, o in zip(grads, outs):
+            if o is not g and (o.dtype != g.dtype or o.shape != g.shape or o.stride() != g.stride() or o.device != dev):
+                raise ValueError("out must hold tensors of the gradients' types, shapes, strides and device")
+    on = _On(dev, stream)
+    norm = on.new((), torch.float32)
+    with on:
+        wp, wb, ws = on.workspace(clip_workspace_size(len(grads)), workspace)
+        rc = mxw_clip_grads([g.data_ptr() for g in grads], None if outs is None else [o.data_ptr() for o in outs],
+                            [g.numel() for g in grads], [_TYPES[g.dtype] for g in grads], 2 if norm_type == 2 else 0,
+                            float(max_norm), float(eps), norm.data_ptr(), wp, wb, on.handle)
+        del ws
+    if rc != 0:
+        raise MxwError("mxw_clip_grads failed (%d): %s" % (rc, strerror(rc)))
+    return norm
+
+
+def grad_norm(grads, norm_type=2.0, stream=None, workspace=None):
+    """The norm of many gradients together, a float32 scalar tensor: the square root of
+    the sum of all squares (in 64 bits), or the largest magnitude (norm_type infinity).
+
+    grads: bf16 and float32 tensors on one GPU, any sizes (None is left out), each
+    filling its memory.  Runs on `stream` (default: the current stream) and does not
+    synchronise; `workspace`: a uint8 device tensor of clip_workspace_size() bytes
+    (default: from torch's caching allocator on that stream)."""
+    return _norm_call(grads, None, 0.0, norm_type, 0.0, stream, workspace)
+
+
+def clip_grad_norm(grads, max_norm, norm_type=2.0, eps=1e-6, out=None, stream=None, workspace=None):
+    """Gradients scaled by min(1, max_norm / (norm + eps)), norm = grad_norm(grads,
+    norm_type), in place or into the tensors of `out` (one for every gradient, of its
+    type, shape and strides).  Returns the norm before clipping.
+
+    The factor is float32 and the product rounded once to the gradient's type.  A NaN
+    makes everything NaN; an infinity makes the norm infinite and the factor 0.  No two
+    gradients may share memory.  Arguments otherwise as grad_norm."""
+    if not (max_norm >= 0.0 and eps >= 0.0):
+        raise ValueError("max_norm and eps must not be negative")
+    if out is None:
+        grads = [grads] if isinstance(grads, torch.Tensor) else [g for g in grads if g is not None]
+        out = grads
+    return _norm_call(grads, out, max_norm, norm_type, eps, stream, workspace)
+
+
+# ---- few tokens, 4-bit weights ------------------------------------------------
+
+def mxw_linear_4bit(x, ldx, codes, scales, zeros, format, group, T, K, N, out, out_type, stream=0):
+    """Raw C-ABI call on device addresses (ints; zeros may be 0); format: 1 MXFP4,
+    2 integers; out_type: 0 bf16, 1 float32.  Returns the status code."""
+    return _load().mxw_linear_4bit(x, ldx, codes, scales, zeros, format, group, T, K, N, out, out_type, stream)
+
+
+def linear_4bit(x, codes, scales, zeros=None, dtype=torch.bfloat16, out=None, stream=None):
+    """x [T, K] (bf16, up to 64 tokens, rows any multiple of 8 elements apart) times
+    4-bit weights: out [T, N] = x W^T, bf16 or float32 (`dtype`).
+
+    codes: uint8 [N, K/2], element 2 i of a row in the low half of byte i.  With scales
+    uint8 [N, K/32] the weights are MXFP4 (E2M1 and E8M0, as quantize_rows(w, "mxfp4")
+    makes them); with scales bf16 [N, K/group], group 32, 64 or 128, they are
+    (code - zero) scale, zeros uint8 [N, K/group] or None for 8.  Runs on `stream`
+    (default: the current stream) and does not synchronise."""
+    if x.dtype != torch.bfloat16:
+        raise TypeError("x must be bfloat16")
+    if codes.dtype != torch.uint8 or scales.dtype not in (torch.uint8, torch.bfloat16):
+        raise TypeError("codes must be uint8, scales uint8 or bfloat16")
+    if dtype not in _TYPES:
+        raise TypeError("dtype must be bfloat16 or float32")
+    dev = x.device
+    ldx = _matrix(x, "x", None)
+    T, K = x.shape
+    if codes.dim() != 2 or scales.dim() != 2 or codes.shape[0] == 0:
+        raise ValueError("codes and scales must be 2-D")
+    N = codes.shape[0]
+    fp4 = scales.dtype == torch.uint8
+    groups = scales.shape[1]
+    group = K // groups if groups else 0
+    if codes.shape[1] * 2 != K or scales.shape[0] != N or group * groups != K or group not in ((32,) if fp4 else (32, 64, 128)):
+        raise ValueError("shape mismatch: x %s codes %s scales %s" % (tuple(x.shape), tuple(codes.shape), tuple(scales.shape)))
+    for name, t in (("codes", codes), ("scales", scales)):
+        if t.device != dev or not t.is_contiguous():
+            raise ValueError("%s must be contiguous and on the same GPU as x" % name)
+    if zeros is not None and (fp4 or zeros.dtype != torch.uint8 or zeros.shape != scales.shape or zeros.device != dev or
+                              not zeros.is_contiguous()):
+        raise ValueError("zeros must be a contiguous uint8 tensor of the scales' shape (with bf16 scales)")
+    on = _On(dev, stream)
+    out = _output(out, "out", (T, N), dtype, on)
+    with on:
+        rc = mxw_linear_4bit(x.data_ptr(), ldx, codes.data_ptr(), scales.data_ptr(),
+                             0 if zeros is None else zeros.data_ptr(), 1 if fp4 else 2, group, T, K, N, out.data_ptr(),
+                             _TYPES[dtype], on.handle) if T else 0
+    if rc != 0:
+        raise MxwError("mxw_linear_4bit failed (%d): %s" % (rc, strerror(rc)))
+    return out

@@ -1,0 +1,261 @@
+// grad_norm.hip -- the norm of many gradients together, and their clipping to it
+// (mxw_clip_grads, declared in include/mxfp8_wgrad.h), for gfx950.
+//
+//     n = (sum g^2)^(1/2)  or  max |g|;      out = g min(1, max_norm / (n + eps))
+//
+// Two passes, since the factor is known only after the last gradient is read: bound by
+// reading HBM twice and writing it once.  The first leaves a partial result for each
+// workgroup, whose share of the tiles depends on the sizes alone; every workgroup of the
+// second adds all partials in one order, so no launch stands between them and the bits
+// are the same run to run.  Squares are summed in 64 bits: a product of two FP32 values
+// neither overflows nor vanishes there.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <vector>
+
+#include "device.h"
+#include "mx.h"
+#include "mxfp8_wgrad.h"
+
+namespace {
+
+using namespace mxw;
+
+constexpr int kTileVecs = 4, kTileElems = 256 * 8 * kTileVecs;  // elements of a tile
+constexpr int kMost = 96;                                       // tensors of a launch (its arguments: 4 KiB at most)
+constexpr int kBlocks = 2048;                                   // workgroups of a launch
+
+struct Item {
+  const void* g;
+  void* out;
+  int64_t n;
+  int32_t first;  // its first tile
+  int32_t f32;
+};
+struct NormArgs {
+  Item item[kMost];
+  double max_norm, eps;
+  float* norm;
+  double* part;     // this launch's (first pass), all (second)
+  int32_t items, tiles, parts;
+};
+static_assert(sizeof(NormArgs) <= 4096, "a kernel's arguments");
+
+__device__ __forceinline__ int item_of(const NormArgs& a, int tile) {
+  int lo = 0, hi = a.items - 1;  // the last with first <= tile
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.item[mid].first <= tile)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ double join(double x, double y, bool top) {
+  // largest: NaN wins
+  return top ? (x > y || x != x ? x : y) : x + y;
+}
+
+template <bool TOP>
+__device__ __forceinline__ double block_join(double v) {
+  __shared__ double red[4];
+  for (int d = 32; d; d >>= 1) v = join(v, __shfl_xor(v, d), TOP);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return join(join(red[0], red[1], TOP), join(red[2], red[3], TOP), TOP);
+}
+
+template <bool TOP, bool F32>
+__device__ __forceinline__ double tile_norm(const Item& it, int64_t at) {
+  double sum[2] = {0.0, 0.0};
+  uint32_t top = 0;
+  Raw8<F32> v[kTileVecs];
+#pragma unroll
+  for (int u = 0; u < kTileVecs; ++u) {
+    const int64_t i = at + (u * 256 + (int)threadIdx.x) * 8;
+    v[u] = Raw8<F32>{};
+    if (i + 8 <= it.n)
+      v[u] = load8<F32>(it.g, i);
+    else if (i < it.n)
+      v[u] = load_some<F32>(it.g, i, (int)(it.n - i));
+  }
+#pragma unroll
+  for (int u = 0; u < kTileVecs; ++u) {
+    float f[8];
+    values<F32>(v[u], f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (TOP)
+        top = max(top, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+      else
+        sum[i & 1] = fma((double)f[i], (double)f[i], sum[i & 1]);
+    }
+  }
+  return TOP ? (double)__uint_as_float(top) : sum[0] + sum[1];
+}
+
+template <bool TOP>
+__global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
+  double v = 0.0;
+  for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+    const Item& it = a.item[item_of(a, tile)];
+    const int64_t at = (int64_t)(tile - it.first) * kTileElems;
+    v = join(v, it.f32 ? tile_norm<TOP, true>(it, at) : tile_norm<TOP, false>(it, at), TOP);
+  }
+  v = block_join<TOP>(v);
+  if (threadIdx.x == 0) a.part[blockIdx.x] = v;
+}
+
+template <bool F32>
+__device__ __forceinline__ void tile_scale(const Item& it, int64_t at, float power, float factor) {
+  Raw8<F32> v[kTileVecs];
+#pragma unroll
+  for (int u = 0; u < kTileVecs; ++u) {
+    const int64_t i = at + (u * 256 + (int)threadIdx.x) * 8;
+    if (i + 8 <= it.n)
+      v[u] = load8<F32>(it.g, i);
+    else if (i < it.n)
+      v[u] = load_some<F32>(it.g, i, (int)(it.n - i));
+  }
+#pragma unroll
+  for (int u = 0; u < kTileVecs; ++u) {
+    const int64_t i = at + (u * 256 + (int)threadIdx.x) * 8;
+    if (i >= it.n) continue;
+    float f[8];
+    values<F32>(v[u], f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = f[j] * power * factor;
+    if (i + 8 <= it.n)
+      store8<F32>(it.out, i, rounded<F32>(f));
+    else
+      store_some<F32>(it.out, i, rounded<F32>(f), (int)(it.n - i));
+  }
+}
+
+// The norm from all partials, and this launch's tensors times the factor (from the last
+// tile back: what the first pass read last may still be in the caches).
+template <bool TOP>
+__global__ __launch_bounds__(256) void scale_kernel(NormArgs a) {
+  double v = 0.0;
+  for (int i = threadIdx.x; i < a.parts; i += 256) v = join(v, a.part[i], TOP);
+  v = block_join<TOP>(v);
+  const double norm = TOP ? v : sqrt(v);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && a.norm) *a.norm = (float)norm;
+  const double ratio = a.max_norm / (norm + a.eps);
+  // a factor below FP32's normal range goes as two, so that it keeps its 24 bits
+  const bool low = ratio < 0x1p-126;
+  const float power = low ? 0x1p-126f : 1.0f;
+  const float factor = ratio >= 1.0 ? 1.0f : (float)(low ? ratio * 0x1p126 : ratio);  // NaN: NaN
+  for (int b = blockIdx.x; b < a.tiles; b += gridDim.x) {
+    const int tile = a.tiles - 1 - b;
+    const Item& it = a.item[item_of(a, tile)];
+    if (factor == 1.0f && it.g == it.out) continue;
+    const int64_t at = (int64_t)(tile - it.first) * kTileElems;
+    if (it.f32)
+      tile_scale<true>(it, at, power, factor);
+    else
+      tile_scale<false>(it, at, power, factor);
+  }
+}
+
+int64_t tiles_of(int64_t n) { return (n + kTileElems - 1) / kTileElems; }
+
+}  // namespace
+
+extern "C" {
+
+int64_t mxw_clip_workspace_size(int count) {
+  if (count < 0 || count > MXW_MAX_TENSORS) return MXW_ERR_DIM;
+  return (int64_t)((count + kMost - 1) / kMost + (count == 0)) * kBlocks * 8;
+}
+
+int mxw_clip_grads(const void* const* grads, void* const* outs, const int64_t* sizes, const int32_t* types, int count,
+                   int norm_type, double max_norm, double eps, float* norm, void* workspace, size_t workspace_bytes,
+                   void* stream) {
+  if (!norm || (count && (!grads || !sizes || !types))) return MXW_ERR_NULL;
+  const int64_t need = mxw_clip_workspace_size(count);
+  if (need < 0 || (norm_type != MXW_NORM_2 && norm_type != MXW_NORM_MAX)) return MXW_ERR_DIM;
+  if (outs && (!(max_norm >= 0.0) || !(eps >= 0.0))) return MXW_ERR_DIM;
+  if ((uintptr_t)norm & 3) return MXW_ERR_ALIGN;
+  int64_t tiles = 0;
+  for (int i = 0; i < count; ++i) {
+    if (sizes[i] < 0 || sizes[i] > ((int64_t)1 << 40) || (types[i] != MXW_BF16 && types[i] != MXW_F32)) return MXW_ERR_DIM;
+    if (sizes[i] == 0) continue;
+    if (!grads[i] || (outs && !outs[i])) return MXW_ERR_NULL;
+    const uintptr_t mask = types[i] == MXW_F32 ? 3 : 1;
+    if (((uintptr_t)grads[i] | (outs ? (uintptr_t)outs[i] : 0)) & mask) return MXW_ERR_ALIGN;
+    tiles += tiles_of(sizes[i]);
+  }
+  if (tiles > 0x7FFFFFFF) return MXW_ERR_DIM;
+  if (outs && count) {  // what is written overlaps nothing but the gradient it comes from, at the same place
+    struct Range {
+      uintptr_t lo, hi;
+      bool written;
+    };
+    std::vector<Range> r;
+    try {
+      r.reserve(2 * (size_t)count);
+    } catch (...) {
+      return MXW_ERR_LAUNCH;
+    }
+    for (int i = 0; i < count; ++i) {
+      const uintptr_t bytes = (uintptr_t)sizes[i] * (types[i] == MXW_F32 ? 4 : 2);
+      if (!bytes) continue;
+      r.push_back({(uintptr_t)outs[i], (uintptr_t)outs[i] + bytes, true});
+      if (grads[i] != outs[i]) r.push_back({(uintptr_t)grads[i], (uintptr_t)grads[i] + bytes, false});
+    }
+    std::sort(r.begin(), r.end(), [](const Range& x, const Range& y) { return x.lo < y.lo; });
+    uintptr_t written = 0, read = 0;  // where what began before ends
+    for (const Range& x : r) {
+      if (x.lo < written || (x.written && x.lo < read)) return MXW_ERR_OVERLAP;
+      (x.written ? written : read) = std::max(x.written ? written : read, x.hi);
+    }
+  }
+  if (!workspace || ((uintptr_t)workspace & 255) || workspace_bytes < (size_t)need) return MXW_ERR_WORKSPACE;
+  if (const int rc = check_device()) return rc;
+  hipStream_t st = (hipStream_t)stream;
+  const bool top = norm_type == MXW_NORM_MAX;
+  int parts = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    int i = 0;
+    bool any = false;
+    do {
+      NormArgs a = {};
+      a.max_norm = max_norm, a.eps = eps;
+      for (; i < count && a.items < kMost; ++i) {
+        if (sizes[i] == 0) continue;
+        a.item[a.items++] = {grads[i], outs ? outs[i] : nullptr, sizes[i], a.tiles, types[i] == MXW_F32};
+        a.tiles += (int32_t)tiles_of(sizes[i]);
+      }
+      const int blocks = std::min(a.tiles, kBlocks);
+      if (pass == 0) {
+        a.part = (double*)workspace + parts;
+        if (blocks) {
+          if (top)
+            norm_kernel<true><<<dim3(blocks), dim3(256), 0, st>>>(a);
+          else
+            norm_kernel<false><<<dim3(blocks), dim3(256), 0, st>>>(a);
+        }
+        parts += blocks;
+      } else {
+        a.part = (double*)workspace, a.parts = parts;
+        a.norm = any ? nullptr : norm;
+        if (!outs) a.tiles = 0, i = count;  // the norm alone
+        const int run = outs ? std::max(blocks, 1) : 1;
+        if (top)
+          scale_kernel<true><<<dim3(run), dim3(256), 0, st>>>(a);
+        else
+          scale_kernel<false><<<dim3(run), dim3(256), 0, st>>>(a);
+        any = true;
+      }
+    } while (i < count);
+  }
+  return hipGetLastError() == hipSuccess ? MXW_OK : MXW_ERR_LAUNCH;
+}
+
+}  // extern "C"

@@ -1,0 +1,154 @@
+// mx.h -- MXFP8 and MXFP4 encoding of values that lie 8 to a lane, and loads and
+// stores of any element alignment, shared by the kernels that write such rows.
+#ifndef MXW_MX_H
+#define MXW_MX_H
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace mxw {
+
+typedef int i4 __attribute__((ext_vector_type(4)));
+typedef int i2 __attribute__((ext_vector_type(2)));
+// the same on an element's alignment (a vector access of any address is legal)
+typedef int i4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+
+// bf16 of f, round to nearest even, NaN kept
+__device__ __forceinline__ uint32_t bf16_bits(float f) {
+  const __bf16 h = (__bf16)f;
+  return __builtin_bit_cast(uint16_t, h);
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  const b2 h = {(__bf16)lo, (__bf16)hi};
+  return __builtin_bit_cast(uint32_t, h);
+}
+
+// 8 elements of a row as they are stored
+template <bool F32>
+struct Raw8 {
+  i4 v[F32 ? 2 : 1];
+};
+
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> load8(const void* base, int64_t at) {
+  Raw8<F32> r;
+  const char* p = (const char*)base + at * (F32 ? 4 : 2);
+  r.v[0] = *(const i4_a2*)p;
+  if (F32) r.v[F32 ? 1 : 0] = *(const i4_a2*)(p + 16);
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ void store8(void* base, int64_t at, const Raw8<F32>& r) {
+  char* p = (char*)base + at * (F32 ? 4 : 2);
+  *(i4_a2*)p = r.v[0];
+  if (F32) *(i4_a2*)(p + 16) = r.v[F32 ? 1 : 0];
+}
+// n < 8 elements at a row's end (the others read as 0)
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> load_some(const void* base, int64_t at, int n) {
+  Raw8<F32> r;
+  r.v[0] = (i4){0, 0, 0, 0};
+  if (F32) r.v[F32 ? 1 : 0] = (i4){0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 7; ++i)
+    if (i < n) {
+      if (F32)
+        r.v[F32 ? i >> 2 : 0][i & 3] = ((const int*)base)[at + i];
+      else
+        r.v[0][i >> 1] |= (int)((uint32_t)((const uint16_t*)base)[at + i] << (16 * (i & 1)));
+    }
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ void store_some(void* base, int64_t at, const Raw8<F32>& r, int n) {
+#pragma unroll
+  for (int i = 0; i < 7; ++i)
+    if (i < n) {
+      if (F32)
+        ((int*)base)[at + i] = r.v[F32 ? i >> 2 : 0][i & 3];
+      else
+        ((uint16_t*)base)[at + i] = (uint16_t)((uint32_t)r.v[0][i >> 1] >> (16 * (i & 1)));
+    }
+}
+
+template <bool F32>
+__device__ __forceinline__ void values(const Raw8<F32>& r, float* f) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    f[i] = F32 ? __int_as_float(r.v[F32 ? i >> 2 : 0][i & 3])
+               : __uint_as_float((i & 1) ? (uint32_t)r.v[0][i >> 1] & 0xFFFF0000u : (uint32_t)r.v[0][i >> 1] << 16);
+}
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> rounded(const float* f) {
+  Raw8<F32> r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (F32) {
+      r.v[0][i] = __float_as_int(f[i]);
+      r.v[F32 ? 1 : 0][i] = __float_as_int(f[4 + i]);
+    } else {
+      r.v[0][i] = (int)bf16_pair(f[2 * i], f[2 * i + 1]);
+    }
+  return r;
+}
+
+// The largest magnitude of a block of 32, 8 values in each of 4 neighbouring
+// lanes, as its bits: of the magnitudes' bits the largest as whole numbers, so that
+// a NaN comes out above infinity.
+__device__ __forceinline__ uint32_t block_top(const float* f) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, true));  // lane ^ 1
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, true));  // lane ^ 2
+  return m;
+}
+// E8M0 byte of a block whose top binade the format's 2^BIN takes: 127 for zeros,
+// 255 (NaN) if the block holds an infinity or a NaN.
+template <int BIN>
+__device__ __forceinline__ int block_scale(uint32_t top) {
+  if (top == 0) return 127;
+  if (top >= 0x7F800000u) return 255;
+  // floor(log2 top) = frexp exponent - 1 (exact, subnormals included)
+  return max(__builtin_amdgcn_frexp_expf(__uint_as_float(top)) - 1 - BIN + 127, 0);
+}
+
+// 8 E4M3 codes of a lane's values under its block's scale byte: to nearest, ties to
+// even, saturated at 448, zeros as +0; 0x7F (NaN) under a NaN scale.  The scaling is a
+// product with a power of two from 2^-119 to 2^127: exact wherever it counts.
+__device__ __forceinline__ i2 encode_e4m3(const float* f, int s) {
+  const float up = __uint_as_float((uint32_t)(254 - min(s, 253)) << 23);
+  i2 q;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = __builtin_amdgcn_fmed3f(f[4 * h + i] * up, -448.0f, 448.0f);
+    int c = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+    c = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], c, true);
+    const uint32_t some = (((uint32_t)c & 0x7F7F7F7Fu) + 0x7F7F7F7Fu & 0x80808080u) >> 7;  // codes that are not +-0
+    q[h] = s == 255 ? 0x7F7F7F7F : (int)((uint32_t)c & some * 0xFFu);
+  }
+  return q;
+}
+
+// 8 E2M1 codes, the first in the lowest half byte: to nearest, ties to even,
+// saturated at 6, zeros as +0 (also under a NaN scale).
+__device__ __forceinline__ uint32_t encode_e2m1(const float* f, int s) {
+  const float up = __uint_as_float((uint32_t)(254 - min(s, 253)) << 23);
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = __builtin_amdgcn_fmed3f(f[i] * up, -6.0f, 6.0f);
+  uint32_t c = 0;
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[0], y[1], 1.0f, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[2], y[3], 1.0f, 1);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[4], y[5], 1.0f, 2);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[6], y[7], 1.0f, 3);
+  const uint32_t some = ((c & 0x77777777u) + 0x77777777u & 0x88888888u) >> 3;
+  return s == 255 ? 0u : c & some * 0xFu;
+}
+
+}  // namespace mxw
+
+#endif  // MXW_MX_H

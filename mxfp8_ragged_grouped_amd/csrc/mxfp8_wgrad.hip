@@ -2173,10 +2173,11 @@ const char* mxw_strerror(int code) {
     case MXW_ERR_LAUNCH: return "kernel launch failed";
     case MXW_ERR_WORKSPACE: return "workspace missing, smaller than the size query returned, or not 256-byte aligned";
     case MXW_ERR_SCRATCH: return "the shape needs more workspace than the library's static scratch (MXW_SCRATCH_BYTES)";
+    case MXW_ERR_OVERLAP: return "what the call writes overlaps itself or an input";
     default: return "unknown error";
   }
 }
 
-int mxw_version(void) { return 600; }
+int mxw_version(void) { return 700; }
 
 }  // extern "C"

@@ -1,0 +1,630 @@
+// tokens.hip -- tokens to their experts' rows and back (mxw_sort_tokens,
+// mxw_dispatch_tokens, mxw_combine_tokens, mxw_combine_tokens_grad) and the row-wise
+// MX quantiser (mxw_quantize_rows), declared in include/mxfp8_wgrad.h, for gfx950.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "device.h"
+#include "mx.h"
+#include "mxfp8_wgrad.h"
+
+namespace {
+
+using namespace mxw;
+
+// ---- the order --------------------------------------------------------------
+//
+// row[c] = first[e] + the number of choices before c of the same expert e: a stable
+// counting sort.  A workgroup takes 16,384 choices, each of its 16 waves a consecutive
+// run; it counts its waves' experts in LDS, turns the counts into first places, and a
+// wave then walks its run 64 choices at a time: of each lane's choice, the lanes of the
+// same expert (a ballot for each bit of the expert's number) before it give its rank.
+// With more than one such piece, a kernel before leaves every piece's counts in the
+// workspace, and each workgroup adds up what comes before its own.  Counting is in whole
+// numbers: any order of the LDS atomics gives the same counts.
+constexpr int kSortWaves = 16, kSortPiece = 16384, kPerLane = kSortPiece / (kSortWaves * 64);
+
+struct SortArgs {
+  const void* ids;
+  int64_t ld;
+  int n, k, E, align;   // n = T k choices
+  int32_t *offs, *counts, *rows;
+  int32_t* part;        // [pieces][E]
+};
+
+template <bool I64>
+__device__ __forceinline__ int expert_of(const SortArgs& a, int c) {
+  const int64_t at = (int64_t)(c / a.k) * a.ld + c % a.k;
+  const int64_t e = I64 ? ((const int64_t*)a.ids)[at] : (int64_t)((const int32_t*)a.ids)[at];
+  return e >= 0 && e < a.E ? (int)e : MXW_MAX_EXPERTS;
+}
+
+// LDS of one piece's counts, by wave
+typedef int32_t WaveCounts[kSortWaves][MXW_MAX_EXPERTS];
+
+// every wave's run of the piece into registers, and the counts of each
+template <bool I64>
+__device__ __forceinline__ void count_piece(const SortArgs& a, int (&e)[kPerLane], WaveCounts& cnt) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int i = tid; i < kSortWaves * MXW_MAX_EXPERTS; i += kSortWaves * 64) (&cnt[0][0])[i] = 0;
+  const int first = blockIdx.x * kSortPiece, here = min(a.n - first, kSortPiece);
+  const int steps = ((here + 63) / 64 + kSortWaves - 1) / kSortWaves;  // of 64 choices, a wave
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    const int c = (wave * steps + i) * 64 + lane;
+    e[i] = i < steps && c < here ? expert_of<I64>(a, first + c) : MXW_MAX_EXPERTS;
+  }
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i)
+    if (e[i] < MXW_MAX_EXPERTS) atomicAdd(&cnt[wave][e[i]], 1);
+  __syncthreads();
+}
+
+template <bool I64>
+__global__ __launch_bounds__(kSortWaves * 64) void sort_count_kernel(SortArgs a) {
+  __shared__ WaveCounts cnt;
+  int e[kPerLane];
+  count_piece<I64>(a, e, cnt);
+  for (int x = threadIdx.x; x < a.E; x += kSortWaves * 64) {
+    int sum = 0;
+    for (int w = 0; w < kSortWaves; ++w) sum += cnt[w][x];
+    a.part[(int64_t)blockIdx.x * a.E + x] = sum;
+  }
+}
+
+template <bool I64>
+__global__ __launch_bounds__(kSortWaves * 64) void sort_place_kernel(SortArgs a) {
+  __shared__ WaveCounts cnt;
+  __shared__ int32_t total[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int e[kPerLane];
+  count_piece<I64>(a, e, cnt);
+  int count = 0, before = 0, run = 0;  // of expert tid: its choices, those of earlier pieces, padded ends
+  if (tid < MXW_MAX_EXPERTS) {
+    if (tid < a.E) {
+      if (gridDim.x == 1) {
+        for (int w = 0; w < kSortWaves; ++w) count += cnt[w][tid];
+      } else {
+#pragma unroll 8
+        for (int p = 0; p < (int)gridDim.x; ++p) {
+          const int v = a.part[(int64_t)p * a.E + tid];
+          count += v;
+          before += p < (int)blockIdx.x ? v : 0;
+        }
+      }
+    }
+    const int padded = (count + a.align - 1) / a.align * a.align;
+    run = padded;
+    for (int d = 1; d < 64; d <<= 1) {
+      const int u = __shfl_up(run, d);
+      if (lane >= d) run += u;
+    }
+    if (lane == 63) total[wave] = run;
+    before -= padded;
+  }
+  __syncthreads();
+  if (tid < a.E) {
+    for (int w = 0; w < wave; ++w) run += total[w];
+    if (blockIdx.x == 0) {
+      a.offs[tid] = run;
+      a.counts[tid] = count;
+    }
+    int at = run + before;  // the expert's first row for this piece
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int v = cnt[w][tid];
+      cnt[w][tid] = at;
+      at += v;
+    }
+  }
+  __syncthreads();
+  const int first = blockIdx.x * kSortPiece, here = min(a.n - first, kSortPiece);
+  const int steps = ((here + 63) / 64 + kSortWaves - 1) / kSortWaves;
+  volatile int32_t* place = cnt[wave];  // only this wave's from here on
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    if (i >= steps) break;
+    uint64_t same = __ballot(e[i] < MXW_MAX_EXPERTS);
+    for (int b = 0; (1 << b) < a.E; ++b) {
+      const uint64_t vote = __ballot((e[i] >> b) & 1);
+      same &= (e[i] >> b) & 1 ? vote : ~vote;
+    }
+    const int rank = __popcll(same & ((1ull << lane) - 1));
+    const int c = (wave * steps + i) * 64 + lane;
+    int row = -1;
+    if (e[i] < MXW_MAX_EXPERTS) {
+      const int at = place[e[i]];
+      row = at + rank;
+      __builtin_amdgcn_wave_barrier();  // every lane has read before the first of each expert writes
+      if (rank == 0) place[e[i]] = at + __popcll(same);
+      __builtin_amdgcn_wave_barrier();
+    }
+    if (c < here) a.rows[first + c] = row;
+  }
+}
+
+// ---- rows -------------------------------------------------------------------
+
+constexpr int kUnroll = 4;
+
+struct RowArgs {
+  const void* x;      // [T, H] the tokens: dispatch's x, the gradient's dout
+  int64_t ldx;
+  const void* y;      // [R, H] the experts' rows
+  int64_t ldy;
+  const int32_t *offs, *counts, *rows;
+  const float* weights;
+  const void* residual;
+  int64_t ldr;
+  int T, k, E, H, R;
+  int pad_blocks, pad_split;
+  void* out;          // [R, H], combine: [T, H]
+  uint8_t *q, *s;     // [R, H], [R, H/32]
+  float* dweights;
+};
+
+// Zeros in the padding rows of expert b / split: rows b % split, + split, ... of them.
+template <bool F32, bool ROWS, bool MX>
+__device__ __forceinline__ void pad_rows(const RowArgs& a, int b) {
+  const int e = b / a.pad_split;
+  const int64_t start = e ? min(max(a.offs[e - 1], 0), a.R) : 0;
+  const int64_t end = min(max(a.offs[e], 0), a.R);
+  for (int64_t r = start + max(a.counts[e], 0) + b % a.pad_split; r < end; r += a.pad_split) {
+    const Raw8<F32> zero = {};
+    for (int c = threadIdx.x * 8; c < a.H; c += 256 * 8) {
+      if (ROWS) {
+        if (c + 8 <= a.H)
+          store8<F32>(a.out, r * a.H + c, zero);
+        else
+          store_some<F32>(a.out, r * a.H + c, zero, a.H - c);
+      }
+      if (MX) {
+        *(i2*)(a.q + r * a.H + c) = (i2){0, 0};
+        if (!(c & 31)) a.s[r * (a.H >> 5) + (c >> 5)] = 127;
+      }
+    }
+  }
+}
+
+// xs[row[t][j]] = x[t]: a token is read once, by W waves, and stored to its k rows.
+template <bool F32, bool ROWS, bool MX, int W>
+__global__ __launch_bounds__(256) void dispatch_kernel(RowArgs a) {
+  if ((int)blockIdx.x < a.pad_blocks) return pad_rows<F32, ROWS, MX>(a, blockIdx.x);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t = (blockIdx.x - a.pad_blocks) * (4 / W) + wave / W;
+  if (t >= a.T) return;
+  const int32_t* rows = a.rows + (int64_t)t * a.k;
+  const int64_t from = t * a.ldx;
+  for (int c0 = ((wave % W) * 64 + (threadIdx.x & 63)) * 8; c0 < a.H; c0 += kUnroll * W * 512) {
+    Raw8<F32> v[kUnroll];
+    i2 q[kUnroll];
+    int s[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int c = c0 + u * W * 512;
+      if (c + 8 <= a.H)
+        v[u] = load8<F32>(a.x, from + c);
+      else if (c < a.H)
+        v[u] = load_some<F32>(a.x, from + c, a.H - c);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (MX && c0 + u * W * 512 < a.H) {
+        float f[8];
+        values<F32>(v[u], f);
+        s[u] = block_scale<8>(block_top(f));
+        q[u] = encode_e4m3(f, s[u]);
+      }
+    for (int j = 0; j < a.k; ++j) {
+      const int64_t r = rows[j];
+      if (r < 0 || r >= a.R) continue;
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int c = c0 + u * W * 512;
+        if (ROWS) {
+          if (c + 8 <= a.H)
+            store8<F32>(a.out, r * a.H + c, v[u]);
+          else if (c < a.H)
+            store_some<F32>(a.out, r * a.H + c, v[u], a.H - c);
+        }
+        if (MX && c < a.H) {
+          *(i2*)(a.q + r * a.H + c) = q[u];
+          if (!(c & 31)) a.s[r * (a.H >> 5) + (c >> 5)] = (uint8_t)s[u];
+        }
+      }
+    }
+  }
+}
+
+// a token's rows and weights, 8 choices at a time (-1: none)
+template <bool WEIGHTS>
+__device__ __forceinline__ void choices(const RowArgs& a, int t, int j0, int (&r)[8], float (&w)[8]) {
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const bool in = j0 + u < a.k;
+    const int row = in ? a.rows[(int64_t)t * a.k + j0 + u] : -1;
+    r[u] = row >= 0 && row < a.R ? row : -1;
+    w[u] = WEIGHTS && r[u] >= 0 ? a.weights[(int64_t)t * a.k + j0 + u] : 1.0f;
+  }
+}
+
+// out[t] = sum_j w[t][j] y[row[t][j]] (+ residual[t]), in the order of the choices
+template <bool F32, bool WEIGHTS, int W>
+__global__ __launch_bounds__(256) void combine_kernel(RowArgs a) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t = blockIdx.x * (4 / W) + wave / W;
+  if (t >= a.T) return;
+  for (int c = ((wave % W) * 64 + (threadIdx.x & 63)) * 8; c < a.H; c += W * 512) {
+    const int n = min(a.H - c, 8);
+    float sum[8] = {};
+    for (int j0 = 0; j0 < a.k; j0 += 8) {
+      int r[8];
+      float w[8];
+      choices<WEIGHTS>(a, t, j0, r, w);
+      Raw8<F32> v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (r[u] >= 0) v[u] = n == 8 ? load8<F32>(a.y, r[u] * a.ldy + c) : load_some<F32>(a.y, r[u] * a.ldy + c, n);
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (r[u] >= 0) {
+          float f[8];
+          values<F32>(v[u], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[u], f[i], sum[i]);
+        }
+    }
+    if (a.residual) {
+      float f[8];
+      values<F32>(n == 8 ? load8<F32>(a.residual, t * a.ldr + c) : load_some<F32>(a.residual, t * a.ldr + c, n), f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += f[i];
+    }
+    if (n == 8)
+      store8<F32>(a.out, (int64_t)t * a.H + c, rounded<F32>(sum));
+    else
+      store_some<F32>(a.out, (int64_t)t * a.H + c, rounded<F32>(sum), n);
+  }
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
+// dy[row[t][j]] = w[t][j] dout[t], dw[t][j] = <dout[t], y[row[t][j]]>
+template <bool F32, bool ROWS, bool MX, int W>
+__global__ __launch_bounds__(256) void combine_grad_kernel(RowArgs a) {
+  __shared__ float red[4][8];
+  if ((int)blockIdx.x < a.pad_blocks) return pad_rows<F32, ROWS, MX>(a, blockIdx.x);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t = (blockIdx.x - a.pad_blocks) * (4 / W) + wave / W;
+  if (W == 1 && t >= a.T) return;
+  for (int j0 = 0; j0 < a.k; j0 += 8) {
+    int r[8];
+    float w[8], dot[8] = {};
+    choices<true>(a, t, j0, r, w);
+    for (int c = ((wave % W) * 64 + lane) * 8; c < a.H; c += W * 512) {
+      const int n = min(a.H - c, 8);
+      float d[8];
+      values<F32>(n == 8 ? load8<F32>(a.x, t * a.ldx + c) : load_some<F32>(a.x, t * a.ldx + c, n), d);
+      Raw8<F32> v[8];
+      if (a.dweights) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (r[u] >= 0) v[u] = n == 8 ? load8<F32>(a.y, r[u] * a.ldy + c) : load_some<F32>(a.y, r[u] * a.ldy + c, n);
+      }
+      if (ROWS || MX) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (r[u] >= 0) {
+            const int64_t at = (int64_t)r[u] * a.H + c;
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = w[u] * d[i];
+            const Raw8<F32> o = rounded<F32>(f);
+            if (ROWS) {
+              if (n == 8)
+                store8<F32>(a.out, at, o);
+              else
+                store_some<F32>(a.out, at, o, n);
+            }
+            if (MX) {
+              values<F32>(o, f);
+              const int s = block_scale<8>(block_top(f));
+              *(i2*)(a.q + at) = encode_e4m3(f, s);
+              if (!(c & 31)) a.s[at >> 5] = (uint8_t)s;
+            }
+          }
+      }
+      if (a.dweights) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (r[u] >= 0) {
+            float f[8];
+            values<F32>(v[u], f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dot[u] = fmaf(d[i], f[i], dot[u]);
+          }
+      }
+    }
+    if (a.dweights) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) dot[u] = wave_sum(dot[u]);
+      if (W > 1) {
+        if (lane < 8) red[wave][lane] = 0.0f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (lane == u) red[wave][u] = dot[u];
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 8; ++u) dot[u] = (red[0][u] + red[1][u]) + (red[2][u] + red[3][u]);
+        __syncthreads();
+      }
+      if (wave % W == 0) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (lane == u && j0 + u < a.k) a.dweights[(int64_t)t * a.k + j0 + u] = dot[u];
+      }
+    }
+  }
+}
+
+// ---- the row-wise quantiser -------------------------------------------------
+//
+// Blocks of 32 along the rows, 8 values a lane, 4 lanes a block: every element is read
+// once and its code written once.
+struct QuantArgs {
+  const void* x;
+  int64_t ldx;
+  int64_t chunks;   // R C / 8
+  int per_row;      // C / 8
+  uint8_t *q, *s;
+};
+
+template <bool F32, bool FP4, bool FLAT>
+__global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
+  const int64_t i0 = (int64_t)blockIdx.x * (256 * kUnroll);
+  // rows of another stride: the row and place of the workgroup's first chunk
+  const int64_t row0 = FLAT ? 0 : i0 / a.per_row;
+  const uint32_t in0 = FLAT ? 0 : (uint32_t)(i0 - row0 * a.per_row);
+  Raw8<F32> v[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t i = i0 + u * 256 + threadIdx.x;
+    if (i >= a.chunks) continue;
+    if (FLAT) {
+      v[u] = load8<F32>(a.x, 8 * i);
+    } else {
+      const uint32_t in = in0 + u * 256 + threadIdx.x, down = in / (uint32_t)a.per_row;
+      v[u] = load8<F32>(a.x, (row0 + down) * a.ldx + 8 * (in - down * (uint32_t)a.per_row));
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t i = i0 + u * 256 + threadIdx.x;
+    if (i >= a.chunks) continue;
+    float f[8];
+    values<F32>(v[u], f);
+    const uint32_t top = block_top(f);
+    const int s = block_scale<FP4 ? 2 : 8>(top);
+    if (FP4)
+      *(uint32_t*)(a.q + 4 * i) = encode_e2m1(f, s);
+    else
+      *(i2*)(a.q + 8 * i) = encode_e4m3(f, s);
+    if (!(i & 3)) a.s[i >> 2] = (uint8_t)s;
+  }
+}
+
+// ---- host -------------------------------------------------------------------
+
+int64_t token_rows(int64_t T, int64_t k, int64_t E, int64_t align) {
+  const int64_t n = T * k;
+  return (n + (n < E ? n : E) * (align - 1)) / align * align;
+}
+
+int check_plan(int T, int k, int E) {
+  if (T < 0 || k < 1 || k > MXW_MAX_CHOICES || E < 1 || E > MXW_MAX_EXPERTS || (int64_t)T * k > MXW_MAX_ROWS)
+    return MXW_ERR_DIM;
+  return MXW_OK;
+}
+
+bool on(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
+
+int launched() { return hipGetLastError() == hipSuccess ? MXW_OK : MXW_ERR_LAUNCH; }
+
+// waves a token: its row in one go where one wave can hold it
+bool one_wave(int H) { return H <= 512; }
+
+// what dispatch and the gradient share: the padding rows' workgroups and the forms
+int plan_pads(RowArgs& a) {
+  a.pad_split = 4;
+  a.pad_blocks = a.E * a.pad_split;
+  return a.pad_blocks;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t mxw_token_rows(int T, int k, int E, int align) {
+  if (check_plan(T, k, E) != MXW_OK || align < 1 || align > 1024) return MXW_ERR_DIM;
+  const int64_t R = token_rows(T, k, E, align);
+  return R <= MXW_MAX_ROWS ? R : MXW_ERR_DIM;
+}
+
+int64_t mxw_sort_workspace_size(int T, int k, int E) {
+  if (check_plan(T, k, E) != MXW_OK) return MXW_ERR_DIM;
+  const int64_t pieces = ((int64_t)T * k + kSortPiece - 1) / kSortPiece;
+  return pieces > 1 ? pieces * E * 4 : 0;
+}
+
+int mxw_sort_tokens(const void* ids, int id_bytes, int64_t ld, int T, int k, int E, int align, int32_t* offs,
+                    int32_t* counts, int32_t* rows, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!offs || !counts || (T != 0 && (!ids || !rows))) return MXW_ERR_NULL;
+  const int64_t R = mxw_token_rows(T, k, E, align);
+  if (R < 0 || (id_bytes != 4 && id_bytes != 8) || ld < k) return MXW_ERR_DIM;
+  if (!on(ids, id_bytes) || !on(offs, 4) || !on(counts, 4) || !on(rows, 4)) return MXW_ERR_ALIGN;
+  const int64_t need = mxw_sort_workspace_size(T, k, E);
+  if (need > 0 && (!workspace || !on(workspace, 256) || workspace_bytes < (size_t)need)) return MXW_ERR_WORKSPACE;
+  if (const int rc = check_device()) return rc;
+  SortArgs a = {ids, ld, T * k, k, E, align, offs, counts, rows, (int32_t*)workspace};
+  const int pieces = T ? (a.n + kSortPiece - 1) / kSortPiece : 1;
+  const dim3 grid(pieces), block(kSortWaves * 64);
+  hipStream_t st = (hipStream_t)stream;
+  if (id_bytes == 8) {
+    if (pieces > 1) sort_count_kernel<true><<<grid, block, 0, st>>>(a);
+    sort_place_kernel<true><<<grid, block, 0, st>>>(a);
+  } else {
+    if (pieces > 1) sort_count_kernel<false><<<grid, block, 0, st>>>(a);
+    sort_place_kernel<false><<<grid, block, 0, st>>>(a);
+  }
+  return launched();
+}
+
+int mxw_dispatch_tokens(const void* x, int type, int64_t ldx, const int32_t* offs, const int32_t* counts,
+                        const int32_t* rows, int T, int k, int E, int H, int R, void* xs, uint8_t* q, uint8_t* s,
+                        void* stream) {
+  if ((!xs && !q) || !q != !s) return MXW_ERR_NULL;
+  if (check_plan(T, k, E) != MXW_OK || H < 1 || H > 65536 || R < 0 || R > MXW_MAX_ROWS || ldx < H ||
+      (type != MXW_BF16 && type != MXW_F32) || (q && (H & 31)))
+    return MXW_ERR_DIM;
+  if (!offs || !counts || (T && (!x || !rows))) return MXW_ERR_NULL;
+  const int size = type == MXW_F32 ? 4 : 2;
+  if (!on(x, size) || !on(xs, size) || !on(offs, 4) || !on(counts, 4) || !on(rows, 4) || !on(q, 8)) return MXW_ERR_ALIGN;
+  if (const int rc = check_device()) return rc;
+  if (T == 0 || R == 0) return MXW_OK;
+  RowArgs a = {};
+  a.x = x, a.ldx = ldx, a.offs = offs, a.counts = counts, a.rows = rows;
+  a.T = T, a.k = k, a.E = E, a.H = H, a.R = R, a.out = xs, a.q = q, a.s = s;
+  const int pads = plan_pads(a);
+  hipStream_t st = (hipStream_t)stream;
+  auto go = [&](auto f32, auto with_rows, auto mx) {
+    constexpr bool F = decltype(f32)::value, RW = decltype(with_rows)::value, M = decltype(mx)::value;
+    if (one_wave(H))
+      dispatch_kernel<F, RW, M, 1><<<dim3(pads + (T + 3) / 4), dim3(256), 0, st>>>(a);
+    else
+      dispatch_kernel<F, RW, M, 4><<<dim3(pads + T), dim3(256), 0, st>>>(a);
+  };
+  using Y = std::true_type;
+  using N = std::false_type;
+  auto forms = [&](auto f32) {
+    if (!q)
+      go(f32, Y{}, N{});
+    else if (!xs)
+      go(f32, N{}, Y{});
+    else
+      go(f32, Y{}, Y{});
+  };
+  if (type == MXW_F32)
+    forms(Y{});
+  else
+    forms(N{});
+  return launched();
+}
+
+int mxw_combine_tokens(const void* y, int type, int64_t ldy, const int32_t* rows, const float* weights,
+                       const void* residual, int64_t ldr, int T, int k, int H, int R, void* out, void* stream) {
+  if (check_plan(T, k, 1) != MXW_OK || H < 1 || H > 65536 || R < 0 || R > MXW_MAX_ROWS || ldy < H ||
+      (residual && ldr < H) || (type != MXW_BF16 && type != MXW_F32))
+    return MXW_ERR_DIM;
+  if (T && (!rows || !out || (R && !y))) return MXW_ERR_NULL;
+  const int size = type == MXW_F32 ? 4 : 2;
+  if (!on(y, size) || !on(residual, size) || !on(out, size) || !on(rows, 4) || !on(weights, 4)) return MXW_ERR_ALIGN;
+  if (const int rc = check_device()) return rc;
+  if (T == 0) return MXW_OK;
+  RowArgs a = {};
+  a.y = y, a.ldy = ldy, a.rows = rows, a.weights = weights, a.residual = residual, a.ldr = ldr;
+  a.T = T, a.k = k, a.H = H, a.R = R, a.out = out;
+  hipStream_t st = (hipStream_t)stream;
+  auto go = [&](auto f32, auto wt) {
+    constexpr bool F = decltype(f32)::value, WT = decltype(wt)::value;
+    if (one_wave(H))
+      combine_kernel<F, WT, 1><<<dim3((T + 3) / 4), dim3(256), 0, st>>>(a);
+    else
+      combine_kernel<F, WT, 4><<<dim3(T), dim3(256), 0, st>>>(a);
+  };
+  using Y = std::true_type;
+  using N = std::false_type;
+  if (type == MXW_F32)
+    weights ? go(Y{}, Y{}) : go(Y{}, N{});
+  else
+    weights ? go(N{}, Y{}) : go(N{}, N{});
+  return launched();
+}
+
+int mxw_combine_tokens_grad(const void* dout, int type, int64_t ldo, const void* y, int64_t ldy, const int32_t* offs,
+                            const int32_t* counts, const int32_t* rows, const float* weights, int T, int k, int E, int H,
+                            int R, void* dy, uint8_t* q, uint8_t* s, float* dweights, void* stream) {
+  if ((!dy && !q && !dweights) || !q != !s) return MXW_ERR_NULL;
+  if (check_plan(T, k, E) != MXW_OK || H < 1 || H > 65536 || R < 0 || R > MXW_MAX_ROWS || ldo < H ||
+      (dweights && ldy < H) || (type != MXW_BF16 && type != MXW_F32) || (q && (H & 31)))
+    return MXW_ERR_DIM;
+  if (((dy || q) && (!offs || !counts)) || (T && (!dout || !rows || !weights || (R && dweights && !y))))
+    return MXW_ERR_NULL;
+  const int size = type == MXW_F32 ? 4 : 2;
+  if (!on(dout, size) || !on(y, size) || !on(dy, size) || !on(offs, 4) || !on(counts, 4) || !on(rows, 4) ||
+      !on(weights, 4) || !on(dweights, 4) || !on(q, 8))
+    return MXW_ERR_ALIGN;
+  if (const int rc = check_device()) return rc;
+  if (T == 0) return MXW_OK;
+  RowArgs a = {};
+  a.x = dout, a.ldx = ldo, a.y = y, a.ldy = ldy, a.offs = offs, a.counts = counts, a.rows = rows, a.weights = weights;
+  a.T = T, a.k = k, a.E = E, a.H = H, a.R = R, a.out = dy, a.q = q, a.s = s, a.dweights = dweights;
+  const int pads = dy || q ? plan_pads(a) : 0;
+  hipStream_t st = (hipStream_t)stream;
+  auto go = [&](auto f32, auto with_rows, auto mx) {
+    constexpr bool F = decltype(f32)::value, RW = decltype(with_rows)::value, M = decltype(mx)::value;
+    if (one_wave(H))
+      combine_grad_kernel<F, RW, M, 1><<<dim3(pads + (T + 3) / 4), dim3(256), 0, st>>>(a);
+    else
+      combine_grad_kernel<F, RW, M, 4><<<dim3(pads + T), dim3(256), 0, st>>>(a);
+  };
+  using Y = std::true_type;
+  using N = std::false_type;
+  auto forms = [&](auto f32) {
+    if (!q)
+      dy ? go(f32, Y{}, N{}) : go(f32, N{}, N{});
+    else
+      dy ? go(f32, Y{}, Y{}) : go(f32, N{}, Y{});
+  };
+  if (type == MXW_F32)
+    forms(Y{});
+  else
+    forms(N{});
+  return launched();
+}
+
+int mxw_quantize_rows(const void* x, int type, int64_t ldx, int64_t R, int C, int format, uint8_t* q, uint8_t* s,
+                      void* stream) {
+  if (R < 0 || R > ((int64_t)1 << 31) || C < 32 || C > 65536 || (C & 31) || ldx < C ||
+      (type != MXW_BF16 && type != MXW_F32) || (format != MXW_MXFP8 && format != MXW_MXFP4))
+    return MXW_ERR_DIM;
+  if (R && (!x || !q || !s)) return MXW_ERR_NULL;
+  if (!on(x, type == MXW_F32 ? 4 : 2) || !on(q, 8)) return MXW_ERR_ALIGN;
+  QuantArgs a = {x, ldx, R * (C >> 3), C >> 3, q, s};
+  const int64_t blocks = (a.chunks + 256 * kUnroll - 1) / (256 * kUnroll);
+  if (blocks > 0x7FFFFFFF / 256) return MXW_ERR_DIM;  // threads of a launch are counted in 32 bits
+  if (const int rc = check_device()) return rc;
+  if (R == 0) return MXW_OK;
+  hipStream_t st = (hipStream_t)stream;
+  auto go = [&](auto f32, auto fp4) {
+    constexpr bool F = decltype(f32)::value, P = decltype(fp4)::value;
+    if (ldx == C || R == 1)
+      quant_rows_kernel<F, P, true><<<dim3((uint32_t)blocks), dim3(256), 0, st>>>(a);
+    else
+      quant_rows_kernel<F, P, false><<<dim3((uint32_t)blocks), dim3(256), 0, st>>>(a);
+  };
+  using Y = std::true_type;
+  using N = std::false_type;
+  if (type == MXW_F32)
+    format == MXW_MXFP4 ? go(Y{}, Y{}) : go(Y{}, N{});
+  else
+    format == MXW_MXFP4 ? go(N{}, Y{}) : go(N{}, N{});
+  return launched();
+}
+
+}  // extern "C"

@@ -1,0 +1,161 @@
+"""The host checks of the tokens' operators, quantize_rows, clip_grad_norm and linear_4bit:
+bad arguments come back as status codes or exceptions before any device access (CPU only)."""
+import pytest
+import torch
+
+import mxfp8_ragged_grouped_amd as mxw
+
+P = 0x10000  # a fake, never-dereferenced device address
+BIG = 1 << 50
+BF16 = torch.bfloat16
+
+
+def call(f, base, over):
+    return f(**dict(base, **over))
+
+
+SORT = dict(ids=P, id_bytes=8, ld=2, T=4, k=2, E=8, align=32, offs=P, counts=P, rows=P, workspace=P, workspace_bytes=BIG)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(ids=0), -1), (dict(offs=0), -1), (dict(counts=0), -1), (dict(rows=0), -1),
+    (dict(id_bytes=2), -2), (dict(ld=1), -2), (dict(T=-1), -2), (dict(k=0), -2), (dict(k=65, ld=65), -2), (dict(E=0), -2),
+    (dict(E=257), -2), (dict(align=0), -2), (dict(align=1025), -2), (dict(T=1 << 23, k=2), -2),
+    (dict(T=(1 << 23) - 8, k=1, E=256, align=1024), -2),   # its rows are over the most
+    (dict(ids=P + 4), -3), (dict(offs=P + 2), -3), (dict(counts=P + 1), -3), (dict(rows=P + 2), -3),
+    (dict(T=9000, workspace=0), -6), (dict(T=9000, workspace=P + 16), -6), (dict(T=9000, workspace_bytes=63), -6),
+])
+def test_sort_host_checks(over, code):
+    assert call(mxw.mxw_sort_tokens, SORT, over) == code
+
+
+def test_sizes():
+    assert mxw.token_rows(0, 2, 8) == 0 and mxw.token_rows(1, 2, 8) == 64 and mxw.token_rows(1, 2, 1) == 32
+    assert mxw.token_rows(100, 2, 8) == (200 + 8 * 31) // 32 * 32 and mxw.token_rows(5, 3, 10, 1) == 15
+    assert mxw.sort_workspace_size(8192, 2, 8) == 0 and mxw.sort_workspace_size(8193, 2, 8) == 2 * 8 * 4
+    assert mxw.clip_workspace_size(0) > 0 and mxw.clip_workspace_size(97) == 2 * mxw.clip_workspace_size(96)
+    for f, args in ((mxw.token_rows, (1 << 23, 2, 8)), (mxw.token_rows, (4, 2, 0)), (mxw.token_rows, (4, 2, 8, 0)),
+                    (mxw.sort_workspace_size, (4, 65, 8)), (mxw.clip_workspace_size, (-1,)),
+                    (mxw.clip_workspace_size, (65537,))):
+        with pytest.raises(mxw.MxwError):
+            f(*args)
+
+
+DISPATCH = dict(x=P, dtype=0, ldx=64, offs=P, counts=P, rows=P, T=4, k=2, E=8, H=64, R=64, xs=P, q=P, s=P)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(x=0), -1), (dict(offs=0), -1), (dict(counts=0), -1), (dict(rows=0), -1), (dict(xs=0, q=0, s=0), -1),
+    (dict(q=0), -1), (dict(s=0), -1),
+    (dict(dtype=2), -2), (dict(ldx=63), -2), (dict(T=-1), -2), (dict(k=0), -2), (dict(E=0), -2), (dict(H=0), -2),
+    (dict(H=48), -2), (dict(H=65568, ldx=65568), -2), (dict(R=-1), -2), (dict(R=(1 << 23) + 1), -2),
+    (dict(x=P + 1), -3), (dict(dtype=1, x=P + 2), -3), (dict(xs=P + 1), -3), (dict(q=P + 4), -3), (dict(rows=P + 2), -3),
+    (dict(offs=P + 2), -3), (dict(counts=P + 1), -3),
+])
+def test_dispatch_host_checks(over, code):
+    assert call(mxw.mxw_dispatch_tokens, DISPATCH, over) == code
+
+
+COMBINE = dict(y=P, dtype=0, ldy=64, rows=P, weights=P, residual=P, ldr=64, T=4, k=2, H=64, R=64, out=P)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(y=0), -1), (dict(rows=0), -1), (dict(out=0), -1),
+    (dict(dtype=-1), -2), (dict(ldy=63), -2), (dict(ldr=63), -2), (dict(T=-1), -2), (dict(k=65), -2), (dict(H=0), -2),
+    (dict(H=65537, ldy=1 << 20, ldr=1 << 20), -2), (dict(R=-1), -2),
+    (dict(y=P + 1), -3), (dict(residual=P + 1), -3), (dict(out=P + 1), -3), (dict(weights=P + 2), -3), (dict(rows=P + 1), -3),
+    (dict(dtype=1, out=P + 2), -3),
+])
+def test_combine_host_checks(over, code):
+    assert call(mxw.mxw_combine_tokens, COMBINE, over) == code
+
+
+GRAD = dict(dout=P, dtype=0, ldo=64, y=P, ldy=64, offs=P, counts=P, rows=P, weights=P, T=4, k=2, E=8, H=64, R=64, dy=P, q=P,
+            s=P, dweights=P)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(dout=0), -1), (dict(y=0), -1), (dict(offs=0), -1), (dict(counts=0), -1), (dict(rows=0), -1), (dict(weights=0), -1),
+    (dict(dy=0, q=0, s=0, dweights=0), -1), (dict(q=0), -1), (dict(s=0), -1),
+    (dict(dtype=2), -2), (dict(ldo=63), -2), (dict(ldy=63), -2), (dict(E=257), -2), (dict(H=40), -2), (dict(R=-1), -2),
+    (dict(dout=P + 1), -3), (dict(y=P + 1), -3), (dict(dy=P + 1), -3), (dict(q=P + 2), -3), (dict(dweights=P + 2), -3),
+])
+def test_grad_host_checks(over, code):
+    assert call(mxw.mxw_combine_tokens_grad, GRAD, over) == code
+
+
+ROWS = dict(x=P, dtype=0, ldx=64, R=10, C=64, format=0, q=P, s=P)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(x=0), -1), (dict(q=0), -1), (dict(s=0), -1),
+    (dict(dtype=2), -2), (dict(ldx=63), -2), (dict(R=-1), -2), (dict(R=(1 << 31) + 1), -2), (dict(C=0), -2), (dict(C=40), -2),
+    (dict(C=65568, ldx=65568), -2), (dict(format=2), -2), (dict(R=1 << 31, C=65536, ldx=65536), -2),
+    (dict(x=P + 1), -3), (dict(dtype=1, x=P + 2), -3), (dict(q=P + 4), -3),
+])
+def test_quantize_rows_host_checks(over, code):
+    assert call(mxw.mxw_quantize_rows, ROWS, over) == code
+
+
+CLIP = dict(grads=[P, 2 * P], outs=[P, 2 * P], sizes=[100, 200], types=[0, 1], norm_type=2, max_norm=1.0, eps=1e-6, norm=P,
+            workspace=P, workspace_bytes=BIG)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(grads=[0, P]), -1), (dict(outs=[P, 0]), -1), (dict(norm=0), -1),
+    (dict(types=[0, 2]), -2), (dict(sizes=[100, -1]), -2), (dict(sizes=[100, (1 << 40) + 1]), -2), (dict(norm_type=1), -2),
+    (dict(max_norm=-1.0), -2), (dict(max_norm=float("nan")), -2), (dict(eps=-1e-9), -2), (dict(eps=float("nan")), -2),
+    (dict(grads=[P + 1, 2 * P], outs=None), -3), (dict(grads=[P, 2 * P + 2], outs=None), -3), (dict(norm=P + 2), -3),
+    (dict(workspace=0), -6), (dict(workspace=P + 128), -6), (dict(workspace_bytes=16), -6),
+    (dict(grads=[P, P], outs=[P, P]), -8), (dict(grads=[P, P + 196], outs=[P, P + 196]), -8),
+    (dict(outs=[P + 2, 2 * P]), -8), (dict(outs=[2 * P, 3 * P]), -8), (dict(outs=[3 * P, 3 * P]), -8),
+])
+def test_clip_host_checks(over, code):
+    assert call(mxw.mxw_clip_grads, CLIP, over) == code
+
+
+LINEAR = dict(x=P, ldx=256, codes=P, scales=P, zeros=0, format=1, group=32, T=4, K=256, N=100, out=P, out_type=0)
+INT = dict(format=2, group=64, zeros=P)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(x=0), -1), (dict(codes=0), -1), (dict(scales=0), -1), (dict(out=0), -1),
+    (dict(format=0), -2), (dict(format=3), -2), (dict(group=64), -2), (dict(zeros=P), -2), (dict(T=-1), -2), (dict(T=65), -2),
+    (dict(K=0), -2), (dict(K=48), -2), (dict(K=65568, ldx=65568), -2), (dict(N=0), -2), (dict(N=(1 << 20) + 1), -2),
+    (dict(ldx=248), -2), (dict(ldx=260), -2), (dict(out_type=2), -2), (dict(INT, group=16), -2), (dict(INT, group=48), -2),
+    (dict(INT, group=128, K=192, ldx=192), -2),
+    (dict(x=P + 8), -3), (dict(codes=P + 4), -3), (dict(out=P + 1), -3), (dict(out_type=1, out=P + 2), -3),
+    (dict(INT, scales=P + 1), -3),
+])
+def test_linear_host_checks(over, code):
+    assert call(mxw.mxw_linear_4bit, LINEAR, over) == code
+
+
+def test_python_faces_validate():
+    """CPU tensors (there is no host fallback), types, shapes and strides."""
+    ids = torch.zeros((4, 2), dtype=torch.int64)
+    x, y, w = torch.zeros((4, 64), dtype=BF16), torch.zeros((64, 64), dtype=BF16), torch.zeros((4, 2))
+    i32 = torch.int32
+    plan = mxw.TokenPlan(torch.zeros(8, dtype=i32), torch.zeros(8, dtype=i32), torch.zeros((4, 2), dtype=i32), 64)
+    codes, scales = torch.zeros((100, 32), dtype=torch.uint8), torch.zeros((100, 2), dtype=torch.uint8)
+    for error, f in (
+            (ValueError, lambda: mxw.sort_tokens(ids, 8)), (TypeError, lambda: mxw.sort_tokens(ids.short(), 8)),
+            (ValueError, lambda: mxw.sort_tokens(ids[0], 8)), (ValueError, lambda: mxw.sort_tokens(ids[:, :0], 8)),
+            (ValueError, lambda: mxw.dispatch_tokens(x, plan)), (TypeError, lambda: mxw.dispatch_tokens(x.half(), plan)),
+            (ValueError, lambda: mxw.combine_tokens(y, plan)), (TypeError, lambda: mxw.combine_tokens(y.half(), plan)),
+            (ValueError, lambda: mxw.combine_tokens_grad(x, y, plan, w)),
+            (TypeError, lambda: mxw.combine_tokens_grad(x.half(), y, plan, w)),
+            (ValueError, lambda: mxw.quantize_rows(x)), (TypeError, lambda: mxw.quantize_rows(x.half())),
+            (ValueError, lambda: mxw.quantize_rows(x, "mxfp6")),
+            (ValueError, lambda: mxw.clip_grad_norm([x], 1.0)), (ValueError, lambda: mxw.grad_norm([])),
+            (TypeError, lambda: mxw.grad_norm([x.half()])), (ValueError, lambda: mxw.grad_norm([x], norm_type=1)),
+            (ValueError, lambda: mxw.clip_grad_norm([x], -1.0)), (ValueError, lambda: mxw.clip_grad_norm([x], float("nan"))),
+            (ValueError, lambda: mxw.linear_4bit(x, codes, scales)), (TypeError, lambda: mxw.linear_4bit(x.float(), codes, scales)),
+            (TypeError, lambda: mxw.linear_4bit(x, codes, scales.half())),
+            (TypeError, lambda: mxw.linear_4bit(x, codes, scales, dtype=torch.float16))):
+        with pytest.raises(error):
+            f()
+
+
+def test_strerror_names_overlap():
+    assert "overlap" in mxw.strerror(-8)
