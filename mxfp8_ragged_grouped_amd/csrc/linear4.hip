@@ -27,6 +27,8 @@ using mxw::i4;
 using mxw::v4f;
 using mxw::v8bf;
 
+typedef unsigned int u2v __attribute__((ext_vector_type(2)));
+
 struct LinArgs {
   const uint16_t* x;
   int64_t ldx;
@@ -34,7 +36,12 @@ struct LinArgs {
   const void* scales;
   const uint8_t* zeros;
   int T, K, N, group;
+  int steps;      // of 256 k, the last one may be partly past K
   int split;      // waves that share a row tile's steps
+  int chunk;      // steps of x that LDS holds at a time, a multiple of split
+  int chunks;
+  int items;      // row tiles of a workgroup's size
+  int f32;        // out is FP32
   void* out;
 };
 
@@ -51,154 +58,381 @@ __device__ __forceinline__ i4 decode_fp4(uint32_t c, float scale) {
   r.w = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 3));
   return r;
 }
-// 8 codes n as the bf16 numbers 16 + n (0x4180 + 8 n), in the order 0 4 1 5 2 6 3 7
+// 8 codes n as the bf16 numbers n.  The bytes 0 .. 15 are E4M3's first 16 numbers,
+// n 2^-9 (its subnormals and the binade above them have one step), so that the scaled
+// conversion makes them whole numbers: 9 operations, where putting n into the bits of
+// 16 + n takes 11 and leaves 16 to be taken off again.
 __device__ __forceinline__ i4 decode_int(uint32_t c) {
+  const uint32_t even = c & 0x0F0F0F0Fu, odd = c >> 4 & 0x0F0F0F0Fu;
+  const int lo = (int)__builtin_amdgcn_perm(odd, even, 0x05010400u), hi = (int)__builtin_amdgcn_perm(odd, even, 0x07030602u);
   i4 r;
-  r.x = (int)((c << 3 & 0x00780078u) | 0x41804180u);
-  r.y = (int)((c >> 1 & 0x00780078u) | 0x41804180u);
-  r.z = (int)((c >> 5 & 0x00780078u) | 0x41804180u);
-  r.w = (int)((c >> 9 & 0x00780078u) | 0x41804180u);
-  return r;
-}
-// 8 tokens' values in that order
-__device__ __forceinline__ i4 like_codes(const i4& v) {
-  i4 r;
-  r.x = (int)__builtin_amdgcn_perm((uint32_t)v.z, (uint32_t)v.x, 0x05040100u);
-  r.y = (int)__builtin_amdgcn_perm((uint32_t)v.z, (uint32_t)v.x, 0x07060302u);
-  r.z = (int)__builtin_amdgcn_perm((uint32_t)v.w, (uint32_t)v.y, 0x05040100u);
-  r.w = (int)__builtin_amdgcn_perm((uint32_t)v.w, (uint32_t)v.y, 0x07060302u);
+  r.x = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false));
+  r.y = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true));
+  r.z = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false));
+  r.w = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true));
   return r;
 }
 
 // 4 x 4 words turned over between the 4 rows of 16 lanes: of lane (n, b), word i
 // becomes word b of lane (n, i)
 __device__ __forceinline__ i4 turn(i4 v) {
-  typedef unsigned int u2 __attribute__((ext_vector_type(2)));
-  u2 p = __builtin_amdgcn_permlane32_swap((uint32_t)v.x, (uint32_t)v.z, false, false);
-  u2 q = __builtin_amdgcn_permlane32_swap((uint32_t)v.y, (uint32_t)v.w, false, false);
-  u2 r = __builtin_amdgcn_permlane16_swap(p.x, q.x, false, false);
-  u2 s = __builtin_amdgcn_permlane16_swap(p.y, q.y, false, false);
+  const u2v p = __builtin_amdgcn_permlane32_swap((uint32_t)v.x, (uint32_t)v.z, false, false);
+  const u2v q = __builtin_amdgcn_permlane32_swap((uint32_t)v.y, (uint32_t)v.w, false, false);
+  const u2v r = __builtin_amdgcn_permlane16_swap(p.x, q.x, false, false);
+  const u2v s = __builtin_amdgcn_permlane16_swap(p.y, q.y, false, false);
   return (i4){(int)r.x, (int)r.y, (int)s.x, (int)s.y};
 }
 
-template <bool OUT32>
-__device__ __forceinline__ void put(const LinArgs& a, int t, int n, float v) {
-  if (t < a.T && n < a.N) {
-    if (OUT32)
-      ((float*)a.out)[(int64_t)t * a.N + n] = v;
-    else
-      ((uint16_t*)a.out)[(int64_t)t * a.N + n] = (uint16_t)mxw::bf16_bits(v);
-  }
+// LDS-direct load of BYTES (1, 2, 16) a lane from offset voff + soff of the buffer, to 4 (16)
+// bytes l of LDS byte `lds`; the range check leaves soff out, lanes out of the range write
+// zeros
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+template <int BYTES>
+__device__ __forceinline__ void load_lds(const __amdgpu_buffer_rsrc_t& rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
+  static_assert(BYTES == 1 || BYTES == 2 || BYTES == 16, "a byte, a 16-bit word or four words");
+  if (BYTES == 1)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, %3 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+                 : "memory", "m0");
+  else if (BYTES == 2)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ushort %1, %2, %3 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+                 : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// all but the last N loads of this wave have landed
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
+  asm volatile("" ::: "memory");
+}
+// every LDS read of this wave has returned
+__device__ __forceinline__ void wait_reads() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);
 }
 
-// A workgroup: 4 / split row tiles of 16, each by `split` waves that take steps in turn.
-template <bool FP4, int TT, int D, bool OUT32>
-__global__ __launch_bounds__(256) void linear4_kernel(LinArgs a) {
-  __shared__ float red[3][TT * 4][64];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int part = wave % a.split;
-  const int n0 = (blockIdx.x * (4 / a.split) + wave / a.split) * 16;
-  const int n = lane & 15, b = lane >> 4;
-  const int64_t row = min(n0 + n, a.N - 1);
-  const uint8_t* w = a.w + row * (a.K >> 1) + 16 * b;
-  const int blocks = a.K >> 5, steps = (blocks + 3) >> 2;
-  const uint16_t* x[TT];
-#pragma unroll
-  for (int i = 0; i < TT; ++i) x[i] = a.x + min(16 * i + n, a.T - 1) * a.ldx + (FP4 ? 32 * b : 8 * b);
-  const int groups = FP4 ? blocks : a.K / a.group;
-  const int per = FP4 ? 1 : a.group >> 5;  // blocks of a group
-  const uint8_t* s8 = (const uint8_t*)a.scales + row * groups;
-  const uint16_t* s16 = (const uint16_t*)a.scales + row * groups;
-  const uint8_t* zero = a.zeros ? a.zeros + row * groups : nullptr;
+constexpr uint32_t kOut = 0xC0000000u;   // an offset past every buffer's range: loads give 0 and read nothing
 
-  v4f sum[TT];
+// What a wave's slot of the ring holds for each 16 rows of a step of 256 k: 2 KiB of codes,
+// and a word for every scale and zero.
+template <int GC, int RT>
+struct Slot {
+  static constexpr int kScaleLoads = GC == 0 || GC == 4 ? 2 * RT : GC == 2 ? RT : (RT + 1) / 2;
+  static constexpr int kLoads = 2 * RT + kScaleLoads * (GC == 0 ? 1 : 2);
+  static constexpr int kScales = 2048 * RT, kZeros = kScales + 256 * kScaleLoads;
+  static constexpr int kBytes = kZeros + (GC == 0 ? 0 : 256 * kScaleLoads);
+};
+
+// A workgroup: WAVES / split row tiles of 16 RT, each by `split` waves that take steps of
+// 256 k in turn.  GC: groups of 128 k of integers (128 / group), 0: MXFP4.  R: how many of
+// its 4 tokens a lane sums up (1 for a single token).
+//
+// The tokens are held in LDS, all of K (CH = 0), or CH steps at a time in two buffers,
+// loaded straight to LDS a piece ahead.  16 bytes of token t at place p of its row lie at
+// p' ^ t % 16 (p': place_of below): the LDS takes 256 bytes at a time, from lanes 0 .. 3 and
+// 12 .. 15 of 16 and 4 .. 11 of the next 16, and their reads meet every bank once (with p
+// itself half of them met another: a fifth of the kernel's time at 64 tokens).
+//
+// A wave brings its own rows' codes to its own ring of D slots in LDS, whole cache lines
+// a load: read straight into the MFMA's layout, 16 lanes touch 16 lines, which makes the
+// vector memory path the bound (3.4 TB/s where this reaches TODO).  The ring runs on across
+// pieces and row tiles.  Every step issues the same number of loads, which the waits count:
+// what is past the end gets an offset out of its buffer's range and lands as zeros.
+template <int GC, int TT, int RT, int D, int WAVES, int R, int CH>
+__global__ __launch_bounds__(WAVES * 64) void linear4_kernel(LinArgs a) {
+  constexpr bool FP4 = GC == 0, TURN = GC > 1, PIECES = CH > 0;
+  using S = Slot<GC, RT>;
+  extern __shared__ __align__(1024) uint8_t lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int part = wave % a.split, sub = wave / a.split, subs = WAVES / a.split;
+  const int n = lane & 15, b = lane >> 4;
+  const int blocks = a.K >> 5, groups = FP4 ? blocks : a.K / a.group;
+  const uint32_t wrow = (uint32_t)a.K >> 1;
+  const uint32_t ring = wave * (D * S::kBytes), tokens0 = WAVES * (D * S::kBytes);
+
+  // ---- tokens to LDS -----------------------------------------------------------
+  // place in 128 k of the 16 bytes that lane b reads q-th
+  auto place_of = [](int b, int q) { return TURN ? 4 * q + b : 4 * (2 * (b & 1) + ((b ^ b >> 1) & 1)) + q; };
+  // and which of the row's 16 bytes lie at a place
+  auto source_of = [](int p) {
+    const int u = p >> 2;
+    return TURN ? p : (p & ~12) | 4 * ((u >> 1 & 1) + 2 * ((u ^ u >> 1) & 1));
+  };
+  const int chunk = PIECES ? CH : a.chunk, per_row = chunk * 32;   // steps, and 16 bytes of a token, that LDS holds
+  const int pieces = (PIECES ? 16 * TT : a.T) * per_row;
+  const int rounds = PIECES ? TT * CH * 8 / WAVES : (pieces + WAVES * 64 - 1) / (WAVES * 64);
+  const uint32_t buf = rounds * (WAVES * 1024);
+  const __amdgpu_buffer_rsrc_t xr =
+      mxw::buffer_of(a.x, mxw::range_of(((int64_t)(a.T - 1) * a.ldx + a.K) * 2));
+  auto token_piece = [&](int h, int c, bool whole) {   // its offset, without the piece's
+    const int i = (h * WAVES + wave) * 64 + lane, t = i / per_row, p = source_of((i - t * per_row) ^ (t & 15));
+    return t < a.T && (whole || (c * per_row + p) * 8 < a.K) ? (uint32_t)(t * (int)a.ldx + 8 * p) * 2u : kOut;
+  };
+  constexpr int kRounds = PIECES ? TT * CH * 8 / WAVES : 1;
+  uint32_t xo[kRounds];
+  if (PIECES) {
 #pragma unroll
-  for (int i = 0; i < TT; ++i) sum[i] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-  i4 codes[D], xv[D][TT][4];
-  uint32_t sc[D][4], ze[D][4];
-  auto load = [&](int d, int step) {
-    const bool in = 4 * step + b < blocks;
-    codes[d] = (i4){0, 0, 0, 0};
-    if (in) codes[d] = __builtin_nontemporal_load((const i4*)(w + 64 * step));
-    if (FP4) {
-      sc[d][0] = in ? s8[4 * step + b] : 0;
+    for (int h = 0; h < kRounds; ++h) xo[h] = token_piece(h, 0, true);
+  }
+  auto fetch = [&](int c, uint32_t to) {
+    const bool whole = (c + 1) * chunk * 256 <= a.K;
+    if (PIECES && whole) {
 #pragma unroll
-      for (int i = 0; i < TT; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) xv[d][i][q] = in ? *(const i4*)(x[i] + 128 * step + 8 * q) : (i4){0, 0, 0, 0};
+      for (int h = 0; h < kRounds; ++h) load_lds<16>(xr, to + (h * WAVES + wave) * 1024, xo[h], c * chunk * 512);
     } else {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int block = 4 * step + q < blocks ? 4 * step + q : 0;
-        sc[d][q] = s16[block / per];
-        ze[d][q] = zero ? zero[block / per] : 8;
-#pragma unroll
-        for (int i = 0; i < TT; ++i) xv[d][i][q] = *(const i4*)(x[i] + 32 * block);
-      }
+      for (int h = 0; h < rounds; ++h)
+        load_lds<16>(xr, to + (h * WAVES + wave) * 1024, token_piece(h, c, whole), c * chunk * 512);
     }
   };
+
+  // ---- weights: a cursor that runs D steps ahead --------------------------------
+  const int ends = a.chunks * chunk;       // steps of a row tile, rounded up
+  int item = blockIdx.x, at = part;
+  __amdgpu_buffer_rsrc_t wr, sr, zr;
+  auto seek = [&] {
+    const int64_t row0 = ((int64_t)item * subs + sub) * (16 * RT), left = item < a.items ? a.N - row0 : 0;
+    const int64_t base = left > 0 ? row0 : 0;
+    wr = mxw::buffer_of(a.w + base * wrow, mxw::range_of(left * wrow));
+    sr = mxw::buffer_of((const uint8_t*)a.scales + base * groups * (FP4 ? 1 : 2),
+                        mxw::range_of(left * groups * (FP4 ? 1 : 2)));
+    if (!FP4) zr = mxw::buffer_of(a.zeros + base * groups, a.zeros ? mxw::range_of(left * groups) : 0u);
+  };
+  // codes: 8 rows of 128 bytes a load, 16 bytes c of row i at c ^ (i / 2) % 8; scales and
+  // zeros: a word each, g of row i at g ^ 4 where i / 8 is odd and a row has 8 (bank conflicts)
+  constexpr int kPer = FP4 ? 8 : 2 * GC;   // scales of a row and step
+  uint32_t wo[2 * RT], so[S::kScaleLoads];
+#pragma unroll
+  for (int j = 0; j < 2 * RT; ++j) {
+    const int row = 8 * j + (lane >> 3);
+    wo[j] = row * wrow + 16 * ((lane & 7) ^ ((row >> 1) & 7));
+  }
+  auto group_of = [&](int j) { return (lane % kPer) ^ (kPer == 8 ? 4 * (j & 1) : 0); };
+#pragma unroll
+  for (int j = 0; j < S::kScaleLoads; ++j) {
+    const int row = (j * 64 + lane) / kPer;
+    so[j] = row < 16 * RT ? (uint32_t)(row * groups + group_of(j)) : kOut >> 1;
+  }
+  auto load = [&](int d) {
+    const uint32_t to = ring + d * S::kBytes;
+    const bool whole = 8 * at + 8 <= blocks;
+#pragma unroll
+    for (int j = 0; j < 2 * RT; ++j) {
+      uint32_t o = wo[j];
+      if (!whole) o = 8 * at + ((lane & 7) ^ ((8 * j + (lane >> 3)) >> 1 & 7)) < blocks ? o : kOut;
+      load_lds<16>(wr, to + 1024 * j, o, 128 * at);
+    }
+#pragma unroll
+    for (int j = 0; j < S::kScaleLoads; ++j) {
+      uint32_t o = so[j];
+      if (!whole) o = kPer * at + group_of(j) < groups ? o : kOut >> 1;
+      load_lds<FP4 ? 1 : 2>(sr, to + S::kScales + 256 * j, FP4 ? o : 2 * o, kPer * at * (FP4 ? 1 : 2));
+      if (!FP4) load_lds<1>(zr, to + S::kZeros + 256 * j, o, kPer * at);
+    }
+    at += a.split;
+    if (at >= ends) {
+      at = part;
+      item += gridDim.x;
+      seek();
+    }
+  };
+
+  v4f sum[RT][TT];
   const i4 ones = {0x3F803F80, 0x3F803F80, 0x3F803F80, 0x3F803F80};
-  auto use = [&](int d, int step) {
-    if (FP4) {
-      const float s = __uint_as_float(sc[d][0] << 23);
+  const v4f none = {0.0f, 0.0f, 0.0f, 0.0f};
+  // this lane's token rows in LDS (past T: the last, whose sums are not stored), and in
+  // 128 k its 16 bytes of q
+  uint32_t token[TT], place[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const i4 v = decode_fp4((uint32_t)codes[d][q], s);
+  for (int i = 0; i < TT; ++i)
+    token[i] = (uint32_t)((PIECES ? 16 * i : min(16 * i + n, a.T - 1)) * per_row * 16);
 #pragma unroll
-        for (int i = 0; i < TT; ++i) sum[i] = mfma(xv[d][i][q], v, sum[i]);
+  for (int q = 0; q < 4; ++q) place[q] = (uint32_t)((PIECES ? n * per_row * 16 : 0) + (place_of(b, q) ^ n) * 16);
+  // the step in slot d, its tokens from LDS byte `from` on
+  auto use = [&](int d, uint32_t from) {
+    const uint8_t* slot = lds + (ring + d * S::kBytes);
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h, from += 256) {
+      // the rows' operands, and of each group the scale and minus the scale times the zero
+      constexpr int G = FP4 ? 1 : GC, Q = 4 / G;
+      i4 v[RT][4];
+      float s[RT][G], z[RT][G];
+#pragma unroll
+      for (int j = 0; j < RT; ++j) {
+        i4 c = *(const i4*)(slot + 2048 * j + 128 * n + (((4 * h + b) ^ (n >> 1)) << 4));
+        const int flip = kPer == 8 ? n >> 3 : 0;   // the half of the row's words
+        const uint8_t* words = slot + 4 * ((16 * j + n) * kPer + (kPer == 8 ? 4 * (h ^ flip) + (FP4 ? b : 0) : GC * h));
+        if (TURN) c = turn(c);
+        if (FP4) {
+          s[j][0] = __uint_as_float(*(const uint32_t*)(words + S::kScales) << 23);
+        } else {
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            s[j][g] = __uint_as_float(*(const uint32_t*)(words + S::kScales + 4 * g) << 16);
+            z[j][g] = -s[j][g] * (a.zeros ? (float)*(const uint32_t*)(words + S::kZeros + 4 * g) : 8.0f);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[j][q] = FP4 ? decode_fp4((uint32_t)c[q], s[j][0]) : decode_int((uint32_t)c[q]);
       }
-    } else {
-      const i4 c = turn(codes[d]);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (4 * step + q >= blocks) continue;
-        const i4 v = decode_int((uint32_t)c[q]);
-        const float s = __uint_as_float(sc[d][q] << 16), z = s * (float)(16 + ze[d][q]);
+      for (int i = 0; i < TT; ++i) {
+        i4 x[4];
 #pragma unroll
-        for (int i = 0; i < TT; ++i) {
-          const v4f none = {0.0f, 0.0f, 0.0f, 0.0f};
-          const i4 xp = like_codes(xv[d][i][q]);
-          const v4f dot = mfma(xp, v, none), all = mfma(xp, ones, none);
+        for (int q = 0; q < 4; ++q) x[q] = *(const i4*)(lds + (from + token[i] + place[q]));
+        if (FP4) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) sum[i][r] = fmaf(s, dot[r], fmaf(-z, all[r], sum[i][r]));
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int j = 0; j < RT; ++j) sum[j][i] = mfma(x[q], v[j][q], sum[j][i]);
+        } else {
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            v4f all = none, dot[RT];
+#pragma unroll
+            for (int j = 0; j < RT; ++j) dot[j] = none;
+#pragma unroll
+            for (int q = g * Q; q < (g + 1) * Q; ++q) {
+              all = mfma(x[q], ones, all);
+#pragma unroll
+              for (int j = 0; j < RT; ++j) dot[j] = mfma(x[q], v[j][q], dot[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < RT; ++j)
+#pragma unroll
+              for (int r = 0; r < R; ++r) sum[j][i][r] = fmaf(s[j][g], dot[j][r], fmaf(z[j][g], all[r], sum[j][i][r]));
+          }
         }
       }
     }
   };
+  auto put = [&](int64_t row0) {
 #pragma unroll
-  for (int d = 0; d < D; ++d)
-    if (part + d * a.split < steps) load(d, part + d * a.split);
-  for (int step = part; step < steps; step += D * a.split) {
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      const int now = step + d * a.split;
-      if (now >= steps) break;
-      use(d, now);
-      if (now + D * a.split < steps) load(d, now + D * a.split);
-    }
-  }
-  if (a.split > 1) {
-    if (part > 0) {
+    for (int j = 0; j < RT; ++j) {
+      const int64_t row = row0 + 16 * j + n;
+      if (row >= a.N) continue;
 #pragma unroll
       for (int i = 0; i < TT; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) red[wave - 1][4 * i + r][lane] = sum[i][r];
+        for (int r = 0; r < R; ++r) {
+          const int t = 16 * i + 4 * b + r;
+          if (t >= a.T) continue;
+          if (a.f32)
+            ((float*)a.out)[(int64_t)t * a.N + row] = sum[j][i][r];
+          else
+            ((uint16_t*)a.out)[(int64_t)t * a.N + row] = (uint16_t)mxw::bf16_bits(sum[j][i][r]);
+        }
     }
-    __syncthreads();
-    if (part > 0) return;
-    for (int p = 1; p < a.split; ++p)
+  };
+
+  seek();
+  fetch(0, tokens0);
 #pragma unroll
-      for (int i = 0; i < TT; ++i)
+  for (int d = 0; d < D; ++d) load(d);
+  mxw::stage_barrier<D * S::kLoads>();
+  uint32_t now = 0;   // the buffer of the piece
+  int slot = 0;
+  for (int it = blockIdx.x; it < a.items; it += gridDim.x) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sum[i][r] += red[wave + p - 1][4 * i + r][lane];
+    for (int j = 0; j < RT; ++j)
+#pragma unroll
+      for (int i = 0; i < TT; ++i) sum[j][i] = none;
+    for (int c = 0; c < a.chunks; ++c) {
+      // the next piece of x, or the first again for the next row tile
+      const bool more = PIECES && (c + 1 < a.chunks || it + (int)gridDim.x < a.items);
+      if (more) fetch(c + 1 < a.chunks ? c + 1 : 0, tokens0 + (buf - now));
+#pragma unroll 1
+      for (int of = part; of < chunk; of += a.split) {
+        if (c * chunk + of < a.steps) {
+          wait_loads<(D - 1) * S::kLoads>();
+          use(slot, tokens0 + now + 512 * of);
+          wait_reads();   // the slot's next load may overwrite it
+        }
+        load(slot);
+        slot = slot + 1 == D ? 0 : slot + 1;
+      }
+      if (more) {
+        // loads after the piece's: at least a step's
+        mxw::stage_barrier<S::kLoads>();
+        now = buf - now;
+      }
+    }
+    const int64_t row0 = ((int64_t)it * subs + sub) * (16 * RT);
+    if (RT == 1 && a.split > 1) {   // the parts are added in their order
+      float* red = (float*)(lds + tokens0 + (PIECES ? 2 : 1) * buf) + sub * (a.split - 1) * (TT * 256);
+      mxw::stage_barrier<D * S::kLoads>();
+      if (part > 0) {
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+#pragma unroll
+          for (int r = 0; r < R; ++r) red[(((part - 1) * TT + i) * 4 + r) * 64 + lane] = sum[0][i][r];
+      }
+      mxw::stage_barrier<D * S::kLoads>();
+      if (part == 0) {
+        for (int p = 1; p < a.split; ++p)
+#pragma unroll
+          for (int i = 0; i < TT; ++i)
+#pragma unroll
+            for (int r = 0; r < R; ++r) sum[0][i][r] += red[(((p - 1) * TT + i) * 4 + r) * 64 + lane];
+        put(row0);
+      }
+    } else {
+      put(row0);
+    }
   }
-#pragma unroll
-  for (int i = 0; i < TT; ++i)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) put<OUT32>(a, 16 * i + 4 * b + r, n0 + n, sum[i][r]);
+  wait_loads<0>();   // no load outlives the ring's use
 }
 
 bool on(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
+
+constexpr int kLds = 160 * 1024;
+
+// CH: the steps of a piece where x does not fit in LDS, and then the most that a tile's steps
+// are split
+template <int GC, int TT, int RT, int D, int WAVES, int CH, int R = 4>
+int launch(LinArgs a, hipStream_t st) {
+  const int tiles = (a.N + 15) / 16;
+  constexpr int ring = WAVES * D * Slot<GC, RT>::kBytes;
+  a.split = 1;
+  while (RT == 1 && a.split < WAVES && tiles * a.split < 256 * WAVES && a.steps >= 2 * a.split) a.split *= 2;
+  auto joined = [&] { return a.split > 1 ? (WAVES - WAVES / a.split) * TT * 1024 : 0; };
+  a.chunk = (a.steps + a.split - 1) / a.split * a.split;
+  a.chunks = 1;
+  int lds = ring + (a.T * a.chunk * 512 + WAVES * 1024 - 1) / (WAVES * 1024) * (WAVES * 1024) + joined();
+  const bool pieces = lds > kLds;
+  if (pieces) {
+    while (a.split > CH) a.split /= 2;
+    a.chunk = CH;
+    a.chunks = (a.steps + CH - 1) / CH;
+    lds = ring + 2 * TT * CH * 8192 + joined();
+    static_assert(ring + 2 * TT * CH * 8192 + (RT == 1 ? (WAVES - WAVES / CH) * TT * 1024 : 0) <= kLds, "LDS");
+  }
+  const int rows = WAVES / a.split * RT;   // 16-row tiles of a workgroup
+  a.items = (tiles + rows - 1) / rows;
+  const dim3 grid(a.items < 256 ? a.items : 256), block(WAVES * 64);
+  if (pieces)
+    linear4_kernel<GC, TT, RT, D, WAVES, R, CH><<<grid, block, lds, st>>>(a);
+  else
+    linear4_kernel<GC, TT, RT, D, WAVES, R, 0><<<grid, block, lds, st>>>(a);
+  return hipGetLastError() == hipSuccess ? MXW_OK : MXW_ERR_LAUNCH;
+}
+template <int GC>
+int launch(const LinArgs& a, hipStream_t st) {
+  const bool wide = (a.N + 15) / 16 >= 4096;
+  if (a.T == 1) return wide ? launch<GC, 1, 2, 2, 8, 4, 1>(a, st) : launch<GC, 1, 1, 2, 8, 4, 1>(a, st);
+  if (a.T <= 16) return wide ? launch<GC, 1, 2, 2, 8, 4>(a, st) : launch<GC, 1, 1, 2, 8, 4>(a, st);
+  if (a.T <= 32) return wide ? launch<GC, 2, 2, 2, 8, 2>(a, st) : launch<GC, 2, 1, 2, 4, 4>(a, st);
+  return wide ? launch<GC, 4, 2, 2, 8, 1>(a, st) : launch<GC, 4, 1, 2, 4, 2>(a, st);
+}
 
 }  // namespace
 
@@ -207,7 +441,7 @@ extern "C" int mxw_linear_4bit(const uint16_t* x, int64_t ldx, const uint8_t* co
                                int out_type, void* stream) {
   const bool fp4 = format == MXW_MXFP4;
   if ((!fp4 && format != MXW_INT4) || T < 0 || T > MXW_MOE_MAX_TOKENS || K < 32 || K > 65536 || N < 1 ||
-      N > (1 << 20) || ldx < K || (ldx & 7) || (out_type != MXW_BF16 && out_type != MXW_F32) ||
+      N > (1 << 20) || ldx < K || (ldx & 7) || ldx > (1 << 23) || (out_type != MXW_BF16 && out_type != MXW_F32) ||
       (fp4 ? group != 32 || zeros : group != 32 && group != 64 && group != 128) || K % group)
     return MXW_ERR_DIM;
   if (!codes || !scales || (T && (!x || !out))) return MXW_ERR_NULL;
@@ -215,27 +449,9 @@ extern "C" int mxw_linear_4bit(const uint16_t* x, int64_t ldx, const uint8_t* co
     return MXW_ERR_ALIGN;
   if (const int rc = check_device()) return rc;
   if (T == 0) return MXW_OK;
-  const int tiles = (N + 15) / 16, steps = (K + 127) / 128;
-  int split = 1;
-  while (split < 4 && tiles * split < 2048 && steps >= 4 * split) split *= 2;
-  LinArgs a = {x, ldx, codes, scales, zeros, T, K, N, group, split, out};
-  const dim3 grid((tiles + 4 / split - 1) / (4 / split)), block(256);
+  LinArgs a = {};
+  a.x = x, a.ldx = ldx, a.w = codes, a.scales = scales, a.zeros = zeros;
+  a.T = T, a.K = K, a.N = N, a.group = group, a.steps = (K + 255) / 256, a.f32 = out_type == MXW_F32, a.out = out;
   hipStream_t st = (hipStream_t)stream;
-  auto go = [&](auto f, auto o) {
-    constexpr bool F = decltype(f)::value, O = decltype(o)::value;
-    switch ((T + 15) / 16) {
-      case 1: linear4_kernel<F, 1, 4, O><<<grid, block, 0, st>>>(a); break;
-      case 2: linear4_kernel<F, 2, 2, O><<<grid, block, 0, st>>>(a); break;
-      case 3: linear4_kernel<F, 3, 2, O><<<grid, block, 0, st>>>(a); break;
-      default: linear4_kernel<F, 4, 2, O><<<grid, block, 0, st>>>(a); break;
-    }
-  };
-  using Y = std::true_type;
-  using No = std::false_type;
-  const bool o32 = out_type == MXW_F32;
-  if (fp4)
-    o32 ? go(Y{}, Y{}) : go(Y{}, No{});
-  else
-    o32 ? go(No{}, Y{}) : go(No{}, No{});
-  return hipGetLastError() == hipSuccess ? MXW_OK : MXW_ERR_LAUNCH;
+  return fp4 ? launch<0>(a, st) : group == 128 ? launch<1>(a, st) : group == 64 ? launch<2>(a, st) : launch<4>(a, st);
 }
