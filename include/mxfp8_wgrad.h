@@ -617,7 +617,7 @@ int64_t mxw_moe_workspace_size(int T, int E, int k, int H, int I);
  *   align    1 .. 1024 (32 is what mxfp8_wgrad_grouped needs, 16 bf16_wgrad_grouped).
  *   offs, counts  int32 [E];  rows  int32 [T, k]; fully overwritten.
  *   workspace, workspace_bytes  256-byte aligned device memory of at least
- *            mxw_sort_workspace_size(T, k, E) bytes (NULL if that is 0: up to 16,384
+ *            mxw_sort_workspace_size(T, k, E) bytes (NULL if that is 0: up to 4,096
  *            choices); contents undefined on entry and exit.
  *
  * mxw_token_rows gives the rows that any ids of these sizes fit in, a multiple of

@@ -53,8 +53,10 @@ scale pre-shuffle.  wgrad() and wgrad_bf16() use the _ws variants unless
 plain=True, taking the workspace from torch's caching allocator on the
 stream the call runs on (or from `workspace`, a uint8 device tensor).
 """
+import array
 import collections
 import ctypes
+import functools
 import os
 
 import torch
@@ -805,6 +807,13 @@ the rows that the runs fit in whatever the ids (a Python number)."""
 _TYPES = {torch.bfloat16: 0, torch.float32: 1}
 
 
+@functools.lru_cache(maxsize=1024)
+def _sort_sizes(T, k, E, align):
+    """Rows and workspace of a sort: functions of the sizes alone, and a call of each
+    takes 0.5 us."""
+    return token_rows(T, k, E, align), sort_workspace_size(T, k, E)
+
+
 def token_rows(T, k, E, align=32):
     """Rows that T tokens' k choices among E experts fit in, each expert's run a
     multiple of align.  Raises MxwError if that is over 8,388,608."""
@@ -849,11 +858,10 @@ def sort_tokens(ids, E, align=32, stream=None, workspace=None):
     if k > 1 and ids.stride(1) != 1 or T > 1 and ids.stride(0) < k:
         raise ValueError("ids must have a contiguous last axis and rows at least a row apart")
     E, align = int(E), int(align)
-    size = token_rows(T, k, E, align)
+    size, need = _sort_sizes(T, k, E, align)
     on = _On(dev, stream)
     offs, counts, rows = on.new((E,), torch.int32), on.new((E,), torch.int32), on.new((T, k), torch.int32)
     with on:
-        need = sort_workspace_size(T, k, E)
         wp, wb, ws = on.workspace(need, workspace) if need else (0, 0, None)
         rc = mxw_sort_tokens(ids.data_ptr(), ids.element_size(), ids.stride(0) if T > 1 else k, T, k, E, align,
                              offs.data_ptr(), counts.data_ptr(), rows.data_ptr(), wp, wb, on.handle)
@@ -866,16 +874,27 @@ def sort_tokens(ids, E, align=32, stream=None, workspace=None):
 def _plan(plan, dev):
     """(offs, counts, rows, size, T, k, E) of a plan, checked."""
     offs, counts, rows, size = plan
+    i32, index = torch.int32, dev.index
+    if (rows.dtype is i32 and offs.dtype is i32 and counts.dtype is i32 and rows.is_contiguous() and offs.is_contiguous()
+            and counts.is_contiguous() and rows.get_device() == offs.get_device() == counts.get_device() == index
+            and rows.dim() == 2 and offs.dim() == 1 and counts.shape == offs.shape):
+        T, k = rows.shape
+        return offs, counts, rows, size, T, k, offs.shape[0]
+    # what is wrong with it
     if rows.dim() != 2 or offs.dim() != 1 or counts.shape != offs.shape:
         raise ValueError("plan: offs and counts must be [E] and rows [T, k]")
     for name, t in (("offs", offs), ("counts", counts), ("rows", rows)):
         if t.dtype != torch.int32 or t.device != dev or not t.is_contiguous():
             raise ValueError("plan: %s must be a contiguous int32 tensor on the same GPU" % name)
-    return offs, counts, rows, int(size), rows.shape[0], rows.shape[1], offs.shape[0]
+    raise ValueError("plan must be on the same GPU")
 
 
 def _matrix(t, name, rows, H=None, dtype=None, dev=None):
     """Row stride of a [rows, H] matrix with a contiguous last axis, checked."""
+    if t.is_contiguous() and t.dim() == 2 and t.is_cuda and (t.dtype is dtype if dtype is not None else t.dtype in _TYPES):
+        shape = t.shape
+        if shape[1] and rows in (None, shape[0]) and H in (None, shape[1]) and (dev is None or t.get_device() == dev.index):
+            return shape[1]
     if t.dtype not in _TYPES or (dtype is not None and t.dtype != dtype):
         raise TypeError("%s must be %s, got %s" % (name, "bfloat16 or float32" if dtype is None else dtype, t.dtype))
     if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (H is not None and t.shape[1] != H) or not t.shape[1]:
@@ -892,7 +911,7 @@ def _output(t, name, shape, dtype, on):
     """`t` checked, or a new tensor."""
     if t is None:
         return on.new(shape, dtype)
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != on._dev:
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != on._dev.index:
         raise ValueError("%s must be a contiguous %s %s tensor on the same device" % (name, dtype, list(shape)))
     return t
 
@@ -957,7 +976,7 @@ def mxw_combine_tokens(y, dtype, ldy, rows, weights, residual, ldr, T, k, H, R, 
 
 
 def _weights(weights, T, k, dev):
-    if weights.dtype != torch.float32 or tuple(weights.shape) != (T, k) or weights.device != dev or (
+    if (weights.dtype is not torch.float32 or weights.shape != (T, k) or weights.get_device() != dev.index or
             not weights.is_contiguous()):
         raise ValueError("weights must be a contiguous float32 [T, k] tensor on the same GPU")
 
@@ -1023,7 +1042,7 @@ def combine_tokens_grad(dout, y, plan, weights, rows=True, mxfp8=False, dy=None,
     if (dy is not None and not rows) or ((q is not None or s is not None) and not mxfp8):
         raise ValueError("dy is an output of rows=True, q and s are outputs of mxfp8=True")
     on = _On(dev, stream)
-    dweights = on.new((T, k), torch.float32)
+    dweights = torch.empty_like(weights) if stream is None else on.new((T, k), torch.float32)
     if rows:
         dy = _output(dy, "dy", (R, H), dout.dtype, on)
     if mxfp8:
@@ -1064,9 +1083,9 @@ def quantize_rows(x, format="mxfp8", q=None, s=None, stream=None):
         raise TypeError("x must be bfloat16 or float32, got %s" % x.dtype)
     if format not in _FORMATS:
         raise ValueError("format must be 'mxfp8' or 'mxfp4'")
-    if x.dim() < 1 or x.device.type != "cuda":
+    if x.dim() < 1 or not x.is_cuda:
         raise ValueError("x must be a tensor of at least one axis on the GPU")
-    shape = tuple(x.shape)
+    shape = x.shape
     C = shape[-1]
     if C == 0 or C % 32:
         raise ValueError("x's last axis must be a multiple of 32, got %d" % C)
@@ -1081,6 +1100,7 @@ def quantize_rows(x, format="mxfp8", q=None, s=None, stream=None):
     on = _On(x.device, stream)
     if q is not None and q.dtype == getattr(torch, "float8_e4m3fn", None):
         q = q.view(torch.uint8)
+    shape = tuple(shape)
     q = _output(q, "q", shape[:-1] + (C if format == "mxfp8" else C // 2,), torch.uint8, on)
     s = _output(s, "s", shape[:-1] + (C // 32,), torch.uint8, on)
     with on:
@@ -1102,15 +1122,18 @@ def clip_workspace_size(count):
     return int(rc)
 
 
+_clip_size = functools.lru_cache(maxsize=1024)(clip_workspace_size)
+
+
 def mxw_clip_grads(grads, outs, sizes, types, norm_type, max_norm, eps, norm, workspace, workspace_bytes, stream=0):
     """Raw C-ABI call: lists of device addresses (outs None: the norm alone), element
     counts and types (0 bf16, 1 float32); norm_type: 2, or 0 for the largest magnitude.
     Returns the status code."""
-    n = len(grads)
-    P = ctypes.c_void_p * n
-    return _load().mxw_clip_grads(P(*grads), None if outs is None else P(*outs), (ctypes.c_int64 * n)(*sizes),
-                                  (ctypes.c_int32 * n)(*types), n, norm_type, max_norm, eps, norm, workspace,
-                                  workspace_bytes, stream)
+    grads, sizes, types = array.array("Q", grads), array.array("q", sizes), array.array("i", types)
+    outs = None if outs is None else array.array("Q", outs)
+    return _load().mxw_clip_grads(grads.buffer_info()[0], None if outs is None else outs.buffer_info()[0],
+                                  sizes.buffer_info()[0], types.buffer_info()[0], len(grads), norm_type, max_norm, eps,
+                                  norm, workspace, workspace_bytes, stream)
 
 
 def _dense(t):
@@ -1125,33 +1148,38 @@ def _dense(t):
     return True
 
 
-def _norm_call(grads, outs, max_norm, norm_type, eps, stream, workspace, device=None):
-    grads = [grads] if isinstance(grads, torch.Tensor) else [g for g in grads if g is not None]
+def _grads(grads):
+    return [grads] if isinstance(grads, torch.Tensor) else [g for g in grads if g is not None]
+
+
+def _norm_call(grads, outs, max_norm, norm_type, eps, stream, workspace):
     if norm_type not in (2, float("inf")):
         raise ValueError("norm_type must be 2 or infinity")
     if not grads:
         raise ValueError("no gradients")
     dev = grads[0].device
-    for g in grads:
-        if g.dtype not in _TYPES:
-            raise TypeError("gradients must be bfloat16 or float32, got %s" % g.dtype)
-        if g.device != dev or dev.type != "cuda":
-            raise ValueError("gradients must be on one GPU")
-        if not _dense(g):
-            raise ValueError("gradients must fill their memory (contiguous or permuted axes)")
-    if outs is not None:
+    index = dev.index
+    types = [_TYPES.get(g.dtype, -1) for g in grads]
+    if -1 in types:
+        raise TypeError("gradients must be bfloat16 or float32, got %s" % grads[types.index(-1)].dtype)
+    if dev.type != "cuda" or any([g.get_device() != index for g in grads]):
+        raise ValueError("gradients must be on one GPU")
+    plain = all([g.is_contiguous() for g in grads])
+    if not plain and not all(_dense(g) for g in grads):
+        raise ValueError("gradients must fill their memory (contiguous or permuted axes)")
+    if outs is not None and outs is not grads:
         outs = [outs] if isinstance(outs, torch.Tensor) else list(outs)
         if len(outs) != len(grads):
             raise ValueError("out must hold a tensor for every gradient")
-        for g, o in zip(grads, outs):
-            if o is not g and (o.dtype != g.dtype or o.shape != g.shape or o.stride() != g.stride() or o.device != dev):
-                raise ValueError("out must hold tensors of the gradients' types, shapes, strides and device")
+        if any([o.dtype is not g.dtype or o.get_device() != index or o.shape != g.shape for g, o in zip(grads, outs)]) or not (
+                plain and all([o.is_contiguous() for o in outs]) or all(o.stride() == g.stride() for g, o in zip(grads, outs))):
+            raise ValueError("out must hold tensors of the gradients' types, shapes, strides and device")
     on = _On(dev, stream)
     norm = on.new((), torch.float32)
     with on:
-        wp, wb, ws = on.workspace(clip_workspace_size(len(grads)), workspace)
+        wp, wb, ws = on.workspace(_clip_size(len(grads)), workspace)
         rc = mxw_clip_grads([g.data_ptr() for g in grads], None if outs is None else [o.data_ptr() for o in outs],
-                            [g.numel() for g in grads], [_TYPES[g.dtype] for g in grads], 2 if norm_type == 2 else 0,
+                            [g.numel() for g in grads], types, 2 if norm_type == 2 else 0,
                             float(max_norm), float(eps), norm.data_ptr(), wp, wb, on.handle)
         del ws
     if rc != 0:
@@ -1167,7 +1195,7 @@ def grad_norm(grads, norm_type=2.0, stream=None, workspace=None):
     filling its memory.  Runs on `stream` (default: the current stream) and does not
     synchronise; `workspace`: a uint8 device tensor of clip_workspace_size() bytes
     (default: from torch's caching allocator on that stream)."""
-    return _norm_call(grads, None, 0.0, norm_type, 0.0, stream, workspace)
+    return _norm_call(_grads(grads), None, 0.0, norm_type, 0.0, stream, workspace)
 
 
 def clip_grad_norm(grads, max_norm, norm_type=2.0, eps=1e-6, out=None, stream=None, workspace=None):
@@ -1180,10 +1208,8 @@ def clip_grad_norm(grads, max_norm, norm_type=2.0, eps=1e-6, out=None, stream=No
     gradients may share memory.  Arguments otherwise as grad_norm."""
     if not (max_norm >= 0.0 and eps >= 0.0):
         raise ValueError("max_norm and eps must not be negative")
-    if out is None:
-        grads = [grads] if isinstance(grads, torch.Tensor) else [g for g in grads if g is not None]
-        out = grads
-    return _norm_call(grads, out, max_norm, norm_type, eps, stream, workspace)
+    grads = _grads(grads)
+    return _norm_call(grads, grads if out is None else out, max_norm, norm_type, eps, stream, workspace)
 
 
 # ---- few tokens, 4-bit weights ------------------------------------------------
@@ -1220,9 +1246,8 @@ def linear_4bit(x, codes, scales, zeros=None, dtype=torch.bfloat16, out=None, st
     group = K // groups if groups else 0
     if codes.shape[1] * 2 != K or scales.shape[0] != N or group * groups != K or group not in ((32,) if fp4 else (32, 64, 128)):
         raise ValueError("shape mismatch: x %s codes %s scales %s" % (tuple(x.shape), tuple(codes.shape), tuple(scales.shape)))
-    for name, t in (("codes", codes), ("scales", scales)):
-        if t.device != dev or not t.is_contiguous():
-            raise ValueError("%s must be contiguous and on the same GPU as x" % name)
+    if not (codes.is_contiguous() and scales.is_contiguous() and codes.get_device() == scales.get_device() == dev.index):
+        raise ValueError("codes and scales must be contiguous and on the same GPU as x")
     if zeros is not None and (fp4 or zeros.dtype != torch.uint8 or zeros.shape != scales.shape or zeros.device != dev or
                               not zeros.is_contiguous()):
         raise ValueError("zeros must be a contiguous uint8 tensor of the scales' shape (with bf16 scales)")

@@ -145,7 +145,7 @@ struct Slot {
 //
 // A wave brings its own rows' codes to its own ring of D slots in LDS, whole cache lines
 // a load: read straight into the MFMA's layout, 16 lanes touch 16 lines, which makes the
-// vector memory path the bound (3.4 TB/s where this reaches TODO).  The ring runs on across
+// vector memory path the bound (one token, 128,000 x 7168: 143 us; this 88).  The ring runs on across
 // pieces and row tiles.  Every step issues the same number of loads, which the waits count:
 // what is past the end gets an offset out of its buffer's range and lands as zeros.
 template <int GC, int TT, int RT, int D, int WAVES, int R, int CH>
@@ -257,60 +257,76 @@ __global__ __launch_bounds__(WAVES * 64) void linear4_kernel(LinArgs a) {
     token[i] = (uint32_t)((PIECES ? 16 * i : min(16 * i + n, a.T - 1)) * per_row * 16);
 #pragma unroll
   for (int q = 0; q < 4; ++q) place[q] = (uint32_t)((PIECES ? n * per_row * 16 : 0) + (place_of(b, q) ^ n) * 16);
-  // the step in slot d, its tokens from LDS byte `from` on
-  auto use = [&](int d, uint32_t from) {
+  // A step's codes, and of its groups the scale and minus the scale times the zero, from slot d
+  constexpr int G = FP4 ? 1 : GC, Q = 4 / G;
+  i4 codes[2][RT];
+  float scale[2][RT][G], zero[2][RT][G];
+  auto take = [&](int d) {
     const uint8_t* slot = lds + (ring + d * S::kBytes);
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h, from += 256) {
-      // the rows' operands, and of each group the scale and minus the scale times the zero
-      constexpr int G = FP4 ? 1 : GC, Q = 4 / G;
-      i4 v[RT][4];
-      float s[RT][G], z[RT][G];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int j = 0; j < RT; ++j) {
-        i4 c = *(const i4*)(slot + 2048 * j + 128 * n + (((4 * h + b) ^ (n >> 1)) << 4));
+        codes[h][j] = *(const i4*)(slot + 2048 * j + 128 * n + (((4 * h + b) ^ (n >> 1)) << 4));
         const int flip = kPer == 8 ? n >> 3 : 0;   // the half of the row's words
         const uint8_t* words = slot + 4 * ((16 * j + n) * kPer + (kPer == 8 ? 4 * (h ^ flip) + (FP4 ? b : 0) : GC * h));
-        if (TURN) c = turn(c);
-        if (FP4) {
-          s[j][0] = __uint_as_float(*(const uint32_t*)(words + S::kScales) << 23);
-        } else {
 #pragma unroll
-          for (int g = 0; g < G; ++g) {
-            s[j][g] = __uint_as_float(*(const uint32_t*)(words + S::kScales + 4 * g) << 16);
-            z[j][g] = -s[j][g] * (a.zeros ? (float)*(const uint32_t*)(words + S::kZeros + 4 * g) : 8.0f);
-          }
+        for (int g = 0; g < G; ++g) {
+          const uint32_t s = *(const uint32_t*)(words + S::kScales + 4 * g);
+          scale[h][j][g] = __uint_as_float(FP4 ? s << 23 : s << 16);
+          if (!FP4)
+            zero[h][j][g] = -scale[h][j][g] * (a.zeros ? (float)*(const uint32_t*)(words + S::kZeros + 4 * g) : 8.0f);
         }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[j][q] = FP4 ? decode_fp4((uint32_t)c[q], s[j][0]) : decode_int((uint32_t)c[q]);
       }
+  };
+  // Its products with the tokens from LDS byte `from` on, 16 tokens of 128 k at a time.  The
+  // reads of the next ones are set before the products: left to itself the compiler reads
+  // each operand when it needs it, and waits.
+  auto use = [&](uint32_t from) {
+    i4 v[RT][4], x[2][4];
+    auto read = [&](int u) {
 #pragma unroll
-      for (int i = 0; i < TT; ++i) {
-        i4 x[4];
+      for (int q = 0; q < 4; ++q)
+        x[u & 1][q] = *(const i4*)(lds + (from + place[q]) + (token[u % TT] + 256 * (u / TT)));
+    };
+    read(0);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) x[q] = *(const i4*)(lds + (from + token[i] + place[q]));
-        if (FP4) {
+    for (int u = 0; u < 2 * TT; ++u) {
+      const int h = u / TT, i = u % TT;
+      if (i == 0) {
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+          const i4 c = TURN ? turn(codes[h][j]) : codes[h][j];
 #pragma unroll
           for (int q = 0; q < 4; ++q)
+            v[j][q] = FP4 ? decode_fp4((uint32_t)c[q], scale[h][j][0]) : decode_int((uint32_t)c[q]);
+        }
+      }
+      if (u + 1 < 2 * TT) read(u + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      const i4(&xu)[4] = x[u & 1];
+      if (FP4) {
 #pragma unroll
-            for (int j = 0; j < RT; ++j) sum[j][i] = mfma(x[q], v[j][q], sum[j][i]);
-        } else {
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
-          for (int g = 0; g < G; ++g) {
-            v4f all = none, dot[RT];
+          for (int j = 0; j < RT; ++j) sum[j][i] = mfma(xu[q], v[j][q], sum[j][i]);
+      } else {
 #pragma unroll
-            for (int j = 0; j < RT; ++j) dot[j] = none;
+        for (int g = 0; g < G; ++g) {
+          v4f all = none, dot[RT];
 #pragma unroll
-            for (int q = g * Q; q < (g + 1) * Q; ++q) {
-              all = mfma(x[q], ones, all);
+          for (int j = 0; j < RT; ++j) dot[j] = none;
 #pragma unroll
-              for (int j = 0; j < RT; ++j) dot[j] = mfma(x[q], v[j][q], dot[j]);
-            }
+          for (int q = g * Q; q < (g + 1) * Q; ++q) {
+            all = mfma(xu[q], ones, all);
 #pragma unroll
-            for (int j = 0; j < RT; ++j)
-#pragma unroll
-              for (int r = 0; r < R; ++r) sum[j][i][r] = fmaf(s[j][g], dot[j][r], fmaf(z[j][g], all[r], sum[j][i][r]));
+            for (int j = 0; j < RT; ++j) dot[j] = mfma(xu[q], v[j][q], dot[j]);
           }
+#pragma unroll
+          for (int j = 0; j < RT; ++j)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+              sum[j][i][r] = fmaf(scale[h][j][g], dot[j][r], fmaf(zero[h][j][g], all[r], sum[j][i][r]));
         }
       }
     }
@@ -349,15 +365,17 @@ __global__ __launch_bounds__(WAVES * 64) void linear4_kernel(LinArgs a) {
     for (int c = 0; c < a.chunks; ++c) {
       // the next piece of x, or the first again for the next row tile
       const bool more = PIECES && (c + 1 < a.chunks || it + (int)gridDim.x < a.items);
-      if (more) fetch(c + 1 < a.chunks ? c + 1 : 0, tokens0 + (buf - now));
 #pragma unroll 1
       for (int of = part; of < chunk; of += a.split) {
-        if (c * chunk + of < a.steps) {
-          wait_loads<(D - 1) * S::kLoads>();
-          use(slot, tokens0 + now + 512 * of);
-          wait_reads();   // the slot's next load may overwrite it
-        }
+        const bool real = c * chunk + of < a.steps;
+        wait_loads<(D - 1) * S::kLoads>();
+        if (real) take(slot);
+        // the slot is free, and its load has D - 1 steps and this one's products to land; the
+        // next piece's loads go before it, so that the wait for them leaves it out
+        wait_reads();
+        if (more && of == part) fetch(c + 1 < a.chunks ? c + 1 : 0, tokens0 + (buf - now));
         load(slot);
+        if (real) use(tokens0 + now + 512 * of);
         slot = slot + 1 == D ? 0 : slot + 1;
       }
       if (more) {
@@ -428,10 +446,10 @@ int launch(LinArgs a, hipStream_t st) {
 template <int GC>
 int launch(const LinArgs& a, hipStream_t st) {
   const bool wide = (a.N + 15) / 16 >= 4096;
-  if (a.T == 1) return wide ? launch<GC, 1, 2, 2, 8, 4, 1>(a, st) : launch<GC, 1, 1, 2, 8, 4, 1>(a, st);
-  if (a.T <= 16) return wide ? launch<GC, 1, 2, 2, 8, 4>(a, st) : launch<GC, 1, 1, 2, 8, 4>(a, st);
-  if (a.T <= 32) return wide ? launch<GC, 2, 2, 2, 8, 2>(a, st) : launch<GC, 2, 1, 2, 4, 4>(a, st);
-  return wide ? launch<GC, 4, 2, 2, 8, 1>(a, st) : launch<GC, 4, 1, 2, 4, 2>(a, st);
+  if (a.T == 1) return wide ? launch<GC, 1, 2, 1, 8, 4, 1>(a, st) : launch<GC, 1, 1, 2, 8, 4, 1>(a, st);
+  if (a.T <= 16) return wide ? launch<GC, 1, 2, 1, 8, 4>(a, st) : launch<GC, 1, 1, 2, 8, 4>(a, st);
+  if (a.T <= 32) return wide ? launch<GC, 2, 2, 1, 8, 2>(a, st) : launch<GC, 2, 1, 2, 4, 4>(a, st);
+  return wide ? launch<GC, 4, 2, 1, 8, 1>(a, st) : launch<GC, 4, 1, 2, 4, 2>(a, st);
 }
 
 }  // namespace

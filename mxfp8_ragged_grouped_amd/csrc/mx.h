@@ -30,19 +30,32 @@ struct Raw8 {
   i4 v[F32 ? 2 : 1];
 };
 
-template <bool F32>
+// NT: past the caches (data that is not met again before they have turned over)
+template <bool F32, bool NT = false>
 __device__ __forceinline__ Raw8<F32> load8(const void* base, int64_t at) {
   Raw8<F32> r;
-  const char* p = (const char*)base + at * (F32 ? 4 : 2);
-  r.v[0] = *(const i4_a2*)p;
-  if (F32) r.v[F32 ? 1 : 0] = *(const i4_a2*)(p + 16);
+  const i4_a2* p = (const i4_a2*)((const char*)base + at * (F32 ? 4 : 2));
+#pragma unroll
+  for (int i = 0; i < (F32 ? 2 : 1); ++i) r.v[i] = NT ? __builtin_nontemporal_load(p + i) : p[i];
   return r;
 }
-template <bool F32>
+template <bool NT, class T>
+__device__ __forceinline__ void store(T* p, const T& v) {
+  if (NT)
+    __builtin_nontemporal_store(v, p);
+  else
+    *p = v;
+}
+template <bool F32, bool NT = false>
 __device__ __forceinline__ void store8(void* base, int64_t at, const Raw8<F32>& r) {
-  char* p = (char*)base + at * (F32 ? 4 : 2);
-  *(i4_a2*)p = r.v[0];
-  if (F32) *(i4_a2*)(p + 16) = r.v[F32 ? 1 : 0];
+  i4_a2* p = (i4_a2*)((char*)base + at * (F32 ? 4 : 2));
+#pragma unroll
+  for (int i = 0; i < (F32 ? 2 : 1); ++i) {
+    if (NT)
+      __builtin_nontemporal_store(r.v[i], p + i);
+    else
+      p[i] = r.v[i];
+  }
 }
 // n < 8 elements at a row's end (the others read as 0)
 template <bool F32>

@@ -17,14 +17,14 @@ using namespace mxw;
 // ---- the order --------------------------------------------------------------
 //
 // row[c] = first[e] + the number of choices before c of the same expert e: a stable
-// counting sort.  A workgroup takes 16,384 choices, each of its 16 waves a consecutive
-// run; it counts its waves' experts in LDS, turns the counts into first places, and a
+// counting sort.  A workgroup takes a piece of 1,024 to 16,384 choices, each of its 16 waves a
+// consecutive run; it counts its waves' experts in LDS, turns the counts into first places, and a
 // wave then walks its run 64 choices at a time: of each lane's choice, the lanes of the
 // same expert (a ballot for each bit of the expert's number) before it give its rank.
 // With more than one such piece, a kernel before leaves every piece's counts in the
 // workspace, and each workgroup adds up what comes before its own.  Counting is in whole
 // numbers: any order of the LDS atomics gives the same counts.
-constexpr int kSortWaves = 16, kSortPiece = 16384, kPerLane = kSortPiece / (kSortWaves * 64);
+constexpr int kSortWaves = 16, kSortThreads = kSortWaves * 64;
 
 struct SortArgs {
   const void* ids;
@@ -45,43 +45,42 @@ __device__ __forceinline__ int expert_of(const SortArgs& a, int c) {
 typedef int32_t WaveCounts[kSortWaves][MXW_MAX_EXPERTS];
 
 // every wave's run of the piece into registers, and the counts of each
-template <bool I64>
-__device__ __forceinline__ void count_piece(const SortArgs& a, int (&e)[kPerLane], WaveCounts& cnt) {
+template <bool I64, int PER>
+__device__ __forceinline__ void count_piece(const SortArgs& a, int (&e)[PER], WaveCounts& cnt) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int i = tid; i < kSortWaves * MXW_MAX_EXPERTS; i += kSortWaves * 64) (&cnt[0][0])[i] = 0;
-  const int first = blockIdx.x * kSortPiece, here = min(a.n - first, kSortPiece);
-  const int steps = ((here + 63) / 64 + kSortWaves - 1) / kSortWaves;  // of 64 choices, a wave
+  for (int i = tid; i < kSortWaves * MXW_MAX_EXPERTS; i += kSortThreads) (&cnt[0][0])[i] = 0;
+  const int first = blockIdx.x * (PER * kSortThreads), here = min(a.n - first, PER * kSortThreads);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int c = (wave * PER + i) * 64 + lane;
+    e[i] = c < here ? expert_of<I64>(a, first + c) : MXW_MAX_EXPERTS;
+  }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kPerLane; ++i) {
-    const int c = (wave * steps + i) * 64 + lane;
-    e[i] = i < steps && c < here ? expert_of<I64>(a, first + c) : MXW_MAX_EXPERTS;
-  }
-#pragma unroll
-  for (int i = 0; i < kPerLane; ++i)
+  for (int i = 0; i < PER; ++i)
     if (e[i] < MXW_MAX_EXPERTS) atomicAdd(&cnt[wave][e[i]], 1);
   __syncthreads();
 }
 
-template <bool I64>
-__global__ __launch_bounds__(kSortWaves * 64) void sort_count_kernel(SortArgs a) {
+template <bool I64, int PER>
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
   __shared__ WaveCounts cnt;
-  int e[kPerLane];
-  count_piece<I64>(a, e, cnt);
-  for (int x = threadIdx.x; x < a.E; x += kSortWaves * 64) {
+  int e[PER];
+  count_piece<I64, PER>(a, e, cnt);
+  for (int x = threadIdx.x; x < a.E; x += kSortThreads) {
     int sum = 0;
     for (int w = 0; w < kSortWaves; ++w) sum += cnt[w][x];
     a.part[(int64_t)blockIdx.x * a.E + x] = sum;
   }
 }
 
-template <bool I64>
-__global__ __launch_bounds__(kSortWaves * 64) void sort_place_kernel(SortArgs a) {
+template <bool I64, int PER>
+__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
   __shared__ WaveCounts cnt;
   __shared__ int32_t total[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int e[kPerLane];
-  count_piece<I64>(a, e, cnt);
+  int e[PER];
+  count_piece<I64, PER>(a, e, cnt);
   int count = 0, before = 0, run = 0;  // of expert tid: its choices, those of earlier pieces, padded ends
   if (tid < MXW_MAX_EXPERTS) {
     if (tid < a.E) {
@@ -120,19 +119,18 @@ __global__ __launch_bounds__(kSortWaves * 64) void sort_place_kernel(SortArgs a)
     }
   }
   __syncthreads();
-  const int first = blockIdx.x * kSortPiece, here = min(a.n - first, kSortPiece);
-  const int steps = ((here + 63) / 64 + kSortWaves - 1) / kSortWaves;
+  const int first = blockIdx.x * (PER * kSortThreads), here = min(a.n - first, PER * kSortThreads);
   volatile int32_t* place = cnt[wave];  // only this wave's from here on
 #pragma unroll
-  for (int i = 0; i < kPerLane; ++i) {
-    if (i >= steps) break;
+  for (int i = 0; i < PER; ++i) {
+    if ((wave * PER + i) * 64 >= here) break;
     uint64_t same = __ballot(e[i] < MXW_MAX_EXPERTS);
     for (int b = 0; (1 << b) < a.E; ++b) {
       const uint64_t vote = __ballot((e[i] >> b) & 1);
       same &= (e[i] >> b) & 1 ? vote : ~vote;
     }
     const int rank = __popcll(same & ((1ull << lane) - 1));
-    const int c = (wave * steps + i) * 64 + lane;
+    const int c = (wave * PER + i) * 64 + lane;
     int row = -1;
     if (e[i] < MXW_MAX_EXPERTS) {
       const int at = place[e[i]];
@@ -147,7 +145,7 @@ __global__ __launch_bounds__(kSortWaves * 64) void sort_place_kernel(SortArgs a)
 
 // ---- rows -------------------------------------------------------------------
 
-constexpr int kUnroll = 4;
+constexpr int kUnroll = 2;
 
 struct RowArgs {
   const void* x;      // [T, H] the tokens: dispatch's x, the gradient's dout
@@ -189,7 +187,7 @@ __device__ __forceinline__ void pad_rows(const RowArgs& a, int b) {
 }
 
 // xs[row[t][j]] = x[t]: a token is read once, by W waves, and stored to its k rows.
-template <bool F32, bool ROWS, bool MX, int W>
+template <bool F32, bool ROWS, bool MX, int W, bool NT>
 __global__ __launch_bounds__(256) void dispatch_kernel(RowArgs a) {
   if ((int)blockIdx.x < a.pad_blocks) return pad_rows<F32, ROWS, MX>(a, blockIdx.x);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -205,7 +203,7 @@ __global__ __launch_bounds__(256) void dispatch_kernel(RowArgs a) {
     for (int u = 0; u < kUnroll; ++u) {
       const int c = c0 + u * W * 512;
       if (c + 8 <= a.H)
-        v[u] = load8<F32>(a.x, from + c);
+        v[u] = load8<F32, NT>(a.x, from + c);
       else if (c < a.H)
         v[u] = load_some<F32>(a.x, from + c, a.H - c);
     }
@@ -225,12 +223,12 @@ __global__ __launch_bounds__(256) void dispatch_kernel(RowArgs a) {
         const int c = c0 + u * W * 512;
         if (ROWS) {
           if (c + 8 <= a.H)
-            store8<F32>(a.out, r * a.H + c, v[u]);
+            store8<F32, NT>(a.out, r * a.H + c, v[u]);
           else if (c < a.H)
             store_some<F32>(a.out, r * a.H + c, v[u], a.H - c);
         }
         if (MX && c < a.H) {
-          *(i2*)(a.q + r * a.H + c) = q[u];
+          store<NT>((i2*)(a.q + r * a.H + c), q[u]);
           if (!(c & 31)) a.s[r * (a.H >> 5) + (c >> 5)] = (uint8_t)s[u];
         }
       }
@@ -251,7 +249,7 @@ __device__ __forceinline__ void choices(const RowArgs& a, int t, int j0, int (&r
 }
 
 // out[t] = sum_j w[t][j] y[row[t][j]] (+ residual[t]), in the order of the choices
-template <bool F32, bool WEIGHTS, int W>
+template <bool F32, bool WEIGHTS, int W, bool NT>
 __global__ __launch_bounds__(256) void combine_kernel(RowArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t = blockIdx.x * (4 / W) + wave / W;
@@ -266,7 +264,7 @@ __global__ __launch_bounds__(256) void combine_kernel(RowArgs a) {
       Raw8<F32> v[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        if (r[u] >= 0) v[u] = n == 8 ? load8<F32>(a.y, r[u] * a.ldy + c) : load_some<F32>(a.y, r[u] * a.ldy + c, n);
+        if (r[u] >= 0) v[u] = n == 8 ? load8<F32, NT>(a.y, r[u] * a.ldy + c) : load_some<F32>(a.y, r[u] * a.ldy + c, n);
 #pragma unroll
       for (int u = 0; u < 8; ++u)
         if (r[u] >= 0) {
@@ -283,7 +281,7 @@ __global__ __launch_bounds__(256) void combine_kernel(RowArgs a) {
       for (int i = 0; i < 8; ++i) sum[i] += f[i];
     }
     if (n == 8)
-      store8<F32>(a.out, (int64_t)t * a.H + c, rounded<F32>(sum));
+      store8<F32, NT>(a.out, (int64_t)t * a.H + c, rounded<F32>(sum));
     else
       store_some<F32>(a.out, (int64_t)t * a.H + c, rounded<F32>(sum), n);
   }
@@ -296,7 +294,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // dy[row[t][j]] = w[t][j] dout[t], dw[t][j] = <dout[t], y[row[t][j]]>
-template <bool F32, bool ROWS, bool MX, int W>
+template <bool F32, bool ROWS, bool MX, int W, bool NT>
 __global__ __launch_bounds__(256) void combine_grad_kernel(RowArgs a) {
   __shared__ float red[4][8];
   if ((int)blockIdx.x < a.pad_blocks) return pad_rows<F32, ROWS, MX>(a, blockIdx.x);
@@ -315,7 +313,7 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(RowArgs a) {
       if (a.dweights) {
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-          if (r[u] >= 0) v[u] = n == 8 ? load8<F32>(a.y, r[u] * a.ldy + c) : load_some<F32>(a.y, r[u] * a.ldy + c, n);
+          if (r[u] >= 0) v[u] = n == 8 ? load8<F32, NT>(a.y, r[u] * a.ldy + c) : load_some<F32>(a.y, r[u] * a.ldy + c, n);
       }
       if (ROWS || MX) {
 #pragma unroll
@@ -328,14 +326,14 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(RowArgs a) {
             const Raw8<F32> o = rounded<F32>(f);
             if (ROWS) {
               if (n == 8)
-                store8<F32>(a.out, at, o);
+                store8<F32, NT>(a.out, at, o);
               else
                 store_some<F32>(a.out, at, o, n);
             }
             if (MX) {
               values<F32>(o, f);
               const int s = block_scale<8>(block_top(f));
-              *(i2*)(a.q + at) = encode_e4m3(f, s);
+              store<NT>((i2*)(a.q + at), encode_e4m3(f, s));
               if (!(c & 31)) a.s[at >> 5] = (uint8_t)s;
             }
           }
@@ -385,7 +383,7 @@ struct QuantArgs {
   uint8_t *q, *s;
 };
 
-template <bool F32, bool FP4, bool FLAT>
+template <bool F32, bool FP4, bool FLAT, bool NT>
 __global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
   const int64_t i0 = (int64_t)blockIdx.x * (256 * kUnroll);
   // rows of another stride: the row and place of the workgroup's first chunk
@@ -397,10 +395,10 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
     const int64_t i = i0 + u * 256 + threadIdx.x;
     if (i >= a.chunks) continue;
     if (FLAT) {
-      v[u] = load8<F32>(a.x, 8 * i);
+      v[u] = load8<F32, NT>(a.x, 8 * i);
     } else {
       const uint32_t in = in0 + u * 256 + threadIdx.x, down = in / (uint32_t)a.per_row;
-      v[u] = load8<F32>(a.x, (row0 + down) * a.ldx + 8 * (in - down * (uint32_t)a.per_row));
+      v[u] = load8<F32, NT>(a.x, (row0 + down) * a.ldx + 8 * (in - down * (uint32_t)a.per_row));
     }
   }
 #pragma unroll
@@ -412,9 +410,9 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
     const uint32_t top = block_top(f);
     const int s = block_scale<FP4 ? 2 : 8>(top);
     if (FP4)
-      *(uint32_t*)(a.q + 4 * i) = encode_e2m1(f, s);
+      store<NT>((uint32_t*)(a.q + 4 * i), encode_e2m1(f, s));
     else
-      *(i2*)(a.q + 8 * i) = encode_e4m3(f, s);
+      store<NT>((i2*)(a.q + 8 * i), encode_e4m3(f, s));
     if (!(i & 3)) a.s[i >> 2] = (uint8_t)s;
   }
 }
@@ -424,6 +422,19 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
 int64_t token_rows(int64_t T, int64_t k, int64_t E, int64_t align) {
   const int64_t n = T * k;
   return (n + (n < E ? n : E) * (align - 1)) / align * align;
+}
+
+// Choices of a lane of the sort: one workgroup alone up to 4,096 choices (6 us, two launches
+// take 8), then the fewest that keep the pieces' counts, which every workgroup adds up, small
+// next to the rest: 196,608 choices 11.2 us with 2 and 27.7 with 16, 800,000 over 256 experts
+// 26.2 with 2, 19.5 with 4, 3.2 million 181, 73 and 40 with 2, 4 and 16.
+int sort_per(int64_t n) {
+  if (n <= 1024) return 1;
+  if (n <= 2048) return 2;
+  if (n <= 4096) return 4;
+  if (n <= (1 << 19)) return 2;
+  if (n <= (1 << 21)) return 4;
+  return 16;
 }
 
 int check_plan(int T, int k, int E) {
@@ -438,6 +449,12 @@ int launched() { return hipGetLastError() == hipSuccess ? MXW_OK : MXW_ERR_LAUNC
 
 // waves a token: its row in one go where one wave can hold it
 bool one_wave(int H) { return H <= 512; }
+
+// Loads and stores past the caches where a call moves more than they hold (256 MB): 262,144
+// rows of 2048 joined in 199 us, with cached ones 228; 65,536 rows of 7168 quantised in 221 and
+// 239.  Below that whoever reads the result next finds it there: 4,096 tokens through 8 of 32
+// experts, dispatched, joined and both gradients, 129 us, all past the caches 138.
+bool past_caches(int64_t bytes) { return bytes > ((int64_t)256 << 20); }
 
 // what dispatch and the gradient share: the padding rows' workgroups and the forms
 int plan_pads(RowArgs& a) {
@@ -458,7 +475,7 @@ int64_t mxw_token_rows(int T, int k, int E, int align) {
 
 int64_t mxw_sort_workspace_size(int T, int k, int E) {
   if (check_plan(T, k, E) != MXW_OK) return MXW_ERR_DIM;
-  const int64_t pieces = ((int64_t)T * k + kSortPiece - 1) / kSortPiece;
+  const int64_t n = (int64_t)T * k, piece = (int64_t)sort_per(n) * kSortThreads, pieces = (n + piece - 1) / piece;
   return pieces > 1 ? pieces * E * 4 : 0;
 }
 
@@ -472,16 +489,26 @@ int mxw_sort_tokens(const void* ids, int id_bytes, int64_t ld, int T, int k, int
   if (need > 0 && (!workspace || !on(workspace, 256) || workspace_bytes < (size_t)need)) return MXW_ERR_WORKSPACE;
   if (const int rc = check_device()) return rc;
   SortArgs a = {ids, ld, T * k, k, E, align, offs, counts, rows, (int32_t*)workspace};
-  const int pieces = T ? (a.n + kSortPiece - 1) / kSortPiece : 1;
-  const dim3 grid(pieces), block(kSortWaves * 64);
   hipStream_t st = (hipStream_t)stream;
-  if (id_bytes == 8) {
-    if (pieces > 1) sort_count_kernel<true><<<grid, block, 0, st>>>(a);
-    sort_place_kernel<true><<<grid, block, 0, st>>>(a);
-  } else {
-    if (pieces > 1) sort_count_kernel<false><<<grid, block, 0, st>>>(a);
-    sort_place_kernel<false><<<grid, block, 0, st>>>(a);
-  }
+  auto go = [&](auto i64, auto per) {
+    constexpr bool I = decltype(i64)::value;
+    constexpr int PER = decltype(per)::value;
+    const int pieces = T ? (a.n + PER * kSortThreads - 1) / (PER * kSortThreads) : 1;
+    if (pieces > 1) sort_count_kernel<I, PER><<<dim3(pieces), dim3(kSortThreads), 0, st>>>(a);
+    sort_place_kernel<I, PER><<<dim3(pieces), dim3(kSortThreads), 0, st>>>(a);
+  };
+  auto pieces = [&](auto i64) {
+    switch (sort_per(a.n)) {
+      case 1: go(i64, std::integral_constant<int, 1>{}); break;
+      case 2: go(i64, std::integral_constant<int, 2>{}); break;
+      case 4: go(i64, std::integral_constant<int, 4>{}); break;
+      default: go(i64, std::integral_constant<int, 16>{});
+    }
+  };
+  if (id_bytes == 8)
+    pieces(std::true_type{});
+  else
+    pieces(std::false_type{});
   return launched();
 }
 
@@ -501,13 +528,16 @@ int mxw_dispatch_tokens(const void* x, int type, int64_t ldx, const int32_t* off
   a.x = x, a.ldx = ldx, a.offs = offs, a.counts = counts, a.rows = rows;
   a.T = T, a.k = k, a.E = E, a.H = H, a.R = R, a.out = xs, a.q = q, a.s = s;
   const int pads = plan_pads(a);
+  const bool nt = past_caches((int64_t)T * H * (size + k * ((xs ? size : 0) + (q ? 1 : 0))));
   hipStream_t st = (hipStream_t)stream;
   auto go = [&](auto f32, auto with_rows, auto mx) {
     constexpr bool F = decltype(f32)::value, RW = decltype(with_rows)::value, M = decltype(mx)::value;
     if (one_wave(H))
-      dispatch_kernel<F, RW, M, 1><<<dim3(pads + (T + 3) / 4), dim3(256), 0, st>>>(a);
+      nt ? dispatch_kernel<F, RW, M, 1, true><<<dim3(pads + (T + 3) / 4), dim3(256), 0, st>>>(a)
+         : dispatch_kernel<F, RW, M, 1, false><<<dim3(pads + (T + 3) / 4), dim3(256), 0, st>>>(a);
     else
-      dispatch_kernel<F, RW, M, 4><<<dim3(pads + T), dim3(256), 0, st>>>(a);
+      nt ? dispatch_kernel<F, RW, M, 4, true><<<dim3(pads + T), dim3(256), 0, st>>>(a)
+         : dispatch_kernel<F, RW, M, 4, false><<<dim3(pads + T), dim3(256), 0, st>>>(a);
   };
   using Y = std::true_type;
   using N = std::false_type;
@@ -539,13 +569,16 @@ int mxw_combine_tokens(const void* y, int type, int64_t ldy, const int32_t* rows
   RowArgs a = {};
   a.y = y, a.ldy = ldy, a.rows = rows, a.weights = weights, a.residual = residual, a.ldr = ldr;
   a.T = T, a.k = k, a.H = H, a.R = R, a.out = out;
+  const bool nt = past_caches((int64_t)T * H * size * (k + 1));
   hipStream_t st = (hipStream_t)stream;
   auto go = [&](auto f32, auto wt) {
     constexpr bool F = decltype(f32)::value, WT = decltype(wt)::value;
     if (one_wave(H))
-      combine_kernel<F, WT, 1><<<dim3((T + 3) / 4), dim3(256), 0, st>>>(a);
+      nt ? combine_kernel<F, WT, 1, true><<<dim3((T + 3) / 4), dim3(256), 0, st>>>(a)
+         : combine_kernel<F, WT, 1, false><<<dim3((T + 3) / 4), dim3(256), 0, st>>>(a);
     else
-      combine_kernel<F, WT, 4><<<dim3(T), dim3(256), 0, st>>>(a);
+      nt ? combine_kernel<F, WT, 4, true><<<dim3(T), dim3(256), 0, st>>>(a)
+         : combine_kernel<F, WT, 4, false><<<dim3(T), dim3(256), 0, st>>>(a);
   };
   using Y = std::true_type;
   using N = std::false_type;
@@ -575,13 +608,16 @@ int mxw_combine_tokens_grad(const void* dout, int type, int64_t ldo, const void*
   a.x = dout, a.ldx = ldo, a.y = y, a.ldy = ldy, a.offs = offs, a.counts = counts, a.rows = rows, a.weights = weights;
   a.T = T, a.k = k, a.E = E, a.H = H, a.R = R, a.out = dy, a.q = q, a.s = s, a.dweights = dweights;
   const int pads = dy || q ? plan_pads(a) : 0;
+  const bool nt = past_caches((int64_t)T * H * (size + k * ((dweights ? size : 0) + (dy ? size : 0) + (q ? 1 : 0))));
   hipStream_t st = (hipStream_t)stream;
   auto go = [&](auto f32, auto with_rows, auto mx) {
     constexpr bool F = decltype(f32)::value, RW = decltype(with_rows)::value, M = decltype(mx)::value;
     if (one_wave(H))
-      combine_grad_kernel<F, RW, M, 1><<<dim3(pads + (T + 3) / 4), dim3(256), 0, st>>>(a);
+      nt ? combine_grad_kernel<F, RW, M, 1, true><<<dim3(pads + (T + 3) / 4), dim3(256), 0, st>>>(a)
+         : combine_grad_kernel<F, RW, M, 1, false><<<dim3(pads + (T + 3) / 4), dim3(256), 0, st>>>(a);
     else
-      combine_grad_kernel<F, RW, M, 4><<<dim3(pads + T), dim3(256), 0, st>>>(a);
+      nt ? combine_grad_kernel<F, RW, M, 4, true><<<dim3(pads + T), dim3(256), 0, st>>>(a)
+         : combine_grad_kernel<F, RW, M, 4, false><<<dim3(pads + T), dim3(256), 0, st>>>(a);
   };
   using Y = std::true_type;
   using N = std::false_type;
@@ -610,13 +646,16 @@ int mxw_quantize_rows(const void* x, int type, int64_t ldx, int64_t R, int C, in
   if (blocks > 0x7FFFFFFF / 256) return MXW_ERR_DIM;  // threads of a launch are counted in 32 bits
   if (const int rc = check_device()) return rc;
   if (R == 0) return MXW_OK;
+  const bool nt = past_caches(R * C * (type == MXW_F32 ? 5 : 3));
   hipStream_t st = (hipStream_t)stream;
   auto go = [&](auto f32, auto fp4) {
     constexpr bool F = decltype(f32)::value, P = decltype(fp4)::value;
     if (ldx == C || R == 1)
-      quant_rows_kernel<F, P, true><<<dim3((uint32_t)blocks), dim3(256), 0, st>>>(a);
+      nt ? quant_rows_kernel<F, P, true, true><<<dim3((uint32_t)blocks), dim3(256), 0, st>>>(a)
+         : quant_rows_kernel<F, P, true, false><<<dim3((uint32_t)blocks), dim3(256), 0, st>>>(a);
     else
-      quant_rows_kernel<F, P, false><<<dim3((uint32_t)blocks), dim3(256), 0, st>>>(a);
+      nt ? quant_rows_kernel<F, P, false, true><<<dim3((uint32_t)blocks), dim3(256), 0, st>>>(a)
+         : quant_rows_kernel<F, P, false, false><<<dim3((uint32_t)blocks), dim3(256), 0, st>>>(a);
   };
   using Y = std::true_type;
   using N = std::false_type;

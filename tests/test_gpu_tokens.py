@@ -74,7 +74,8 @@ def same_bits(a, b):
 @pytest.mark.parametrize("T,k,E,align,empty", [
     (0, 2, 8, 32, 0), (1, 1, 1, 32, 0), (1, 2, 8, 32, 0), (1, 64, 256, 1, 0), (5, 3, 10, 7, 0.3), (64, 8, 256, 32, 0),
     (301, 3, 10, 32, 0.25), (300, 4, 3, 1024, 0.1), (1000, 1, 255, 16, 0), (4095, 4, 129, 32, 0), (4096, 4, 129, 32, 0),
-    (16385, 1, 2, 32, 0.5), (5000, 9, 256, 32, 0.05), (40, 2, 8, 32, 1.0), (70000, 2, 37, 32, 0)])
+    (1024, 1, 8, 32, 0), (1025, 1, 8, 32, 0.1), (2049, 1, 256, 32, 0), (4097, 1, 2, 32, 0.5), (16385, 1, 2, 32, 0.5),
+    (5000, 9, 256, 32, 0.05), (40, 2, 8, 32, 1.0), (70000, 2, 37, 32, 0)])
 @pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
 def test_sort(T, k, E, align, empty, dtype):
     say("sort T=%d k=%d E=%d align=%d empty=%g %s" % (T, k, E, align, empty, dtype))
@@ -107,9 +108,10 @@ def test_sort_ids_beyond_32_bits_and_strided():
         assert plan.rows[3, 1].item() == -1
 
 
-def test_sort_largest():
-    """8,388,608 choices, the most there may be, against a stable sort."""
-    ids = make_ids(1 << 20, 7, 200, 9, 0.01, torch.int32)
+@pytest.mark.parametrize("T", [75000, 100000, 1 << 20])
+def test_sort_many(T):
+    """525,000, 700,000 and 7,340,032 choices against a stable sort."""
+    ids = make_ids(T, 7, 200, 9, 0.01, torch.int32)
     plan = mxw.sort_tokens(ids, 200)
     flat = ids.view(-1).long()
     flat = torch.where((flat < 0) | (flat >= 200), 200, flat)

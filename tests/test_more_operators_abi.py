@@ -32,7 +32,7 @@ def test_sort_host_checks(over, code):
 def test_sizes():
     assert mxw.token_rows(0, 2, 8) == 0 and mxw.token_rows(1, 2, 8) == 64 and mxw.token_rows(1, 2, 1) == 32
     assert mxw.token_rows(100, 2, 8) == (200 + 8 * 31) // 32 * 32 and mxw.token_rows(5, 3, 10, 1) == 15
-    assert mxw.sort_workspace_size(8192, 2, 8) == 0 and mxw.sort_workspace_size(8193, 2, 8) == 2 * 8 * 4
+    assert mxw.sort_workspace_size(2048, 2, 8) == 0 and mxw.sort_workspace_size(2049, 2, 8) == 3 * 8 * 4
     assert mxw.clip_workspace_size(0) > 0 and mxw.clip_workspace_size(97) == 2 * mxw.clip_workspace_size(96)
     for f, args in ((mxw.token_rows, (1 << 23, 2, 8)), (mxw.token_rows, (4, 2, 0)), (mxw.token_rows, (4, 2, 8, 0)),
                     (mxw.sort_workspace_size, (4, 65, 8)), (mxw.clip_workspace_size, (-1,)),
