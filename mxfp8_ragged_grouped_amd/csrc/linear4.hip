@@ -445,11 +445,25 @@ int launch(LinArgs a, hipStream_t st) {
 }
 template <int GC>
 int launch(const LinArgs& a, hipStream_t st) {
-  const bool wide = (a.N + 15) / 16 >= 4096;
+  const int tiles = (a.N + 15) / 16;
+  // More tiles than one for each wave of a full device: two a wave, so that each read of the
+  // tokens serves both (64 tokens, K 7168, integers: 34,000 rows 59 us for MXFP4, with one 76;
+  // 32,000 rows, one round either way, 90 and 65).
+  const bool wide = tiles > 2048;
   if (a.T == 1) return wide ? launch<GC, 1, 2, 1, 8, 4, 1>(a, st) : launch<GC, 1, 1, 2, 8, 4, 1>(a, st);
   if (a.T <= 16) return wide ? launch<GC, 1, 2, 1, 8, 4>(a, st) : launch<GC, 1, 1, 2, 8, 4>(a, st);
-  if (a.T <= 32) return wide ? launch<GC, 2, 2, 1, 8, 2>(a, st) : launch<GC, 2, 1, 2, 4, 4>(a, st);
-  return wide ? launch<GC, 4, 2, 1, 8, 1>(a, st) : launch<GC, 4, 1, 2, 4, 2>(a, st);
+  // Half as many waves a workgroup where few tiles meet tokens that only fit in pieces: pieces
+  // leave room for few parts of K, and more workgroups take the tiles (64 tokens, K 7168: 8,192
+  // rows 22 us, with 8 waves 39; 20,000 rows 55 and 40.  24 tokens, 4,096 rows: K 7168 15 us
+  // and 25, K 2048, which fits, 8.7 and 7.4).
+  const bool few = tiles <= 1024 && a.T * a.steps * 512 + 8 * 2 * Slot<GC, 1>::kBytes > kLds;
+  if (a.T <= 32)
+    return wide  ? launch<GC, 2, 2, 1, 8, 2>(a, st)
+           : few ? launch<GC, 2, 1, 2, 4, 4>(a, st)
+                 : launch<GC, 2, 1, 2, 8, 2>(a, st);
+  return wide  ? launch<GC, 4, 2, 1, 8, 1>(a, st)
+         : few ? launch<GC, 4, 1, 2, 4, 2>(a, st)
+               : launch<GC, 4, 1, 2, 8, 1>(a, st);
 }
 
 }  // namespace
