@@ -2,11 +2,14 @@
 
     python examples/train_and_serve.py [--steps 60] [--tokens 2048]
 
-Every large product of a step runs in this library: the experts' forward and
-data-gradient GEMMs on MXFP8 operands (fwd), the loss over the vocabulary with
-its gradients (vocab_cross_entropy), the experts' weight gradients (wgrad) and
-their orthogonalised updates (orthogonalize).  Afterwards the same experts,
-quantised once more, answer single tokens and small batches (moe_layer).
+Every large product of a step runs in this library, and what stands between them: tokens
+to their experts' rows and back with the gradient (sort_tokens, dispatch_tokens,
+combine_tokens, combine_tokens_grad), the experts' forward and data-gradient GEMMs on
+MXFP8 operands (fwd, quantize_rows), the loss over the vocabulary with its gradients
+(vocab_cross_entropy), the experts' weight gradients (wgrad), the gradients' clipping
+(clip_grad_norm) and the orthogonalised updates (orthogonalize).  Afterwards the same
+experts, quantised once more, answer single tokens and small batches (moe_layer), with the
+words' logits from 4-bit weights (linear_4bit).
 
 The task is synthetic: the next word is a fixed function of the current one, so
 a table look-up through the experts can learn it.  The embedding and the router
@@ -23,13 +26,7 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import mxfp8_ragged_grouped_amd as mxw  # noqa: E402
 
 VOCAB, HIDDEN, WIDTH, EXPERTS, TOP_K = 1000, 256, 128, 8, 2
-
-
-def quantize_rows(x):
-    """MXFP8 of bf16 x [..., R, C] with the 32-element blocks along C."""
-    rows = x.reshape(-1, x.shape[-1])
-    q, s = mxw.quantize_tokens(rows.t().contiguous())
-    return q.view(x.shape), s.view(*x.shape[:-1], x.shape[-1] // 32)
+MAX_NORM = 1.0
 
 
 class Model:
@@ -52,47 +49,31 @@ class Model:
         w, ids = p.topk(TOP_K, dim=1)
         return ids, w / w.sum(1, keepdim=True)
 
-    def group(self, ids):
-        """Rows by expert, each expert's run padded to a multiple of 32 (the
-        weight gradient's block): source token of every row (-1: padding), the
-        choice it came from, and the runs' cumulative ends."""
-        flat = ids.flatten()
-        order = torch.argsort(flat, stable=True)
-        counts = torch.bincount(flat, minlength=EXPERTS)
-        padded = (counts + 31) // 32 * 32
-        ends = padded.cumsum(0)
-        first = ends - padded - (counts.cumsum(0) - counts)
-        rows = torch.arange(len(flat), device=flat.device) + first[flat[order]]
-        choice = torch.full((int(ends[-1]),), -1, dtype=torch.int64, device=flat.device)
-        choice[rows] = order
-        return choice, ends.to(torch.int32)
-
     def step(self, words, targets, lr):
         """One training step; the loss as a tensor."""
         x = self.embedding[words]
         ids, weights = self.routing(x)
-        choice, offs = self.group(ids)
-        token, real = choice.clamp(min=0) // TOP_K, (choice >= 0)[:, None]
-        xs = torch.where(real, x[token], torch.zeros_like(x[token]))
-        share = torch.where(real[:, 0], weights.flatten()[choice.clamp(min=0)], torch.zeros_like(token, dtype=torch.float32))
+        plan = mxw.sort_tokens(ids, EXPERTS)
 
         # forward
-        gate_up, down = self.gate_up.to(torch.bfloat16), self.down.to(torch.bfloat16)
-        gu = mxw.fwd(*quantize_rows(xs), *quantize_rows(gate_up), offs).float()
+        xs, xq, xscales = mxw.dispatch_tokens(x, plan, mxfp8=True)
+        gu = mxw.fwd(xq, xscales, *mxw.quantize_rows(self.gate_up), plan.offs).float()
         gate, up = gu[:, :WIDTH], gu[:, WIDTH:]
         sig = torch.sigmoid(gate)
         h = (gate * sig * up).to(torch.bfloat16)
-        out = mxw.fwd(*quantize_rows(h), *quantize_rows(down), offs).float()
-        y = x.float().index_add(0, token, out * share[:, None] * real)
+        out = mxw.fwd(*mxw.quantize_rows(h), *mxw.quantize_rows(self.down), plan.offs)
+        y = mxw.combine_tokens(out, plan, weights, residual=x)
 
         # the loss, and back
-        loss, dy, dwords = mxw.vocab_cross_entropy(y.to(torch.bfloat16), self.words.to(torch.bfloat16), targets)
-        dout = (dy.float()[token] * share[:, None] * real).to(torch.bfloat16)
-        dh = mxw.fwd(*quantize_rows(dout), *quantize_rows(down.transpose(1, 2).contiguous()), offs).float()
+        loss, dy, dwords = mxw.vocab_cross_entropy(y, self.words.to(torch.bfloat16), targets)
+        dout, dq, dscales, _ = mxw.combine_tokens_grad(dy, out, plan, weights, mxfp8=True)
+        dh = mxw.fwd(dq, dscales, *mxw.quantize_rows(self.down.transpose(1, 2).contiguous()), plan.offs).float()
         dgate = dh * up * (sig + gate * sig * (1 - sig))
         dgu = torch.cat([dgate, dh * gate * sig], 1).to(torch.bfloat16)
+        offs = plan.offs
         grads = [mxw.wgrad(*mxw.quantize_tokens(dgu, offs), *mxw.quantize_tokens(xs, offs), offs),
                  mxw.wgrad(*mxw.quantize_tokens(dout, offs), *mxw.quantize_tokens(h, offs), offs)]
+        mxw.clip_grad_norm(grads + [dwords], MAX_NORM)
 
         # the experts: orthogonalised momentum; the vocabulary: plain descent
         for weight, momentum, grad in zip((self.gate_up, self.down), self.momenta, grads):
@@ -104,14 +85,14 @@ class Model:
 
     def serve(self):
         """The layer for single tokens and small batches: words -> logits."""
-        qgu, sgu = quantize_rows(self.gate_up.to(torch.bfloat16))
-        qd, sd = quantize_rows(self.down.to(torch.bfloat16))
-        words = self.words.to(torch.bfloat16).float().t()
+        qgu, sgu = mxw.quantize_rows(self.gate_up)
+        qd, sd = mxw.quantize_rows(self.down)
+        qw, sw = mxw.quantize_rows(self.words, "mxfp4")
 
         def logits(prompt):
             x = self.embedding[prompt]
             out, _, _ = mxw.moe_layer(x, self.router, qgu, sgu, qd, sd, TOP_K)
-            return (x.float() + out.float()) @ words
+            return mxw.linear_4bit(x + out, qw, sw, dtype=torch.float32)
 
         return logits
 

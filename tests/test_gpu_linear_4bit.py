@@ -3,9 +3,8 @@
 Tolerance.  MXFP4: the weights enter exactly, each product of two bf16 numbers is exact in
 float32, and a sum of K terms rounds at most K times by half a step of 2^-24 (a whole one,
 2^-23, if the matrix unit cuts instead) of a partial sum that the sum of magnitudes S
-bounds: K 2^-23 S.  Integers: code and zero enter as 16 + code and 16 + zero, so S is that
-of x (16 + code) s and of x (16 + zero) s, and four more roundings for each group.  The
-result's rounding to bf16 adds 2^-8 of it.
+bounds: K 2^-23 S.  Integers: code and zero enter apart, so S is that of x code s and of x zero s,
+and there are four more roundings for each group.  The result's rounding to bf16 adds 2^-8 of it.
 """
 import pytest
 import torch
@@ -47,7 +46,7 @@ def reference(x, codes, scales, zeros):
     else:
         s = scales.double().repeat_interleave(group, 1)
         z = 8 if zeros is None else zeros.long().repeat_interleave(group, 1)
-        v, size = (n - z) * s, (32 + n + z) * s.abs()
+        v, size = (n - z) * s, (n + z) * s.abs()
     return x.double() @ v.mT, x.double().abs() @ size.mT
 
 
@@ -109,6 +108,21 @@ def test_many_rows(group):
         say("linear_4bit T=%d K=%d N=%d group=%s" % (T, K, N, group))
         args = make(T, K, N, group, N, group is not None)
         check(mxw.linear_4bit(*args), *args, "N=%d" % N)
+
+
+@pytest.mark.parametrize("group,zeros", FORMS)
+@pytest.mark.parametrize("T,K,N", [(1, 7200, 34001), (9, 7200, 36017), (16, 4192, 33000), (23, 4192, 40001), (32, 2144, 66000),
+                                   (37, 1120, 40001), (64, 2080, 33041),      # two tiles of rows a wave
+                                   (16, 7200, 20001), (20, 7200, 20001), (48, 2080, 20001), (64, 3104, 17000),
+                                   (12, 12320, 700), (20, 7200, 3001), (32, 4192, 16384), (33, 2080, 3001),
+                                   (64, 7200, 100), (64, 65536, 40)])
+def test_every_form(T, K, N, group, zeros):
+    """Tokens that fit in LDS and that come in pieces, one and two row tiles a wave, parts of K,
+    several rounds of workgroups, and ends inside a step, with rows and tokens to spare."""
+    K = K // (group or 32) * (group or 32)
+    say("linear_4bit T=%d K=%d N=%d group=%s zeros=%s" % (T, K, N, group, zeros))
+    args = make(T, K, N, group, T + N, zeros)
+    check(mxw.linear_4bit(*args, dtype=F32, out=poisoned(T, N, F32)), *args, "T=%d K=%d N=%d" % (T, K, N))
 
 
 def test_each_code_and_place():
