@@ -618,7 +618,8 @@ int64_t mxw_moe_workspace_size(int T, int E, int k, int H, int I);
  *   offs, counts  int32 [E];  rows  int32 [T, k]; fully overwritten.
  *   workspace, workspace_bytes  256-byte aligned device memory of at least
  *            mxw_sort_workspace_size(T, k, E) bytes (NULL if that is 0: up to 4,096
- *            choices); contents undefined on entry and exit.
+ *            choices); contents undefined on entry and exit, in use until the
+ *            call's work is done.
  *
  * mxw_token_rows gives the rows that any ids of these sizes fit in, a multiple of
  * align: what to allocate without reading offs on the host.  MXW_ERR_DIM if that is
@@ -740,14 +741,15 @@ int mxw_quantize_rows(const void* x, int type, int64_t ldx, int64_t R, int C, in
  *   norm_type  MXW_NORM_2 or MXW_NORM_MAX.   max_norm, eps  >= 0.
  *   norm     DEVICE memory, one FP32: n before clipping.
  *   workspace, workspace_bytes  256-byte aligned device memory of at least
- *            mxw_clip_workspace_size(count) bytes; contents undefined on entry and exit.
+ *            mxw_clip_workspace_size(count) bytes; contents undefined on entry and exit,
+ *            in use until the call's work is done.
  *
  * Squares are summed in 64 bits: the norm neither overflows nor vanishes before FP32
  * does.  The product with the factor is FP32, rounded once.  A NaN makes the norm and
  * all outputs NaN; an infinity makes the norm infinite and the factor 0 (its own element
  * NaN), unless max_norm is infinite too (NaN).  Bitwise reproducible run to run.
- * Effects: enqueues two kernels for every 96 tensors on `stream`, allocates nothing on
- * the device, keeps no state, does not synchronise; graph-capturable (the addresses are
+ * Effects: enqueues two kernels for every 96 tensors (one more if there are more) on
+ * `stream`, allocates nothing on the device, keeps no state, does not synchronise; graph-capturable (the addresses are
  * the kernels' arguments).
  */
 int mxw_clip_grads(const void* const* grads, void* const* outs, const int64_t* sizes, const int32_t* types, int count,
@@ -764,7 +766,8 @@ int64_t mxw_clip_workspace_size(int count);
  *     MXW_INT4:   v = (code - zero) scale
  *
  * Arguments (caller-owned DEVICE memory):
- *   x, ldx   bf16 [T, K], rows ldx >= K elements apart (a multiple of 8), 16-byte aligned.
+ *   x, ldx   bf16 [T, K], rows ldx >= K elements apart (a multiple of 8, up to 2^23), 16-byte
+ *            aligned.
  *   codes    uint8 [N, K/2], element 2 i of a row in the low half of byte i; contiguous,
  *            16-byte aligned.
  *   scales   [N, K/group]: E8M0 bytes (MXW_MXFP4) or bf16 (MXW_INT4), contiguous.
@@ -774,9 +777,11 @@ int64_t mxw_clip_workspace_size(int count);
  *   out, out_type  [T, N] MXW_BF16 or MXW_F32, contiguous, fully overwritten.
  *
  * The numbers that MXFP4 codes stand for are exact in bf16 where they are normal there
- * (below 2^-126 they are 0, beyond bf16's range infinity); integer codes enter as whole
- * numbers, and each group's FP32 sum is scaled.  All sums are FP32.  A token's result
- * does not depend on the other tokens' values.  Bitwise reproducible run to run.
+ * (below 2^-126 they are 0, beyond bf16's range infinity); integer codes and zeros enter as
+ * whole numbers, summed apart, and each group's FP32 sums are scaled: an infinity in x then
+ * gives NaN where the formula may give an infinity.  All sums are FP32.  A token's result
+ * does not depend on the other tokens' values; its last bits can depend on T and N, by which
+ * K is split.  Bitwise reproducible run to run.
  * Effects: one kernel on `stream`, allocates nothing, keeps no state, does not
  * synchronise; graph-capturable.
  */

@@ -7,7 +7,8 @@
 // reading HBM twice and writing it once.  The first leaves a partial result for each
 // workgroup, whose share of the tiles depends on the sizes alone; every workgroup of the
 // second adds all partials in one order, so no launch stands between them and the bits
-// are the same run to run.  Squares are summed in 64 bits: a product of two FP32 values
+// are the same run to run (with more tensors than one launch takes, a workgroup adds the
+// partials of all launches first).  Squares are summed in 64 bits: a product of two FP32 values
 // neither overflows nor vanishes there.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -26,6 +27,7 @@ using namespace mxw;
 constexpr int kTileVecs = 4, kTileElems = 256 * 8 * kTileVecs;  // elements of a tile
 constexpr int kMost = 96;                                       // tensors of a launch (its arguments: 4 KiB at most)
 constexpr int kBlocks = 2048;                                   // workgroups of a launch
+constexpr int kHead = 256;                                      // bytes before the partials, all of them as one
 
 struct Item {
   const void* g;
@@ -137,6 +139,15 @@ __device__ __forceinline__ void tile_scale(const Item& it, int64_t at, float pow
   }
 }
 
+// All partials as one.
+template <bool TOP>
+__global__ __launch_bounds__(256) void join_kernel(const double* part, int parts, double* to) {
+  double v = 0.0;
+  for (int i = threadIdx.x; i < parts; i += 256) v = join(v, part[i], TOP);
+  v = block_join<TOP>(v);
+  if (threadIdx.x == 0) *to = v;
+}
+
 // The norm from all partials, and this launch's tensors times the factor.
 template <bool TOP, bool NT>
 __global__ __launch_bounds__(256) void scale_kernel(NormArgs a) {
@@ -169,7 +180,7 @@ extern "C" {
 
 int64_t mxw_clip_workspace_size(int count) {
   if (count < 0 || count > MXW_MAX_TENSORS) return MXW_ERR_DIM;
-  return (int64_t)((count + kMost - 1) / kMost + (count == 0)) * kBlocks * 8;
+  return kHead + (int64_t)((count + kMost - 1) / kMost + (count == 0)) * kBlocks * 8;
 }
 
 int mxw_clip_grads(const void* const* grads, void* const* outs, const int64_t* sizes, const int32_t* types, int count,
@@ -223,6 +234,7 @@ int mxw_clip_grads(const void* const* grads, void* const* outs, const int64_t* s
   if (const int rc = check_device()) return rc;
   hipStream_t st = (hipStream_t)stream;
   const bool top = norm_type == MXW_NORM_MAX;
+  double* const partials = (double*)((char*)workspace + kHead);
   int parts = 0;
   for (int pass = 0; pass < 2; ++pass) {
     int i = 0;
@@ -237,7 +249,7 @@ int mxw_clip_grads(const void* const* grads, void* const* outs, const int64_t* s
       }
       const int blocks = std::min(a.tiles, kBlocks);
       if (pass == 0) {
-        a.part = (double*)workspace + parts;
+        a.part = partials + parts;
         if (blocks) {
           if (top)
             nt ? norm_kernel<true, true><<<dim3(blocks), dim3(256), 0, st>>>(a)
@@ -248,7 +260,14 @@ int mxw_clip_grads(const void* const* grads, void* const* outs, const int64_t* s
         }
         parts += blocks;
       } else {
-        a.part = (double*)workspace, a.parts = parts;
+        const bool joined = count > kMost;
+        if (joined && !any) {
+          if (top)
+            join_kernel<true><<<dim3(1), dim3(256), 0, st>>>(partials, parts, (double*)workspace);
+          else
+            join_kernel<false><<<dim3(1), dim3(256), 0, st>>>(partials, parts, (double*)workspace);
+        }
+        a.part = joined ? (double*)workspace : partials, a.parts = joined ? 1 : parts;
         a.norm = any ? nullptr : norm;
         if (!outs) a.tiles = 0, i = count;  // the norm alone
         const int run = outs ? std::max(blocks, 1) : 1;

@@ -211,6 +211,21 @@ def test_weights_that_quantize_rows_made():
     assert (got.double() - want).norm() < 0.2 * want.norm()
 
 
+def test_scales_past_32_bits():
+    """A scale plane of over 1.6 GB, K ending inside a step: nothing past K comes in."""
+    K, N = 65312, 820000
+    say("linear_4bit K=%d N=%d" % (K, N))
+    codes = torch.zeros((N, K // 2), dtype=torch.uint8, device=DEV)
+    scales = torch.full((N, K // 32), 255, dtype=torch.uint8, device=DEV)  # NaN, where nothing is looked at
+    rows = [0, 1, 15, 16, 300000, N - 17, N - 1]
+    x, some, ss, _ = make(1, K, len(rows), None, 7)
+    codes[rows], scales[rows] = some, ss
+    got = mxw.linear_4bit(x, codes, scales, dtype=F32)
+    check(got[:, rows].contiguous(), x, some, ss, None, "rows")
+    del codes, scales
+    torch.cuda.empty_cache()
+
+
 def test_weights_past_32_bits():
     """Codes of over 2^31 bytes."""
     K, N = 65536, 70000

@@ -33,7 +33,7 @@ def test_sizes():
     assert mxw.token_rows(0, 2, 8) == 0 and mxw.token_rows(1, 2, 8) == 64 and mxw.token_rows(1, 2, 1) == 32
     assert mxw.token_rows(100, 2, 8) == (200 + 8 * 31) // 32 * 32 and mxw.token_rows(5, 3, 10, 1) == 15
     assert mxw.sort_workspace_size(2048, 2, 8) == 0 and mxw.sort_workspace_size(2049, 2, 8) == 3 * 8 * 4
-    assert mxw.clip_workspace_size(0) > 0 and mxw.clip_workspace_size(97) == 2 * mxw.clip_workspace_size(96)
+    assert mxw.clip_workspace_size(0) > 0 and mxw.clip_workspace_size(96) < mxw.clip_workspace_size(97)
     for f, args in ((mxw.token_rows, (1 << 23, 2, 8)), (mxw.token_rows, (4, 2, 0)), (mxw.token_rows, (4, 2, 8, 0)),
                     (mxw.sort_workspace_size, (4, 65, 8)), (mxw.clip_workspace_size, (-1,)),
                     (mxw.clip_workspace_size, (65537,))):
@@ -122,7 +122,7 @@ INT = dict(format=2, group=64, zeros=P)
     (dict(x=0), -1), (dict(codes=0), -1), (dict(scales=0), -1), (dict(out=0), -1),
     (dict(format=0), -2), (dict(format=3), -2), (dict(group=64), -2), (dict(zeros=P), -2), (dict(T=-1), -2), (dict(T=65), -2),
     (dict(K=0), -2), (dict(K=48), -2), (dict(K=65568, ldx=65568), -2), (dict(N=0), -2), (dict(N=(1 << 20) + 1), -2),
-    (dict(ldx=248), -2), (dict(ldx=260), -2), (dict(out_type=2), -2), (dict(INT, group=16), -2), (dict(INT, group=48), -2),
+    (dict(ldx=248), -2), (dict(ldx=260), -2), (dict(ldx=(1 << 23) + 8), -2), (dict(out_type=2), -2), (dict(INT, group=16), -2), (dict(INT, group=48), -2),
     (dict(INT, group=128, K=192, ldx=192), -2),
     (dict(x=P + 8), -3), (dict(codes=P + 4), -3), (dict(out=P + 1), -3), (dict(out_type=1, out=P + 2), -3),
     (dict(INT, scales=P + 1), -3),
