@@ -287,10 +287,19 @@ __global__ __launch_bounds__(256) void combine_kernel(RowArgs a) {
   }
 }
 
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp(float v) {   // lanes without a source add 0
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, false));
+}
+// the sum over a wave, in every lane
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+  v += dpp<0x111, 0xF>(v);  // lane i takes from i - 1, 2, 4, 8 of its row of 16
+  v += dpp<0x112, 0xF>(v);
+  v += dpp<0x114, 0xF>(v);
+  v += dpp<0x118, 0xF>(v);
+  v += dpp<0x142, 0xA>(v);  // lane 15 of rows 0, 2 into rows 1, 3
+  v += dpp<0x143, 0xC>(v);  // lane 31 into rows 2, 3
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
 // dy[row[t][j]] = w[t][j] dout[t], dw[t][j] = <dout[t], y[row[t][j]]>
@@ -301,11 +310,15 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(RowArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t = (blockIdx.x - a.pad_blocks) * (4 / W) + wave / W;
   if (W == 1 && t >= a.T) return;
+  const bool live = t < a.T;   // two tokens of a workgroup meet at its barriers
   for (int j0 = 0; j0 < a.k; j0 += 8) {
     int r[8];
     float w[8], dot[8] = {};
-    choices<true>(a, t, j0, r, w);
-    for (int c = ((wave % W) * 64 + lane) * 8; c < a.H; c += W * 512) {
+    if (live)
+      choices<true>(a, t, j0, r, w);
+    else
+      for (int u = 0; u < 8; ++u) r[u] = -1, w[u] = 0.0f;
+    for (int c = ((wave % W) * 64 + lane) * 8; c < a.H && live; c += W * 512) {
       const int n = min(a.H - c, 8);
       float d[8];
       values<F32>(n == 8 ? load8<F32>(a.x, t * a.ldx + c) : load_some<F32>(a.x, t * a.ldx + c, n), d);
@@ -351,18 +364,23 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(RowArgs a) {
     }
     if (a.dweights) {
 #pragma unroll
-      for (int u = 0; u < 8; ++u) dot[u] = wave_sum(dot[u]);
+      for (int u = 0; u < 8; ++u)
+        if (j0 + u < a.k) dot[u] = wave_sum(dot[u]);
       if (W > 1) {
-        if (lane < 8) red[wave][lane] = 0.0f;
 #pragma unroll
         for (int u = 0; u < 8; ++u)
           if (lane == u) red[wave][u] = dot[u];
         __syncthreads();
+        const int first = wave / W * W;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) dot[u] = (red[0][u] + red[1][u]) + (red[2][u] + red[3][u]);
+        for (int u = 0; u < 8; ++u) {
+          float v = red[first][u] + red[first + 1][u];
+          if (W == 4) v += red[2][u] + red[3][u];
+          dot[u] = v;
+        }
         __syncthreads();
       }
-      if (wave % W == 0) {
+      if (wave % W == 0 && live) {
 #pragma unroll
         for (int u = 0; u < 8; ++u)
           if (lane == u && j0 + u < a.k) a.dweights[(int64_t)t * a.k + j0 + u] = dot[u];
@@ -447,8 +465,22 @@ bool on(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1
 
 int launched() { return hipGetLastError() == hipSuccess ? MXW_OK : MXW_ERR_LAUNCH; }
 
-// waves a token: its row in one go where one wave can hold it
-bool one_wave(int H) { return H <= 512; }
+// f(W, NT) with the waves of a token and the way past the caches as constants.  W waves take
+// 512 W columns at a time; 4 leave few tokens spread over the device, and fewer have less idle
+// lanes at a short row's end and, in the gradient, sums to join: rows of 2048, bf16, 8 each for
+// 32,768 tokens joined 199 us with 4, 206 with 2, 213 with 1; of 1500, 4 each for 30,000, 116
+// with 4 and 107 with 2; their gradients at 1280 155, 125 and 117; rows of 1284 dispatched, 8
+// each for 10,253 tokens, 69, 75 and 82.
+template <class F>
+void with_waves(int H, int one, int two, bool nt, F f) {
+  auto w = [&](auto c) { nt ? f(c, std::true_type{}) : f(c, std::false_type{}); };
+  if (H <= one)
+    w(std::integral_constant<int, 1>{});
+  else if (H <= two)
+    w(std::integral_constant<int, 2>{});
+  else
+    w(std::integral_constant<int, 4>{});
+}
 
 // Loads and stores past the caches where a call moves more than they hold (256 MB): 262,144
 // rows of 2048 joined in 199 us, with cached ones 228; 65,536 rows of 7168 quantised in 221 and
@@ -532,12 +564,10 @@ int mxw_dispatch_tokens(const void* x, int type, int64_t ldx, const int32_t* off
   hipStream_t st = (hipStream_t)stream;
   auto go = [&](auto f32, auto with_rows, auto mx) {
     constexpr bool F = decltype(f32)::value, RW = decltype(with_rows)::value, M = decltype(mx)::value;
-    if (one_wave(H))
-      nt ? dispatch_kernel<F, RW, M, 1, true><<<dim3(pads + (T + 3) / 4), dim3(256), 0, st>>>(a)
-         : dispatch_kernel<F, RW, M, 1, false><<<dim3(pads + (T + 3) / 4), dim3(256), 0, st>>>(a);
-    else
-      nt ? dispatch_kernel<F, RW, M, 4, true><<<dim3(pads + T), dim3(256), 0, st>>>(a)
-         : dispatch_kernel<F, RW, M, 4, false><<<dim3(pads + T), dim3(256), 0, st>>>(a);
+    with_waves(H, 512, 1024, nt, [&](auto w, auto past) {
+      constexpr int W = decltype(w)::value, per = 4 / W;   // tokens of a workgroup
+      dispatch_kernel<F, RW, M, W, decltype(past)::value><<<dim3(pads + (T + per - 1) / per), dim3(256), 0, st>>>(a);
+    });
   };
   using Y = std::true_type;
   using N = std::false_type;
@@ -573,12 +603,10 @@ int mxw_combine_tokens(const void* y, int type, int64_t ldy, const int32_t* rows
   hipStream_t st = (hipStream_t)stream;
   auto go = [&](auto f32, auto wt) {
     constexpr bool F = decltype(f32)::value, WT = decltype(wt)::value;
-    if (one_wave(H))
-      nt ? combine_kernel<F, WT, 1, true><<<dim3((T + 3) / 4), dim3(256), 0, st>>>(a)
-         : combine_kernel<F, WT, 1, false><<<dim3((T + 3) / 4), dim3(256), 0, st>>>(a);
-    else
-      nt ? combine_kernel<F, WT, 4, true><<<dim3(T), dim3(256), 0, st>>>(a)
-         : combine_kernel<F, WT, 4, false><<<dim3(T), dim3(256), 0, st>>>(a);
+    with_waves(H, 1024, 1536, nt, [&](auto w, auto past) {
+      constexpr int W = decltype(w)::value, per = 4 / W;
+      combine_kernel<F, WT, W, decltype(past)::value><<<dim3((T + per - 1) / per), dim3(256), 0, st>>>(a);
+    });
   };
   using Y = std::true_type;
   using N = std::false_type;
@@ -612,12 +640,10 @@ int mxw_combine_tokens_grad(const void* dout, int type, int64_t ldo, const void*
   hipStream_t st = (hipStream_t)stream;
   auto go = [&](auto f32, auto with_rows, auto mx) {
     constexpr bool F = decltype(f32)::value, RW = decltype(with_rows)::value, M = decltype(mx)::value;
-    if (one_wave(H))
-      nt ? combine_grad_kernel<F, RW, M, 1, true><<<dim3(pads + (T + 3) / 4), dim3(256), 0, st>>>(a)
-         : combine_grad_kernel<F, RW, M, 1, false><<<dim3(pads + (T + 3) / 4), dim3(256), 0, st>>>(a);
-    else
-      nt ? combine_grad_kernel<F, RW, M, 4, true><<<dim3(pads + T), dim3(256), 0, st>>>(a)
-         : combine_grad_kernel<F, RW, M, 4, false><<<dim3(pads + T), dim3(256), 0, st>>>(a);
+    with_waves(H, 1536, 1536, nt, [&](auto w, auto past) {
+      constexpr int W = decltype(w)::value, per = 4 / W;
+      combine_grad_kernel<F, RW, M, W, decltype(past)::value><<<dim3(pads + (T + per - 1) / per), dim3(256), 0, st>>>(a);
+    });
   };
   using Y = std::true_type;
   using N = std::false_type;

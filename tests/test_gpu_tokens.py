@@ -140,7 +140,7 @@ def plain_dispatch(x, plan, xs):
     return xs
 
 
-HS = [1, 7, 8, 9, 33, 64, 505, 511, 512, 513, 520, 1001, 2047, 2048, 2052, 4100, 8200]
+HS = [1, 7, 8, 9, 33, 64, 505, 511, 512, 513, 520, 1001, 1024, 1030, 1536, 1540, 2047, 2048, 2052, 4100, 8200]
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
