@@ -653,7 +653,8 @@ int64_t mxw_sort_workspace_size(int T, int k, int E);
  *   R        rows of the outputs, 0 .. MXW_MAX_ROWS.
  *   xs       [R, H] of `type`, contiguous, or NULL.
  *   q, s     uint8 [R, H] and [R, H/32], contiguous, or both NULL; q 8-byte aligned.
- * The outputs overlap no input.  Effects: one kernel on `stream`, allocates nothing,
+ * What is written overlaps neither itself nor an input (MXW_ERR_OVERLAP, as in
+ * mxw_sort_tokens and the entries below; strided rows count with what lies between them).  Effects: one kernel on `stream`, allocates nothing,
  * keeps no state, does not synchronise; graph-capturable.
  */
 int mxw_dispatch_tokens(const void* x, int type, int64_t ldx, const int32_t* offs, const int32_t* counts,
@@ -711,7 +712,7 @@ int mxw_combine_tokens_grad(const void* dout, int type, int64_t ldo, const void*
  * with b = 8 and the largest 448 (MXFP8, as mxfp8_quantize_tokens), b = 2 and 6 (MXFP4).
  *
  *   x, type, ldx  [R, C] MXW_BF16 or MXW_F32, rows ldx >= C elements apart.
- *   R        >= 0, at most 2^31 and 2^36 elements in all.  C  a multiple of 32, 32 .. 65536.
+ *   R        >= 0, at most 2^31 and 2^35 - 4096 elements in all.  C  a multiple of 32, 32 .. 65536.
  *   q        uint8 [R, C] (MXFP8) or [R, C/2] (MXFP4: element 2 i in the low half of byte
  *            i), contiguous, 8-byte aligned.  s  uint8 [R, C/32], contiguous.
  * Effects: one kernel on `stream`, allocates nothing, keeps no state, does not

@@ -816,6 +816,12 @@ the rows that the runs fit in whatever the ids (a Python number)."""
 _TYPES = {torch.bfloat16: 0, torch.float32: 1}
 
 
+def _fits(*sizes):
+    """ctypes would cut sizes past 32 bits without a word."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise ValueError("sizes past 2^31 - 1: %s" % (sizes,))
+
+
 @functools.lru_cache(maxsize=1024)
 def _sort_sizes(T, k, E, align):
     """Rows and workspace of a sort: functions of the sizes alone, and a call of each
@@ -826,6 +832,7 @@ def _sort_sizes(T, k, E, align):
 def token_rows(T, k, E, align=32):
     """Rows that T tokens' k choices among E experts fit in, each expert's run a
     multiple of align.  Raises MxwError if that is over 8,388,608."""
+    _fits(int(T), int(k), int(E), int(align))
     rc = _load().mxw_token_rows(int(T), int(k), int(E), int(align))
     if rc < 0:
         raise MxwError("mxw_token_rows failed: %s" % strerror(rc))
@@ -835,6 +842,7 @@ def token_rows(T, k, E, align=32):
 def sort_workspace_size(T, k, E):
     """Bytes of workspace sort_tokens needs (0: none).  Raises MxwError on a
     status code."""
+    _fits(int(T), int(k), int(E))
     rc = _load().mxw_sort_workspace_size(int(T), int(k), int(E))
     if rc < 0:
         raise MxwError("mxw_sort_workspace_size failed: %s" % strerror(rc))
@@ -867,6 +875,7 @@ def sort_tokens(ids, E, align=32, stream=None, workspace=None):
     if k > 1 and ids.stride(1) != 1 or T > 1 and ids.stride(0) < k:
         raise ValueError("ids must have a contiguous last axis and rows at least a row apart")
     E, align = int(E), int(align)
+    _fits(T, k, E, align)
     size, need = _sort_sizes(T, k, E, align)
     on = _On(dev, stream)
     offs, counts, rows = on.new((E,), torch.int32), on.new((E,), torch.int32), on.new((T, k), torch.int32)
@@ -947,9 +956,9 @@ def dispatch_tokens(x, plan, rows=True, mxfp8=False, out=None, q=None, s=None, s
 
     The padding rows of every expert become zeros; rows past the last run are left as
     they were (uninitialised in new tensors; the grouped products do not read them).
-    `out`, `q` and `s` (optional) are contiguous tensors of at most or more rows than
-    plan.size: rows that they do not have are skipped.  The gradient with respect to x is
-    combine_tokens(dxs, plan).  Runs on `stream` (default: the current stream) and does
+    `out`, `q` and `s` (optional) are contiguous tensors of any one number of rows:
+    rows that they do not have are skipped.  They may not share memory with an input.
+    The gradient with respect to x is combine_tokens(dxs, plan).  Runs on `stream` (default: the current stream) and does
     not synchronise."""
     ldx = _matrix(x, "x", None)
     dev = x.device
@@ -964,6 +973,7 @@ def dispatch_tokens(x, plan, rows=True, mxfp8=False, out=None, q=None, s=None, s
     for t in (out, q, s):
         if t is not None and t.dim() == 2:
             R = t.shape[0]
+    _fits(T, k, E, H, R)
     on = _On(dev, stream)
     if rows:
         out = _output(out, "out", (R, H), x.dtype, on)
@@ -1003,6 +1013,7 @@ def combine_tokens(y, plan, weights=None, residual=None, out=None, stream=None):
     dev = y.device
     offs, counts, rows, _, T, k, E = _plan(plan, dev)
     R, H = y.shape
+    _fits(T, k, H, R)
     ldr = 0 if residual is None else _matrix(residual, "residual", T, H, y.dtype, dev)
     if weights is not None:
         _weights(weights, T, k, dev)
@@ -1045,6 +1056,7 @@ def combine_tokens_grad(dout, y, plan, weights, rows=True, mxfp8=False, dy=None,
         raise ValueError("dout has %d tokens, the plan %d" % (dout.shape[0], T))
     ldy = _matrix(y, "y", None, H, dout.dtype, dev)
     R = y.shape[0]
+    _fits(T, k, E, H, R)
     _weights(weights, T, k, dev)
     if not rows and not mxfp8:
         raise ValueError("nothing to write: rows and mxfp8 are both False")
@@ -1106,6 +1118,7 @@ def quantize_rows(x, format="mxfp8", q=None, s=None, stream=None):
         except RuntimeError:
             raise ValueError("x's rows must be one stride apart") from None
         R = x.numel() // C
+    _fits(C)
     on = _On(x.device, stream)
     if q is not None and q.dtype == getattr(torch, "float8_e4m3fn", None):
         q = q.view(torch.uint8)
@@ -1250,6 +1263,7 @@ def linear_4bit(x, codes, scales, zeros=None, dtype=torch.bfloat16, out=None, st
     if codes.dim() != 2 or scales.dim() != 2 or codes.shape[0] == 0:
         raise ValueError("codes and scales must be 2-D")
     N = codes.shape[0]
+    _fits(T, K, N)
     fp4 = scales.dtype == torch.uint8
     groups = scales.shape[1]
     group = K // groups if groups else 0

@@ -488,6 +488,10 @@ extern "C" int mxw_linear_4bit(const uint16_t* x, int64_t ldx, const uint8_t* co
   if (!codes || !scales || (T && (!x || !out))) return MXW_ERR_NULL;
   if (!on(x, 16) || !on(codes, 16) || !on(scales, fp4 ? 1 : 2) || !on(out, out_type == MXW_F32 ? 4 : 2))
     return MXW_ERR_ALIGN;
+  const int64_t groups = (int64_t)N * (K / group);
+  if (mxw::overlap<5>({{out, (int64_t)T * N * (out_type == MXW_F32 ? 4 : 2)}, {x, T, ldx, K, 2}, {codes, (int64_t)N * K / 2},
+                       {scales, groups * (fp4 ? 1 : 2)}, {zeros, groups}}, 1))
+    return MXW_ERR_OVERLAP;
   if (const int rc = check_device()) return rc;
   if (T == 0) return MXW_OK;
   LinArgs a = {};

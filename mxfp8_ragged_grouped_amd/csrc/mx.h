@@ -8,6 +8,27 @@
 
 namespace mxw {
 
+// The bytes of a host call's argument (none: NULL, or no rows), to find outputs that overlap
+// themselves or an input.
+struct Span {
+  uintptr_t lo = 0, hi = 0;
+  Span() {}
+  Span(const void* p, int64_t bytes) {
+    if (p && bytes > 0) lo = (uintptr_t)p, hi = lo + (uintptr_t)bytes;
+  }
+  // rows of H elements, ld apart
+  Span(const void* p, int64_t rows, int64_t ld, int64_t H, int size)
+      : Span(p, rows > 0 ? (int64_t)((((uint64_t)rows - 1) * (uint64_t)ld + (uint64_t)H) * (uint64_t)size) : 0) {}
+};
+// whether one of the first `outs` meets another of them or any span behind them
+template <int N>
+bool overlap(const Span (&s)[N], int outs) {
+  for (int i = 0; i < outs; ++i)
+    for (int j = i + 1; j < N; ++j)
+      if (s[i].lo < s[j].hi && s[j].lo < s[i].hi) return true;
+  return false;
+}
+
 typedef int i4 __attribute__((ext_vector_type(4)));
 typedef int i2 __attribute__((ext_vector_type(2)));
 // the same on an element's alignment (a vector access of any address is legal)

@@ -524,6 +524,9 @@ int mxw_sort_tokens(const void* ids, int id_bytes, int64_t ld, int T, int k, int
   if (!on(ids, id_bytes) || !on(offs, 4) || !on(counts, 4) || !on(rows, 4)) return MXW_ERR_ALIGN;
   const int64_t need = mxw_sort_workspace_size(T, k, E);
   if (need > 0 && (!workspace || !on(workspace, 256) || workspace_bytes < (size_t)need)) return MXW_ERR_WORKSPACE;
+  const int64_t plan = (int64_t)T * k * 4;
+  if (overlap<5>({{offs, 4 * E}, {counts, 4 * E}, {rows, plan}, {workspace, need}, {ids, T, ld, k, id_bytes}}, 4))
+    return MXW_ERR_OVERLAP;
   if (const int rc = check_device()) return rc;
   SortArgs a = {ids, ld, T * k, k, E, align, offs, counts, rows, (int32_t*)workspace};
   hipStream_t st = (hipStream_t)stream;
@@ -559,6 +562,9 @@ int mxw_dispatch_tokens(const void* x, int type, int64_t ldx, const int32_t* off
   if (!offs || !counts || (T && (!x || !rows))) return MXW_ERR_NULL;
   const int size = type == MXW_F32 ? 4 : 2;
   if (!on(x, size) || !on(xs, size) || !on(offs, 4) || !on(counts, 4) || !on(rows, 4) || !on(q, 8)) return MXW_ERR_ALIGN;
+  const int64_t RH = (int64_t)R * H, plan = (int64_t)T * k * 4;
+  if (overlap<7>({{xs, RH * size}, {q, RH}, {s, RH / 32}, {x, T, ldx, H, size}, {offs, 4 * E}, {counts, 4 * E}, {rows, plan}}, 3))
+    return MXW_ERR_OVERLAP;
   if (const int rc = check_device()) return rc;
   if (T == 0 || R == 0) return MXW_OK;
   RowArgs a = {};
@@ -599,6 +605,11 @@ int mxw_combine_tokens(const void* y, int type, int64_t ldy, const int32_t* rows
   if (T && (!rows || !out || (R && !y))) return MXW_ERR_NULL;
   const int size = type == MXW_F32 ? 4 : 2;
   if (!on(y, size) || !on(residual, size) || !on(out, size) || !on(rows, 4) || !on(weights, 4)) return MXW_ERR_ALIGN;
+  const int64_t plan = (int64_t)T * k * 4;
+  const bool itself = residual == out && (ldr == H || T <= 1);
+  if (overlap<5>({{out, (int64_t)T * H * size}, {y, R, ldy, H, size}, {rows, plan}, {weights, plan},
+                  {itself ? nullptr : residual, T, ldr, H, size}}, 1))
+    return MXW_ERR_OVERLAP;
   if (const int rc = check_device()) return rc;
   if (T == 0) return MXW_OK;
   RowArgs a = {};
@@ -635,6 +646,13 @@ int mxw_combine_tokens_grad(const void* dout, int type, int64_t ldo, const void*
   if (!on(dout, size) || !on(y, size) || !on(dy, size) || !on(offs, 4) || !on(counts, 4) || !on(rows, 4) ||
       !on(weights, 4) || !on(dweights, 4) || !on(q, 8))
     return MXW_ERR_ALIGN;
+  const int64_t RH = (int64_t)R * H, plan = (int64_t)T * k * 4;
+  const Span yy(dweights ? y : nullptr, R, ldy, H, size);
+  const bool itself = dy == y && (ldy == H || R <= 1);
+  if (overlap<9>({{dy, RH * size}, {q, RH}, {s, RH / 32}, {dweights, plan}, {dout, T, ldo, H, size}, {weights, plan},
+                  {rows, plan}, {offs, 4 * E}, {counts, 4 * E}}, 4) ||
+      overlap<5>({{itself ? nullptr : dy, RH * size}, {q, RH}, {s, RH / 32}, {dweights, plan}, yy}, 4))
+    return MXW_ERR_OVERLAP;
   if (const int rc = check_device()) return rc;
   if (T == 0) return MXW_OK;
   RowArgs a = {};
@@ -671,10 +689,12 @@ int mxw_quantize_rows(const void* x, int type, int64_t ldx, int64_t R, int C, in
       (type != MXW_BF16 && type != MXW_F32) || (format != MXW_MXFP8 && format != MXW_MXFP4))
     return MXW_ERR_DIM;
   if (R && (!x || !q || !s)) return MXW_ERR_NULL;
-  if (!on(x, type == MXW_F32 ? 4 : 2) || !on(q, 8)) return MXW_ERR_ALIGN;
+  const int size = type == MXW_F32 ? 4 : 2;
+  if (!on(x, size) || !on(q, 8)) return MXW_ERR_ALIGN;
   QuantArgs a = {x, ldx, R * (C >> 3), C >> 3, q, s};
   const int64_t blocks = (a.chunks + 256 * kUnroll - 1) / (256 * kUnroll);
   if (blocks > 0x7FFFFFFF / 256) return MXW_ERR_DIM;  // threads of a launch are counted in 32 bits
+  if (overlap<3>({{q, R * C / (format == MXW_MXFP4 ? 2 : 1)}, {s, R * C / 32}, {x, R, ldx, C, size}}, 2)) return MXW_ERR_OVERLAP;
   if (const int rc = check_device()) return rc;
   if (R == 0) return MXW_OK;
   const bool nt = past_caches(R * C * (type == MXW_F32 ? 5 : 3));

@@ -131,6 +131,63 @@ def test_linear_host_checks(over, code):
     assert call(mxw.mxw_linear_4bit, LINEAR, over) == code
 
 
+def apart(base, **sizes):
+    """The call's arguments, every address its own MiB."""
+    names = [n for n, v in base.items() if v == P]
+    return dict(base, **{n: (i + 1) << 20 for i, n in enumerate(names)}, **sizes)
+
+
+@pytest.mark.parametrize("f,base,pairs", [
+    (mxw.mxw_sort_tokens, apart(SORT, T=9000), [("offs", "ids"), ("rows", "ids"), ("counts", "offs"), ("workspace", "rows")]),
+    (mxw.mxw_dispatch_tokens, apart(DISPATCH), [("xs", "x"), ("q", "x"), ("s", "q"), ("xs", "s"), ("xs", "offs"), ("q", "rows"),
+                                                ("s", "counts")]),
+    (mxw.mxw_combine_tokens, apart(COMBINE), [("out", "y"), ("out", "rows"), ("out", "weights")]),
+    (mxw.mxw_combine_tokens_grad, apart(GRAD), [("dy", "dout"), ("q", "dout"), ("dy", "q"), ("s", "y"), ("q", "y"),
+                                                ("dweights", "weights"), ("dweights", "y"), ("dy", "rows"), ("dy", "dweights")]),
+    (mxw.mxw_quantize_rows, apart(ROWS), [("q", "x"), ("s", "x"), ("s", "q")]),
+    (mxw.mxw_linear_4bit, apart(LINEAR), [("out", "x"), ("out", "codes"), ("out", "scales")]),
+])
+def test_overlaps_are_refused(f, base, pairs):
+    """An output at an input's address or another output's, or that begins in its last
+    bytes (a workspace lies on 256)."""
+    for out, other in pairs:
+        by = 256 if out == "workspace" else 16
+        assert f(**dict(base, **{out: base[other]})) == -8, (out, other)
+        assert f(**dict(base, **{out: base[other] + by})) == -8, (out, other)
+        assert f(**dict(base, **{other: base[out] + by})) == -8, (out, other)
+
+
+def test_overlaps_that_are_meant():
+    """The residual in place and dy over y pass this check (and meet the next), other
+    strides do not, nor does a residual that begins inside the output."""
+    c, g = apart(COMBINE), apart(GRAD)
+    past = mxw.mxw_combine_tokens(**dict(c, T=0))   # what a call that passes every check gives here
+    assert past != -8
+    same = dict(c, residual=c["out"])
+    assert call(mxw.mxw_combine_tokens, same, dict(residual=c["out"] + 2)) == -8
+    assert call(mxw.mxw_combine_tokens, same, dict(ldr=72)) == -8
+    same = dict(g, dy=g["y"])
+    assert call(mxw.mxw_combine_tokens_grad, same, dict(dy=g["y"] + 2)) == -8
+    assert call(mxw.mxw_combine_tokens_grad, same, dict(ldy=72)) == -8
+    if not torch.cuda.is_available():   # with a device these would run
+        assert mxw.mxw_combine_tokens(**dict(c, residual=c["out"])) == past
+        assert mxw.mxw_combine_tokens_grad(**same) == past
+        # an output that ends where the input begins
+        assert call(mxw.mxw_quantize_rows, apart(ROWS), dict(q=(1 << 20) - 640, s=9 << 20)) == past
+    # the norm inside a gradient that is scaled
+    far = dict(CLIP, grads=[P, 2 * P], outs=[P, 2 * P], workspace=16 * P)
+    assert call(mxw.mxw_clip_grads, far, dict(norm=P + 196)) == -8
+
+
+def test_sizes_past_32_bits_are_refused():
+    """They would reach the library cut to 32 bits."""
+    big = 1 << 32
+    for f in (lambda: mxw.token_rows(big + 4, 2, 8), lambda: mxw.sort_workspace_size(4, 2, big + 8),
+              lambda: mxw.token_rows(4, 2, 8, big + 32)):
+        with pytest.raises(ValueError):
+            f()
+
+
 def test_python_faces_validate():
     """CPU tensors (there is no host fallback), types, shapes and strides."""
     ids = torch.zeros((4, 2), dtype=torch.int64)
