@@ -188,12 +188,7 @@ __device__ __forceinline__ void pad_rows(const RowArgs& a, int b) {
   for (int64_t r = start + max(a.counts[e], 0) + b % a.pad_split; r < end; r += a.pad_split) {
     const Raw8<F32> zero = {};
     for (int c = threadIdx.x * 8; c < a.H; c += 256 * 8) {
-      if (ROWS) {
-        if (c + 8 <= a.H)
-          store8<F32>(a.out, r * a.H + c, zero);
-        else
-          store_some<F32>(a.out, r * a.H + c, zero, a.H - c);
-      }
+      if (ROWS) store_row<F32, false, false>(a.out, r * a.H, c, a.H, zero);
       if (MX) {
         *(i2*)(a.q + r * a.H + c) = (i2){0, 0};
         if (!(c & 31)) a.s[r * (a.H >> 5) + (c >> 5)] = 127;
@@ -203,7 +198,7 @@ __device__ __forceinline__ void pad_rows(const RowArgs& a, int b) {
 }
 
 // xs[row[t][j]] = x[t]: a token is read once, by W waves, and stored to its k rows.
-template <bool F32, bool ROWS, bool MX, int W, bool NT>
+template <bool F32, bool ROWS, bool MX, int W, bool NT, bool SHARED>
 __global__ __launch_bounds__(256) void dispatch_kernel(RowArgs a) {
   if ((int)blockIdx.x < a.pad_blocks) return pad_rows<F32, ROWS, MX>(a, blockIdx.x);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -218,10 +213,7 @@ __global__ __launch_bounds__(256) void dispatch_kernel(RowArgs a) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int c = c0 + u * W * 512;
-      if (c + 8 <= a.H)
-        v[u] = load8<F32, NT>(a.x, from + c);
-      else if (c < a.H)
-        v[u] = load_some<F32>(a.x, from + c, a.H - c);
+      if (c < a.H) v[u] = load_row<F32, NT, SHARED>(a.x, from, c, a.H);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
@@ -237,12 +229,7 @@ __global__ __launch_bounds__(256) void dispatch_kernel(RowArgs a) {
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const int c = c0 + u * W * 512;
-        if (ROWS) {
-          if (c + 8 <= a.H)
-            store8<F32, NT>(a.out, r * a.H + c, v[u]);
-          else if (c < a.H)
-            store_some<F32>(a.out, r * a.H + c, v[u], a.H - c);
-        }
+        if (ROWS && c < a.H) store_row<F32, NT, SHARED>(a.out, r * a.H, c, a.H, v[u]);
         if (MX && c < a.H) {
           store<NT>((i2*)(a.q + r * a.H + c), q[u]);
           if (!(c & 31)) a.s[r * (a.H >> 5) + (c >> 5)] = (uint8_t)s[u];
@@ -265,13 +252,12 @@ __device__ __forceinline__ void choices(const RowArgs& a, int t, int j0, int (&r
 }
 
 // out[t] = sum_j w[t][j] y[row[t][j]] (+ residual[t]), in the order of the choices
-template <bool F32, bool WEIGHTS, int W, bool NT>
+template <bool F32, bool WEIGHTS, int W, bool NT, bool SHARED>
 __global__ __launch_bounds__(256) void combine_kernel(RowArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t = blockIdx.x * (4 / W) + wave / W;
   if (t >= a.T) return;
   for (int c = ((wave % W) * 64 + (threadIdx.x & 63)) * 8; c < a.H; c += W * 512) {
-    const int n = min(a.H - c, 8);
     float sum[8] = {};
     for (int j0 = 0; j0 < a.k; j0 += 8) {
       int r[8];
@@ -280,7 +266,7 @@ __global__ __launch_bounds__(256) void combine_kernel(RowArgs a) {
       Raw8<F32> v[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        if (r[u] >= 0) v[u] = n == 8 ? load8<F32, NT>(a.y, r[u] * a.ldy + c) : load_some<F32>(a.y, r[u] * a.ldy + c, n);
+        if (r[u] >= 0) v[u] = load_row<F32, NT, SHARED>(a.y, r[u] * a.ldy, c, a.H);
 #pragma unroll
       for (int u = 0; u < 8; ++u)
         if (r[u] >= 0) {
@@ -292,14 +278,11 @@ __global__ __launch_bounds__(256) void combine_kernel(RowArgs a) {
     }
     if (a.residual) {
       float f[8];
-      values<F32>(n == 8 ? load8<F32>(a.residual, t * a.ldr + c) : load_some<F32>(a.residual, t * a.ldr + c, n), f);
+      values<F32>(load_row<F32, false, SHARED>(a.residual, t * a.ldr, c, a.H), f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum[i] += f[i];
     }
-    if (n == 8)
-      store8<F32, NT>(a.out, (int64_t)t * a.H + c, rounded<F32>(sum));
-    else
-      store_some<F32>(a.out, (int64_t)t * a.H + c, rounded<F32>(sum), n);
+    store_row<F32, NT, SHARED>(a.out, (int64_t)t * a.H, c, a.H, rounded<F32>(sum));
   }
 }
 
@@ -320,7 +303,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 
 // dy[row[t][j]] = w[t][j] dout[t], dw[t][j] = <dout[t], y[row[t][j]]>, by one wave a token or
 // the workgroup's four
-template <bool F32, bool ROWS, bool MX, int W, bool NT>
+template <bool F32, bool ROWS, bool MX, int W, bool NT, bool SHARED>
 __global__ __launch_bounds__(256) void combine_grad_kernel(RowArgs a) {
   __shared__ float red[4][8];
   if ((int)blockIdx.x < a.pad_blocks) return pad_rows<F32, ROWS, MX>(a, blockIdx.x);
@@ -334,28 +317,23 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(RowArgs a) {
     for (int c = ((wave % W) * 64 + lane) * 8; c < a.H; c += W * 512) {
       const int n = min(a.H - c, 8);
       float d[8];
-      values<F32>(n == 8 ? load8<F32>(a.x, t * a.ldx + c) : load_some<F32>(a.x, t * a.ldx + c, n), d);
+      values<F32>(load_row<F32, false, SHARED>(a.x, t * a.ldx, c, a.H), d);
       Raw8<F32> v[8];
       if (a.dweights) {
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-          if (r[u] >= 0) v[u] = n == 8 ? load8<F32, NT>(a.y, r[u] * a.ldy + c) : load_some<F32>(a.y, r[u] * a.ldy + c, n);
+          if (r[u] >= 0) v[u] = load_row<F32, NT, SHARED>(a.y, r[u] * a.ldy, c, a.H);
       }
       if (ROWS || MX) {
 #pragma unroll
         for (int u = 0; u < 8; ++u)
           if (r[u] >= 0) {
-            const int64_t at = (int64_t)r[u] * a.H + c;
+            const int64_t row = (int64_t)r[u] * a.H, at = row + c;
             float f[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) f[i] = w[u] * d[i];
             const Raw8<F32> o = rounded<F32>(f);
-            if (ROWS) {
-              if (n == 8)
-                store8<F32, NT>(a.out, at, o);
-              else
-                store_some<F32>(a.out, at, o, n);
-            }
+            if (ROWS) store_row<F32, NT, SHARED>(a.out, row, c, a.H, o);
             if (MX) {
               values<F32>(o, f);
               const int s = block_scale<8>(block_top(f));
@@ -365,6 +343,17 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(RowArgs a) {
           }
       }
       if (a.dweights) {
+        if (SHARED && n < 8) {   // the lane before sums the first 8 - n
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[i] = i + n >= 8 ? d[i] : 0.0f;
+#pragma unroll
+          for (int i = 0; i < (F32 ? 8 : 4); ++i) {
+            const int own = F32 ? (i + n >= 8 ? -1 : 0)
+                                : (2 * i + n >= 8 ? 0xFFFF : 0) | (2 * i + 1 + n >= 8 ? (int)0xFFFF0000u : 0);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u].v[i >> 2][i & 3] &= own;
+          }
+        }
 #pragma unroll
         for (int u = 0; u < 8; ++u)
           if (r[u] >= 0) {
@@ -487,6 +476,9 @@ void with_waves(int H, bool nt, F f) {
   H <= ONE ? w(std::integral_constant<int, 1>{}) : w(std::integral_constant<int, 4>{});
 }
 
+// whether lanes may share columns (load_row): not where one stores over what another reads
+bool may_share(int H, bool in_place) { return !(H & 7) || (H > 8 && !in_place); }
+
 // Loads and stores past the caches where a call moves more than they hold (256 MB): 262,144
 // rows of 2048 joined in 199 us, with cached ones 228; 65,536 rows of 7168 quantised in 221 and
 // 239.  Below that whoever reads the result next finds it there: 4,096 tokens through 8 of 32
@@ -575,9 +567,13 @@ int mxw_dispatch_tokens(const void* x, int type, int64_t ldx, const int32_t* off
   hipStream_t st = (hipStream_t)stream;
   auto go = [&](auto f32, auto with_rows, auto mx) {
     constexpr bool F = decltype(f32)::value, RW = decltype(with_rows)::value, M = decltype(mx)::value;
+    if (!M && !may_share(H, false)) {
+      dispatch_kernel<F, RW, false, 1, false, false><<<dim3(pads + (T + 3) / 4), dim3(256), 0, st>>>(a);
+      return;
+    }
     with_waves<512, 1024>(H, nt, [&](auto w, auto past) {
       constexpr int W = decltype(w)::value, per = 4 / W;   // tokens of a workgroup
-      dispatch_kernel<F, RW, M, W, decltype(past)::value><<<dim3(pads + (T + per - 1) / per), dim3(256), 0, st>>>(a);
+      dispatch_kernel<F, RW, M, W, decltype(past)::value, true><<<dim3(pads + (T + per - 1) / per), dim3(256), 0, st>>>(a);
     });
   };
   using Y = std::true_type;
@@ -616,12 +612,18 @@ int mxw_combine_tokens(const void* y, int type, int64_t ldy, const int32_t* rows
   a.y = y, a.ldy = ldy, a.rows = rows, a.weights = weights, a.residual = residual, a.ldr = ldr;
   a.T = T, a.k = k, a.H = H, a.R = R, a.out = out;
   const bool nt = past_caches((int64_t)T * H * size * (k + 1));
+  const bool shared = may_share(H, residual == out);
   hipStream_t st = (hipStream_t)stream;
   auto go = [&](auto f32, auto wt) {
     constexpr bool F = decltype(f32)::value, WT = decltype(wt)::value;
     with_waves<1024, 1536>(H, nt, [&](auto w, auto past) {
       constexpr int W = decltype(w)::value, per = 4 / W;
-      combine_kernel<F, WT, W, decltype(past)::value><<<dim3((T + per - 1) / per), dim3(256), 0, st>>>(a);
+      constexpr bool P = decltype(past)::value;
+      const dim3 grid((T + per - 1) / per);
+      if (shared)
+        combine_kernel<F, WT, W, P, true><<<grid, dim3(256), 0, st>>>(a);
+      else
+        combine_kernel<F, WT, W, P, false><<<grid, dim3(256), 0, st>>>(a);
     });
   };
   using Y = std::true_type;
@@ -659,13 +661,19 @@ int mxw_combine_tokens_grad(const void* dout, int type, int64_t ldo, const void*
   a.x = dout, a.ldx = ldo, a.y = y, a.ldy = ldy, a.offs = offs, a.counts = counts, a.rows = rows, a.weights = weights;
   a.T = T, a.k = k, a.E = E, a.H = H, a.R = R, a.out = dy, a.q = q, a.s = s, a.dweights = dweights;
   const int pads = dy || q ? plan_pads(a) : 0;
+  const bool shared = may_share(H, dweights && dy == y);
   const bool nt = past_caches((int64_t)T * H * (size + k * ((dweights ? size : 0) + (dy ? size : 0) + (q ? 1 : 0))));
   hipStream_t st = (hipStream_t)stream;
   auto go = [&](auto f32, auto with_rows, auto mx) {
     constexpr bool F = decltype(f32)::value, RW = decltype(with_rows)::value, M = decltype(mx)::value;
     with_waves<1536, 1536>(H, nt, [&](auto w, auto past) {
       constexpr int W = decltype(w)::value, per = 4 / W;
-      combine_grad_kernel<F, RW, M, W, decltype(past)::value><<<dim3(pads + (T + per - 1) / per), dim3(256), 0, st>>>(a);
+      constexpr bool P = decltype(past)::value;
+      const dim3 grid(pads + (T + per - 1) / per);
+      if (M || shared)
+        combine_grad_kernel<F, RW, M, W, P, true><<<grid, dim3(256), 0, st>>>(a);
+      else
+        combine_grad_kernel<F, RW, false, W, P, false><<<grid, dim3(256), 0, st>>>(a);
     });
   };
   using Y = std::true_type;

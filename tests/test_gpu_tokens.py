@@ -361,6 +361,53 @@ def test_grad_in_y_itself():
         assert got is y and same_bits(y[:end], dy[:end]) and same_bits(again, dw)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H", [3, 7, 8, 9, 15, 115, 501, 1001, 2047, 3949])
+def test_in_place_at_row_ends(H, dtype):
+    """Rows that end inside a lane's 8 columns: the same bits in place (out over the
+    residual, dy over y) as into other tensors, again and again."""
+    T, k, E = 700, 9, 16
+    say("in place %s H=%d" % (dtype, H))
+    ids = make_ids(T, k, E, 70, 0.2)
+    plan = mxw.sort_tokens(ids, E)
+    x, w = values((T, H), 71, dtype), torch.rand((T, k), device=DEV)
+    y = values((plan.size, H), 72, dtype)
+    out = mxw.combine_tokens(y, plan, w, residual=x)
+    dy, dw = mxw.combine_tokens_grad(x, y, plan, w)
+    end = plan.offs[-1].item()
+    for _ in range(4):
+        there = x.clone()
+        assert same_bits(mxw.combine_tokens(y, plan, w, residual=there, out=there), out)
+        there = y.clone()
+        got, gw = mxw.combine_tokens_grad(x, there, plan, w, dy=there)
+        assert got is there and same_bits(got[:end], dy[:end]) and same_bits(gw, dw)
+        assert same_bits(got[end:], y[end:])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H", [9, 15, 115, 2047])
+def test_infinities_before_a_row_end(H, dtype):
+    """An infinity in a column that lanes share counts once, as an infinity, and a NaN in
+    y's meets no other."""
+    T, k, E = 40, 2, 4
+    ids = make_ids(T, k, E, 73)
+    plan = mxw.sort_tokens(ids, E)
+    for col in {max(H - 8, 0), H // 8 * 8 - 1, H - 1}:
+        dout = torch.ones((T, H), dtype=dtype, device=DEV)
+        y = torch.ones((plan.size, H), dtype=dtype, device=DEV)
+        dout[3, col] = float("inf")
+        y[plan.rows[7, 1].item(), col] = float("nan")
+        w = torch.ones((T, k), device=DEV)
+        dy, dw = mxw.combine_tokens_grad(dout, y, plan, w)
+        want = torch.full((T, k), float(H), device=DEV)
+        want[3] = float("inf")
+        want[7, 1] = float("nan")
+        assert torch.equal(dw.nan_to_num(nan=-1.0), want.nan_to_num(nan=-1.0))
+        out = mxw.combine_tokens(y, plan, w)
+        bad = out.isnan()
+        assert bad[7, col] and bad.sum() == 1
+
+
 def test_gradients_against_differences():
     """f(y, w) = <out, d> in float32: its central differences along random directions.
     f is linear in y and in w, so that a difference over 2 h is exact but for roundings:
