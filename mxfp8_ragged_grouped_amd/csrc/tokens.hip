@@ -14,8 +14,8 @@
 //
 // Measured, bytes read and written once (one MI355X; a large copy 4.9 to 5.2 TB/s, reading or
 // filling alone 6.9): 98,304 tokens of the 16B shape to 2 of 8 experts, bf16 and MXFP8 264 us
-// (6.1 TB/s); 32,768 tokens joined from 8 rows of 2048 199 us (6.1); the gradient of 16,384
-// tokens of the 671B shape, 8 rows each, 762 us (5.2, half of it stores); 65,536 x 7168 to
+// (6.1 TB/s); 32,768 tokens joined from 8 rows of 2048 202 us (6.0); the gradient of 16,384
+// tokens of the 671B shape, 8 rows each, 766 us (5.2, half of it stores); 65,536 x 7168 to
 // MXFP8 216 us (6.6).  One token: 3 us a kernel and the host's call.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
