@@ -464,10 +464,11 @@ int launched() { return hipGetLastError() == hipSuccess ? MXW_OK : MXW_ERR_LAUNC
 
 // f(W, NT) with the waves of a token and the way past the caches as constants.  W waves take
 // 512 W columns at a time; 4 leave few tokens spread over the device, and fewer have less idle
-// lanes at a short row's end and, in the gradient, sums to join: rows of 2048, bf16, 8 each for
-// 32,768 tokens joined 199 us with 4, 206 with 2, 213 with 1; of 1500, 4 each for 30,000, 116
-// with 4 and 107 with 2; their gradients at 1280 155, 125 and 117; rows of 1284 dispatched, 8
-// each for 10,253 tokens, 69, 75 and 82.
+// lanes at a short row's end and, in the gradient, sums to join.  30,000 tokens joined from 4
+// rows, with 1, 2 and 4 waves: 600 columns bf16 44, 41 and 46 us, 900 float32 115, 111 and 114,
+// 1100 75, 68 and 68, 1500 95, 87 and 81; 32,768 from 8 of 2048 217, 208 and 202.  Dispatched to 2:
+// 501 columns 28.6, 28.8 and 30.0, 1001 48, 47 and 51, 1284 to 8 76, 65 and 65.  Gradients, 1 and 4:
+// 1024 columns 50 and 85, 1501 93 and 103, 1700 113 and 103.
 template <int ONE, int TWO, class F>
 void with_waves(int H, bool nt, F f) {
   auto w = [&](auto c) { nt ? f(c, std::true_type{}) : f(c, std::false_type{}); };
@@ -616,7 +617,7 @@ int mxw_combine_tokens(const void* y, int type, int64_t ldy, const int32_t* rows
   hipStream_t st = (hipStream_t)stream;
   auto go = [&](auto f32, auto wt) {
     constexpr bool F = decltype(f32)::value, WT = decltype(wt)::value;
-    with_waves<1024, 1536>(H, nt, [&](auto w, auto past) {
+    with_waves<512, 1024>(H, nt, [&](auto w, auto past) {
       constexpr int W = decltype(w)::value, per = 4 / W;
       constexpr bool P = decltype(past)::value;
       const dim3 grid((T + per - 1) / per);
