@@ -168,7 +168,7 @@ __global__ __launch_bounds__(256) void scale_kernel(NormArgs a) {
   const float factor = ratio >= 1.0 ? 1.0f : (float)(low ? ratio * 0x1p126 : ratio);  // NaN: NaN
   for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
     const Item& it = a.item[item_of(a, tile)];
-    if (factor == 1.0f && it.g == it.out) continue;
+    if (!low && factor == 1.0f && it.g == it.out) continue;  // low: a rest that rounds to 1 still stands beside 2^-126
     const int64_t at = (int64_t)(tile - it.first) * kTileElems;
     if (it.f32)
       tile_scale<true, NT>(it, at, power, factor);

@@ -122,6 +122,30 @@ def test_edges_of_max_norm():
     assert all(torch.equal(g, o) for g, o in zip(grads, out))
 
 
+@pytest.mark.parametrize("norm_type", [2, INF])
+@pytest.mark.parametrize("max_norm", [2.0 ** -126 * (1 - 2.0 ** -30), 2.0 ** -126 * (1 - 2.0 ** -20), 2.0 ** -126,
+                                      2.0 ** -126 * (1 + 2.0 ** -30), 2.0 ** -127, 1.7 * 2.0 ** -133, 2.0 ** -149])
+def test_factors_below_float32s_normal_range(max_norm, norm_type):
+    """In place as into other tensors.  The norm is 1 exactly, so the factor is max_norm,
+    and 2^-126 (1 - 2^-30) is 2^-126 and a rest that rounds to 1."""
+    say("clip in place by a factor of %g, norm %s" % (max_norm, norm_type))
+    first = torch.zeros(9000, device=DEV)
+    first[[0, 700, 8191, 8999]] = torch.tensor([0.5, -0.5, 0.5, -0.5], device=DEV) if norm_type == 2 else \
+        torch.tensor([0.5, -1.0, 0.25, 0.75], device=DEV)
+    grads = [first, torch.zeros(300, dtype=BF16, device=DEV)]
+    if norm_type == INF:
+        grads[1][7:9] = torch.tensor([-1.0, 0.375])
+    assert norm_of(grads, norm_type) == 1.0
+    out = [torch.full_like(g, float("nan")) for g in grads]
+    assert mxw.clip_grad_norm(grads, max_norm, norm_type, eps=0.0, out=out).item() == 1.0
+    inside = [g.clone() for g in grads]
+    assert mxw.clip_grad_norm(inside, max_norm, norm_type, eps=0.0).item() == 1.0
+    for g, o, i in zip(grads, out, inside):
+        close(o, g, max_norm)
+        close(i, g, max_norm)
+        assert torch.equal(i, o)
+
+
 def test_shapes_alignment_and_none():
     g = torch.Generator(device=DEV).manual_seed(6)
     room = torch.randn((3, 40, 50), generator=g, device=DEV)
