@@ -211,7 +211,6 @@ int mxw_clip_grads(const void* const* grads, void* const* outs, const int64_t* s
   // 366 us, 415); below that the scaled gradients stay for whoever reads them next.
   const bool nt = bytes > ((int64_t)256 << 20);
   if (tiles > 0x7FFFFFFF - kBlocks) return MXW_ERR_DIM;  // a workgroup counts up to kBlocks past them
-  bool norm_inside = false;
   if (outs && count) {  // what is written overlaps nothing but the gradient it comes from, at the same place
     struct Range {
       uintptr_t lo, hi;
@@ -234,11 +233,16 @@ int mxw_clip_grads(const void* const* grads, void* const* outs, const int64_t* s
     for (const Range& x : r) {
       if (x.lo < written || (x.written && x.lo < read)) return MXW_ERR_OVERLAP;
       (x.written ? written : read) = std::max(x.written ? written : read, x.hi);
-      norm_inside |= (uintptr_t)norm >= x.lo && (uintptr_t)norm < x.hi;
     }
   }
   if (!workspace || ((uintptr_t)workspace & 255) || workspace_bytes < (size_t)need) return MXW_ERR_WORKSPACE;
-  if (norm_inside) return MXW_ERR_OVERLAP;
+  // the norm and the workspace are written too, while the gradients are still read
+  const Span writes[2] = {{norm, 4}, {workspace, need}};
+  if (overlap<2>(writes, 2)) return MXW_ERR_OVERLAP;
+  for (int i = 0; i < count; ++i) {
+    const int64_t size = sizes[i] * (types[i] == MXW_F32 ? 4 : 2);
+    if (overlap<4>({writes[0], writes[1], {grads[i], size}, {outs ? outs[i] : nullptr, size}}, 2)) return MXW_ERR_OVERLAP;
+  }
   if (const int rc = check_device()) return rc;
   hipStream_t st = (hipStream_t)stream;
   const bool top = norm_type == MXW_NORM_MAX;

@@ -179,6 +179,36 @@ def test_overlaps_that_are_meant():
     assert call(mxw.mxw_clip_grads, far, dict(norm=P + 196)) == -8
 
 
+CLIP_APART = dict(CLIP, grads=[1 << 20, 2 << 20], outs=[3 << 20, 4 << 20], norm=5 << 20, workspace=6 << 20)   # bf16 [100], float32 [200]
+
+
+@pytest.mark.parametrize("outs", [CLIP_APART["outs"], CLIP_APART["grads"], None])
+def test_clip_norm_and_workspace_lie_apart(outs):
+    """The norm's four bytes and the workspace are written: they may share nothing with a
+    gradient, an output or each other, for the norm alone as for clipping."""
+    need = mxw.clip_workspace_size(2)
+    base = dict(CLIP_APART, outs=outs)
+    for at, size in list(zip(base["grads"], (200, 800))) + list(zip(outs or [], (200, 800))):
+        for norm in (at, at + 4, at + size - 4):
+            assert call(mxw.mxw_clip_grads, base, dict(norm=norm)) == -8, (at, norm)
+        for ws in (at, at + size // 256 * 256 - (256 if size % 256 == 0 else 0), at - need + 256 - need % 256):
+            assert ws % 256 == 0 and ws < at + size and ws + need > at
+            assert call(mxw.mxw_clip_grads, base, dict(workspace=ws)) == -8, (at, ws)
+    # a bf16 tensor may begin inside the norm
+    for name in ("grads", "outs"):
+        if base[name]:
+            assert call(mxw.mxw_clip_grads, base, {name: [base["norm"] + 2, base[name][1]]}) == -8, name
+    ws = base["workspace"]
+    for norm in (ws, ws + 256, ws + need - 4):
+        assert call(mxw.mxw_clip_grads, base, dict(norm=norm)) == -8, norm
+    if not torch.cuda.is_available():   # with a device these would run
+        past = mxw.mxw_combine_tokens(**dict(apart(COMBINE), T=0))   # what a call that passes every check gives here
+        for fine in (dict(), dict(norm=ws - 4), dict(norm=ws + need), dict(norm=base["grads"][0] - 4),
+                     dict(norm=base["grads"][0] + 200), dict(workspace=base["grads"][1] + 1024),
+                     dict(workspace=base["grads"][0] - need - (256 - need % 256) % 256)):
+            assert call(mxw.mxw_clip_grads, base, fine) == past != -8, fine
+
+
 def test_sizes_past_32_bits_are_refused():
     """They would reach the library cut to 32 bits."""
     big = 1 << 32
