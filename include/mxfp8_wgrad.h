@@ -779,8 +779,9 @@ int64_t mxw_clip_workspace_size(int count);
  *
  * The numbers that MXFP4 codes stand for are exact in bf16 where they are normal there
  * (below 2^-126 they are 0, beyond bf16's range infinity); integer codes and zeros enter as
- * whole numbers, summed apart, and each group's FP32 sums are scaled: an infinity in x then
- * gives NaN where the formula may give an infinity.  All sums are FP32.  A token's result
+ * whole numbers, summed apart, and each group's FP32 difference is scaled: an infinity in x then
+ * gives NaN where the formula may give an infinity, and a group's sums of x times its codes
+ * must stay in FP32's range (x up to 2^116 keeps them there).  All sums are FP32.  A token's result
  * does not depend on the other tokens' values; its last bits can depend on T and N, by which
  * K is split.  Bitwise reproducible run to run.
  * Effects: one kernel on `stream`, allocates nothing, keeps no state, does not

@@ -266,7 +266,7 @@ __global__ __launch_bounds__(WAVES * 64) void linear4_kernel(LinArgs a) {
     token[i] = (uint32_t)((PIECES ? 16 * i : min(16 * i + n, a.T - 1)) * per_row * 16);
 #pragma unroll
   for (int q = 0; q < 4; ++q) place[q] = (uint32_t)((PIECES ? n * per_row * 16 : 0) + (place_of(b, q) ^ n) * 16);
-  // A step's codes, and of its groups the scale and minus the scale times the zero, from slot d
+  // A step's codes, and of its groups the scale and minus the zero, from slot d
   constexpr int G = FP4 ? 1 : GC, Q = 4 / G;
   i4 codes[2][RT];
   float scale[2][RT][G], zero[2][RT][G];
@@ -284,7 +284,7 @@ __global__ __launch_bounds__(WAVES * 64) void linear4_kernel(LinArgs a) {
           const uint32_t s = *(const uint32_t*)(words + S::kScales + 4 * g);
           scale[h][j][g] = __uint_as_float(FP4 ? s << 23 : s << 16);
           if (!FP4)
-            zero[h][j][g] = -scale[h][j][g] * (a.zeros ? (float)*(const uint32_t*)(words + S::kZeros + 4 * g) : 8.0f);
+            zero[h][j][g] = a.zeros ? -(float)*(const uint32_t*)(words + S::kZeros + 4 * g) : -8.0f;
         }
       }
   };
@@ -335,7 +335,8 @@ __global__ __launch_bounds__(WAVES * 64) void linear4_kernel(LinArgs a) {
           for (int j = 0; j < RT; ++j)
 #pragma unroll
             for (int r = 0; r < R; ++r)
-              sum[j][i][r] = fmaf(scale[h][j][g], dot[j][r], fmaf(zero[h][j][g], all[r], sum[j][i][r]));
+              // the scale last: times a zero it may leave FP32's range where the sum does not
+              sum[j][i][r] = fmaf(scale[h][j][g], fmaf(zero[h][j][g], all[r], dot[j][r]), sum[j][i][r]);
         }
       }
     }

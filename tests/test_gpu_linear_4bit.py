@@ -163,6 +163,48 @@ def test_scales_at_the_ends():
     check(got[:, keep], x, codes[keep], scales[keep], None, "other rows")
 
 
+@pytest.mark.parametrize("scale", [255, 254, 253, 251, 2, 1, 0])
+def test_a_single_weight_under_scales_at_the_ends(scale):
+    """MXFP4: one code a row and one 1 a token (2^60 under the lowest scales, so that the
+    result is far from float32's ends), the rest zeros, so that an output is a single
+    weight.  In bf16's normal range it is exact, past it infinity (0 stays 0), below it 0
+    or exact, and under the NaN scale NaN."""
+    x0 = 1.0 if scale > 127 else 2.0 ** 60
+    for K, T, N in ((32, 1, 16), (288, 3, 16), (288, 20, 16 * 2100)):   # the last: two row tiles a wave
+        for place in (0, 13, K - 1):
+            codes = torch.zeros((N, K // 2), dtype=torch.uint8, device=DEV)
+            code = torch.arange(N, dtype=torch.uint8, device=DEV) % 16
+            codes[:, place // 2] = code << 4 * (place % 2)
+            scales = torch.full((N, K // 32), 127, dtype=torch.uint8, device=DEV)
+            scales[:, place // 32] = scale
+            x = torch.zeros((T, K), dtype=BF16, device=DEV)
+            x[T - 1, place] = x0
+            got = mxw.linear_4bit(x, codes, scales, dtype=F32, out=poisoned(T, N, F32))[T - 1].double()
+            if scale == 255:
+                assert got.isnan().all()
+                continue
+            v = E2M1[code.long()] * 2.0 ** (scale - 127)
+            low, high = (v != 0) & (v.abs() < 2.0 ** -126), v.abs() >= 2.0 ** 128
+            say("scale %d K=%d place %d: %d below, %d above" % (scale, K, place, int(low.sum()), int(high.sum())))
+            assert torch.equal(got[~low & ~high], v[~low & ~high] * x0)
+            assert torch.equal(got[high], torch.sign(v[high]) * float("inf"))
+            assert ((got[low] == 0) | (got[low] == v[low] * x0)).all()
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("scale,tokens", [(126, -100), (124, -60), (-126, 100), (-133, 60)])
+def test_integers_under_scales_at_the_ends(scale, tokens, group):
+    """Scales that times a zero leave float32's range, or that are bf16's smallest, with
+    tokens that bring the result back: the definition's value."""
+    for T, K, N, zeros in ((1, 256, 40, True), (5, 640, 100, False), (40, 1152, 33, True), (20, 256, 34000, True)):
+        say("linear_4bit scale 2^%d T=%d K=%d N=%d group=%d" % (scale, T, K, N, group))
+        x, codes, scales, z = make(T, K, N, group, K + group, zeros)
+        size = torch.rand(scales.shape, generator=torch.Generator(device=DEV).manual_seed(3), device=DEV) + 1.0
+        scales = (torch.copysign(size, scales.float()) * 2.0 ** scale).to(BF16)
+        x = (x.float() * 2.0 ** tokens).to(BF16)
+        check(mxw.linear_4bit(x, codes, scales, zeros=z, dtype=F32), x, codes, scales, z, "scale 2^%d" % scale)
+
+
 @pytest.mark.parametrize("group", [None, 32, 128])
 def test_tokens_stay_apart(group):
     """No token's bits depend on the others' values, NaN and infinity among them."""
