@@ -818,8 +818,8 @@ _TYPES = {torch.bfloat16: 0, torch.float32: 1}
 
 def _fits(*sizes):
     """ctypes would cut sizes past 32 bits without a word."""
-    if max(sizes) > 0x7FFFFFFF:
-        raise ValueError("sizes past 2^31 - 1: %s" % (sizes,))
+    if max(sizes) > 0x7FFFFFFF or min(sizes) < -0x80000000:
+        raise ValueError("sizes past 32 bits: %s" % (sizes,))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -1138,6 +1138,7 @@ def quantize_rows(x, format="mxfp8", q=None, s=None, stream=None):
 def clip_workspace_size(count):
     """Bytes of workspace clip_grad_norm and grad_norm need for so many tensors.
     Raises MxwError on a status code."""
+    _fits(int(count))
     rc = _load().mxw_clip_workspace_size(int(count))
     if rc < 0:
         raise MxwError("mxw_clip_workspace_size failed: %s" % strerror(rc))

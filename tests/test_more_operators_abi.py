@@ -218,6 +218,16 @@ def test_sizes_past_32_bits_are_refused():
             f()
 
 
+def test_sizes_past_32_bits_of_either_sign_are_refused():
+    """Cut to 32 bits, all of these would be sizes that the library takes."""
+    big = 1 << 32
+    for f in (lambda: mxw.token_rows(4 - big, 2, 8), lambda: mxw.token_rows(4, 2, 8 - big), lambda: mxw.token_rows(4, 2, 8, 32 - big),
+              lambda: mxw.sort_workspace_size(9000 - big, 2, 8), lambda: mxw.clip_workspace_size(big),
+              lambda: mxw.clip_workspace_size(big + 5), lambda: mxw.clip_workspace_size(5 - big)):
+        with pytest.raises(ValueError):
+            f()
+
+
 def test_python_faces_validate():
     """CPU tensors (there is no host fallback), types, shapes and strides."""
     ids = torch.zeros((4, 2), dtype=torch.int64)
