@@ -527,7 +527,8 @@ int mxw_sort_tokens(const void* ids, int id_bytes, int64_t ld, int T, int k, int
     constexpr bool I = decltype(i64)::value;
     constexpr int PER = decltype(per)::value;
     const int pieces = T ? (a.n + PER * kSortThreads - 1) / (PER * kSortThreads) : 1;
-    if (pieces > 1) sort_count_kernel<I, PER><<<dim3(pieces), dim3(kSortThreads), 0, st>>>(a);
+    if constexpr (PER > 1)   // 1: one piece
+      if (pieces > 1) sort_count_kernel<I, PER><<<dim3(pieces), dim3(kSortThreads), 0, st>>>(a);
     sort_place_kernel<I, PER><<<dim3(pieces), dim3(kSortThreads), 0, st>>>(a);
   };
   auto pieces = [&](auto i64) {
@@ -572,10 +573,11 @@ int mxw_dispatch_tokens(const void* x, int type, int64_t ldx, const int32_t* off
   hipStream_t st = (hipStream_t)stream;
   auto go = [&](auto f32, auto with_rows, auto mx) {
     constexpr bool F = decltype(f32)::value, RW = decltype(with_rows)::value, M = decltype(mx)::value;
-    if (!M && !may_share(a.H, false)) {
-      dispatch_kernel<F, RW, false, 1, false, false><<<dim3(pads + (T + 3) / 4), dim3(256), 0, st>>>(a);
-      return;
-    }
+    if constexpr (!M)   // MXFP8 rows are whole blocks
+      if (!may_share(a.H, false)) {
+        dispatch_kernel<F, RW, M, 1, false, false><<<dim3(pads + (T + 3) / 4), dim3(256), 0, st>>>(a);
+        return;
+      }
     with_waves<512, 1024>(a.H, nt, [&](auto w, auto past) {
       constexpr int W = decltype(w)::value, per = 4 / W;   // tokens of a workgroup
       dispatch_kernel<F, RW, M, W, decltype(past)::value, true><<<dim3(pads + (T + per - 1) / per), dim3(256), 0, st>>>(a);
@@ -677,8 +679,8 @@ int mxw_combine_tokens_grad(const void* dout, int type, int64_t ldo, const void*
       const dim3 grid(pads + (T + per - 1) / per);
       if (M || shared)
         combine_grad_kernel<F, RW, M, W, P, true><<<grid, dim3(256), 0, st>>>(a);
-      else
-        combine_grad_kernel<F, RW, false, W, P, false><<<grid, dim3(256), 0, st>>>(a);
+      else if constexpr (!M && (RW || W == 1))   // rows of under 8 columns, or dy over y
+        combine_grad_kernel<F, RW, M, W, P, false><<<grid, dim3(256), 0, st>>>(a);
     });
   };
   using Y = std::true_type;
