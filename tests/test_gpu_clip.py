@@ -204,6 +204,28 @@ def test_repeats_streams_and_graphs():
         assert all(torch.equal(o, e) for o, e in zip(out, eager))
 
 
+@pytest.mark.parametrize("norm_type", [2, INF])
+def test_more_than_the_caches_hold(norm_type):
+    """Over 256 MB in all, where loads and stores go past the caches: float32 and bf16, ends
+    inside 8 elements, more tensors than a launch takes, to others and in place."""
+    sizes = [30000003, 70000005, 20000001, 5, 8193] + [1000 + 7 * i for i in range(100)]
+    say("clip %d tensors, %d elements, norm %s" % (len(sizes), sum(sizes), norm_type))
+    grads = tensors(sizes, 8)
+    assert sum(g.numel() * g.element_size() for g in grads) > 1 << 28
+    n = norm_of(grads, norm_type)
+    assert abs(mxw.grad_norm(grads, norm_type).item() - n) <= 2.0 ** -24 * n
+    for max_norm in (0.25 * n, 4 * n):
+        out = [torch.full_like(g, float("nan")) for g in grads]
+        got = mxw.clip_grad_norm(grads, max_norm, norm_type, out=out)
+        assert abs(got.item() - n) <= 2.0 ** -24 * n
+        for g, o in zip(grads, out):
+            close(o, g, min(1.0, max_norm / (n + 1e-6)))
+        kept = [g.clone() for g in grads]
+        assert mxw.clip_grad_norm(grads, max_norm, norm_type).item() == got.item()
+        assert all(torch.equal(g, o) for g, o in zip(grads, out))
+        grads = kept
+
+
 def test_offsets_past_32_bits():
     """A tensor of over 2^31 elements whose last ones count."""
     n = (1 << 31) + 12345

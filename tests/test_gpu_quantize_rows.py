@@ -163,6 +163,25 @@ def test_offsets_past_32_bits():
         assert (q[:-3] == 0).all() and (s[:-3] == 127).all()
 
 
+@pytest.mark.parametrize("format", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_more_than_the_caches_hold(dtype, format):
+    """Over 256 MB in all, where loads and stores go past the caches: the bytes of the same
+    rows a part at a time, from rows together and from rows that start on any element."""
+    C, ld = 2080, 2083
+    R = (1 << 28) // (C * (5 if dtype == torch.float32 else 3)) + 777
+    say("quantize_rows R=%d C=%d %s %s" % (R, C, dtype, format))
+    g = torch.Generator(device=DEV).manual_seed(6)
+    wide = (torch.randn((R * ld + 1,), generator=g, device=DEV) * 3.0).to(dtype)
+    apart = torch.as_strided(wide, (R, C), (ld, 1), 1)
+    together = apart.contiguous()
+    parts = [mxw.quantize_rows(t, format) for t in together.split(R // 4 + 1)]
+    want = [torch.cat([p[i] for p in parts]) for i in range(2)]
+    for x in (together, apart):
+        q, s = mxw.quantize_rows(x, format, q=torch.full_like(want[0], 0xAA), s=torch.full_like(want[1], 0xAA))
+        assert torch.equal(q, want[0]) and torch.equal(s, want[1])
+
+
 def test_streams_and_graphs():
     g = torch.Generator(device=DEV).manual_seed(4)
     x = torch.randn((300, 160), generator=g, device=DEV)

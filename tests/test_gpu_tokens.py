@@ -499,6 +499,97 @@ def test_repeats_streams_and_graphs():
         same(kept, all_of(ids, x, dout, w))
 
 
+def past_the_caches(H, dtype, k=4, E=8):
+    """(plan, parts of it with a quarter of the tokens) of a call that moves over 256 MB,
+    where loads and stores go past the caches; a part's call moves less."""
+    T = (1 << 28) // (H * dtype.itemsize * (k + 1)) + 1001
+    say("over 256 MB: T=%d k=%d H=%d %s" % (T, k, H, dtype))
+    plan = mxw.sort_tokens(make_ids(T, k, E, H, 0.05), E)
+    cuts = [(a, min(a + T // 4 + 1, T)) for a in range(0, T, T // 4 + 1)]
+    return plan, [(slice(a, b), plan._replace(rows=plan.rows[a:b].contiguous())) for a, b in cuts]
+
+
+LONG = [501, 512, 901, 1024, 1501, 1701, 2048]   # one, two and four waves a token, whole rows and shared ends
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H", LONG)
+def test_dispatch_past_the_caches(H, dtype):
+    plan, parts = past_the_caches(H, dtype)
+    x = values((plan.rows.shape[0], H), 70, dtype)
+    got, want = poison((plan.size, H), dtype), poison((plan.size, H), dtype)
+    mxw.dispatch_tokens(x, plan, out=got)
+    for at, part in parts:
+        mxw.dispatch_tokens(x[at], part, out=want)
+    assert same_bits(got, want) and not got[:plan.offs[-1].item()].isnan().any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H", [480, 992, 1504])
+@pytest.mark.parametrize("rows", [True, False])
+def test_dispatch_mxfp8_past_the_caches(H, dtype, rows):
+    plan, parts = past_the_caches(H, dtype, k=8 if dtype == BF16 else 4)
+    T, k = plan.rows.shape
+    if not rows:   # codes alone are fewer bytes: the tokens count more than once
+        T = (1 << 28) // (H * (dtype.itemsize + k)) + 1001
+        plan = mxw.sort_tokens(make_ids(T, k, 8, H, 0.05), 8)
+        parts = [(slice(a, a + T // 4 + 1), plan._replace(rows=plan.rows[a:a + T // 4 + 1].contiguous()))
+                 for a in range(0, T, T // 4 + 1)]
+    x = values((T, H), 71, dtype)
+    both = []
+    for _ in range(2):
+        both.append((poison((plan.size, H), dtype) if rows else None, poison((plan.size, H), torch.uint8),
+                     poison((plan.size, H // 32), torch.uint8)))
+    mxw.dispatch_tokens(x, plan, rows=rows, mxfp8=True, out=both[0][0], q=both[0][1], s=both[0][2])
+    for at, part in parts:
+        mxw.dispatch_tokens(x[at], part, rows=rows, mxfp8=True, out=both[1][0], q=both[1][1], s=both[1][2])
+    for got, want in zip(*both):
+        assert got is want is None or same_bits(got, want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H", LONG)
+def test_combine_past_the_caches(H, dtype):
+    """With weights and a residual, into another tensor and into the residual itself."""
+    plan, parts = past_the_caches(H, dtype)
+    T, k = plan.rows.shape
+    y, r = values((plan.size, H), 72, dtype), values((T, H), 73, dtype)
+    w = torch.rand((T, k), device=DEV)
+    want = torch.cat([mxw.combine_tokens(y, part, w[at].contiguous(), residual=r[at]) for at, part in parts])
+    got = mxw.combine_tokens(y, plan, w, residual=r, out=poison((T, H), dtype))
+    assert same_bits(got, want) and not got.isnan().any()
+    mxw.combine_tokens(y, plan, w, residual=r, out=r)
+    assert same_bits(r, want)
+    want = torch.cat([mxw.combine_tokens(y, part) for at, part in parts])
+    assert same_bits(mxw.combine_tokens(y, plan, out=poison((T, H), dtype)), want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H", LONG)
+def test_grad_past_the_caches(H, dtype):
+    """Into other tensors, with MXFP8 rows where the row has whole blocks, and over y itself."""
+    plan, parts = past_the_caches(H, dtype)
+    T, k = plan.rows.shape
+    y, dout = values((plan.size, H), 74, dtype), values((T, H), 75, dtype)
+    w = torch.rand((T, k), device=DEV)
+    mx = H % 32 == 0
+
+    def outputs():
+        both = dict(dy=poison((plan.size, H), dtype))
+        if mx:
+            both.update(q=poison((plan.size, H), torch.uint8), s=poison((plan.size, H // 32), torch.uint8))
+        return both
+
+    got, want = outputs(), outputs()
+    dw = mxw.combine_tokens_grad(dout, y, plan, w, mxfp8=mx, **got)[-1]
+    dws = [mxw.combine_tokens_grad(dout[at], y, part, w[at].contiguous(), mxfp8=mx, **want)[-1] for at, part in parts]
+    assert all(same_bits(got[n], want[n]) for n in got) and same_bits(dw, torch.cat(dws))
+    assert not dw.isnan().any() and not got["dy"][:plan.offs[-1].item()].isnan().any()
+    dw = mxw.combine_tokens_grad(dout, y, plan, w, dy=y)[-1]
+    end = plan.offs[-1].item()
+    assert same_bits(dw, torch.cat(dws)) and same_bits(y[:end], want["dy"][:end])
+
+
 def test_offsets_past_32_bits():
     """Rows whose offsets pass 2^31 elements and 2^32 bytes."""
     T, k, E, H = 40000, 8, 4, 7168
