@@ -748,7 +748,8 @@ int mxw_quantize_rows(const void* x, int type, int64_t ldx, int64_t R, int C, in
  * Squares are summed in 64 bits: the norm neither overflows nor vanishes before FP32
  * does.  The product with the factor is FP32, rounded once.  A NaN makes the norm and
  * all outputs NaN; an infinity makes the norm infinite and the factor 0 (its own element
- * NaN), unless max_norm is infinite too (NaN).  Bitwise reproducible run to run.
+ * NaN), unless max_norm is infinite too (NaN).  Where n + eps is 0 the factor is 1.  Bitwise
+ * reproducible run to run.
  * Effects: enqueues two kernels for every 96 tensors (one more if there are more) on
  * `stream`, allocates nothing on the device, keeps no state, does not synchronise; graph-capturable (the addresses are
  * the kernels' arguments).

@@ -161,7 +161,8 @@ __global__ __launch_bounds__(256) void scale_kernel(NormArgs a) {
   v = block_join<TOP>(v);
   const double norm = TOP ? v : sqrt(v);
   if (blockIdx.x == 0 && threadIdx.x == 0 && a.norm) *a.norm = (float)norm;
-  const double ratio = a.max_norm / (norm + a.eps);
+  const double over = norm + a.eps;
+  const double ratio = over == 0.0 ? 1.0 : a.max_norm / over;   // 0: zeros, which any factor keeps
   // a factor below FP32's normal range goes as two, so that it keeps its 24 bits
   const bool low = ratio < 0x1p-126;
   const float power = low ? 0x1p-126f : 1.0f;

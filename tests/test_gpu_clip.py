@@ -146,6 +146,18 @@ def test_factors_below_float32s_normal_range(max_norm, norm_type):
         assert torch.equal(i, o)
 
 
+@pytest.mark.parametrize("norm_type", [2, INF])
+def test_zeros_with_nothing_to_divide_by(norm_type):
+    """norm, eps and max_norm all 0: zeros stay zeros, of their sign, in place and elsewhere."""
+    for max_norm in (0.0, 1.0):
+        grads = [torch.zeros(9000, device=DEV), -torch.zeros(11, dtype=BF16, device=DEV)]
+        out = [torch.full_like(g, float("nan")) for g in grads]
+        assert mxw.clip_grad_norm(grads, max_norm, norm_type, eps=0.0, out=out).item() == 0
+        assert all(torch.equal(o.view(torch.uint8), g.view(torch.uint8)) for o, g in zip(out, grads))
+        assert mxw.clip_grad_norm(grads, max_norm, norm_type, eps=0.0).item() == 0
+        assert all(torch.equal(o.view(torch.uint8), g.view(torch.uint8)) for o, g in zip(out, grads))
+
+
 def test_shapes_alignment_and_none():
     g = torch.Generator(device=DEV).manual_seed(6)
     room = torch.randn((3, 40, 50), generator=g, device=DEV)
