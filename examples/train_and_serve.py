@@ -9,7 +9,8 @@ MXFP8 operands (fwd, quantize_rows), the loss over the vocabulary with its gradi
 (vocab_cross_entropy), the experts' weight gradients (wgrad), the gradients' clipping
 (clip_grad_norm) and the orthogonalised updates (orthogonalize).  Afterwards the same
 experts, quantised once more, answer single tokens and small batches (moe_layer), with the
-words' logits from 4-bit weights (linear_4bit).
+words' logits from 4-bit weights (linear_4bit): a quarter of the bytes of bf16 words, with one
+bit behind the leading one instead of seven, a loss of precision that this task's logits bear.
 
 The task is synthetic: the next word is a fixed function of the current one, so
 a table look-up through the experts can learn it.  The embedding and the router

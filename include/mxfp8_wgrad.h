@@ -654,8 +654,9 @@ int64_t mxw_sort_workspace_size(int T, int k, int E);
  *   xs       [R, H] of `type`, contiguous, or NULL.
  *   q, s     uint8 [R, H] and [R, H/32], contiguous, or both NULL; q 8-byte aligned.
  * What is written overlaps neither itself nor an input (MXW_ERR_OVERLAP, as in
- * mxw_sort_tokens and the entries below; strided rows count with what lies between them).  Effects: one kernel on `stream`, allocates nothing,
- * keeps no state, does not synchronise; graph-capturable.
+ * mxw_sort_tokens and the entries below; strided rows count with what lies between them).
+ * Effects: one kernel on `stream`, allocates nothing, keeps no state, does not synchronise;
+ * graph-capturable.
  */
 int mxw_dispatch_tokens(const void* x, int type, int64_t ldx, const int32_t* offs, const int32_t* counts,
                         const int32_t* rows, int T, int k, int E, int H, int R, void* xs, uint8_t* q, uint8_t* s,
@@ -737,7 +738,8 @@ int mxw_quantize_rows(const void* x, int type, int64_t ldx, int64_t R, int C, in
  *   grads, outs, sizes, types  HOST arrays of `count` entries, read during the call:
  *            device addresses, element counts (0 .. 2^40; a NULL address with 0) and
  *            MXW_BF16 or MXW_F32.  outs[i] may be grads[i] (in place); otherwise nothing
- *            that is written may overlap (MXW_ERR_OVERLAP).  outs NULL: the norm alone.
+ *            that is written (norm and workspace too) may overlap (MXW_ERR_OVERLAP).  outs
+ *            NULL: the norm alone.
  *   count    0 .. MXW_MAX_TENSORS (0: norm 0).
  *   norm_type  MXW_NORM_2 or MXW_NORM_MAX.   max_norm, eps  >= 0.
  *   norm     DEVICE memory, one FP32: n before clipping.
@@ -746,13 +748,14 @@ int mxw_quantize_rows(const void* x, int type, int64_t ldx, int64_t R, int C, in
  *            in use until the call's work is done.
  *
  * Squares are summed in 64 bits: the norm neither overflows nor vanishes before FP32
- * does.  The product with the factor is FP32, rounded once.  A NaN makes the norm and
+ * does.  The product with the factor is FP32 (by 2^-126 first where the factor is below that),
+ * rounded once more for bf16 outputs.  A NaN makes the norm and
  * all outputs NaN; an infinity makes the norm infinite and the factor 0 (its own element
  * NaN), unless max_norm is infinite too (NaN).  Where n + eps is 0 the factor is 1.  Bitwise
  * reproducible run to run.
  * Effects: enqueues two kernels for every 96 tensors (one more if there are more) on
- * `stream`, allocates nothing on the device, keeps no state, does not synchronise; graph-capturable (the addresses are
- * the kernels' arguments).
+ * `stream`, allocates nothing on the device, keeps no state, does not synchronise;
+ * graph-capturable (the addresses are the kernels' arguments).
  */
 int mxw_clip_grads(const void* const* grads, void* const* outs, const int64_t* sizes, const int32_t* types, int count,
                    int norm_type, double max_norm, double eps, float* norm, void* workspace, size_t workspace_bytes,
@@ -778,13 +781,13 @@ int64_t mxw_clip_workspace_size(int count);
  *   T        0 .. MXW_MOE_MAX_TOKENS.  N  1 .. 2^20.  K  a multiple of group, up to 65536.
  *   out, out_type  [T, N] MXW_BF16 or MXW_F32, contiguous, fully overwritten.
  *
- * The numbers that MXFP4 codes stand for are exact in bf16 where they are normal there
- * (below 2^-126 they are 0, beyond bf16's range infinity); integer codes and zeros enter as
- * whole numbers, summed apart, and each group's FP32 difference is scaled: an infinity in x then
- * gives NaN where the formula may give an infinity, and a group's sums of x times its codes
- * must stay in FP32's range (x up to 2^116 keeps them there).  All sums are FP32.  A token's result
- * does not depend on the other tokens' values; its last bits can depend on T and N, by which
- * K is split.  Bitwise reproducible run to run.
+ * The numbers that MXFP4 codes stand for enter as bf16, exactly, subnormals included (2^128
+ * and beyond as infinity); integer codes and zeros enter as whole numbers, summed apart, and
+ * each group's FP32 difference is scaled: an infinity in x then gives NaN where the formula may
+ * give an infinity, and a group's sums of x times its codes must stay in FP32's range (x up to
+ * 2^116 keeps them there).  All sums are FP32.  A token's result does not depend on the other
+ * tokens' values; its last bits can depend on T and N, by which K is split.  Bitwise
+ * reproducible run to run.
  * Effects: one kernel on `stream`, allocates nothing, keeps no state, does not
  * synchronise; graph-capturable.
  */

@@ -958,8 +958,8 @@ def dispatch_tokens(x, plan, rows=True, mxfp8=False, out=None, q=None, s=None, s
     they were (uninitialised in new tensors; the grouped products do not read them).
     `out`, `q` and `s` (optional) are contiguous tensors of any one number of rows:
     rows that they do not have are skipped.  They may not share memory with an input.
-    The gradient with respect to x is combine_tokens(dxs, plan).  Runs on `stream` (default: the current stream) and does
-    not synchronise."""
+    The gradient with respect to x is combine_tokens(dxs, plan).  Runs on `stream` (default:
+    the current stream) and does not synchronise."""
     ldx = _matrix(x, "x", None)
     dev = x.device
     offs, counts, where, R, T, k, E = _plan(plan, dev)
@@ -1226,9 +1226,10 @@ def clip_grad_norm(grads, max_norm, norm_type=2.0, eps=1e-6, out=None, stream=No
     norm_type), in place or into the tensors of `out` (one for every gradient, of its
     type, shape and strides).  Returns the norm before clipping.
 
-    The factor is float32 and the product rounded once to the gradient's type.  A NaN
-    makes everything NaN; an infinity makes the norm infinite and the factor 0.  No two
-    gradients may share memory.  Arguments otherwise as grad_norm."""
+    The factor and the product are float32; the product is then rounded to the gradient's
+    type.  A NaN makes everything NaN; an infinity makes the norm infinite and the factor 0;
+    where norm + eps is 0 the factor is 1.  No two gradients may share memory, nor a gradient
+    and the workspace.  Arguments otherwise as grad_norm."""
     if not (max_norm >= 0.0 and eps >= 0.0):
         raise ValueError("max_norm and eps must not be negative")
     grads = _grads(grads)

@@ -10,14 +10,16 @@
 // and 16 weight rows as the second, so that a lane holds sums of one weight row and its
 // group's scale is a number of the lane's own.
 //
-// Measured (one MI355X, other weights from call to call): 128,000 rows of K 7168, one token
-// 89 us (MXFP4, 5.5 TB/s of codes and scales; reading alone reaches 7.0), 97 (integers, groups
-// of 128), 124 (groups of 32); 64 tokens 135, 198 and 303: there a step's products (96 of 16
-// cycles a wave, a third of them the tokens' own sums for the zeros), its other operations
-// (340 of 4) and its bytes each take a third to a half of the time, and two waves a SIMD
-// overlap them poorly; other orders of the same work (products and decoding alternating,
-// deeper prefetch of either operand, priorities, 16 waves) gained nothing or lost.  32,000 rows
-// of K 2048, one token: 8.9 us, of which launch and first loads take half.
+// Measured (one MI355X, other weights from call to call, 300 calls in a row): 128,000 rows of K
+// 7168, one token 87 us (MXFP4, 5.6 TB/s of codes and scales; reading alone reaches 7.0), 96
+// (integers, groups of 128), 123 (groups of 32); 64 tokens 144, 210 and 316 (the first hundred
+// calls after a pause up to a third longer, until the clock has settled): there operations
+// bound it, not memory.  A step's products (96 of 16 cycles a wave, a third of them the tokens'
+// own sums for the zeros) keep the matrix unit busy for 40% of the time and its other
+// operations (340 of 4 to 5 cycles) the vector unit for about as much; other orders of the same
+// work (products and decoding alternating, deeper prefetch of either operand, priorities, 16
+// waves) gained nothing or lost.  32,000 rows of K 2048, one token: 8.9 us, of which launch and
+// first loads take half.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -457,8 +459,10 @@ template <int GC>
 int launch(const LinArgs& a, hipStream_t st) {
   const int tiles = (a.N + 15) / 16;
   // More tiles than one for each wave of a full device: two a wave, so that each read of the
-  // tokens serves both (64 tokens, K 7168, integers: 34,000 rows 59 us for MXFP4, with one 76;
-  // 32,000 rows, one round either way, 90 and 65).
+  // tokens serves both (64 tokens, K 7168: 34,000 rows of MXFP4 60 us, with one 76; 32,000 rows
+  // of integers, one round either way, 90 and 65).  A round is then 65,536 rows, and row counts
+  // between rounds pay for a whole one, up to twice a full one's time a row: MXFP4, 64 tokens,
+  // 34,000 rows 60 us, 66,000 126, 100,000 132, 128,000 144; one token 38, 74, 81 and 87.
   const bool wide = tiles > 2048;
   if (a.T == 1) return wide ? launch<GC, 1, 2, 1, 8, 4, 1>(a, st) : launch<GC, 1, 1, 2, 8, 4, 1>(a, st);
   if (a.T <= 16) return wide ? launch<GC, 1, 2, 1, 8, 4>(a, st) : launch<GC, 1, 1, 2, 8, 4>(a, st);
